@@ -90,7 +90,13 @@ enum {
     QSW_CNT_QMM_GEMV = 3,     /* affine_qmm, small-M kernel */
     QSW_CNT_SILU_MUL = 4,     /* elementwise silu*mul */
     QSW_CNT_GEMV_STREAM = 5,  /* small-M calls (fused or affine_qmm) served by the warp-streamed kernel */
-    QSW_NUM_COUNTERS = 6
+    QSW_CNT_FP4_QUANTIZE = 6,
+    QSW_CNT_FP4_DEQUANTIZE = 7,
+    QSW_CNT_FP4_LINEAR = 8,   /* qsw_fp4_linear and qsw_fp4_grouped_linear */
+    QSW_CNT_MOE_ROUTE = 9,
+    QSW_CNT_FP4_MOE = 10,     /* qsw_fp4_moe_mlp */
+    QSW_CNT_NORM = 11,        /* qsw_rms_norm and qsw_post_norm */
+    QSW_NUM_COUNTERS = 12
 };
 
 /*
@@ -248,6 +254,140 @@ QSW_API int qsw_get_stream_k(void);
  */
 QSW_API qsw_status qsw_silu_mul(const void *g, const void *u, int64_t n, int variant,
                         void *out, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Operators around the MLP block: microscaled 4-bit floating point, products
+ * grouped by expert, routing, norms.  Inference only, like the rest of the
+ * library (the weights are codes).  Same ownership, execution and error rules
+ * as above.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Microscaled 4-bit formats: e2m1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their
+ * negatives; sign in bit 3), two per byte with the even element in the low
+ * nibble, and one scale per block of consecutive elements of a row.
+ *   QSW_FP4_MX  blocks of 32, scale 2^(floor(log2 amax) - 2) held as E8M0
+ *   QSW_FP4_NV  blocks of 16, scale E4M3(amax / (6 g)) times g, one positive
+ *               f32 g for the whole tensor (the `scale` arguments below; they
+ *               must be 1 for QSW_FP4_MX)
+ * A code is the e2m1 value nearest to x / scale, ties to even, saturating at 6.
+ * A block that holds an infinity or a NaN gets the scale NaN.
+ *
+ * A [rows, K] matrix is `codes`, rows * K/2 bytes, and `scales`, blocks of 128
+ * rows by 4 scales of 512 bytes, row blocks outermost: row r, scale j is byte
+ *     512 * ((r / 128) * ceil(K / (4 * block)) + j / 4)
+ *     + 16 * (r % 32) + 4 * ((r / 32) % 4) + j % 4.
+ * Bytes of rows past the last are never read for their values; those of scales
+ * past the last must be 0 (qsw_fp4_quantize writes them).  A stack of matrices
+ * is their codes and their scale blocks one after the other.
+ */
+typedef enum {
+    QSW_FP4_MX = 0,
+    QSW_FP4_NV = 1
+} qsw_fp4_format;
+
+/* Bytes of the scale blocks of `groups` matrices [rows, K]; 0 for arguments
+ * that no call accepts. */
+QSW_API size_t qsw_fp4_scale_bytes(int64_t groups, int64_t rows, int64_t K, int fmt);
+
+/* Quantise x [groups, rows, K] (act_dtype) to codes and scales, and back.
+ * K a multiple of 32; all pointers 16-byte aligned. */
+QSW_API qsw_status qsw_fp4_quantize(const void *x, int64_t groups, int64_t rows, int64_t K, int fmt, float scale,
+                           int act_dtype, uint8_t *codes, uint8_t *scales, void *stream);
+QSW_API qsw_status qsw_fp4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t groups, int64_t rows,
+                           int64_t K, int fmt, float scale, int act_dtype, void *out, void *stream);
+
+/*
+ * y[M, N] = T( Q(x) . W^T ): x [M, K] is quantised to the weights' format (with
+ * the tensor scale x_scale) into the workspace, then multiplied on the
+ * block-scaled tensor core with f32 accumulation.  W: codes [N, K/2] and scale
+ * blocks, w_scale a device pointer to its f32 tensor scale (NULL: 1).  K a
+ * multiple of 32; x, w, w_scales 16-byte aligned, workspace 256-byte aligned
+ * with at least qsw_fp4_workspace_bytes(M, K, 1, fmt) bytes.  The workspace
+ * need not be cleared; calls that can run concurrently must not share it.
+ */
+QSW_API size_t qsw_fp4_workspace_bytes(int64_t rows, int64_t K, int groups, int fmt);
+QSW_API qsw_status qsw_fp4_linear(const void *x, int64_t M, int64_t K, int64_t N, int fmt, float x_scale,
+                           const uint8_t *w, const uint8_t *w_scales, const float *w_scale, int act_dtype,
+                           void *y, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * The same with the rows of x sorted by group and a matrix per group: rows
+ * offsets[e] .. offsets[e+1] - 1 are multiplied with W[e] (codes [groups, N,
+ * K/2], a stack's scale blocks, w_scale [groups] or NULL).  offsets is
+ * [groups + 1] int32 on the device, not decreasing from 0 to rows; a group may
+ * be empty.  Offsets outside that are clamped to it (nothing is read or written
+ * out of range); rows that no group covers are left unwritten.  At most 1024
+ * groups.
+ */
+QSW_API qsw_status qsw_fp4_grouped_linear(const void *x, int64_t rows, int64_t K, int64_t N, int groups,
+                           const int *offsets, int fmt, float x_scale, const uint8_t *w,
+                           const uint8_t *w_scales, const float *w_scale, int act_dtype, void *y,
+                           void *workspace, size_t workspace_bytes, void *stream);
+
+/* Logits may also be f32. */
+enum { QSW_LOGITS_F32 = 2 };
+typedef enum {
+    QSW_ROUTE_SOFTMAX = 0,   /* weights are a softmax over all logits */
+    QSW_ROUTE_SIGMOID = 1    /* weights are 1 / (1 + e^-logit) */
+} qsw_route_scoring;
+
+/*
+ * Routing: per token the k largest of E logits (the lowest index first among
+ * equals; NaN counts as -infinity) and their weights, largest logit first.
+ * renormalize: the chosen weights are divided by their sum; then all are
+ * multiplied by `scale`.  A row without any logit above -infinity gets the
+ * weights 0.
+ *   ids      int32 [T, k]  experts        weights  f32 [T, k]
+ *   offsets  int32 [E + 1] first row of each expert in the expert-sorted order
+ *   slots    int32 [T, k]  row of (token, choice) in that order
+ *   order    int32 [T * k] the pair token * k + choice of each row
+ * Rows of one expert are in token order.  E <= 1024, k <= 32; ids 16-byte
+ * aligned.  logit_dtype: qsw_act_dtype or QSW_LOGITS_F32.
+ */
+QSW_API qsw_status qsw_moe_route(const void *logits, int64_t T, int E, int k, int logit_dtype, int scoring,
+                           int renormalize, float scale, int *ids, float *weights, int *offsets, int *slots,
+                           int *order, void *stream);
+
+/*
+ * The MLP of a mixture of experts, with the routing of qsw_moe_route:
+ *     hidden = silu(Q(x) . Wg[e]^T) * (Q(x) . Wu[e]^T)          in f32
+ *     y[t]   = T( residual[t] + sum_j weights[t, j] T(Q(hidden) . Wd[e]^T) )
+ * with x [T, H] quantised with the tensor scale x_scale and hidden with h_scale.
+ * wgu is [E, 2 I, H/2] with gate and up rows in alternating runs of 16 (rows
+ * 32 i .. 32 i + 15 are gate features 16 i .. 16 i + 15, the next 16 the same
+ * features' up rows), wd [E, H, I/2]; gu_scale and d_scale [E] or NULL.  H and
+ * I multiples of 32.  residual [T, H] or NULL; it may be y.  A token's experts
+ * must be distinct, as qsw_moe_route's are.  Each expert's row is rounded to T
+ * before the weighted sum, which is one f32 sum per token in the order of its
+ * choices: the same bits every time.
+ */
+QSW_API size_t qsw_fp4_moe_workspace_bytes(int64_t T, int k, int64_t H, int64_t I, int E, int fmt);
+QSW_API qsw_status qsw_fp4_moe_mlp(const void *x, int64_t T, int64_t H, int64_t I, int E, int k, int fmt,
+                           float x_scale, float h_scale, const float *weights, const int *offsets,
+                           const int *slots, const int *order, const uint8_t *wgu, const uint8_t *wgu_scales,
+                           const float *gu_scale, const uint8_t *wd, const uint8_t *wd_scales,
+                           const float *d_scale, const void *residual, int act_dtype, void *y,
+                           void *workspace, size_t workspace_bytes, void *stream);
+
+/* out = T( x * rsqrt(mean(x^2) + eps) * weight ), weight [H] or NULL (1).
+ * Any H up to 32768; statistics in f32. */
+QSW_API qsw_status qsw_rms_norm(const void *x, const void *weight, int64_t rows, int64_t H, float eps,
+                           int act_dtype, void *out, void *stream);
+
+/*
+ * What stands between two blocks, in one pass over the rows:
+ *     z     = y * rsqrt(mean(y^2) + eps) * w_post     (norm_y; else z = y)
+ *     h'    = h + scale * gate * z                     h_out = T(h')
+ *     n_out = T( h' * rsqrt(mean(h'^2) + eps) * w_next )
+ * n_out is computed from h' before it is rounded.  w_post, w_next [H] or NULL
+ * (1); n_out may be NULL.  gate: NULL, or [gate_rows, gate_cols] with gate_cols
+ * H or 1 and gate_rows a divisor of rows: row r takes gate row
+ * r / (rows / gate_rows).  h_out may be h, n_out may be y.
+ */
+QSW_API qsw_status qsw_post_norm(const void *h, const void *y, int norm_y, const void *w_post, const void *gate,
+                           int64_t gate_rows, int64_t gate_cols, float scale, const void *w_next, int64_t rows,
+                           int64_t H, float eps, int act_dtype, void *h_out, void *n_out, void *stream);
 
 /* Synchronise `stream`, then read and clear the device error word.
  * Returns QSW_ERR_BOUNDS if a debug-build check failed (libqswiglu_debug.so

@@ -163,6 +163,12 @@ qsw_status fused_forward(const void *x, int64_t M, int64_t H, int64_t I, const u
 
 }  // namespace
 
+namespace qsw {
+int device_sm_count() { return sm_count(); }
+uint64_t wait_timeout_ns() { return g_timeout_ns.load(); }
+void count_call(int counter) { g_counters[counter].fetch_add(1, std::memory_order_relaxed); }
+}  // namespace qsw
+
 extern "C" {
 
 qsw_status qswiglu_forward_ex(const void *x, int64_t M, int64_t H, int64_t I, const uint32_t *wg, const void *sg,
@@ -288,12 +294,13 @@ qsw_status qsw_silu_mul(const void *g, const void *u, int64_t n, int variant, vo
 
 qsw_status qsw_check_device_errors(void *stream) {
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return QSW_ERR_CUDA;
-  unsigned int a = 0, b = 0, c = 0;
+  unsigned int a = 0, b = 0, c = 0, d = 0;
   if (qsw::prefill_take_errors(&a) != cudaSuccess) return QSW_ERR_CUDA;
   if (qsw::gemv_take_errors(&b) != cudaSuccess) return QSW_ERR_CUDA;
   if (qsw::gemv_stream_take_errors(&c) != cudaSuccess) return QSW_ERR_CUDA;
-  if ((a | b | c) & qsw::DEVERR_BOUNDS) return QSW_ERR_BOUNDS;
-  return (a | b | c) ? QSW_ERR_TIMEOUT : QSW_OK;
+  if (qsw::fp4_gemm_take_errors(&d) != cudaSuccess) return QSW_ERR_CUDA;
+  if ((a | b | c | d) & qsw::DEVERR_BOUNDS) return QSW_ERR_BOUNDS;
+  return (a | b | c | d) ? QSW_ERR_TIMEOUT : QSW_OK;
 }
 
 void qsw_set_gemv_max_m(int m) {
@@ -347,6 +354,6 @@ const char *qsw_status_string(qsw_status s) {
   }
 }
 
-int qsw_version(void) { return 105; }
+int qsw_version(void) { return 106; }
 
 }  // extern "C"

@@ -76,6 +76,65 @@ cudaError_t launch_prefill(const void *x, int64_t M, int64_t K, int64_t N, const
 cudaError_t launch_silu_mul(const void *g, const void *u, int64_t n, int variant, int act, void *out,
                             cudaStream_t stream);
 
+// ------------------------------------------------- block operators ---------
+// Microscaled 4-bit products, routing and norms (qsw_fp4*.cu, qsw_moe.cu,
+// qsw_norm.cu).  `dependent`: launched as a programmatic dependent of the kernel
+// before it on the stream.
+
+// Quantise `groups` stacked [rows, K] matrices.
+cudaError_t launch_fp4_quantize(const void *x, int64_t groups, int64_t rows, int64_t K, int fmt, int act, float g,
+                                uint8_t *codes, uint8_t *scales, int num_sms, cudaStream_t stream);
+
+// Quantise rows sorted by group, each group's scale blocks starting a new row
+// block.  order: row r of the result is row order[r] / fan of x (null: row r).
+cudaError_t launch_fp4_quantize_ragged(const void *x, int64_t rows, int64_t K, const int *offsets, int groups,
+                                       const int *order, int fan, int fmt, int act, float g, uint8_t *codes,
+                                       uint8_t *scales, int num_sms, cudaStream_t stream, bool dependent);
+
+cudaError_t launch_fp4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t groups, int64_t rows,
+                                  int64_t K, int fmt, int act, float g, void *out, int num_sms, cudaStream_t stream);
+
+struct Fp4GemmArgs {
+  const uint8_t *x_codes, *x_scales;   // [rows, K] sorted by group, ragged scale blocks
+  int64_t rows, max_group;             // no group has more than max_group rows
+  const int *offsets;                  // [groups + 1] on the device; null: one group
+  int groups;
+  const uint8_t *w_codes, *w_scales;   // [groups, N, K]
+  int64_t N, K;
+  const float *w_scale;                // [groups] on the device; null: 1
+  float x_scale;
+  int fmt, act;
+  bool swiglu;                         // N = 2 I interleaved gate and up rows, result held in 4 bits
+  void *out;                           // linear: [rows, N] in the activation dtype
+  uint8_t *h_codes, *h_scales;         // swiglu: [rows, I], ragged scale blocks
+  float h_scale;
+};
+cudaError_t launch_fp4_gemm(const Fp4GemmArgs &a, int num_sms, uint64_t timeout_ns, cudaStream_t stream,
+                            bool dependent);
+cudaError_t fp4_gemm_take_errors(unsigned int *out);
+
+cudaError_t launch_moe_route(const void *logits, int logit_dtype, int64_t T, int E, int k, int scoring,
+                             int renormalize, float scale, int *ids, float *weights, int *offsets, int *slots,
+                             int *order, cudaStream_t stream);
+cudaError_t launch_moe_combine(const void *rows, int64_t n_rows, const int *slots, const float *weights,
+                               const void *residual, int64_t T, int k, int64_t H, int act, void *y,
+                               cudaStream_t stream, bool dependent);
+
+struct NormArgs {
+  const void *h, *y, *w_post, *gate, *w_next;
+  int64_t gate_rows, gate_cols;
+  int64_t rows, H;
+  int norm_y, act;
+  float scale, eps;
+  void *h_out, *n_out;
+};
+cudaError_t launch_norm(const NormArgs &a, cudaStream_t stream);
+
+// Shared state of the C entry points (qsw_api.cu).
+int device_sm_count();
+uint64_t wait_timeout_ns();
+void count_call(int counter);
+
 // Largest M the small-M kernel accepts.
 constexpr int64_t kGemvMaxM = 32;
 

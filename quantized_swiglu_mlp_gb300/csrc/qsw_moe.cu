@@ -1,0 +1,266 @@
+// The router of a mixture of experts and the combination of its experts' rows.
+//
+// topk_kernel: per token the k largest logits (the lowest index first among
+// equals) and their weights.  Selection looks at the logits themselves -- softmax
+// and sigmoid keep their order -- so it is exact whatever the exponential does.
+// sort_kernel: the stable counting sort of the (token, choice) pairs by expert.
+// combine_kernel: y[t] = T(sum_j weights[t, j] rows[slots[t, j]] (+ residual[t])),
+// each token summing its own rows in order: no atomics, the same bits every time.
+#include "qsw_fp4.cuh"
+#include "qsw_internal.h"
+
+namespace qsw {
+namespace {
+
+constexpr int kTopkWarps = 8;
+
+template <class L>
+__device__ __forceinline__ float load_logit(const L *p);
+template <>
+__device__ __forceinline__ float load_logit<float>(const float *p) { return __ldg(p); }
+template <>
+__device__ __forceinline__ float load_logit<ActBf16>(const ActBf16 *p) {
+  return ActBf16::lo(__ldg(reinterpret_cast<const unsigned short *>(p)));
+}
+template <>
+__device__ __forceinline__ float load_logit<ActF16>(const ActF16 *p) {
+  return ActF16::lo(__ldg(reinterpret_cast<const unsigned short *>(p)));
+}
+
+// A float's bits in an order-preserving unsigned form that is never 0; NaN
+// counts as -infinity, -0 as +0.
+__device__ __forceinline__ uint32_t order_key(float v) {
+  if (v != v) v = -INFINITY;
+  const uint32_t b = __float_as_uint(v + 0.0f);
+  return (b & 0x80000000u) ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k);
+}
+
+// One warp per token; lane l holds experts l, l + 32, ... (PER of them).  Each of
+// the k rounds takes the warp's largest key and, among its holders, the lowest
+// index (key 0: taken or past the end).
+template <class L, int PER>
+__global__ void __launch_bounds__(kTopkWarps * 32)
+    topk_kernel(const L *__restrict__ logits, int64_t T, int E, int k, int scoring, int renormalize, float scale,
+                int *ids, float *weights) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * kTopkWarps + (threadIdx.x >> 5);
+  if (t >= T) return;
+  const int wide = static_cast<int>(sizeof(L) == 4 ? 1 : 0);
+  const uint8_t *row = reinterpret_cast<const uint8_t *>(logits) + t * E * (wide ? 4 : 2);
+  uint32_t key[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int e = lane + 32 * i;
+    key[i] = e < E ? order_key(load_logit<L>(reinterpret_cast<const L *>(row + e * (wide ? 4 : 2)))) : 0u;
+  }
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) top = max(top, key[i]);
+  top = __reduce_max_sync(0xffffffffu, top);
+  const float peak = key_value(top);
+  const bool none = peak == -INFINITY;      // every logit masked: all weights 0
+  float sum = 0.0f;
+  if (scoring == QSW_ROUTE_SOFTMAX && !renormalize) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const float v = key_value(key[i]);
+      if (key[i]) sum += v == peak ? 1.0f : expf(v - peak);
+    }
+#pragma unroll
+    for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  }
+  // round j's choice stays with lane j
+  float mine = 0.0f;
+  int id = 0;
+  for (int j = 0; j < k; ++j) {
+    uint32_t best = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) best = max(best, key[i]);
+    best = __reduce_max_sync(0xffffffffu, best);
+    int at = 0x7FFFFFFF;
+#pragma unroll
+    for (int i = PER - 1; i >= 0; --i)
+      if (key[i] == best) at = lane + 32 * i;
+    at = __reduce_min_sync(0xffffffffu, at);
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (at == lane + 32 * i) key[i] = 0;
+    const float v = key_value(best);
+    float p;
+    if (scoring == QSW_ROUTE_SIGMOID)
+      p = 1.0f / (1.0f + expf(-v));
+    else
+      p = none ? 0.0f : v == peak ? 1.0f : expf(v - peak);
+    if (lane == j) {
+      mine = p;
+      id = at;
+    }
+    if (renormalize) sum += p;
+  }
+  if (lane < k) {
+    float w = mine;
+    if (scoring == QSW_ROUTE_SOFTMAX || renormalize) w = sum > 0.0f ? mine / sum : 0.0f;
+    ids[t * k + lane] = id;
+    weights[t * k + lane] = w * scale;
+  }
+}
+
+constexpr int kSortThreads = 1024;
+
+// One CTA per expert e.  Each thread scans a contiguous run of the T k ids and
+// counts those below e and those equal to it; the block's exclusive sums give
+// the expert's first row and each match's place, in the order of the pairs.
+// Ids outside [0, E) are ignored (their slot is -1).
+__global__ void __launch_bounds__(kSortThreads)
+    sort_kernel(const int *__restrict__ ids, int64_t n, int E, int *offsets, int *slots, int *order) {
+  griddep_wait();
+  griddep_launch_dependents();
+  __shared__ int warp_eq[32], warp_lt[32];
+  const int e = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t per = ((n + blockDim.x - 1) / blockDim.x + 3) & ~int64_t(3);
+  const int64_t a = tid * per < n ? tid * per : n, b = a + per < n ? a + per : n;
+  int eq = 0, lt = 0;
+  int64_t i = a;
+  for (; i + 4 <= b; i += 4) {
+    const int4 v = __ldg(reinterpret_cast<const int4 *>(ids + i));
+    eq += (v.x == e) + (v.y == e) + (v.z == e) + (v.w == e);
+    lt += (v.x >= 0 && v.x < e) + (v.y >= 0 && v.y < e) + (v.z >= 0 && v.z < e) + (v.w >= 0 && v.w < e);
+  }
+  for (; i < b; ++i) {
+    const int v = __ldg(ids + i);
+    eq += v == e;
+    lt += v >= 0 && v < e;
+  }
+  int incl = eq;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, incl, d);
+    if (lane >= d) incl += o;
+  }
+  lt = __reduce_add_sync(0xffffffffu, lt);
+  if (lane == 31) {
+    warp_eq[warp] = incl;
+    warp_lt[warp] = lt;
+  }
+  __syncthreads();
+  const int warps = blockDim.x >> 5;
+  int before = 0, first = 0, total = 0;
+  for (int w = 0; w < warps; ++w) {
+    before += w < warp ? warp_eq[w] : 0;
+    total += warp_eq[w];
+    first += warp_lt[w];
+  }
+  if (tid == 0) {
+    offsets[e] = first;
+    if (e == E - 1) offsets[E] = first + total;
+  }
+  int at = first + before + incl - eq;
+  for (i = a; i < b; ++i) {
+    const int v = __ldg(ids + i);
+    if (v == e) {
+      slots[i] = at;
+      order[at] = static_cast<int>(i);
+      ++at;
+    } else if (e == 0 && (v < 0 || v >= E)) {
+      slots[i] = -1;
+    }
+  }
+}
+
+// One warp per token and run of 256 columns; 8 columns per lane.
+template <class A>
+__global__ void __launch_bounds__(256)
+    combine_kernel(const uint16_t *__restrict__ rows, int64_t n_rows, const int *__restrict__ slots,
+                   const float *__restrict__ weights, const uint16_t *residual, int64_t T, int k, int64_t H,
+                   int chunks, uint16_t *y) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int64_t w = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+  const int64_t t = w / chunks;
+  const int64_t h = (w - t * chunks) * 256 + lane * 8;
+  if (t >= T || h >= H) return;
+  float acc[8] = {};
+  if (residual) {
+    const uint4 v = *reinterpret_cast<const uint4 *>(residual + t * H + h);
+    const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      acc[2 * i] = A::lo(q[i]);
+      acc[2 * i + 1] = A::hi(q[i]);
+    }
+  }
+  for (int j = 0; j < k; ++j) {
+    const int s = __ldg(slots + t * k + j);
+    if (s < 0 || s >= n_rows) continue;
+    const float g = __ldg(weights + t * k + j);
+    const uint4 v = __ldg(reinterpret_cast<const uint4 *>(rows + static_cast<int64_t>(s) * H + h));
+    const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      acc[2 * i] = fmaf(g, A::lo(q[i]), acc[2 * i]);
+      acc[2 * i + 1] = fmaf(g, A::hi(q[i]), acc[2 * i + 1]);
+    }
+  }
+  *reinterpret_cast<uint4 *>(y + t * H + h) = make_uint4(A::pack2(acc[0], acc[1]), A::pack2(acc[2], acc[3]),
+                                                        A::pack2(acc[4], acc[5]), A::pack2(acc[6], acc[7]));
+}
+
+template <class L>
+cudaError_t launch_topk(const void *logits, int64_t T, int E, int k, int scoring, int renormalize, float scale,
+                        int *ids, float *weights, cudaStream_t stream) {
+  const dim3 grid(static_cast<unsigned>((T + kTopkWarps - 1) / kTopkWarps));
+  const auto *l = static_cast<const L *>(logits);
+#define QSW_TOPK(P) \
+  launch_on(topk_kernel<L, P>, grid, kTopkWarps * 32, 0, stream, false, l, T, E, k, scoring, renormalize, scale, ids, weights)
+  if (E <= 32) return QSW_TOPK(1);
+  if (E <= 64) return QSW_TOPK(2);
+  if (E <= 128) return QSW_TOPK(4);
+  if (E <= 256) return QSW_TOPK(8);
+  if (E <= 512) return QSW_TOPK(16);
+  return QSW_TOPK(32);
+#undef QSW_TOPK
+}
+
+}  // namespace
+
+cudaError_t launch_moe_route(const void *logits, int logit_dtype, int64_t T, int E, int k, int scoring,
+                             int renormalize, float scale, int *ids, float *weights, int *offsets, int *slots,
+                             int *order, cudaStream_t stream) {
+  cudaError_t e;
+  if (T > 0) {
+    if (logit_dtype == QSW_LOGITS_F32)
+      e = launch_topk<float>(logits, T, E, k, scoring, renormalize, scale, ids, weights, stream);
+    else if (logit_dtype == QSW_ACT_BF16)
+      e = launch_topk<ActBf16>(logits, T, E, k, scoring, renormalize, scale, ids, weights, stream);
+    else
+      e = launch_topk<ActF16>(logits, T, E, k, scoring, renormalize, scale, ids, weights, stream);
+    if (e != cudaSuccess) return e;
+  }
+  const int64_t n = T * k;
+  const int threads = n >= kSortThreads * 4 ? kSortThreads : n > 512 ? 256 : 64;
+  return launch_on(sort_kernel, dim3(static_cast<unsigned>(E)), threads, 0, stream, T > 0, ids, n, E, offsets, slots,
+                   order);
+}
+
+cudaError_t launch_moe_combine(const void *rows, int64_t n_rows, const int *slots, const float *weights,
+                               const void *residual, int64_t T, int k, int64_t H, int act, void *y,
+                               cudaStream_t stream, bool dependent) {
+  const int chunks = static_cast<int>((H + 255) / 256);
+  const dim3 grid(static_cast<unsigned>((T * chunks + 7) / 8));
+  const auto *r = static_cast<const uint16_t *>(rows);
+  const auto *res = static_cast<const uint16_t *>(residual);
+  auto *o = static_cast<uint16_t *>(y);
+  if (act == ActF16::kId)
+    return launch_on(combine_kernel<ActF16>, grid, 256, 0, stream, dependent, r, n_rows, slots, weights, res, T, k, H,
+                     chunks, o);
+  return launch_on(combine_kernel<ActBf16>, grid, 256, 0, stream, dependent, r, n_rows, slots, weights, res, T, k, H,
+                   chunks, o);
+}
+
+}  // namespace qsw

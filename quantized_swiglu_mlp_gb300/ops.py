@@ -15,9 +15,11 @@ library's *_ex entry points with that dtype.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
+from typing import NamedTuple
 
 import torch
 
@@ -28,18 +30,27 @@ DEBUG_LIB_PATH = os.path.join(_HERE, "lib", "libqswiglu_debug.so")   # built wit
 MATCH, F32, DEBUG_GATE, DEBUG_UP = 0, 1, 2, 3
 VARIANTS = {"match": MATCH, "f32": F32, "debug_gate": DEBUG_GATE, "debug_up": DEBUG_UP}
 CNT_FUSED_TC, CNT_FUSED_GEMV, CNT_QMM_TC, CNT_QMM_GEMV, CNT_SILU_MUL, CNT_GEMV_STREAM = range(6)
-NUM_COUNTERS = 6
+CNT_FP4_QUANTIZE, CNT_FP4_DEQUANTIZE, CNT_FP4_LINEAR, CNT_MOE_ROUTE, CNT_FP4_MOE, CNT_NORM = range(6, 12)
+NUM_COUNTERS = 12
 STATUS = {0: "QSW_OK", 1: "QSW_ERR_INVALID_ARG", 2: "QSW_ERR_UNSUPPORTED", 3: "QSW_ERR_CUDA",
           4: "QSW_ERR_TIMEOUT", 5: "QSW_ERR_BOUNDS"}
 STREAM_K_OFF, STREAM_K_AUTO, STREAM_K_ALWAYS = 0, 1, 2
 ACT_BF16, ACT_F16 = 0, 1
 SMALL_M_AUTO, SMALL_M_RING, SMALL_M_STREAM = 0, 1, 2
+FP4_MX, FP4_NV = 0, 1
+FP4_FORMATS = {"mx": FP4_MX, "nv": FP4_NV}
+FP4_BLOCK = {FP4_MX: 32, FP4_NV: 16}
+LOGITS_F32 = 2
+ROUTE_SOFTMAX, ROUTE_SIGMOID = 0, 1
 EXPORTED = ("qswiglu_forward", "affine_qmm", "qswiglu_forward_ws", "affine_qmm_ws", "qswiglu_forward_noalloc",
             "qswiglu_forward_ex", "affine_qmm_ex", "qsw_silu_mul_ex", "qsw_mlp_forward_ex", "qsw_workspace_bytes",
             "qsw_set_stream_k", "qsw_get_stream_k", "qsw_silu_mul", "qsw_check_device_errors",
             "qsw_set_gemv_max_m", "qsw_get_gemv_max_m", "qsw_set_early_weight_stream",
             "qsw_get_early_weight_stream", "qsw_set_small_m_kernel", "qsw_get_small_m_kernel", "qsw_set_wait_timeout_ns", "qsw_debug_withhold_next_fill", "qsw_debug_build",
-            "qsw_get_counters", "qsw_reset_counters", "qsw_status_string", "qsw_version")
+            "qsw_get_counters", "qsw_reset_counters", "qsw_status_string", "qsw_version",
+            "qsw_fp4_scale_bytes", "qsw_fp4_quantize", "qsw_fp4_dequantize", "qsw_fp4_workspace_bytes",
+            "qsw_fp4_linear", "qsw_fp4_grouped_linear", "qsw_moe_route", "qsw_fp4_moe_workspace_bytes",
+            "qsw_fp4_moe_mlp", "qsw_rms_norm", "qsw_post_norm")
 
 _lock = threading.Lock()
 _lib = None
@@ -101,6 +112,30 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.qsw_status_string.argtypes = [i32]
         lib.qsw_status_string.restype = ctypes.c_char_p
         lib.qsw_version.restype = i32
+        f32 = ctypes.c_float
+        lib.qsw_fp4_scale_bytes.argtypes = [i64, i64, i64, i32]
+        lib.qsw_fp4_scale_bytes.restype = sz
+        lib.qsw_fp4_quantize.argtypes = [p, i64, i64, i64, i32, f32, i32, p, p, p]
+        lib.qsw_fp4_quantize.restype = i32
+        lib.qsw_fp4_dequantize.argtypes = [p, p, i64, i64, i64, i32, f32, i32, p, p]
+        lib.qsw_fp4_dequantize.restype = i32
+        lib.qsw_fp4_workspace_bytes.argtypes = [i64, i64, i32, i32]
+        lib.qsw_fp4_workspace_bytes.restype = sz
+        lib.qsw_fp4_linear.argtypes = [p, i64, i64, i64, i32, f32, p, p, p, i32, p, p, sz, p]
+        lib.qsw_fp4_linear.restype = i32
+        lib.qsw_fp4_grouped_linear.argtypes = [p, i64, i64, i64, i32, p, i32, f32, p, p, p, i32, p, p, sz, p]
+        lib.qsw_fp4_grouped_linear.restype = i32
+        lib.qsw_moe_route.argtypes = [p, i64, i32, i32, i32, i32, i32, f32, p, p, p, p, p, p]
+        lib.qsw_moe_route.restype = i32
+        lib.qsw_fp4_moe_workspace_bytes.argtypes = [i64, i32, i64, i64, i32, i32]
+        lib.qsw_fp4_moe_workspace_bytes.restype = sz
+        lib.qsw_fp4_moe_mlp.argtypes = [p, i64, i64, i64, i32, i32, i32, f32, f32, p, p, p, p, p, p, p, p, p, p, p,
+                                        i32, p, p, sz, p]
+        lib.qsw_fp4_moe_mlp.restype = i32
+        lib.qsw_rms_norm.argtypes = [p, p, i64, i64, f32, i32, p, p]
+        lib.qsw_rms_norm.restype = i32
+        lib.qsw_post_norm.argtypes = [p, p, i32, p, p, i64, i64, f32, p, i64, i64, f32, i32, p, p, p]
+        lib.qsw_post_norm.restype = i32
         _lib = lib
         return lib
 
@@ -362,6 +397,296 @@ def unfused_swiglu(x, wg, sg, bg, gs_g, bits_g, wu, su, bu, gs_u, bits_u, varian
     g = affine_qmm(x, wg, sg, bg, gs_g, bits_g, stream=stream, workspace=workspace)
     u = affine_qmm(x, wu, su, bu, gs_u, bits_u, stream=stream, workspace=workspace)
     return qsw_silu_mul(g, u, variant, out=g, stream=stream)
+
+
+# ------------------------------------------------------------------------
+# Microscaled 4-bit floating point, experts, routing, norms.  Formats, layouts
+# and formulas: include/qswiglu.h.
+# ------------------------------------------------------------------------
+
+def _on(stream):
+    """Context in which buffers belong to `stream`, so that the allocator does
+    not hand them to other streams' work while that stream still uses them."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream)
+                             else torch.cuda.ExternalStream(int(stream)))
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _output(out, name, shape, dtype, device):
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _need(out, name, (dtype,), device)
+    n = 1
+    for d in shape:
+        n *= d
+    if out.numel() != n:
+        raise ValueError(f"{name} has the wrong size")
+    return out
+
+
+def _fp4_format(fmt) -> int:
+    if fmt not in FP4_BLOCK:
+        raise ValueError("fmt must be FP4_MX or FP4_NV")
+    return int(fmt)
+
+
+def fp4_scale_shape(rows: int, K: int, fmt: int) -> tuple[int, int, int]:
+    """Shape of the scale blocks of a [rows, K] matrix: row blocks of 128, blocks of 4 scales, 512 bytes."""
+    per = 4 * FP4_BLOCK[_fp4_format(fmt)]
+    return (rows + 127) // 128, (K + per - 1) // per, 512
+
+
+def _fp4_weight(w, scales, w_scale, K, fmt, name, device, groups=None):
+    """Checks a 4-bit matrix (or stack of `groups`) with rows of K elements; returns its row count."""
+    _need(w, name, (torch.uint8,), device)
+    _need(scales, f"{name} scales", (torch.uint8,), device)
+    lead = () if groups is None else (groups,)
+    if w.dim() != len(lead) + 2 or w.shape[:-2] != lead or w.shape[-1] * 2 != K:
+        raise ValueError(f"{name} must be {[*lead, 'rows', K // 2]} bytes of codes, got {tuple(w.shape)}")
+    n = w.shape[-2]
+    if scales.shape != (*lead, *fp4_scale_shape(n, K, fmt)):
+        raise ValueError(f"{name} scales must be {(*lead, *fp4_scale_shape(n, K, fmt))}, got {tuple(scales.shape)}")
+    if w_scale is not None:
+        _need(w_scale, f"{name} tensor scale", (torch.float32,), device)
+        if w_scale.numel() != (groups or 1):
+            raise ValueError(f"{name} tensor scale must have one value per matrix")
+    return n
+
+
+def fp4_quantize(x, fmt=FP4_NV, scale=1.0, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """(codes, scales) of x [rows, K], or of a stack [groups, rows, K], in 4 bits.
+
+    codes uint8 [..., rows, K/2], scales uint8 [..., row blocks, scale blocks,
+    512].  scale: the tensor's f32 scale (FP4_NV only).
+    """
+    lib = load_library()
+    _need(x, "x", tuple(_ACT))
+    if x.dim() not in (2, 3):
+        raise ValueError("x must be [rows, K] or [groups, rows, K]")
+    rows, K = x.shape[-2:]
+    groups = x.shape[0] if x.dim() == 3 else 1
+    with _on(stream):
+        codes = torch.empty((*x.shape[:-1], K // 2), dtype=torch.uint8, device=x.device)
+        scales = torch.empty((*x.shape[:-2], *fp4_scale_shape(rows, K, fmt)), dtype=torch.uint8, device=x.device)
+    _check("qsw_fp4_quantize", lib.qsw_fp4_quantize(x.data_ptr(), groups, rows, K, fmt, scale, _ACT[x.dtype],
+                                                    codes.data_ptr(), scales.data_ptr(), _stream_ptr(stream)))
+    return codes, scales
+
+
+def fp4_dequantize(codes, scales, fmt=FP4_NV, scale=1.0, dtype=torch.bfloat16, out=None, stream=None) -> torch.Tensor:
+    """The [rows, K] matrix (or stack) that codes and scales stand for, rounded to `dtype`."""
+    lib = load_library()
+    if dtype not in _ACT:
+        raise TypeError(f"dtype must be one of {tuple(_ACT)}")
+    _need(codes, "codes", (torch.uint8,))
+    if codes.dim() not in (2, 3):
+        raise ValueError("codes must be [rows, K/2] or [groups, rows, K/2]")
+    groups = codes.shape[0] if codes.dim() == 3 else None
+    rows, K = codes.shape[-2], codes.shape[-1] * 2
+    _fp4_weight(codes, scales, None, K, fmt, "codes", codes.device, groups)
+    with _on(stream):
+        out = _output(out, "out", (*codes.shape[:-1], K), dtype, codes.device)
+    _check("qsw_fp4_dequantize", lib.qsw_fp4_dequantize(codes.data_ptr(), scales.data_ptr(),
+                                                        1 if groups is None else groups, rows, K, fmt, scale,
+                                                        _ACT[dtype], out.data_ptr(), _stream_ptr(stream)))
+    return out
+
+
+def fp4_linear(x, w, w_scales, fmt=FP4_NV, x_scale=1.0, w_scale=None, out=None, stream=None) -> torch.Tensor:
+    """y = T(Q(x) . W^T), W held in 4 bits; returns [..., N].
+
+    w uint8 [N, K/2] and w_scales as fp4_quantize returns them; x_scale: the
+    f32 scale x is quantised with, w_scale: W's, one f32 on the device (None: 1).
+    """
+    lib = load_library()
+    _need(x, "x", tuple(_ACT))
+    K = x.shape[-1]
+    M = x.numel() // K if K else 0
+    dev = x.device
+    N = _fp4_weight(w, w_scales, w_scale, K, fmt, "w", dev)
+    nbytes = lib.qsw_fp4_workspace_bytes(M, K, 1, fmt)
+    with _on(stream):
+        out = _output(out, "out", (*x.shape[:-1], N), x.dtype, dev)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    _check("qsw_fp4_linear", lib.qsw_fp4_linear(x.data_ptr(), M, K, N, fmt, x_scale, w.data_ptr(), w_scales.data_ptr(),
+                                                _ptr(w_scale), _ACT[x.dtype], out.data_ptr(), ws.data_ptr(), nbytes,
+                                                _stream_ptr(stream)))
+    return out
+
+
+def fp4_grouped_linear(x, offsets, w, w_scales, fmt=FP4_NV, x_scale=1.0, w_scale=None, out=None,
+                       stream=None) -> torch.Tensor:
+    """y[r] = T(Q(x[r]) . W[e]^T) for the rows offsets[e] <= r < offsets[e+1]; returns [rows, N].
+
+    offsets int32 [groups + 1] on the device, from 0 to rows; w uint8 [groups,
+    N, K/2] with a stack's scales, w_scale f32 [groups] or None.
+    """
+    lib = load_library()
+    _need(x, "x", tuple(_ACT))
+    dev = x.device
+    _need(offsets, "offsets", (torch.int32,), dev)
+    if x.dim() != 2 or offsets.dim() != 1 or offsets.numel() < 2:
+        raise ValueError("x must be [rows, K] and offsets [groups + 1]")
+    rows, K = x.shape
+    groups = offsets.numel() - 1
+    N = _fp4_weight(w, w_scales, w_scale, K, fmt, "w", dev, groups)
+    nbytes = lib.qsw_fp4_workspace_bytes(rows, K, groups, fmt)
+    with _on(stream):
+        out = _output(out, "out", (rows, N), x.dtype, dev)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    _check("qsw_fp4_grouped_linear",
+           lib.qsw_fp4_grouped_linear(x.data_ptr(), rows, K, N, groups, offsets.data_ptr(), fmt, x_scale, w.data_ptr(),
+                                      w_scales.data_ptr(), _ptr(w_scale), _ACT[x.dtype], out.data_ptr(), ws.data_ptr(),
+                                      nbytes, _stream_ptr(stream)))
+    return out
+
+
+class MoeRoute(NamedTuple):
+    """What moe_route returns and fp4_moe_mlp takes (see qsw_moe_route)."""
+    ids: torch.Tensor        # int32 [T, k]  chosen experts, largest logit first
+    weights: torch.Tensor    # f32 [T, k]
+    offsets: torch.Tensor    # int32 [E + 1] first row of each expert in the expert-sorted order
+    slots: torch.Tensor      # int32 [T, k]  row of each (token, choice) in that order
+    order: torch.Tensor      # int32 [T * k] the pair token * k + choice of each row
+
+
+def moe_route(logits, k, scoring=ROUTE_SOFTMAX, renormalize=True, scale=1.0, stream=None) -> MoeRoute:
+    """The k largest of each row of logits [T, E] (f32, bf16 or f16), their weights and the expert-sorted order."""
+    lib = load_library()
+    _need(logits, "logits", (torch.float32, *_ACT))
+    if logits.dim() != 2:
+        raise ValueError("logits must be [T, E]")
+    T, E = logits.shape
+    if not 0 < k <= E:
+        raise ValueError("k must be between 1 and the number of experts")
+    dev = logits.device
+    with _on(stream):
+        ids = torch.empty((T, k), dtype=torch.int32, device=dev)
+        weights = torch.empty((T, k), dtype=torch.float32, device=dev)
+        offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
+        slots = torch.empty((T, k), dtype=torch.int32, device=dev)
+        order = torch.empty(T * k, dtype=torch.int32, device=dev)
+    _check("qsw_moe_route", lib.qsw_moe_route(logits.data_ptr(), T, E, k, _ACT.get(logits.dtype, LOGITS_F32), scoring,
+                                              renormalize, scale, ids.data_ptr(), weights.data_ptr(),
+                                              offsets.data_ptr(), slots.data_ptr(), order.data_ptr(),
+                                              _stream_ptr(stream)))
+    return MoeRoute(ids, weights, offsets, slots, order)
+
+
+def interleave_gate_up(gate, up) -> torch.Tensor:
+    """[..., 2 I, K] with the rows of gate and up [..., I, K] in alternating
+    runs of 16: the layout of fp4_moe_mlp's gate and up weights (quantise the
+    result with fp4_quantize)."""
+    if gate.shape != up.shape or gate.shape[-2] % 16:
+        raise ValueError("gate and up must have the same shape, rows a multiple of 16")
+    pair = torch.stack((gate.unflatten(-2, (-1, 16)), up.unflatten(-2, (-1, 16))), -3)
+    return pair.flatten(-4, -2)
+
+
+def fp4_moe_mlp(x, route, wgu, wgu_scales, wd, wd_scales, fmt=FP4_NV, x_scale=1.0, h_scale=1.0, gu_scale=None,
+                d_scale=None, residual=None, out=None, stream=None) -> torch.Tensor:
+    """The MLP of a mixture of experts: y[t] = residual[t] + sum_j w[t, j] MLP_e(t, j)(x[t]); returns [T, H].
+
+    route: moe_route's result.  wgu uint8 [E, 2 I, H/2] with gate and up rows
+    interleaved (interleave_gate_up), wd uint8 [E, H, I/2]; their scales as
+    fp4_quantize returns them for a stack; gu_scale, d_scale f32 [E] or None.
+    x_scale, h_scale: the f32 scales that x and the hidden activations are
+    quantised with.
+    """
+    lib = load_library()
+    _need(x, "x", tuple(_ACT))
+    dev, dt = x.device, x.dtype
+    _need(route.weights, "route.weights", (torch.float32,), dev)
+    for name in ("offsets", "slots", "order"):
+        _need(getattr(route, name), f"route.{name}", (torch.int32,), dev)
+    if x.dim() != 2:
+        raise ValueError("x must be [T, H]")
+    T, H = x.shape
+    E, k = route.offsets.numel() - 1, route.weights.shape[-1]
+    if route.weights.shape != (T, k) or route.slots.shape != (T, k) or route.order.numel() != T * k:
+        raise ValueError("route does not belong to x")
+    rows = _fp4_weight(wgu, wgu_scales, gu_scale, H, fmt, "wgu", dev, E)
+    if rows % 2:
+        raise ValueError("wgu must have 2 I rows")
+    I = rows // 2
+    if _fp4_weight(wd, wd_scales, d_scale, I, fmt, "wd", dev, E) != H:
+        raise ValueError("wd must have H rows")
+    if residual is not None:
+        _need(residual, "residual", (dt,), dev)
+        if residual.numel() != T * H:
+            raise ValueError("residual has the wrong size")
+    nbytes = lib.qsw_fp4_moe_workspace_bytes(T, k, H, I, E, fmt)
+    with _on(stream):
+        out = _output(out, "out", (T, H), dt, dev)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    _check("qsw_fp4_moe_mlp",
+           lib.qsw_fp4_moe_mlp(x.data_ptr(), T, H, I, E, k, fmt, x_scale, h_scale, route.weights.data_ptr(),
+                               route.offsets.data_ptr(), route.slots.data_ptr(), route.order.data_ptr(),
+                               wgu.data_ptr(), wgu_scales.data_ptr(), _ptr(gu_scale), wd.data_ptr(),
+                               wd_scales.data_ptr(), _ptr(d_scale), _ptr(residual), _ACT[dt], out.data_ptr(),
+                               ws.data_ptr(), nbytes, _stream_ptr(stream)))
+    return out
+
+
+def _norm_vector(w, name, H, like):
+    if w is not None:
+        _need(w, name, (like.dtype,), like.device)
+        if w.shape != (H,):
+            raise ValueError(f"{name} must be [{H}]")
+    return _ptr(w)
+
+
+def rms_norm(x, weight=None, eps=1e-6, out=None, stream=None) -> torch.Tensor:
+    """T(x * rsqrt(mean(x^2) + eps) * weight) over the last dimension."""
+    lib = load_library()
+    _need(x, "x", tuple(_ACT))
+    H = x.shape[-1]
+    w = _norm_vector(weight, "weight", H, x)
+    with _on(stream):
+        out = _output(out, "out", x.shape, x.dtype, x.device)
+    _check("qsw_rms_norm", lib.qsw_rms_norm(x.data_ptr(), w, x.numel() // H if H else 0, H, eps, _ACT[x.dtype],
+                                            out.data_ptr(), _stream_ptr(stream)))
+    return out
+
+
+def post_norm(h, y, weight=None, gate=None, scale=1.0, next_weight=None, eps=1e-6, norm=True, next_norm=True,
+              out=None, next_out=None, stream=None):
+    """h' = h + scale * gate * norm(y) * weight and n = norm(h') * next_weight.
+
+    h, y [..., H].  norm=False leaves y as it is (no weight then);
+    next_norm=False returns h' alone, else (h', n).  gate: None, [H], or
+    [gate_rows, H] or [gate_rows, 1] with gate_rows dividing the row count.
+    `out` may be h, `next_out` may be y.
+    """
+    lib = load_library()
+    _need(h, "h", tuple(_ACT))
+    _need(y, "y", (h.dtype,), h.device)
+    if y.shape != h.shape:
+        raise ValueError("h and y must have the same shape")
+    H = h.shape[-1]
+    rows = h.numel() // H if H else 0
+    w, wn = _norm_vector(weight, "weight", H, h), _norm_vector(next_weight, "next_weight", H, h)
+    gate_rows = gate_cols = 0
+    if gate is not None:
+        _need(gate, "gate", (h.dtype,), h.device)
+        if gate.dim() == 1:
+            gate_rows, gate_cols = 1, gate.shape[0]
+        elif gate.dim() == 2:
+            gate_rows, gate_cols = gate.shape
+        else:
+            raise ValueError("gate must be [H], [gate_rows, H] or [gate_rows, 1]")
+    with _on(stream):
+        out = _output(out, "out", h.shape, h.dtype, h.device)
+        n = _output(next_out, "next_out", h.shape, h.dtype, h.device) if next_norm else None
+    _check("qsw_post_norm", lib.qsw_post_norm(h.data_ptr(), y.data_ptr(), bool(norm), w, _ptr(gate), gate_rows,
+                                              gate_cols, scale, wn, rows, H, eps, _ACT[h.dtype], out.data_ptr(),
+                                              _ptr(n), _stream_ptr(stream)))
+    return (out, n) if next_norm else out
 
 
 def qsw_check_device_errors(stream=None) -> None:

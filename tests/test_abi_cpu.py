@@ -208,3 +208,112 @@ def test_debug_build_is_built_and_exports_the_same_abi(lib):
     assert dbg.qsw_debug_build() == 1 and lib.qsw_debug_build() == 0
     dbg.qsw_status_string.restype = ctypes.c_char_p
     assert b"debug" in dbg.qsw_status_string(5)
+
+
+# ------------------------------------------------- operators around the block
+
+MX, NV = 0, 1
+BIG = 1 << 40
+
+
+def test_fp4_sizes(lib):
+    assert lib.qsw_fp4_scale_bytes(1, 1, 32, NV) == 512
+    assert lib.qsw_fp4_scale_bytes(1, 128, 64, NV) == 512
+    assert lib.qsw_fp4_scale_bytes(1, 129, 96, NV) == 4 * 512
+    assert lib.qsw_fp4_scale_bytes(3, 129, 128, MX) == 6 * 512
+    assert lib.qsw_fp4_scale_bytes(1, 4, 48, NV) == 0           # K not a multiple of 32
+    assert lib.qsw_fp4_scale_bytes(1, 4, 64, 2) == 0
+    assert lib.qsw_fp4_workspace_bytes(8, 64, 3, NV) == 256 + 4 * 512
+    assert lib.qsw_fp4_workspace_bytes(8, 64, 0, NV) == 0
+    assert lib.qsw_fp4_moe_workspace_bytes(0, 2, 64, 64, 4, MX) >= 2 * 4 * 512
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(rows=0), OK), (dict(groups=0), OK), (dict(rows=-1), INVALID), (dict(K=0), INVALID), (dict(K=48), UNSUPPORTED),
+    (dict(fmt=2), INVALID), (dict(scale=0.0), INVALID), (dict(scale=float("nan")), INVALID),
+    (dict(scale=float("inf")), INVALID), (dict(fmt=MX, scale=2.0), INVALID), (dict(act=2), INVALID),
+    (dict(x=0), INVALID), (dict(codes=FAKE + 8), UNSUPPORTED), (dict(scales=FAKE + 4), UNSUPPORTED),
+    (dict(rows=1 << 31), UNSUPPORTED), (dict(groups=1 << 31), UNSUPPORTED),
+])
+def test_fp4_quantize_refuses(lib, kw, code):
+    a = dict(x=FAKE, groups=1, rows=4, K=64, fmt=NV, scale=1.0, act=0, codes=FAKE, scales=FAKE) | kw
+    assert lib.qsw_fp4_quantize(a["x"], a["groups"], a["rows"], a["K"], a["fmt"], a["scale"], a["act"], a["codes"],
+                                a["scales"], None) == code
+    assert lib.qsw_fp4_dequantize(a["codes"], a["scales"], a["groups"], a["rows"], a["K"], a["fmt"], a["scale"],
+                                  a["act"], a["x"], None) == code
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(rows=0), OK), (dict(rows=0, x=0, y=0, ws=0), OK), (dict(rows=-1), INVALID), (dict(N=0), INVALID),
+    (dict(K=40), UNSUPPORTED), (dict(act=3), INVALID), (dict(w=0), INVALID), (dict(w=FAKE + 8), UNSUPPORTED),
+    (dict(w_scale=FAKE + 2), UNSUPPORTED), (dict(x=0), INVALID), (dict(ws=0), INVALID), (dict(ws=FAKE + 16), UNSUPPORTED),
+    (dict(ws_bytes=8), INVALID), (dict(y=FAKE + 1), UNSUPPORTED), (dict(N=1 << 31), UNSUPPORTED),
+])
+def test_fp4_products_refuse(lib, kw, code):
+    a = dict(x=FAKE, rows=4, K=64, N=32, scale=1.0, w=FAKE, w_scales=FAKE, w_scale=None, act=0, y=FAKE, ws=FAKE,
+             ws_bytes=BIG) | kw
+    rest = (a["w"], a["w_scales"], a["w_scale"], a["act"], a["y"], a["ws"], a["ws_bytes"], None)
+    assert lib.qsw_fp4_linear(a["x"], a["rows"], a["K"], a["N"], NV, a["scale"], *rest) == code
+    assert lib.qsw_fp4_grouped_linear(a["x"], a["rows"], a["K"], a["N"], 3, FAKE, NV, a["scale"], *rest) == code
+
+
+def test_fp4_grouped_linear_refuses_groups(lib):
+    call = lambda groups, offsets: lib.qsw_fp4_grouped_linear(FAKE, 0, 64, 32, groups, offsets, NV, 1.0, FAKE, FAKE,  # noqa: E731
+                                                              None, 0, FAKE, FAKE, BIG, None)
+    assert call(3, FAKE) == OK
+    assert call(0, FAKE) == INVALID
+    assert call(3, None) == INVALID
+    assert call(1025, FAKE) == UNSUPPORTED
+    assert call(3, FAKE + 2) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(T=-1), INVALID), (dict(E=0), INVALID), (dict(k=0), INVALID), (dict(k=9), INVALID), (dict(dtype=3), INVALID),
+    (dict(scoring=2), INVALID), (dict(scale=float("inf")), INVALID), (dict(E=2000), UNSUPPORTED),
+    (dict(E=64, k=33), UNSUPPORTED), (dict(T=1 << 31), UNSUPPORTED), (dict(logits=0), INVALID), (dict(offsets=0), INVALID),
+    (dict(ids=FAKE + 4), UNSUPPORTED), (dict(logits=FAKE + 2), UNSUPPORTED),
+])
+def test_moe_route_refuses(lib, kw, code):
+    a = dict(logits=FAKE, T=4, E=8, k=2, dtype=2, scoring=0, scale=1.0, ids=FAKE, offsets=FAKE) | kw
+    assert lib.qsw_moe_route(a["logits"], a["T"], a["E"], a["k"], a["dtype"], a["scoring"], 1, a["scale"], a["ids"],
+                             FAKE, a["offsets"], FAKE, FAKE, None) == code
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(T=0), OK), (dict(T=-1), INVALID), (dict(k=9), INVALID), (dict(H=40), UNSUPPORTED), (dict(I=40), UNSUPPORTED),
+    (dict(h_scale=0.0), INVALID), (dict(fmt=MX, h_scale=0.5), INVALID), (dict(wd=0), INVALID), (dict(ws_bytes=64), INVALID),
+    (dict(residual=FAKE + 2), UNSUPPORTED), (dict(y=0), INVALID), (dict(E=1025), UNSUPPORTED),
+])
+def test_fp4_moe_mlp_refuses(lib, kw, code):
+    a = dict(T=4, H=64, I=64, E=8, k=2, fmt=NV, h_scale=1.0, wd=FAKE, residual=None, y=FAKE, ws_bytes=BIG) | kw
+    assert lib.qsw_fp4_moe_mlp(FAKE, a["T"], a["H"], a["I"], a["E"], a["k"], a["fmt"], 1.0, a["h_scale"], FAKE, FAKE,
+                               FAKE, FAKE, FAKE, FAKE, None, a["wd"], FAKE, None, a["residual"], 0, a["y"], FAKE,
+                               a["ws_bytes"], None) == code
+
+
+def test_norms_refuse(lib):
+    rms = lambda rows=4, H=64, eps=1e-6, act=0, x=FAKE: lib.qsw_rms_norm(x, None, rows, H, eps, act, FAKE, None)  # noqa: E731
+    assert rms(rows=0) == OK
+    assert rms(rows=-1) == INVALID and rms(H=0) == INVALID and rms(eps=-1.0) == INVALID and rms(act=2) == INVALID
+    assert rms(eps=float("nan")) == INVALID and rms(x=0) == INVALID
+    assert rms(H=32769) == UNSUPPORTED and rms(x=FAKE + 1) == UNSUPPORTED
+
+    def post(h=FAKE, norm=1, w=None, gate=None, gr=0, gc=0, scale=1.0, rows=4, out=FAKE):
+        return lib.qsw_post_norm(h, FAKE, norm, w, gate, gr, gc, scale, None, rows, 64, 1e-6, 0, out, None, None)
+    assert post(rows=0) == OK
+    assert post(h=0) == INVALID and post(out=0) == INVALID and post(scale=float("nan")) == INVALID
+    assert post(norm=0, w=FAKE) == INVALID
+    assert post(gate=FAKE, gr=3, gc=64) == INVALID and post(gate=FAKE, gr=2, gc=32) == INVALID
+    assert post(gate=FAKE, gr=0, gc=64) == INVALID
+    assert post(gate=FAKE + 1, gr=2, gc=64) == UNSUPPORTED
+
+
+def test_block_bindings_refuse_host_tensors(lib):
+    import torch
+    x, u8 = torch.zeros(2, 64, dtype=torch.bfloat16), torch.zeros(2, 32, dtype=torch.uint8)
+    r = ops.MoeRoute(*[torch.zeros(2, 1, dtype=torch.int32)] * 5)
+    for call in (lambda: ops.fp4_quantize(x), lambda: ops.fp4_dequantize(u8, u8), lambda: ops.fp4_linear(x, u8, u8),
+                 lambda: ops.fp4_grouped_linear(x, u8, u8, u8), lambda: ops.moe_route(x, 2),
+                 lambda: ops.fp4_moe_mlp(x, r, u8, u8, u8, u8), lambda: ops.rms_norm(x), lambda: ops.post_norm(x, x)):
+        with pytest.raises(ValueError):
+            call()
