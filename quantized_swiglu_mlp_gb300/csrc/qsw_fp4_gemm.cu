@@ -19,10 +19,10 @@
 // are never read.  The rows keep their place r mod 128, so that the scale block's
 // lanes fit: the A descriptor starts that many rows before the copied ones.
 //
-// One persistent CTA per SM, 10 warps: warp 0 issues the copies (a ring of
-// stages of 256 elements of K: 128-byte swizzled code tiles by TMA, scale blocks
-// by bulk copies), warp 1 moves the scales into tensor memory and issues the
-// MMAs, warps 2-9 run the epilogue.  Tensor memory: two accumulators of 192
+// One persistent CTA per SM, 11 warps: warps 0 and 10 issue the weights' and the
+// activations' copies (a ring of stages of 256 elements of K: 128-byte swizzled
+// code tiles by TMA, scale blocks by bulk copies), warp 1 moves the scales into
+// tensor memory and issues the MMAs, warps 2-9 run the epilogue.  Tensor memory: two accumulators of 192
 // columns, so that a tile's epilogue runs under the next tile's products, and
 // two scale buffers of 48 columns.
 //
@@ -43,7 +43,8 @@ __device__ unsigned int g_fp4_error;
 constexpr int kTileTokens = 192;
 constexpr int kMaxStages = 16;
 constexpr int kEpiWarps = 8;
-constexpr int kThreads = 32 * (2 + kEpiWarps);
+constexpr int kWarpW = 0, kWarpMma = 1, kWarpEpi0 = 2, kWarpX = kWarpEpi0 + kEpiWarps;
+constexpr int kThreads = 32 * (kWarpX + 1);
 constexpr int kStageK = 256;                 // elements of K per stage: one 128-byte swizzle row
 constexpr int kSfCol = 2 * kTileTokens;      // first scale column of tensor memory
 constexpr int kSfCols = 48;                  // per scale buffer: 16 weight, 32 token columns
@@ -64,7 +65,7 @@ struct GemmParams {
   int k_blocks;             // scale blocks along K
   int w_row_blocks;         // scale row blocks of a group's weights
   int rt, bt;               // weight rows and most tokens of a tile
-  int x_box, x_rows;        // rows of one TMA box of x, and of a stage
+  int x_box, x_rows;        // rows of the small TMA box of x, and of a stage (the large box)
   int x_sf;                 // scale row blocks of x in a stage
   int stages;
   int x_off, w_off, sf_off, ex_off, table_off;   // byte offsets in shared memory
@@ -127,13 +128,26 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
                : "memory");
 }
 
-// One 512-byte scale block (32 rows of 16 bytes) into four columns of tensor
-// memory, repeated in the four lane quarters.
-__device__ __forceinline__ void scales_to_tmem(uint32_t taddr, uint32_t smem_addr) {
+// Descriptor of a 512-byte scale block: 32 rows of 16 bytes, no swizzle.
+__device__ __forceinline__ uint64_t scales_desc(uint32_t smem_addr) {
   uint64_t d = (smem_addr & 0x3FFFFu) >> 4;
   d |= static_cast<uint64_t>(128 >> 4) << 32;   // 8 rows of 16 bytes
-  d |= static_cast<uint64_t>(1) << 46;          // descriptor version, no swizzle
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+  d |= static_cast<uint64_t>(1) << 46;          // descriptor version
+  return d;
+}
+// A scale block into four columns of tensor memory, repeated in the four lane
+// quarters.
+__device__ __forceinline__ void scales_to_tmem(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+// One thread of a converged warp.  The copies and products are issued by a
+// thread chosen this way: the compiler then keeps their operands in uniform
+// registers (chosen with `lane == 0`, each instruction took about 100 cycles).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
 }
 
 template <int FMT>
@@ -162,6 +176,31 @@ __device__ __forceinline__ uint32_t fp4_idesc(int n) {
          (8u << 24);                         // M / 16
 }
 
+// The copies and products of one stage: `nkb` scale blocks, `steps` products of 64
+// elements of K.  One thread's copies and products run in the order of issue.
+template <int FMT, int XSF>
+__device__ __forceinline__ void issue_stage(uint32_t d, uint32_t idesc, uint64_t wd, uint64_t xd, uint32_t sf,
+                                            uint64_t sfd, uint32_t x_col, int nkb, int steps, bool first) {
+  constexpr int kSfPerStage = kStageK / Fp4<FMT>::kSfK;
+#pragma unroll
+  for (int kb = 0; kb < kSfPerStage; ++kb) {
+    if (kb >= nkb) break;
+    scales_to_tmem(sf + kb * 4, sfd + kb * (kSfBytes >> 4));
+#pragma unroll
+    for (int b = 0; b < XSF; ++b)
+      scales_to_tmem(sf + 16 + kb * 8 + b * 4, sfd + (kSfPerStage * (1 + b) + kb) * (kSfBytes >> 4));
+  }
+#pragma unroll
+  for (int kk = 0; kk < kStageK / 64; ++kk) {
+    if (kk >= steps) break;
+    const int kb = FMT == FP4_MX ? kk >> 1 : kk;
+    // MX: an MMA takes two of a scale block's four scales
+    const uint32_t sel = FMT == FP4_MX ? static_cast<uint32_t>(kk & 1) * 2u : 0u;
+    umma_fp4<FMT>(d, wd + 2 * kk, xd + 2 * kk, idesc | (sel << 4) | (sel << 29), sf + kb * 4, sf + 16 + kb * 8 + x_col,
+                  first && kk == 0 ? 0u : 1u);
+  }
+}
+
 __device__ __forceinline__ void bar_sync_half(int id) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(kEpiWarps * 16) : "memory");
 }
@@ -182,7 +221,7 @@ __device__ __forceinline__ bool bar_and_half(int id, bool ok) {
 template <class A, int FMT, bool SWIGLU>
 __global__ void __launch_bounds__(kThreads, 1)
     fp4_gemm_kernel(const __grid_constant__ GemmParams p, const __grid_constant__ CUtensorMap tm_w,
-                    const __grid_constant__ CUtensorMap tm_x) {
+                    const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_xb) {
   constexpr int kSfPerStage = kStageK / Fp4<FMT>::kSfK;   // scale blocks per stage: 2 (MX), 4 (NV)
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -191,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ int abort_word;
   volatile int *abort_flag = &abort_word;
   int *table = reinterpret_cast<int *>(smem + p.table_off);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   unsigned int *err = &g_fp4_error;
   const int S = p.stages;
 
@@ -201,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], 2);      // both producers
       mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -213,12 +252,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
     prefetch_tensormap(&tm_w);
     prefetch_tensormap(&tm_x);
+    prefetch_tensormap(&tm_xb);
   }
-  if (warp == 1) {
+  if (warp == kWarpMma) {
     tmem_alloc(&tmem_slot, 512);
     tmem_relinquish();
   }
-  if (warp == 2) {
+  if (warp == kWarpEpi0) {
     // group table: offsets (clamped, so that no table of the caller leads
     // outside the buffers) and the first tile id of each group
     int *first = table + p.groups + 1;
@@ -251,141 +291,141 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
   const int k_stages = ceil_div(p.K, kStageK);
 
-  if (warp == 0) {
-    // ---------------------------------------------------------- producer ----
-    if (lane == 0) {
-      const int x_stage = p.x_rows * 128, w_stage = p.rt * 128;
+  // Ring positions are counted, not divided: a division by the run-time stage
+  // count in every iteration cost the issuing thread more than its products.
+  if (warp == kWarpW || warp == kWarpX) {
+    // --------------------------------------------------------- producers ----
+    // One warp copies the weights' codes and scales, another the
+    // activations': each stage's barrier gets one arrival from both.
+    if (elect_one()) {
+      const bool w_side = warp == kWarpW;
+      const int stage = (w_side ? p.rt : p.x_rows) * 128;
       const int sf_stage = kSfPerStage * kSfBytes * (1 + p.x_sf);
-      bool ok = true;
-      // the two halves of a stage's copies: weights, then (after the
-      // dependency wait) activations
-      auto load_w = [&](const Tile &t, int ks, int s) {
-        const int kb0 = ks * kSfPerStage, nkb = min(kSfPerStage, p.k_blocks - kb0);
-        const int x_boxes = ceil_div(t.n, p.x_box);
-        const int xb0 = t.t0 / kSfRows, x_sf = ceil_div(t.t0 + t.n, kSfRows) - xb0;
-        debug_check(x_boxes * p.x_box <= p.x_rows && x_sf <= p.x_sf, err);
-        mbar_arrive_expect_tx(&full[s], w_stage + x_boxes * p.x_box * 128 + nkb * kSfBytes * (1 + x_sf));
-        tma_load_2d(smem + p.w_off + s * w_stage, &tm_w, &full[s], ks * 128, t.e * p.N + t.w0);
-        const int64_t wb = static_cast<int64_t>(t.e) * p.w_row_blocks + t.w0 / kSfRows;
-        bulk_load(smem + p.sf_off + s * sf_stage, p.w_scales + (wb * p.k_blocks + kb0) * kSfBytes, nkb * kSfBytes,
-                  &full[s]);
-      };
-      auto load_x = [&](const Tile &t, int ks, int s) {
-        const int kb0 = ks * kSfPerStage, nkb = min(kSfPerStage, p.k_blocks - kb0);
-        const int x_boxes = ceil_div(t.n, p.x_box);
-        const int xb0 = t.t0 / kSfRows, x_sf = ceil_div(t.t0 + t.n, kSfRows) - xb0;
-        for (int b = 0; b < x_boxes; ++b)
-          tma_load_2d(smem + p.x_off + s * x_stage + b * p.x_box * 128, &tm_x, &full[s], ks * 128,
-                      t.off + t.t0 + b * p.x_box);
-        const int64_t base = (p.offsets ? ragged_row_block(t.off, t.e) : 0) + xb0;
-        for (int b = 0; b < x_sf; ++b)
-          bulk_load(smem + p.sf_off + s * sf_stage + kSfPerStage * kSfBytes * (1 + b),
-                    p.x_scales + ((base + b) * p.k_blocks + kb0) * kSfBytes, nkb * kSfBytes, &full[s]);
-      };
+      uint8_t *codes = smem + (w_side ? p.w_off : p.x_off);
+      uint8_t *sf = smem + p.sf_off + (w_side ? 0 : kSfPerStage * kSfBytes);
       TileWalk walk(table, p);
       Tile t;
-      int n_fill = 0;
-      // weights of the first stages before the wait: the ring is empty
-      const bool any = walk.get(p, t);
-      const int early = any ? min(S, k_stages) : 0;
-      for (int ks = 0; ks < early; ++ks) load_w(t, ks, ks);
-      griddep_wait();
-      griddep_launch_dependents();
-      bool more = any;
+      int s = 0, filled = 0;
+      uint32_t phase = 1;      // parity that a free slot's barrier shows: the first round passes at once
+      bool ok = true, more = walk.get(p, t);
+      // the weights' first stages go out before the wait
+      if (!w_side) {
+        griddep_wait();
+        griddep_launch_dependents();
+      }
       while (more && ok) {
+        const int64_t block = w_side ? static_cast<int64_t>(t.e) * p.w_row_blocks + t.w0 / kSfRows
+                                     : (p.offsets ? ragged_row_block(t.off, t.e) : 0) + t.t0 / kSfRows;
+        const uint8_t *sf_src = (w_side ? p.w_scales : p.x_scales) + block * p.k_blocks * kSfBytes;
+        const int64_t sf_row = static_cast<int64_t>(p.k_blocks) * kSfBytes;
+        const int blocks = w_side ? 1 : ceil_div(t.t0 + t.n, kSfRows) - t.t0 / kSfRows;
+        const int row = w_side ? t.e * p.N + t.w0 : t.off + t.t0;
+        // x: one box of bt rows, or boxes of 64 where they come to less
+        const int boxes = w_side || t.n > p.x_rows - p.x_box ? 1 : ceil_div(t.n, p.x_box);
+        const bool whole = w_side || t.n > p.x_rows - p.x_box;
+        const int bytes = whole ? stage : boxes * p.x_box * 128;
+        const CUtensorMap *tm = w_side ? &tm_w : whole ? &tm_x : &tm_xb;
+        debug_check(blocks <= p.x_sf && t.n * 128 <= (w_side ? kSfRows * 256 : bytes), err);
         for (int ks = 0; ks < k_stages; ++ks) {
-          const int s = n_fill % S;
-          if (n_fill >= early) {
-            if (!mbar_wait(&empty[s], ((n_fill / S) & 1) ^ 1u, abort_flag, p.timeout_ns, err)) {
-              ok = false;
-              break;
-            }
-            load_w(t, ks, s);
+          const int nkb = min(kSfPerStage, p.k_blocks - ks * kSfPerStage) * kSfBytes;
+          if (!mbar_wait(&empty[s], phase, abort_flag, p.timeout_ns, err)) {
+            ok = false;
+            break;
           }
-          load_x(t, ks, s);
-          ++n_fill;
+          uint64_t *bar = &full[s];
+          mbar_arrive_expect_tx(bar, bytes + nkb * blocks);
+          for (int b = 0; b < boxes; ++b)
+            tma_load_2d(codes + s * stage + b * p.x_box * 128, tm, bar, ks * 128, row + b * p.x_box);
+          for (int b = 0; b < blocks; ++b)
+            bulk_load(sf + s * sf_stage + b * kSfPerStage * kSfBytes, sf_src + b * sf_row, nkb, bar);
+          sf_src += kSfPerStage * kSfBytes;
+          ++filled;
+          if (++s == S) {
+            s = 0;
+            phase ^= 1;
+          }
         }
         walk.next();
         more = walk.get(p, t);
       }
       if (!ok) {
         // let the copies already issued land before the CTA's memory goes away
-        for (int s = 0; s < S && s < n_fill; ++s) {
-          const int last = s + ((n_fill - 1 - s) / S) * S;
-          mbar_wait_drain(&full[s], (last / S) & 1, 100000000ull);
+        for (int i = 0; i < S && i < filled; ++i) {
+          const int last = i + ((filled - 1 - i) / S) * S;
+          mbar_wait_drain(&full[i], (last / S) & 1, 100000000ull);
         }
       }
     }
     __syncwarp();
-  } else if (warp == 1) {
+  } else if (warp == kWarpMma) {
     // --------------------------------------------------------- MMA issuer ---
-    if (lane == 0) {
-      const int x_stage = p.x_rows * 128, w_stage = p.rt * 128;
-      const int sf_stage = kSfPerStage * kSfBytes * (1 + p.x_sf);
-      TileWalk walk(table, p);
-      Tile t;
-      int n_it = 0, n_tile = 0;
-      bool ok = true;
-      for (; ok && walk.get(p, t); walk.next(), ++n_tile) {
-        const int buf = n_tile & 1;
-        if (!mbar_wait(&acc_empty[buf], ((n_tile >> 1) & 1) ^ 1u, abort_flag, p.timeout_ns, err)) {
-          ok = false;
-          break;
-        }
-        const uint32_t d = tmem + buf * kTileTokens;
-        const uint32_t idesc = fp4_idesc<FMT>(t.n);
-        const int shift = t.w0 & (kSfRows - 1);              // lane of the tile's first weight row
-        const uint32_t x_col = (t.t0 & 64) ? 2u : 0u;        // scale column of the tile's first token
-        const int x_sf = ceil_div(t.t0 + t.n, kSfRows) - t.t0 / kSfRows;
-        for (int ks = 0; ks < k_stages; ++ks, ++n_it) {
-          const int s = n_it % S;
-          // this iteration's scale buffer was read by the products two
-          // iterations ago; their commit is the release of that stage
-          if (n_it >= 2 && !mbar_wait(&empty[(n_it - 2) % S], ((n_it - 2) / S) & 1, abort_flag, p.timeout_ns, err)) {
-            ok = false;
-            break;
-          }
-          if (!mbar_wait(&full[s], (n_it / S) & 1, abort_flag, p.timeout_ns, err)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t sf = tmem + kSfCol + (n_it & 1) * kSfCols;
-          const uint32_t sfs = smem_u32(smem + p.sf_off + s * sf_stage);
-          const int nkb = min(kSfPerStage, p.k_blocks - ks * kSfPerStage);
-          for (int kb = 0; kb < nkb; ++kb) {
-            scales_to_tmem(sf + kb * 4, sfs + kb * kSfBytes);
-            for (int b = 0; b < x_sf; ++b)
-              scales_to_tmem(sf + 16 + kb * 8 + b * 4, sfs + (kSfPerStage * (1 + b) + kb) * kSfBytes);
-          }
-          const uint64_t wd = umma_desc_sw128(smem_u32(smem + p.w_off + s * w_stage) - shift * 128);
-          const uint64_t xd = umma_desc_sw128(smem_u32(smem + p.x_off + s * x_stage));
-          const int steps = min(kStageK / 64, ceil_div(p.K - ks * kStageK, 64));
-          for (int kk = 0; kk < steps; ++kk) {
-            const int kb = FMT == FP4_MX ? kk >> 1 : kk;
-            // MX: an MMA takes two of a scale block's four scales
-            const uint32_t sel = FMT == FP4_MX ? static_cast<uint32_t>(kk & 1) * 2u : 0u;
-            umma_fp4<FMT>(d, wd + 2 * kk, xd + 2 * kk, idesc | (sel << 4) | (sel << 29), sf + kb * 4,
-                          sf + 16 + kb * 8 + x_col, (ks | kk) ? 1u : 0u);
-          }
+    // The whole warp walks the tiles and waits, one elected lane issues: with
+    // control flow and operands the same in all lanes, descriptors and
+    // addresses live in uniform registers, as these instructions want them.
+    const bool issuer = elect_one();
+    const uint32_t x_stage = p.x_rows * 128 >> 4, w_stage = p.rt * 128 >> 4;
+    const uint32_t sf_stage = kSfPerStage * kSfBytes * (1 + p.x_sf) >> 4;
+    TileWalk walk(table, p);
+    Tile t;
+    int s = 0, n_tile = 0;
+    uint32_t phase = 0, it = 0;
+    bool ok = true;
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+      if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, p.timeout_ns, err)) != 0;
+    };
+    for (; ok && walk.get(p, t); walk.next(), ++n_tile) {
+      const int buf = n_tile & 1;
+      ok = wait(&acc_empty[buf], ((n_tile >> 1) & 1) ^ 1u);
+      if (!ok) break;
+      const int n = __shfl_sync(0xffffffffu, t.n, 0), t0 = __shfl_sync(0xffffffffu, t.t0, 0);
+      const int w0 = __shfl_sync(0xffffffffu, t.w0, 0);
+      const uint32_t d = tmem + buf * kTileTokens;
+      const uint32_t idesc = fp4_idesc<FMT>(n);
+      const int shift = w0 & (kSfRows - 1);              // lane of the tile's first weight row
+      const uint32_t x_col = (t0 & 64) ? 2u : 0u;        // scale column of the tile's first token
+      const int x_sf = ceil_div(t0 + n, kSfRows) - t0 / kSfRows;
+      const uint64_t wd0 = umma_desc_sw128(smem_u32(smem + p.w_off) - shift * 128);
+      const uint64_t xd0 = umma_desc_sw128(smem_u32(smem + p.x_off));
+      const uint64_t sfd0 = scales_desc(smem_u32(smem + p.sf_off));
+      int kb_left = p.k_blocks, steps_left = ceil_div(p.K, 64);
+      for (int ks = 0; ks < k_stages; ++ks) {
+        ok = wait(&full[s], phase);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t sf = tmem + kSfCol + (it & 1) * kSfCols;
+        const uint64_t wd = wd0 + s * w_stage, xd = xd0 + s * x_stage, sfd = sfd0 + s * sf_stage;
+        if (issuer) {
+          if (x_sf == 1)
+            issue_stage<FMT, 1>(d, idesc, wd, xd, sf, sfd, x_col, kb_left, steps_left, ks == 0);
+          else
+            issue_stage<FMT, 2>(d, idesc, wd, xd, sf, sfd, x_col, kb_left, steps_left, ks == 0);
           umma_commit(&empty[s]);
         }
-        if (ok) umma_commit(&acc_full[buf]);
+        __syncwarp();
+        kb_left -= kSfPerStage;
+        steps_left -= kStageK / 64;
+        ++it;
+        if (++s == S) {
+          s = 0;
+          phase ^= 1;
+        }
       }
-      if (!ok) {
-        umma_commit(&mma_done);
-        mbar_wait_drain(&mma_done, 0, 100000000ull);
-      }
+      if (ok && issuer) umma_commit(&acc_full[buf]);
+    }
+    if (!ok && issuer) {
+      umma_commit(&mma_done);
+      mbar_wait_drain(&mma_done, 0, 100000000ull);
     }
     __syncwarp();
   } else {
     // ------------------------------------------------------------ epilogue --
     // Two halves of four warps (one per lane quarter) take alternate runs of
     // 32 tokens.
-    const int ew = warp - 2, half = ew >> 2;
+    const int ew = warp - kWarpEpi0, half = ew >> 2;
     const int quarter = warp & 3;                  // the TMEM lanes this warp may read
     const int bar = 1 + half;
     const int htid = (ew & 3) * 32 + lane;         // thread within the half
@@ -492,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, 512);
+  if (warp == kWarpMma) tmem_dealloc(tmem, 512);
 }
 
 // -------------------------------------------------------------------- host --
@@ -569,16 +609,18 @@ cudaError_t launch_gemm(const Fp4GemmArgs &a, GemmParams p, int num_sms, cudaStr
   bytes += 1024;   // base alignment
   if (bytes > kSmemLimit) return cudaErrorInvalidValue;
 
-  CUtensorMap tm_w, tm_x;
+  CUtensorMap tm_w, tm_x, tm_xb;
   if (!encode_codes(&tm_w, a.w_codes, static_cast<int64_t>(p.groups) * p.N, p.K, p.rt) ||
-      !encode_codes(&tm_x, a.x_codes, p.rows, p.K, p.x_box))
+      !encode_codes(&tm_x, a.x_codes, p.rows, p.K, p.x_rows))
     return cudaErrorInvalidValue;
+  tm_xb = tm_x;
+  if (p.x_box != p.x_rows && !encode_codes(&tm_xb, a.x_codes, p.rows, p.K, p.x_box)) return cudaErrorInvalidValue;
   // no more CTAs than tiles can exist
   const int64_t token_tiles_max = static_cast<int64_t>(p.rows) / p.bt + (p.groups < p.rows ? p.groups : p.rows);
   const int64_t most = token_tiles_max * p.n_tiles;
   const int grid = static_cast<int>(most < num_sms ? most : num_sms);
   return launch_on(kernel, dim3(static_cast<unsigned>(grid)), kThreads, static_cast<size_t>(bytes), stream, dependent,
-                   p, tm_w, tm_x);
+                   p, tm_w, tm_x, tm_xb);
 }
 
 }  // namespace
