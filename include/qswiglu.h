@@ -342,8 +342,8 @@ typedef enum {
  *   offsets  int32 [E + 1] first row of each expert in the expert-sorted order
  *   slots    int32 [T, k]  row of (token, choice) in that order
  *   order    int32 [T * k] the pair token * k + choice of each row
- * Rows of one expert are in token order.  E <= 1024, k <= 32; ids 16-byte
- * aligned.  logit_dtype: qsw_act_dtype or QSW_LOGITS_F32.
+ * Rows of one expert are in token order.  E <= 1024, k <= 32.  logit_dtype:
+ * qsw_act_dtype or QSW_LOGITS_F32.
  */
 QSW_API qsw_status qsw_moe_route(const void *logits, int64_t T, int E, int k, int logit_dtype, int scoring,
                            int renormalize, float scale, int *ids, float *weights, int *offsets, int *slots,
@@ -364,8 +364,8 @@ QSW_API qsw_status qsw_moe_route(const void *logits, int64_t T, int E, int k, in
  */
 QSW_API size_t qsw_fp4_moe_workspace_bytes(int64_t T, int k, int64_t H, int64_t I, int E, int fmt);
 QSW_API qsw_status qsw_fp4_moe_mlp(const void *x, int64_t T, int64_t H, int64_t I, int E, int k, int fmt,
-                           float x_scale, float h_scale, const float *weights, const int *offsets,
-                           const int *slots, const int *order, const uint8_t *wgu, const uint8_t *wgu_scales,
+                           float x_scale, float h_scale, const int *ids, const float *weights,
+                           const int *offsets, const int *slots, const uint8_t *wgu, const uint8_t *wgu_scales,
                            const float *gu_scale, const uint8_t *wd, const uint8_t *wd_scales,
                            const float *d_scale, const void *residual, int act_dtype, void *y,
                            void *workspace, size_t workspace_bytes, void *stream);

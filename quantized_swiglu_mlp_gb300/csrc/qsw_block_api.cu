@@ -65,8 +65,7 @@ qsw_status grouped_linear(const void *x, int64_t rows, int64_t K, int64_t N, int
   auto *codes = static_cast<uint8_t *>(workspace);
   uint8_t *scales = codes + up256(static_cast<size_t>(rows * (K / 2)));
   const cudaError_t e =
-      offsets ? qsw::launch_fp4_quantize_ragged(x, rows, K, offsets, groups, nullptr, 1, fmt, act, x_scale, codes,
-                                                scales, sms, s, false)
+      offsets ? qsw::launch_fp4_quantize_ragged(x, rows, K, offsets, groups, fmt, act, x_scale, codes, scales, sms, s)
               : qsw::launch_fp4_quantize(x, 1, rows, K, fmt, act, x_scale, codes, scales, sms, s);
   if (e != cudaSuccess) return QSW_ERR_CUDA;
   qsw::Fp4GemmArgs a = {};
@@ -174,7 +173,7 @@ qsw_status qsw_moe_route(const void *logits, int64_t T, int E, int k, int logit_
   if (!std::isfinite(scale)) return QSW_ERR_INVALID_ARG;
   if (E > kMaxGroups || k > kMaxTopK || T > kMaxRows / k) return QSW_ERR_UNSUPPORTED;
   if (!offsets || (T > 0 && (!logits || !ids || !weights || !slots || !order))) return QSW_ERR_INVALID_ARG;
-  if (!aligned(logits, logit_dtype == QSW_LOGITS_F32 ? 4 : 2) || !aligned(ids, 16) || !aligned(weights, 4) ||
+  if (!aligned(logits, logit_dtype == QSW_LOGITS_F32 ? 4 : 2) || !aligned(ids, 4) || !aligned(weights, 4) ||
       !aligned(offsets, 4) || !aligned(slots, 4) || !aligned(order, 4))
     return QSW_ERR_UNSUPPORTED;
   const qsw_status st =
@@ -191,8 +190,8 @@ size_t qsw_fp4_moe_workspace_bytes(int64_t T, int k, int64_t H, int64_t I, int E
 }
 
 qsw_status qsw_fp4_moe_mlp(const void *x, int64_t T, int64_t H, int64_t I, int E, int k, int fmt, float x_scale,
-                           float h_scale, const float *weights, const int *offsets, const int *slots,
-                           const int *order, const uint8_t *wgu, const uint8_t *wgu_scales, const float *gu_scale,
+                           float h_scale, const int *ids, const float *weights, const int *offsets,
+                           const int *slots, const uint8_t *wgu, const uint8_t *wgu_scales, const float *gu_scale,
                            const uint8_t *wd, const uint8_t *wd_scales, const float *d_scale, const void *residual,
                            int act_dtype, void *y, void *workspace, size_t workspace_bytes, void *stream) {
   if (T < 0 || E <= 0 || k <= 0 || k > E) return QSW_ERR_INVALID_ARG;
@@ -204,9 +203,9 @@ qsw_status qsw_fp4_moe_mlp(const void *x, int64_t T, int64_t H, int64_t I, int E
   if ((st = check_weights(wgu, wgu_scales, gu_scale, E, 2 * I)) != QSW_OK) return st;
   if ((st = check_weights(wd, wd_scales, d_scale, E, H)) != QSW_OK) return st;
   if (T == 0) return QSW_OK;
-  if (!x || !y || !weights || !offsets || !slots || !order || !workspace) return QSW_ERR_INVALID_ARG;
+  if (!x || !y || !ids || !weights || !offsets || !slots || !workspace) return QSW_ERR_INVALID_ARG;
   if (!aligned(x, 16) || !aligned(y, 16) || !aligned(residual, 16) || !aligned(workspace, 256) ||
-      !aligned(weights, 4) || !aligned(offsets, 4) || !aligned(slots, 4) || !aligned(order, 4))
+      !aligned(ids, 4) || !aligned(weights, 4) || !aligned(offsets, 4) || !aligned(slots, 4))
     return QSW_ERR_UNSUPPORTED;
   const int64_t R = T * k;
   const MoeWorkspace at(R, H, I, E, fmt);
@@ -218,8 +217,8 @@ qsw_status qsw_fp4_moe_mlp(const void *x, int64_t T, int64_t H, int64_t I, int E
 
   // rows sorted by expert, in 4 bits; gate and up with the SwiGLU, held in
   // 4 bits; down; the tokens' weighted sums
-  cudaError_t e = qsw::launch_fp4_quantize_ragged(x, R, H, offsets, E, order, k, fmt, act_dtype, x_scale,
-                                                  ws + at.x_codes, ws + at.x_scales, sms, s, false);
+  cudaError_t e = qsw::launch_fp4_quantize_fan(x, T, H, k, ids, slots, offsets, E, fmt, act_dtype, x_scale,
+                                               ws + at.x_codes, ws + at.x_scales, s);
   if (e != cudaSuccess) return QSW_ERR_CUDA;
   qsw::Fp4GemmArgs a = {};
   a.x_codes = ws + at.x_codes;
@@ -272,7 +271,7 @@ qsw_status qsw_rms_norm(const void *x, const void *weight, int64_t rows, int64_t
   a.act = act_dtype;
   a.eps = eps;
   a.n_out = out;
-  const qsw_status st = from_cuda(qsw::launch_norm(a, static_cast<cudaStream_t>(stream)));
+  const qsw_status st = from_cuda(qsw::launch_norm(a, qsw::device_sm_count(), static_cast<cudaStream_t>(stream)));
   if (st == QSW_OK) qsw::count_call(QSW_CNT_NORM);
   return st;
 }
@@ -307,7 +306,7 @@ qsw_status qsw_post_norm(const void *h, const void *y, int norm_y, const void *w
   a.act = act_dtype;
   a.h_out = h_out;
   a.n_out = n_out;
-  const qsw_status st = from_cuda(qsw::launch_norm(a, static_cast<cudaStream_t>(stream)));
+  const qsw_status st = from_cuda(qsw::launch_norm(a, qsw::device_sm_count(), static_cast<cudaStream_t>(stream)));
   if (st == QSW_OK) qsw::count_call(QSW_CNT_NORM);
   return st;
 }

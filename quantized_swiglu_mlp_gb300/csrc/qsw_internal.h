@@ -86,10 +86,16 @@ cudaError_t launch_fp4_quantize(const void *x, int64_t groups, int64_t rows, int
                                 uint8_t *codes, uint8_t *scales, int num_sms, cudaStream_t stream);
 
 // Quantise rows sorted by group, each group's scale blocks starting a new row
-// block.  order: row r of the result is row order[r] / fan of x (null: row r).
+// block.
 cudaError_t launch_fp4_quantize_ragged(const void *x, int64_t rows, int64_t K, const int *offsets, int groups,
-                                       const int *order, int fan, int fmt, int act, float g, uint8_t *codes,
-                                       uint8_t *scales, int num_sms, cudaStream_t stream, bool dependent);
+                                       int fmt, int act, float g, uint8_t *codes, uint8_t *scales, int num_sms,
+                                       cudaStream_t stream);
+
+// Quantise tokens x [T, K], each to the rows slots[t, 0 .. k-1] of its groups
+// ids[t, 0 .. k-1] in the order sorted by group.
+cudaError_t launch_fp4_quantize_fan(const void *x, int64_t T, int64_t K, int k, const int *ids, const int *slots,
+                                    const int *offsets, int groups, int fmt, int act, float g, uint8_t *codes,
+                                    uint8_t *scales, cudaStream_t stream);
 
 cudaError_t launch_fp4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t groups, int64_t rows,
                                   int64_t K, int fmt, int act, float g, void *out, int num_sms, cudaStream_t stream);
@@ -128,7 +134,7 @@ struct NormArgs {
   float scale, eps;
   void *h_out, *n_out;
 };
-cudaError_t launch_norm(const NormArgs &a, cudaStream_t stream);
+cudaError_t launch_norm(const NormArgs &a, int num_sms, cudaStream_t stream);
 
 // Shared state of the C entry points (qsw_api.cu).
 int device_sm_count();

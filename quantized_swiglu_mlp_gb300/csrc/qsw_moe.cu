@@ -112,62 +112,83 @@ __global__ void __launch_bounds__(kTopkWarps * 32)
 
 constexpr int kSortThreads = 1024;
 
-// One CTA per expert e.  Each thread scans a contiguous run of the T k ids and
-// counts those below e and those equal to it; the block's exclusive sums give
-// the expert's first row and each match's place, in the order of the pairs.
-// Ids outside [0, E) are ignored (their slot is -1).
+// One CTA per expert e.  Each warp takes a contiguous run of the n = T k ids, 32
+// at a time: the ballots of id == e and id < e count the run, the sums over the
+// warps before it (and of all smaller ids) give the expert's first row and the
+// run's place in it, and the ballots again give each match's rank, so that rows
+// are in the order of the pairs.  Up to 32 ballots stay in a register of their
+// lane (n <= 32768); longer runs are read a second time.  Ids outside [0, E) are
+// ignored (their slot is -1).  Bound by the latency of the loads, so 8 are in
+// flight.
 __global__ void __launch_bounds__(kSortThreads)
-    sort_kernel(const int *__restrict__ ids, int64_t n, int E, int *offsets, int *slots, int *order) {
+    sort_kernel(const int *__restrict__ ids, int n, int E, int *offsets, int *slots, int *order) {
   griddep_wait();
   griddep_launch_dependents();
   __shared__ int warp_eq[32], warp_lt[32];
-  const int e = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t per = ((n + blockDim.x - 1) / blockDim.x + 3) & ~int64_t(3);
-  const int64_t a = tid * per < n ? tid * per : n, b = a + per < n ? a + per : n;
+  const int e = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int words = (n + 31) / 32;                           // groups of 32 ids
+  const int per = (words + warps - 1) / warps;
+  const int w0 = min(warp * per, words), w1 = min(w0 + per, words);
+  auto load = [&](int w) {
+    const int i = w * 32 + lane;
+    return w < w1 && i < n ? __ldg(ids + i) : E;             // past the end: neither equal nor below
+  };
+  constexpr int AHEAD = 8;      // loads in flight: a ballot waits for its own
+  uint32_t kept = 0;
   int eq = 0, lt = 0;
-  int64_t i = a;
-  for (; i + 4 <= b; i += 4) {
-    const int4 v = __ldg(reinterpret_cast<const int4 *>(ids + i));
-    eq += (v.x == e) + (v.y == e) + (v.z == e) + (v.w == e);
-    lt += (v.x >= 0 && v.x < e) + (v.y >= 0 && v.y < e) + (v.z >= 0 && v.z < e) + (v.w >= 0 && v.w < e);
-  }
-  for (; i < b; ++i) {
-    const int v = __ldg(ids + i);
-    eq += v == e;
-    lt += v >= 0 && v < e;
-  }
-  int incl = eq;
+  for (int w = w0; w < w1; w += AHEAD) {
+    int v[AHEAD];
 #pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int o = __shfl_up_sync(0xffffffffu, incl, d);
-    if (lane >= d) incl += o;
+    for (int a = 0; a < AHEAD; ++a) v[a] = load(w + a);
+#pragma unroll
+    for (int a = 0; a < AHEAD; ++a) {
+      const uint32_t match = __ballot_sync(0xffffffffu, v[a] == e);
+      if (((w + a - w0) & 31) == lane) kept = match;
+      eq += __popc(match);
+      lt += v[a] >= 0 && v[a] < e;
+    }
+    if (e == 0) {       // one CTA marks the pairs of no expert
+#pragma unroll
+      for (int a = 0; a < AHEAD; ++a) {
+        const int i = (w + a) * 32 + lane;
+        if ((v[a] < 0 || v[a] >= E) && w + a < w1 && i < n) slots[i] = -1;
+      }
+    }
   }
   lt = __reduce_add_sync(0xffffffffu, lt);
-  if (lane == 31) {
-    warp_eq[warp] = incl;
+  if (lane == 0) {
+    warp_eq[warp] = eq;
     warp_lt[warp] = lt;
   }
   __syncthreads();
-  const int warps = blockDim.x >> 5;
-  int before = 0, first = 0, total = 0;
-  for (int w = 0; w < warps; ++w) {
-    before += w < warp ? warp_eq[w] : 0;
-    total += warp_eq[w];
-    first += warp_lt[w];
-  }
-  if (tid == 0) {
+  const int o_eq = lane < warps ? warp_eq[lane] : 0, o_lt = lane < warps ? warp_lt[lane] : 0;
+  const int before = __reduce_add_sync(0xffffffffu, lane < warp ? o_eq : 0);
+  const int total = __reduce_add_sync(0xffffffffu, o_eq);
+  const int first = __reduce_add_sync(0xffffffffu, o_lt);
+  if (threadIdx.x == 0) {
     offsets[e] = first;
     if (e == E - 1) offsets[E] = first + total;
   }
-  int at = first + before + incl - eq;
-  for (i = a; i < b; ++i) {
-    const int v = __ldg(ids + i);
-    if (v == e) {
-      slots[i] = at;
-      order[at] = static_cast<int>(i);
-      ++at;
-    } else if (e == 0 && (v < 0 || v >= E)) {
-      slots[i] = -1;
+  int at = first + before;
+  auto place = [&](int w, uint32_t match) {
+    if ((match >> lane) & 1u) {
+      const int i = w * 32 + lane;
+      const int pos = at + __popc(match & ((1u << lane) - 1u));
+      slots[i] = pos;
+      order[pos] = i;
+    }
+    at += __popc(match);
+  };
+  if (per <= 32) {
+    // only the groups with a match
+    for (uint32_t left = __ballot_sync(0xffffffffu, kept != 0); left; left &= left - 1) {
+      const int a = __ffs(left) - 1;
+      place(w0 + a, __shfl_sync(0xffffffffu, kept, a));
+    }
+  } else {
+    for (int w = w0; w < w1; ++w) {
+      const uint32_t match = __ballot_sync(0xffffffffu, load(w) == e);
+      if (match) place(w, match);
     }
   }
 }
@@ -242,8 +263,8 @@ cudaError_t launch_moe_route(const void *logits, int logit_dtype, int64_t T, int
       e = launch_topk<ActF16>(logits, T, E, k, scoring, renormalize, scale, ids, weights, stream);
     if (e != cudaSuccess) return e;
   }
-  const int64_t n = T * k;
-  const int threads = n >= kSortThreads * 4 ? kSortThreads : n > 512 ? 256 : 64;
+  const int n = static_cast<int>(T * k);
+  const int threads = n >= 8192 ? kSortThreads : n >= 512 ? 256 : 32;
   return launch_on(sort_kernel, dim3(static_cast<unsigned>(E)), threads, 0, stream, T > 0, ids, n, E, offsets, slots,
                    order);
 }

@@ -271,7 +271,7 @@ def test_fp4_grouped_linear_refuses_groups(lib):
     (dict(T=-1), INVALID), (dict(E=0), INVALID), (dict(k=0), INVALID), (dict(k=9), INVALID), (dict(dtype=3), INVALID),
     (dict(scoring=2), INVALID), (dict(scale=float("inf")), INVALID), (dict(E=2000), UNSUPPORTED),
     (dict(E=64, k=33), UNSUPPORTED), (dict(T=1 << 31), UNSUPPORTED), (dict(logits=0), INVALID), (dict(offsets=0), INVALID),
-    (dict(ids=FAKE + 4), UNSUPPORTED), (dict(logits=FAKE + 2), UNSUPPORTED),
+    (dict(ids=FAKE + 2), UNSUPPORTED), (dict(logits=FAKE + 2), UNSUPPORTED),
 ])
 def test_moe_route_refuses(lib, kw, code):
     a = dict(logits=FAKE, T=4, E=8, k=2, dtype=2, scoring=0, scale=1.0, ids=FAKE, offsets=FAKE) | kw
