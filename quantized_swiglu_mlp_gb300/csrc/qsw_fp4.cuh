@@ -142,21 +142,36 @@ __device__ __forceinline__ uint32_t fp4_code8(const uint4 &w, float inv) {
 }
 
 // Launch on `stream`; `dependent`: as a programmatic dependent of the work
-// before it (the kernel waits with griddep_wait before touching its results).
+// before it (the kernel waits with griddep_wait before touching its results);
+// `cluster`: CTAs per cluster.
 template <class... P, class... Q>
-inline cudaError_t launch_on(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
-                             bool dependent, Q... args) {
+inline cudaError_t launch_clusters(void (*kernel)(P...), dim3 grid, int cluster, int threads, size_t smem,
+                                   cudaStream_t stream, bool dependent, Q... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchAttribute attr[2];
+  unsigned n = 0;
+  if (dependent) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (cluster > 1) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+    ++n;
+  }
   cfg.attrs = attr;
-  cfg.numAttrs = dependent ? 1 : 0;
+  cfg.numAttrs = n;
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+template <class... P, class... Q>
+inline cudaError_t launch_on(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                             bool dependent, Q... args) {
+  return launch_clusters(kernel, grid, 1, threads, smem, stream, dependent, args...);
 }
 
 }  // namespace qsw

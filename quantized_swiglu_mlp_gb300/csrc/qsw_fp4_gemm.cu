@@ -19,10 +19,11 @@
 // are never read.  The rows keep their place r mod 128, so that the scale block's
 // lanes fit: the A descriptor starts that many rows before the copied ones.
 //
-// One persistent CTA per SM, 11 warps: warps 0 and 10 issue the weights' and the
-// activations' copies (a ring of stages of 256 elements of K: 128-byte swizzled
-// code tiles by TMA, scale blocks by bulk copies), warp 1 moves the scales into
-// tensor memory and issues the MMAs, warps 2-9 run the epilogue.  Tensor memory: two accumulators of 192
+// One persistent CTA per SM, 17 warps: warps 0 and 14-16 issue the copies of the
+// weights' and activations' codes and scales (a ring of stages of 256 elements of
+// K: 128-byte swizzled code tiles by TMA, scale blocks by TMA or bulk copies; one
+// warp each, since a copy takes its issuer over 100 cycles), warp 1 moves the
+// scales into tensor memory and issues the MMAs, warps 2-13 run the epilogue.  Tensor memory: two accumulators of 192
 // columns, so that a tile's epilogue runs under the next tile's products, and
 // two scale buffers of 48 columns.
 //
@@ -31,6 +32,7 @@
 // complete before the launch in front of this one began (each kernel of a chain
 // lets the next one start only after its own wait).
 #include <mutex>
+#include <type_traits>
 
 #include "qsw_fp4.cuh"
 #include "qsw_internal.h"
@@ -42,14 +44,21 @@ __device__ unsigned int g_fp4_error;
 
 constexpr int kTileTokens = 192;
 constexpr int kMaxStages = 16;
-constexpr int kEpiWarps = 8;
-constexpr int kWarpW = 0, kWarpMma = 1, kWarpEpi0 = 2, kWarpX = kWarpEpi0 + kEpiWarps;
-constexpr int kThreads = 32 * (kWarpX + 1);
+constexpr int kEpiGroups = 3;                // epilogue groups of four warps
+constexpr int kEpiWarps = 4 * kEpiGroups;
+// Warps: the first producer, the MMA issuer, the epilogue, three more producers.
+constexpr int kWarpMma = 1, kWarpEpi0 = 2, kWarpProd1 = kWarpEpi0 + kEpiWarps;
+constexpr int kThreads = 32 * (kWarpProd1 + 3);
+enum Role : int { W_CODES = 0, W_SCALES = 1, X_CODES = 2, X_SCALES = 3 };   // of the producers
 constexpr int kStageK = 256;                 // elements of K per stage: one 128-byte swizzle row
 constexpr int kSfCol = 2 * kTileTokens;      // first scale column of tensor memory
 constexpr int kSfCols = 48;                  // per scale buffer: 16 weight, 32 token columns
-constexpr int kXPitch = 80;                  // floats per token row of the epilogue's exchange buffer
-constexpr int kXBytes = 32 * kXPitch * 4;    // one buffer: 32 tokens
+// Exchange buffer of an epilogue group, 32 tokens: swiglu, f32 rows of 64
+// features; linear, 16-bit rows of 128.
+constexpr int kHPitch = 80;                  // floats
+constexpr int kYPitch = 136;                 // 16-bit values
+constexpr int kExBytes = 32 * kHPitch * 4;
+static_assert(32 * kYPitch * 2 <= kExBytes, "both layouts fit");
 
 struct GemmParams {
   const uint8_t *w_scales;
@@ -68,7 +77,9 @@ struct GemmParams {
   int x_box, x_rows;        // rows of the small TMA box of x, and of a stage (the large box)
   int x_sf;                 // scale row blocks of x in a stage
   int stages;
-  int x_off, w_off, sf_off, ex_off, table_off;   // byte offsets in shared memory
+  int recs;                 // tiles per CTA at most
+  bool wide;                // rows of the output start at 16-byte boundaries
+  int x_off, w_off, sf_off, ex_off, rec_off, table_off;   // byte offsets in shared memory
   void *out;
   uint8_t *h_codes;
   uint8_t *h_scales;
@@ -77,14 +88,20 @@ struct GemmParams {
   uint64_t timeout_ns;
 };
 
-struct Tile {
+// One tile of a CTA (or of a CTA pair), worked out before the first one starts: the
+// roles walk these records, since finding the next tile from the group table
+// (search, division) in the issuing warp cost more than a short tile's products.
+struct alignas(16) TileRec {
   int e;        // group
-  int off;      // its first row
-  int t0;       // first token of the tile within the group
+  int row;      // first row of x
   int valid;    // tokens
   int n;        // valid rounded up to the MMA's step
-  int w0;       // first weight row within the group
+  int w0;       // first weight row of this CTA within the group
+  int w_block;  // its scale row block
+  int x_block;  // scale row block of the first token's 128 rows
+  int t0;       // first token within the group
 };
+constexpr int kMaxRecs = 256;     // per CTA; more tiles launch more CTAs
 
 __host__ __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
@@ -92,32 +109,36 @@ __host__ __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b -
 // of 64 (the scale lanes of a tile then start at column 0 or 2 of a block).
 __device__ __forceinline__ int token_tiles(int m, int bt) { return ceil_div(m, bt); }
 
-// Walks the CTA's tiles: tile ids count up, token tiles fastest, then weight
-// tiles, then groups.
-struct TileWalk {
-  const int *off;     // [groups + 1] in shared memory
-  const int *first;   // [groups + 1] first tile id of each group
-  int id, e;
-  __device__ __forceinline__ TileWalk(const int *table, const GemmParams &p)
-      : off(table), first(table + p.groups + 1), id(static_cast<int>(blockIdx.x)), e(0) {}
-  __device__ __forceinline__ bool get(const GemmParams &p, Tile &t) {
-    if (id >= first[p.groups]) return false;
-    while (id >= first[e + 1]) ++e;
-    const int m = min(off[e + 1] - off[e], p.max_group);
-    const int nt = token_tiles(m, p.bt);
-    const int local = id - first[e];
-    const int wt = local / nt, tt = local - wt * nt;
-    const int size = nt > 1 ? (ceil_div(m, nt) + 63) & ~63 : m;
-    t.e = e;
-    t.off = off[e];
-    t.t0 = tt * size;
-    t.valid = min(size, m - t.t0);
-    t.n = max(16, (t.valid + 15) & ~15);
-    t.w0 = wt * p.rt;
-    return true;
+// Tile `id` (< the number of tiles): token tiles fastest, then weight tiles, then
+// groups.  off, first: first row and first tile of each group.
+template <bool PAIR>
+__device__ __forceinline__ TileRec make_rec(const GemmParams &p, const int *off, const int *first, int id,
+                                            uint32_t rank) {
+  constexpr int kStep = PAIR ? 32 : 16;      // of an MMA's N
+  int e = 0;                                 // the last group whose first tile is at most id
+  for (int hi = p.groups; hi - e > 1;) {
+    const int mid = (e + hi) >> 1;
+    if (first[mid] <= id)
+      e = mid;
+    else
+      hi = mid;
   }
-  __device__ __forceinline__ void next() { id += static_cast<int>(gridDim.x); }
-};
+  const int m = min(off[e + 1] - off[e], p.max_group);
+  const int nt = token_tiles(m, p.bt);
+  const int local = id - first[e];
+  const int wt = local / nt, tt = local - wt * nt;
+  const int size = nt > 1 ? (ceil_div(m, nt) + 63) & ~63 : m;
+  TileRec t;
+  t.e = e;
+  t.t0 = tt * size;
+  t.row = off[e] + t.t0;
+  t.valid = min(size, m - t.t0);
+  t.n = max(kStep, (t.valid + kStep - 1) & ~(kStep - 1));
+  t.w0 = wt * p.rt + (PAIR ? static_cast<int>(rank) * kSfRows : 0);
+  t.w_block = e * p.w_row_blocks + t.w0 / kSfRows;
+  t.x_block = (p.offsets ? static_cast<int>(ragged_row_block(off[e], e)) : 0) + t.t0 / kSfRows;
+  return t;
+}
 
 // ------------------------------------------------------------- PTX pieces --
 
@@ -137,8 +158,76 @@ __device__ __forceinline__ uint64_t scales_desc(uint32_t smem_addr) {
 }
 // A scale block into four columns of tensor memory, repeated in the four lane
 // quarters.
+template <bool PAIR>
 __device__ __forceinline__ void scales_to_tmem(uint32_t taddr, uint64_t desc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+  if (PAIR)
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+  else
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+// ---- CTA pairs (clusters of two): rank, barriers across the pair, copies that
+// signal the leader's (rank 0) barrier, arrivals on it.
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t leader_address(const void *p) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_u32(p)));
+  return a;
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tma_load_2d_pair(void *dst, const CUtensorMap *map, uint32_t bar, int c0, int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%3, %4}], "
+      "[%2];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(bar), "r"(c0), "r"(c1)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_3d_pair(void *dst, const CUtensorMap *map, uint32_t bar, int c0, int c1,
+                                                 int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%3, %4, "
+      "%5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+// Arrive on `bar` -- of both CTAs of a pair -- once the issued tcgen05 work is done.
+template <bool PAIR>
+__device__ __forceinline__ void commit_to(uint64_t *bar) {
+  if (PAIR)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+  else
+    umma_commit(bar);
+}
+template <bool PAIR>
+__device__ __forceinline__ void tmem_alloc_all(uint32_t *slot) {
+  if (PAIR) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  } else {
+    tmem_alloc(slot, 512);
+    tmem_relinquish();
+  }
+}
+template <bool PAIR>
+__device__ __forceinline__ void tmem_free_all(uint32_t taddr) {
+  if (PAIR)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(512) : "memory");
+  else
+    tmem_dealloc(taddr, 512);
 }
 
 // One thread of a converged warp.  The copies and products are issued by a
@@ -150,45 +239,57 @@ __device__ __forceinline__ bool elect_one() {
   return r != 0;
 }
 
-template <int FMT>
+template <int FMT, bool PAIR>
 __device__ __forceinline__ void umma_fp4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
                                          uint32_t accumulate) {
-  if (FMT == FP4_MX)
+  if constexpr (FMT == FP4_MX && !PAIR)
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
         : "memory");
-  else
+  else if constexpr (FMT == FP4_MX)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+  else if constexpr (!PAIR)
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
         : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
 }
 
-// Instruction descriptor: e2m1 A and B, M = 128; N / 8 and the scale selectors
-// are added per tile and per step.
-template <int FMT>
+// Instruction descriptor: e2m1 A and B, M = 128 (256 over a pair); the scale
+// selectors are added per step.
+template <int FMT, bool PAIR>
 __device__ __forceinline__ uint32_t fp4_idesc(int n) {
   return (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) |
          (FMT == FP4_MX ? 1u << 23 : 0u) |   // E8M0 or E4M3 scales
-         (8u << 24);                         // M / 16
+         ((PAIR ? 16u : 8u) << 24);          // M / 16
 }
 
 // The copies and products of one stage: `nkb` scale blocks, `steps` products of 64
 // elements of K.  One thread's copies and products run in the order of issue.
-template <int FMT, int XSF>
+template <int FMT, int XSF, bool PAIR>
 __device__ __forceinline__ void issue_stage(uint32_t d, uint32_t idesc, uint64_t wd, uint64_t xd, uint32_t sf,
                                             uint64_t sfd, uint32_t x_col, int nkb, int steps, bool first) {
   constexpr int kSfPerStage = kStageK / Fp4<FMT>::kSfK;
 #pragma unroll
   for (int kb = 0; kb < kSfPerStage; ++kb) {
     if (kb >= nkb) break;
-    scales_to_tmem(sf + kb * 4, sfd + kb * (kSfBytes >> 4));
+    scales_to_tmem<PAIR>(sf + kb * 4, sfd + kb * (kSfBytes >> 4));
 #pragma unroll
     for (int b = 0; b < XSF; ++b)
-      scales_to_tmem(sf + 16 + kb * 8 + b * 4, sfd + (kSfPerStage * (1 + b) + kb) * (kSfBytes >> 4));
+      scales_to_tmem<PAIR>(sf + 16 + kb * 8 + b * 4, sfd + (kSfPerStage * (1 + b) + kb) * (kSfBytes >> 4));
   }
 #pragma unroll
   for (int kk = 0; kk < kStageK / 64; ++kk) {
@@ -196,67 +297,115 @@ __device__ __forceinline__ void issue_stage(uint32_t d, uint32_t idesc, uint64_t
     const int kb = FMT == FP4_MX ? kk >> 1 : kk;
     // MX: an MMA takes two of a scale block's four scales
     const uint32_t sel = FMT == FP4_MX ? static_cast<uint32_t>(kk & 1) * 2u : 0u;
-    umma_fp4<FMT>(d, wd + 2 * kk, xd + 2 * kk, idesc | (sel << 4) | (sel << 29), sf + kb * 4, sf + 16 + kb * 8 + x_col,
+    umma_fp4<FMT, PAIR>(d, wd + 2 * kk, xd + 2 * kk, idesc | (sel << 4) | (sel << 29), sf + kb * 4, sf + 16 + kb * 8 + x_col,
                   first && kk == 0 ? 0u : 1u);
   }
 }
 
-__device__ __forceinline__ void bar_sync_half(int id) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(kEpiWarps * 16) : "memory");
+__device__ __forceinline__ void bar_sync_group(int id) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(128) : "memory");
 }
-// All threads of the half agree: every one's `ok`.
-__device__ __forceinline__ bool bar_and_half(int id, bool ok) {
+// All threads of the group agree: every one's `ok`.
+__device__ __forceinline__ bool bar_and_group(int id, bool ok) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
       "bar.red.and.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"(ok ? 1u : 0u), "r"(id), "r"(kEpiWarps * 16)
+      : "r"(ok ? 1u : 0u), "r"(id), "r"(128)
       : "memory");
   return r != 0;
 }
 
+// A group's run of `tokens` rows out of the exchange buffer: features [lo, hi) of
+// the 128-row weight block at column n0 of an [.., N] output.  `wide`: rows start
+// at 16-byte boundaries, 16-byte stores; else pairs from each row's first 4-byte
+// boundary on, single values around them.
+__device__ __forceinline__ void store_rows(const uint16_t *ex, uint16_t *out, int N, int n0, int lo, int hi, int tokens,
+                                           int tid, bool wide) {
+  hi = min(hi, N - n0);
+  if (wide) {
+    const int f = (tid & 15) * 8;
+    if (f < lo || f >= hi) return;
+    uint4 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const uint4 *>(ex + ((tid >> 4) + 8 * i) * kYPitch + f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int tok = (tid >> 4) + 8 * i;
+      if (tok < tokens) *reinterpret_cast<uint4 *>(out + static_cast<int64_t>(tok) * N + n0 + f) = v[i];
+    }
+    return;
+  }
+  for (int tok = tid >> 5; tok < tokens; tok += 4) {
+    uint16_t *dst = out + static_cast<int64_t>(tok) * N + n0;
+    const uint16_t *src = ex + tok * kYPitch;
+    const int odd = static_cast<int>(reinterpret_cast<uintptr_t>(dst) >> 1) & 1;
+    for (int f = (tid & 31) * 2 - odd; f < hi; f += 64) {
+      const bool a = f >= lo, b = f + 1 >= lo && f + 1 < hi;
+      if (a && b)
+        *reinterpret_cast<uint32_t *>(dst + f) = src[f] | static_cast<uint32_t>(src[f + 1]) << 16;
+      else if (a)
+        dst[f] = src[f];
+      else if (b)
+        dst[f + 1] = src[f + 1];
+    }
+  }
+}
+
 // ------------------------------------------------------------------ kernel --
 
-template <class A, int FMT, bool SWIGLU>
+// The tensor maps: weights' codes, activations' codes in large and small boxes
+// and, for pairs, the scale blocks of both.
+struct GemmMaps {
+  CUtensorMap w, x, xb, sfw, sfx;
+};
+
+template <class A, int FMT, bool SWIGLU, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
-    fp4_gemm_kernel(const __grid_constant__ GemmParams p, const __grid_constant__ CUtensorMap tm_w,
-                    const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_xb) {
+    fp4_gemm_kernel(const __grid_constant__ GemmParams p, const __grid_constant__ GemmMaps maps) {
   constexpr int kSfPerStage = kStageK / Fp4<FMT>::kSfK;   // scale blocks per stage: 2 (MX), 4 (NV)
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], mma_done;
   __shared__ uint32_t tmem_slot;
-  __shared__ int abort_word;
+  __shared__ int abort_word, rec_count;
   volatile int *abort_flag = &abort_word;
   int *table = reinterpret_cast<int *>(smem + p.table_off);
+  TileRec *recs = reinterpret_cast<TileRec *>(smem + p.rec_off);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   unsigned int *err = &g_fp4_error;
   const int S = p.stages;
+  const uint32_t rank = PAIR ? cluster_rank() : 0;
+  const int w_rows = PAIR ? kSfRows : p.rt;      // weight rows of this CTA's part of a tile
 
   if constexpr (kDebugBounds) {
-    debug_poison_smem(smem, static_cast<uint32_t>(p.table_off));
+    debug_poison_smem(smem, static_cast<uint32_t>(p.rec_off));
     __syncthreads();
   }
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(&full[s], 2);      // both producers
+      mbar_init(&full[s], 4);      // the four producers
       mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], kEpiWarps);
+      mbar_init(&acc_empty[b], PAIR ? 2 * kEpiWarps : kEpiWarps);
     }
     mbar_init(&mma_done, 1);
     abort_word = 0;
     fence_mbar_init();
-    prefetch_tensormap(&tm_w);
-    prefetch_tensormap(&tm_x);
-    prefetch_tensormap(&tm_xb);
+    prefetch_tensormap(&maps.w);
+    prefetch_tensormap(&maps.x);
+    prefetch_tensormap(&maps.xb);
+    if (PAIR) {
+      prefetch_tensormap(&maps.sfw);
+      prefetch_tensormap(&maps.sfx);
+    }
   }
   if (warp == kWarpMma) {
-    tmem_alloc(&tmem_slot, 512);
-    tmem_relinquish();
+    __syncwarp();
+    tmem_alloc_all<PAIR>(&tmem_slot);
   }
   if (warp == kWarpEpi0) {
     // group table: offsets (clamped, so that no table of the caller leads
@@ -287,111 +436,142 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       total += __shfl_sync(0xffffffffu, sum, 31);
     }
+    __syncwarp();
+    // this CTA's tiles: every gridDim-th from its own index on
+    const int start = static_cast<int>(blockIdx.x) >> (PAIR ? 1 : 0), step = static_cast<int>(gridDim.x) >> (PAIR ? 1 : 0);
+    const int count = total > start ? ceil_div(total - start, step) : 0;
+    debug_check(count <= p.recs, err);
+    for (int j = lane; j < count; j += 32) recs[j] = make_rec<PAIR>(p, table, first, start + j * step, rank);
+    if (lane == 0) rec_count = count;
   }
   tc_fence_before();
   __syncthreads();
+  if (PAIR) cluster_sync();      // the partner's barriers are ready too
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
   const int k_stages = ceil_div(p.K, kStageK);
+  const int tiles = rec_count;
 
   // Ring positions are counted, not divided: a division by the run-time stage
   // count in every iteration cost the issuing thread more than its products.
-  if (warp == kWarpW || warp == kWarpX) {
+  if (warp == 0 || warp >= kWarpProd1) {
     // --------------------------------------------------------- producers ----
-    // One warp copies the weights' codes and scales, another the
-    // activations': each stage's barrier gets one arrival from both.
-    if (elect_one()) {
-      const bool w_side = warp == kWarpW;
-      const int stage = (w_side ? p.rt : p.x_rows) * 128;
-      const int sf_stage = kSfPerStage * kSfBytes * (1 + p.x_sf);
-      uint8_t *codes = smem + (w_side ? p.w_off : p.x_off);
-      uint8_t *sf = smem + p.sf_off + (w_side ? 0 : kSfPerStage * kSfBytes);
-      TileWalk walk(table, p);
-      Tile t;
+    auto produce = [&](auto role) {
+      constexpr int ROLE = decltype(role)::value;
+      constexpr bool X = ROLE == X_CODES || ROLE == X_SCALES, SCALES = ROLE == W_SCALES || ROLE == X_SCALES;
+      // the weights' first stages go out before the wait
+      if (X) griddep_wait();
+      if (ROLE == X_CODES) griddep_launch_dependents();
+      const int stage = SCALES ? kSfPerStage * kSfBytes * (1 + p.x_sf) : (X ? p.x_rows : w_rows) * 128;
+      uint8_t *const base = smem + (SCALES ? p.sf_off + (X ? kSfPerStage * kSfBytes : 0) : X ? p.x_off : p.w_off);
+      const uint32_t leader_full = PAIR ? leader_address(&full[0]) : 0;
       int s = 0, filled = 0;
       uint32_t phase = 1;      // parity that a free slot's barrier shows: the first round passes at once
-      bool ok = true, more = walk.get(p, t);
-      // the weights' first stages go out before the wait
-      if (!w_side) {
-        griddep_wait();
-        griddep_launch_dependents();
-      }
-      while (more && ok) {
-        const int64_t block = w_side ? static_cast<int64_t>(t.e) * p.w_row_blocks + t.w0 / kSfRows
-                                     : (p.offsets ? ragged_row_block(t.off, t.e) : 0) + t.t0 / kSfRows;
-        const uint8_t *sf_src = (w_side ? p.w_scales : p.x_scales) + block * p.k_blocks * kSfBytes;
-        const int64_t sf_row = static_cast<int64_t>(p.k_blocks) * kSfBytes;
-        const int blocks = w_side ? 1 : ceil_div(t.t0 + t.n, kSfRows) - t.t0 / kSfRows;
-        const int row = w_side ? t.e * p.N + t.w0 : t.off + t.t0;
-        // x: one box of bt rows, or boxes of 64 where they come to less
-        const int boxes = w_side || t.n > p.x_rows - p.x_box ? 1 : ceil_div(t.n, p.x_box);
-        const bool whole = w_side || t.n > p.x_rows - p.x_box;
-        const int bytes = whole ? stage : boxes * p.x_box * 128;
-        const CUtensorMap *tm = w_side ? &tm_w : whole ? &tm_x : &tm_xb;
-        debug_check(blocks <= p.x_sf && t.n * 128 <= (w_side ? kSfRows * 256 : bytes), err);
+      bool ok = true;
+      for (int j = 0; ok && j < tiles; ++j) {
+        const TileRec t = recs[j];
+        // codes of x: each CTA of a pair copies half of the tokens; one box of a
+        // stage's rows, or small boxes where they come to less
+        const int n = PAIR ? t.n / 2 : t.n;
+        const bool whole = !X || n > p.x_rows - p.x_box;
+        const int boxes = whole ? 1 : ceil_div(n, p.x_box);
+        const int row = X ? t.row + (PAIR ? static_cast<int>(rank) * n : 0) : t.e * p.N + t.w0;
+        const CUtensorMap *tm = !X ? &maps.w : whole ? &maps.x : &maps.xb;
+        // scale row blocks: a pair's box always holds x_sf of x
+        const int block = X ? t.x_block : t.w_block;
+        const int blocks = !X ? 1 : PAIR ? p.x_sf : ceil_div((t.t0 & (kSfRows - 1)) + t.n, kSfRows);
+        const uint8_t *src = (X ? p.x_scales : p.w_scales) + static_cast<int64_t>(block) * p.k_blocks * kSfBytes;
+        const uint32_t bytes = SCALES ? blocks * kSfPerStage * kSfBytes : whole ? stage : boxes * p.x_box * 128;
+        debug_check(blocks <= p.x_sf && (!X || SCALES || n * 128 <= static_cast<int>(bytes)), err);
         for (int ks = 0; ks < k_stages; ++ks) {
-          const int nkb = min(kSfPerStage, p.k_blocks - ks * kSfPerStage) * kSfBytes;
           if (!mbar_wait(&empty[s], phase, abort_flag, p.timeout_ns, err)) {
             ok = false;
             break;
           }
-          uint64_t *bar = &full[s];
-          mbar_arrive_expect_tx(bar, bytes + nkb * blocks);
-          for (int b = 0; b < boxes; ++b)
-            tma_load_2d(codes + s * stage + b * p.x_box * 128, tm, bar, ks * 128, row + b * p.x_box);
-          for (int b = 0; b < blocks; ++b)
-            bulk_load(sf + s * sf_stage + b * kSfPerStage * kSfBytes, sf_src + b * sf_row, nkb, bar);
-          sf_src += kSfPerStage * kSfBytes;
+          uint8_t *dst = base + s * stage;
+          if constexpr (PAIR) {
+            // the leader's barrier counts both CTAs' bytes
+            const uint32_t bar = leader_full + s * 8;
+            if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * bytes);
+            if constexpr (SCALES) {
+              tma_load_3d_pair(dst, X ? &maps.sfx : &maps.sfw, bar, 0, ks * kSfPerStage, block);
+            } else {
+              tma_load_2d_pair(dst, tm, bar, ks * 128, row);
+              for (int b = 1; b < boxes; ++b)
+                tma_load_2d_pair(dst + b * p.x_box * 128, tm, bar, ks * 128, row + b * p.x_box);
+            }
+          } else if constexpr (SCALES) {
+            const int nkb = min(kSfPerStage, p.k_blocks - ks * kSfPerStage) * kSfBytes;
+            mbar_arrive_expect_tx(&full[s], nkb * blocks);
+            for (int b = 0; b < blocks; ++b)
+              bulk_load(dst + b * kSfPerStage * kSfBytes,
+                        src + (static_cast<int64_t>(b) * p.k_blocks + ks * kSfPerStage) * kSfBytes, nkb, &full[s]);
+          } else {
+            mbar_arrive_expect_tx(&full[s], bytes);
+            tma_load_2d(dst, tm, &full[s], ks * 128, row);
+            for (int b = 1; b < boxes; ++b)
+              tma_load_2d(dst + b * p.x_box * 128, tm, &full[s], ks * 128, row + b * p.x_box);
+          }
           ++filled;
           if (++s == S) {
             s = 0;
             phase ^= 1;
           }
         }
-        walk.next();
-        more = walk.get(p, t);
       }
-      if (!ok) {
+      if (!ok && rank == 0) {
         // let the copies already issued land before the CTA's memory goes away
+        // (a pair's leader waits for both; the partner stays until it has)
         for (int i = 0; i < S && i < filled; ++i) {
           const int last = i + ((filled - 1 - i) / S) * S;
           mbar_wait_drain(&full[i], (last / S) & 1, 100000000ull);
         }
       }
+    };
+    if (elect_one()) {
+      if (warp == 0)
+        produce(std::integral_constant<int, W_CODES>());
+      else if (warp == kWarpProd1)
+        produce(std::integral_constant<int, X_CODES>());
+      else if (warp == kWarpProd1 + 1)
+        produce(std::integral_constant<int, W_SCALES>());
+      else
+        produce(std::integral_constant<int, X_SCALES>());
     }
     __syncwarp();
   } else if (warp == kWarpMma) {
     // --------------------------------------------------------- MMA issuer ---
+    // Of a pair, only the leader's issues, for both CTAs.
     // The whole warp walks the tiles and waits, one elected lane issues: with
     // control flow and operands the same in all lanes, descriptors and
     // addresses live in uniform registers, as these instructions want them.
     const bool issuer = elect_one();
-    const uint32_t x_stage = p.x_rows * 128 >> 4, w_stage = p.rt * 128 >> 4;
+    const uint32_t x_stage = p.x_rows * 128 >> 4, w_stage = w_rows * 128 >> 4;
     const uint32_t sf_stage = kSfPerStage * kSfBytes * (1 + p.x_sf) >> 4;
-    TileWalk walk(table, p);
-    Tile t;
-    int s = 0, n_tile = 0;
+    const uint64_t wd_base = umma_desc_sw128(smem_u32(smem + p.w_off));
+    const uint64_t xd0 = umma_desc_sw128(smem_u32(smem + p.x_off));
+    const uint64_t sfd0 = scales_desc(smem_u32(smem + p.sf_off));
+    const int steps_all = ceil_div(p.K, 64);
+    int s = 0;
     uint32_t phase = 0, it = 0;
     bool ok = true;
     auto wait = [&](uint64_t *bar, uint32_t parity) {
       if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
       return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, p.timeout_ns, err)) != 0;
     };
-    for (; ok && walk.get(p, t); walk.next(), ++n_tile) {
-      const int buf = n_tile & 1;
-      ok = wait(&acc_empty[buf], ((n_tile >> 1) & 1) ^ 1u);
+    for (int j = 0; ok && rank == 0 && j < tiles; ++j) {
+      const int buf = j & 1;
+      const int n = __shfl_sync(0xffffffffu, recs[j].n, 0), t0 = __shfl_sync(0xffffffffu, recs[j].t0, 0);
+      const int w0 = __shfl_sync(0xffffffffu, recs[j].w0, 0);
+      ok = wait(&acc_empty[buf], ((j >> 1) & 1) ^ 1u);
       if (!ok) break;
-      const int n = __shfl_sync(0xffffffffu, t.n, 0), t0 = __shfl_sync(0xffffffffu, t.t0, 0);
-      const int w0 = __shfl_sync(0xffffffffu, t.w0, 0);
       const uint32_t d = tmem + buf * kTileTokens;
-      const uint32_t idesc = fp4_idesc<FMT>(n);
-      const int shift = w0 & (kSfRows - 1);              // lane of the tile's first weight row
+      const uint32_t idesc = fp4_idesc<FMT, PAIR>(n);
       const uint32_t x_col = (t0 & 64) ? 2u : 0u;        // scale column of the tile's first token
-      const int x_sf = ceil_div(t0 + n, kSfRows) - t0 / kSfRows;
-      const uint64_t wd0 = umma_desc_sw128(smem_u32(smem + p.w_off) - shift * 128);
-      const uint64_t xd0 = umma_desc_sw128(smem_u32(smem + p.x_off));
-      const uint64_t sfd0 = scales_desc(smem_u32(smem + p.sf_off));
-      int kb_left = p.k_blocks, steps_left = ceil_div(p.K, 64);
+      const int x_sf = ceil_div((t0 & (kSfRows - 1)) + n, kSfRows);
+      // the descriptor starts w0 mod 128 rows before the tile's first weight row
+      const uint64_t wd0 = wd_base - ((w0 & (kSfRows - 1)) * 128 >> 4);
+      int kb_left = p.k_blocks, steps_left = steps_all;
       for (int ks = 0; ks < k_stages; ++ks) {
         ok = wait(&full[s], phase);
         if (!ok) break;
@@ -400,10 +580,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t wd = wd0 + s * w_stage, xd = xd0 + s * x_stage, sfd = sfd0 + s * sf_stage;
         if (issuer) {
           if (x_sf == 1)
-            issue_stage<FMT, 1>(d, idesc, wd, xd, sf, sfd, x_col, kb_left, steps_left, ks == 0);
+            issue_stage<FMT, 1, PAIR>(d, idesc, wd, xd, sf, sfd, x_col, kb_left, steps_left, ks == 0);
           else
-            issue_stage<FMT, 2>(d, idesc, wd, xd, sf, sfd, x_col, kb_left, steps_left, ks == 0);
-          umma_commit(&empty[s]);
+            issue_stage<FMT, 2, PAIR>(d, idesc, wd, xd, sf, sfd, x_col, kb_left, steps_left, ks == 0);
+          commit_to<PAIR>(&empty[s]);
         }
         __syncwarp();
         kb_left -= kSfPerStage;
@@ -414,38 +594,38 @@ __global__ void __launch_bounds__(kThreads, 1)
           phase ^= 1;
         }
       }
-      if (ok && issuer) umma_commit(&acc_full[buf]);
+      if (ok && issuer) commit_to<PAIR>(&acc_full[buf]);
     }
     if (!ok && issuer) {
-      umma_commit(&mma_done);
+      commit_to<PAIR>(&mma_done);
       mbar_wait_drain(&mma_done, 0, 100000000ull);
     }
     __syncwarp();
   } else {
     // ------------------------------------------------------------ epilogue --
-    // Two halves of four warps (one per lane quarter) take alternate runs of
-    // 32 tokens.
-    const int ew = warp - kWarpEpi0, half = ew >> 2;
+    // Groups of four warps (one per lane quarter) take turns at runs of 32
+    // tokens.  The accumulator has features in lanes and tokens in columns; a
+    // group turns a run around through shared memory, so that a token's features
+    // leave in wide stores.  (Straight from the registers, 2 bytes per lane, a
+    // tile of 192 tokens took 4300 cycles, more than its products.)
+    const int group = (warp - kWarpEpi0) >> 2;
     const int quarter = warp & 3;                  // the TMEM lanes this warp may read
-    const int bar = 1 + half;
-    const int htid = (ew & 3) * 32 + lane;         // thread within the half
-    float *ex = reinterpret_cast<float *>(smem + p.ex_off + half * kXBytes);
-    TileWalk walk(table, p);
-    Tile t;
-    int n_tile = 0;
-    for (; walk.get(p, t); walk.next(), ++n_tile) {
-      const int buf = n_tile & 1;
-      bool ok = mbar_wait(&acc_full[buf], (n_tile >> 1) & 1, abort_flag, p.timeout_ns, err);
-      ok = SWIGLU ? bar_and_half(bar, ok) : __all_sync(0xffffffffu, ok);
+    const int bar = 1 + group;
+    const int gtid = ((warp - kWarpEpi0) & 3) * 32 + lane;         // thread within the group
+    uint8_t *ex = smem + p.ex_off + group * kExBytes;
+    for (int j = 0; j < tiles; ++j) {
+      const TileRec t = recs[j];
+      const int buf = j & 1;
+      bool ok = mbar_wait(&acc_full[buf], (j >> 1) & 1, abort_flag, p.timeout_ns, err);
+      ok = bar_and_group(bar, ok);
       if (!ok) break;
       tc_fence_after();
       const uint32_t acc = tmem + buf * kTileTokens + (static_cast<uint32_t>(quarter) << 21);
       const float alpha = p.x_scale * (p.w_scale ? __ldg(p.w_scale + t.e) : 1.0f);
       const int lane0 = t.w0 & (kSfRows - 1);      // the tile's lanes: [lane0, lane0 + rt)
       const int row_in_block = quarter * 32 + lane;
-      const bool mine = row_in_block >= lane0 && row_in_block < lane0 + p.rt;
-      const bool warp_mine = quarter * 32 < lane0 + p.rt && quarter * 32 + 32 > lane0;
-      for (int c0 = half * 32; c0 < t.valid; c0 += 64) {
+      const bool warp_mine = quarter * 32 < lane0 + w_rows && quarter * 32 + 32 > lane0;
+      for (int c0 = group * 32; c0 < t.valid; c0 += 32 * kEpiGroups) {
         uint32_t r[2][16];
         if (warp_mine) {
           tmem_ld16(acc + c0, r[0]);
@@ -453,38 +633,41 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld_wait();
         }
         if constexpr (!SWIGLU) {
-          const int64_t n = (t.w0 & ~(kSfRows - 1)) + row_in_block;
-          if (mine && n < p.N) {
-            uint16_t *out = static_cast<uint16_t *>(p.out) + static_cast<int64_t>(t.off + t.t0 + c0) * p.N + n;
+          uint16_t *ex16 = reinterpret_cast<uint16_t *>(ex);
+          if (warp_mine) {
 #pragma unroll
             for (int c = 0; c < 32; ++c)
-              if (c0 + c < t.valid) out[static_cast<int64_t>(c) * p.N] = A::store(__uint_as_float(r[c >> 4][c & 15]) * alpha);
+              ex16[c * kYPitch + row_in_block] = A::store(__uint_as_float(r[c >> 4][c & 15]) * alpha);
           }
+          bar_sync_group(bar);
+          store_rows(ex16, static_cast<uint16_t *>(p.out) + static_cast<int64_t>(t.row + c0) * p.N,
+                     p.N, t.w0 & ~(kSfRows - 1), lane0, lane0 + w_rows, min(32, t.valid - c0), gtid, p.wide);
+          bar_sync_group(bar);
         } else {
           if (warp_mine) {
             // lanes 0-15 hold gate rows, 16-31 the same features' up rows: a
             // swap across the half warps gives the lower half the even
             // tokens' pairs and the upper half the odd tokens'
             const bool upper = lane >= 16;
-            float *dst = ex + (lane >> 4) * kXPitch + quarter * 16 + (lane & 15);
+            float *dst = reinterpret_cast<float *>(ex) + (lane >> 4) * kHPitch + quarter * 16 + (lane & 15);
 #pragma unroll
             for (int c = 0; c < 32; c += 2) {
               const float a = __uint_as_float(r[c >> 4][c & 15]) * alpha;
               const float b = __uint_as_float(r[c >> 4][(c & 15) + 1]) * alpha;
               const float other = __shfl_xor_sync(0xffffffffu, upper ? a : b, 16);
               const float g = upper ? other : a, u = upper ? b : other;
-              dst[c * kXPitch] = g * sigmoid_fast(g) * u;
+              dst[c * kHPitch] = g * sigmoid_fast(g) * u;
             }
           }
-          bar_sync_half(bar);
+          bar_sync_group(bar);
           // one token's 16 features per thread: the four loads go in an order
           // that keeps the eight threads of a phase on different banks
-          const int tok = htid >> 2, fq = htid & 3;
+          const int tok = gtid >> 2, fq = gtid & 3;
           const int f0 = (t.w0 & ~(kSfRows - 1)) / 2 + fq * 16;      // first feature
           const int I = p.N / 2;
-          const bool in_tile = fq * 32 >= lane0 && fq * 32 < lane0 + p.rt;
+          const bool in_tile = fq * 32 >= lane0 && fq * 32 < lane0 + w_rows;
           const bool have = in_tile && c0 + tok < t.valid;
-          const float4 *src = reinterpret_cast<const float4 *>(ex + tok * kXPitch + fq * 16);
+          const float4 *src = reinterpret_cast<const float4 *>(reinterpret_cast<float *>(ex) + tok * kHPitch + fq * 16);
           float4 v[4];
           uint32_t amax = 0;
           const int rot = (fq >> 1) + 2 * (tok & 1);
@@ -499,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t byte = fp4_scale_of<FMT>(amax, p.hq, inv);
           const int tl = t.t0 + c0 + tok;       // token within the group
           if (have) {
-            const int64_t blk = (p.offsets ? ragged_row_block(t.off, t.e) : 0) + tl / kSfRows;
+            const int64_t blk = t.x_block - t.t0 / kSfRows + tl / kSfRows;
             const int j = f0 / Fp4<FMT>::kBlock;
             uint8_t *sc = p.h_scales + (blk * p.h_k_blocks + (j >> 2)) * kSfBytes + (tl & 31) * 16 + ((tl >> 5) & 3) * 4;
             if (f0 < I && (FMT == FP4_NV || (fq & 1) == 0)) {
@@ -518,21 +701,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                 codes |= static_cast<uint64_t>(c8 & 0xFFFFu) << (16 * ((i + rot) & 3));
                 codes |= static_cast<uint64_t>(c8 >> 16) << (16 * ((i + 1 + rot) & 3));
               }
-              *reinterpret_cast<uint64_t *>(p.h_codes + static_cast<int64_t>(t.off + tl) * (I / 2) + f0 / 2) = codes;
+              *reinterpret_cast<uint64_t *>(p.h_codes + static_cast<int64_t>(t.row + c0 + tok) * (I / 2) + f0 / 2) = codes;
             }
           }
-          bar_sync_half(bar);
+          bar_sync_group(bar);
         }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&acc_empty[buf]);
+      if (lane == 0) {
+        if (PAIR)
+          mbar_arrive_cluster(leader_address(&acc_empty[buf]));
+        else
+          mbar_arrive(&acc_empty[buf]);
+      }
     }
   }
   tc_fence_before();
   __syncthreads();
+  if (PAIR) cluster_sync();      // nothing of the partner's reaches this CTA any more
   tc_fence_after();
-  if (warp == kWarpMma) tmem_dealloc(tmem, 512);
+  if (warp == kWarpMma) tmem_free_all<PAIR>(tmem);
 }
 
 // -------------------------------------------------------------------- host --
@@ -568,14 +757,32 @@ bool encode_codes(CUtensorMap *map, const void *base, int64_t rows, int64_t K, i
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Tokens per group from which CTA pairs are taken.
+constexpr int kPairTokens = 64;
+
 constexpr int kSmemLimit = 227 * 1024 - 1024;   // less the static part
 
+int64_t ceil_div64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int align_up(int v, int a) { return (v + a - 1) / a * a; }
 
-template <class A, int FMT, bool SWIGLU>
+// Scale blocks [row blocks, k blocks] of 512 bytes as 128 words each; a box is a
+// stage's blocks of `rows` row blocks.
+bool encode_scales(CUtensorMap *map, const void *base, int64_t row_blocks, int64_t k_blocks, int per_stage, int rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {kSfBytes / 4, static_cast<cuuint64_t>(k_blocks), static_cast<cuuint64_t>(row_blocks)};
+  const cuuint64_t strides[2] = {kSfBytes, static_cast<cuuint64_t>(k_blocks) * kSfBytes};
+  const cuuint32_t boxes[3] = {kSfBytes / 4, static_cast<cuuint32_t>(per_stage), static_cast<cuuint32_t>(rows)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<void *>(base), dims, strides, boxes, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <class A, int FMT, bool SWIGLU, bool PAIR>
 cudaError_t launch_gemm(const Fp4GemmArgs &a, GemmParams p, int num_sms, cudaStream_t stream, bool dependent) {
   constexpr int kSfPerStage = kStageK / Fp4<FMT>::kSfK;
-  auto *kernel = fp4_gemm_kernel<A, FMT, SWIGLU>;
+  auto *kernel = fp4_gemm_kernel<A, FMT, SWIGLU, PAIR>;
   static std::once_flag once[64];
   static cudaError_t attr[64];
   int dev = 0;
@@ -590,11 +797,22 @@ cudaError_t launch_gemm(const Fp4GemmArgs &a, GemmParams p, int num_sms, cudaStr
   // shared memory: x stages, weight stages, scale stages, exchange buffers,
   // group table; around the weight stages at least the 128 - rt rows that an
   // MMA reads beyond a short tile
-  const int slack = (kSfRows - p.rt) * 128;
-  const int ex = SWIGLU ? 2 * kXBytes : 0;
+  const int w_rows = PAIR ? kSfRows : p.rt;
+  const int slack = (kSfRows - w_rows) * 128;
+  const int ex = kEpiGroups * kExBytes;
   const int table = align_up(2 * (p.groups + 1) * 4, 16);
-  const int x_stage = p.x_rows * 128, w_stage = p.rt * 128, sf_stage = kSfPerStage * kSfBytes * (1 + p.x_sf);
-  const int fixed = 1024 + 2 * slack + ex + table;
+  // CTAs (pairs): one per SM (two SMs), no more than tiles can exist, and no more
+  // tiles each than there are records
+  const int64_t groups = p.groups < p.rows ? p.groups : p.rows;
+  const int64_t most = (static_cast<int64_t>(p.rows) / p.bt + groups) * p.n_tiles;
+  int64_t slots = PAIR ? num_sms / 2 : num_sms;
+  if (most < slots) slots = most;
+  if (ceil_div64(most, slots) > kMaxRecs) slots = ceil_div64(most, kMaxRecs);
+  if (slots > (1 << 30)) return cudaErrorInvalidValue;
+  p.recs = static_cast<int>(ceil_div64(most, slots));
+  const int recs = p.recs * static_cast<int>(sizeof(TileRec));
+  const int x_stage = p.x_rows * 128, w_stage = w_rows * 128, sf_stage = kSfPerStage * kSfBytes * (1 + p.x_sf);
+  const int fixed = 1024 + 2 * slack + ex + recs + table;
   int S = (kSmemLimit - fixed) / (x_stage + w_stage + sf_stage);
   if (S > kMaxStages) S = kMaxStages;
   if (S < 2) return cudaErrorInvalidValue;
@@ -603,24 +821,44 @@ cudaError_t launch_gemm(const Fp4GemmArgs &a, GemmParams p, int num_sms, cudaStr
   p.w_off = align_up(S * x_stage < slack ? slack : S * x_stage, 1024);
   p.sf_off = p.w_off + S * w_stage;
   p.ex_off = align_up(p.sf_off + S * sf_stage, 128);
-  p.table_off = p.ex_off + ex;
+  p.rec_off = p.ex_off + ex;
+  p.table_off = p.rec_off + recs;
   int bytes = p.table_off + table;
   if (bytes < p.sf_off + slack) bytes = p.sf_off + slack;
   bytes += 1024;   // base alignment
   if (bytes > kSmemLimit) return cudaErrorInvalidValue;
 
-  CUtensorMap tm_w, tm_x, tm_xb;
-  if (!encode_codes(&tm_w, a.w_codes, static_cast<int64_t>(p.groups) * p.N, p.K, p.rt) ||
-      !encode_codes(&tm_x, a.x_codes, p.rows, p.K, p.x_rows))
+  GemmMaps maps;
+  if (!encode_codes(&maps.w, a.w_codes, static_cast<int64_t>(p.groups) * p.N, p.K, w_rows) ||
+      !encode_codes(&maps.x, a.x_codes, p.rows, p.K, p.x_rows))
     return cudaErrorInvalidValue;
-  tm_xb = tm_x;
-  if (p.x_box != p.x_rows && !encode_codes(&tm_xb, a.x_codes, p.rows, p.K, p.x_box)) return cudaErrorInvalidValue;
-  // no more CTAs than tiles can exist
-  const int64_t token_tiles_max = static_cast<int64_t>(p.rows) / p.bt + (p.groups < p.rows ? p.groups : p.rows);
-  const int64_t most = token_tiles_max * p.n_tiles;
-  const int grid = static_cast<int>(most < num_sms ? most : num_sms);
-  return launch_on(kernel, dim3(static_cast<unsigned>(grid)), kThreads, static_cast<size_t>(bytes), stream, dependent,
-                   p, tm_w, tm_x, tm_xb);
+  maps.xb = maps.x;
+  if (p.x_box != p.x_rows && !encode_codes(&maps.xb, a.x_codes, p.rows, p.K, p.x_box)) return cudaErrorInvalidValue;
+  maps.sfw = maps.sfx = maps.x;
+  if (PAIR) {
+    const int64_t x_blocks = a.offsets ? ragged_row_block(p.rows, p.groups) : ceil_div(p.rows, kSfRows);
+    if (!encode_scales(&maps.sfw, a.w_scales, static_cast<int64_t>(p.groups) * p.w_row_blocks, p.k_blocks, kSfPerStage,
+                       1) ||
+        !encode_scales(&maps.sfx, a.x_scales, x_blocks, p.k_blocks, kSfPerStage, p.x_sf))
+      return cudaErrorInvalidValue;
+  }
+  const int grid = static_cast<int>(slots) * (PAIR ? 2 : 1);
+  return launch_clusters(kernel, dim3(static_cast<unsigned>(grid)), PAIR ? 2 : 1, kThreads, static_cast<size_t>(bytes),
+                         stream, dependent, p, maps);
+}
+
+template <bool PAIR>
+cudaError_t dispatch_gemm(const Fp4GemmArgs &a, const GemmParams &p, int num_sms, cudaStream_t stream,
+                          bool dependent) {
+  const bool mx = a.fmt == FP4_MX;
+  if (a.swiglu)
+    return mx ? launch_gemm<ActBf16, FP4_MX, true, PAIR>(a, p, num_sms, stream, dependent)
+              : launch_gemm<ActBf16, FP4_NV, true, PAIR>(a, p, num_sms, stream, dependent);
+  if (a.act == ActF16::kId)
+    return mx ? launch_gemm<ActF16, FP4_MX, false, PAIR>(a, p, num_sms, stream, dependent)
+              : launch_gemm<ActF16, FP4_NV, false, PAIR>(a, p, num_sms, stream, dependent);
+  return mx ? launch_gemm<ActBf16, FP4_MX, false, PAIR>(a, p, num_sms, stream, dependent)
+            : launch_gemm<ActBf16, FP4_NV, false, PAIR>(a, p, num_sms, stream, dependent);
 }
 
 }  // namespace
@@ -642,24 +880,42 @@ cudaError_t launch_fp4_gemm(const Fp4GemmArgs &a, int num_sms, uint64_t timeout_
   p.k_blocks = static_cast<int>(fp4_k_blocks(a.K, a.fmt));
   p.w_row_blocks = ceil_div(p.N, kSfRows);
   p.bt = p.max_group >= kTileTokens ? kTileTokens : align_up(p.max_group, 16);
-  p.x_box = p.bt < 64 ? p.bt : 64;
-  p.x_rows = align_up(p.bt, p.x_box);
   p.x_sf = p.max_group > 128 ? 2 : 1;
   p.out = a.out;
+  p.wide = a.N % 8 == 0 && reinterpret_cast<uintptr_t>(a.out) % 16 == 0;
   p.h_codes = a.h_codes;
   p.h_scales = a.h_scales;
   p.h_k_blocks = a.swiglu ? static_cast<int>(fp4_k_blocks(a.N / 2, a.fmt)) : 0;
   p.hq = make_fp4_scale(a.h_scale);
   p.timeout_ns = timeout_ns;
 
+  // (group, token tile) pairs there can be at most
+  const int64_t groups = p.groups < p.rows ? p.groups : p.rows;
+  const int64_t tiles = static_cast<int64_t>(p.rows) / p.bt + groups;
+
+  // CTA pairs share a tile of 256 weight rows: each copies its own 128 rows and
+  // half of the tokens, which leaves an SM a quarter less to copy per product.
+  // With few tokens per group the weights are all there is to copy, and the tiles
+  // are better spread over single CTAs.
+  if (p.rows / groups >= kPairTokens && tiles * ceil_div(p.N, 256) * 2 >= num_sms) {
+    p.bt = align_up(p.bt, 32);
+    p.x_rows = p.bt / 2;
+    p.x_box = p.x_rows < 32 ? p.x_rows : 32;
+    p.x_rows = align_up(p.x_rows, p.x_box);
+    p.rt = 2 * kSfRows;
+    p.n_tiles = ceil_div(p.N, p.rt);
+    return dispatch_gemm<true>(a, p, num_sms, stream, dependent);
+  }
+
   // Rows of a weight tile: the fewest rounds of the SMs, counted in rows plus a
-  // fixed cost per tile, over the most (group, token tile) pairs there can be.
-  const int64_t pairs = static_cast<int64_t>(p.rows) / p.bt + (p.groups < p.rows ? p.groups : p.rows);
+  // fixed cost per tile.
+  p.x_box = p.bt < 64 ? p.bt : 64;
+  p.x_rows = align_up(p.bt, p.x_box);
   const int least = !a.swiglu ? 16 : a.fmt == FP4_MX ? 64 : 32;   // a hidden block's features within one tile
   int64_t best = -1;
   p.rt = kSfRows;
   for (int rt = kSfRows; rt >= least; rt /= 2) {
-    const int64_t rounds = (pairs * ceil_div(p.N, rt) + num_sms - 1) / num_sms;
+    const int64_t rounds = (tiles * ceil_div(p.N, rt) + num_sms - 1) / num_sms;
     const int64_t cost = rounds * (rt + 16);
     if (best < 0 || cost < best) {
       best = cost;
@@ -667,15 +923,7 @@ cudaError_t launch_fp4_gemm(const Fp4GemmArgs &a, int num_sms, uint64_t timeout_
     }
   }
   p.n_tiles = ceil_div(p.N, p.rt);
-
-  if (a.swiglu)
-    return a.fmt == FP4_MX ? launch_gemm<ActBf16, FP4_MX, true>(a, p, num_sms, stream, dependent)
-                           : launch_gemm<ActBf16, FP4_NV, true>(a, p, num_sms, stream, dependent);
-  if (a.act == ActF16::kId)
-    return a.fmt == FP4_MX ? launch_gemm<ActF16, FP4_MX, false>(a, p, num_sms, stream, dependent)
-                           : launch_gemm<ActF16, FP4_NV, false>(a, p, num_sms, stream, dependent);
-  return a.fmt == FP4_MX ? launch_gemm<ActBf16, FP4_MX, false>(a, p, num_sms, stream, dependent)
-                         : launch_gemm<ActBf16, FP4_NV, false>(a, p, num_sms, stream, dependent);
+  return dispatch_gemm<false>(a, p, num_sms, stream, dependent);
 }
 
 // Read and clear the device error word of this translation unit's kernels.

@@ -141,6 +141,20 @@ def test_linear(dev, fmt, dt, M, N, K):
 
 
 @formats
+@pytest.mark.parametrize("M,N,K", [(256, 20000, 64), (64, 19500, 96), (97, 19585, 288), (193, 13000, 544),
+                                   (200, 10001, 320), (385, 7100, 640), (1030, 5000, 1056)])
+def test_linear_on_cta_pairs(dev, fmt, M, N, K):
+    """Sizes with enough tiles for the two-CTA form: ragged rows of both operands."""
+    x = randn(M + N + K, M, K)
+    w, ws, wg, vals = weight(3, 1, N, K, fmt)
+    y = ops.fp4_linear(x, w[0], ws[0], fmt, x_scale=SCALE[fmt], w_scale=wg)
+    ops.qsw_check_device_errors()
+    a = held(x, fmt)
+    want = a @ vals[0].T
+    check(y, want, ref.half_ulp(want, BF16) * (1 + 2.0 ** -8) + ref.sum_bound(a.abs() @ vals[0].abs().T, K) + 2.0 ** -26)
+
+
+@formats
 def test_linear_is_deterministic_and_flattens(dev, fmt):
     x = randn(1, 3, 5, 512)
     w, ws, wg, _ = weight(4, 1, 320, 512, fmt)
@@ -192,6 +206,13 @@ def test_grouped_linear(dev, fmt, sizes, N, K):
         want = a[s] @ vals[e].T
         check(y[s], want, ref.half_ulp(want, F16) * (1 + 2.0 ** -8) + ref.sum_bound(a[s].abs() @ vals[e].abs().T, K)
               + 2.0 ** -26, e)
+
+
+@formats
+@pytest.mark.parametrize("N,K", [(2100, 160), (1793, 576)])
+def test_grouped_linear_on_cta_pairs(dev, fmt, N, K):
+    """The two-CTA form over ragged groups, empty ones among them."""
+    test_grouped_linear(dev, fmt, [100, 0, 257, 64, 31, 192, 0, 193, 128, 500, 1, 97], N, K)
 
 
 def test_grouped_linear_clamps_offsets(dev):
@@ -333,6 +354,25 @@ def test_moe_mlp_many_tokens_equals_few(dev, fmt):
     y = mlp(slice(None))
     ops.qsw_check_device_errors()
     for a, b in ((0, 1), (13, 14), (100, 117), (300, 430), (699, 700)):
+        assert torch.equal(y[a:b], mlp(slice(a, b))), (a, b)
+
+
+@formats
+def test_moe_mlp_on_cta_pairs(dev, fmt):
+    """A long batch (two-CTA tiles) gives each token the bits that it gets alone."""
+    T, E, k, H, I = 230, 8, 4, 1824, 928
+    x = randn(1, T, H)
+    logits = randn(2, T, E, dt=torch.float32)
+    gu, gus, gug, _ = weight(8, E, 2 * I, H, fmt)
+    d, ds, dg, _ = weight(9, E, H, I, fmt)
+
+    def mlp(rows):
+        return ops.fp4_moe_mlp(x[rows], ops.moe_route(logits[rows], k), gu, gus, d, ds, fmt, x_scale=SCALE[fmt],
+                               h_scale=SCALE[fmt], gu_scale=gug, d_scale=dg)
+    y = mlp(slice(None))
+    ops.qsw_check_device_errors()
+    assert torch.isfinite(y.float()).all()
+    for a, b in ((0, 1), (7, 9), (100, 117), (229, 230)):
         assert torch.equal(y[a:b], mlp(slice(a, b))), (a, b)
 
 
