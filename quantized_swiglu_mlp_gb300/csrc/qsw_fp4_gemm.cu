@@ -23,9 +23,9 @@
 // weights' and activations' codes and scales (a ring of stages of 256 elements of
 // K: 128-byte swizzled code tiles by TMA, scale blocks by TMA or bulk copies; one
 // warp each, since a copy takes its issuer over 100 cycles), warp 1 moves the
-// scales into tensor memory and issues the MMAs, warps 2-13 run the epilogue.  Tensor memory: two accumulators of 192
-// columns, so that a tile's epilogue runs under the next tile's products, and
-// two scale buffers of 48 columns.
+// scales into tensor memory and issues the MMAs, warps 2-13 run the epilogue.
+// Tensor memory: two accumulators of 192 columns, so that a tile's epilogue runs
+// under the next tile's products, and two scale buffers of 48 columns.
 //
 // Programmatic dependent launch: everything a CTA does before griddep_wait --
 // the group table, the weights of its first stages -- reads only what was
@@ -181,8 +181,10 @@ __device__ __forceinline__ uint32_t leader_address(const void *p) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_u32(p)));
   return a;
 }
+// Relaxed: nothing in memory is handed over (a releasing arrival would wait for the
+// thread's global stores to be performed).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void tma_load_2d_pair(void *dst, const CUtensorMap *map, uint32_t bar, int c0, int c1) {
   asm volatile(
@@ -625,6 +627,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int lane0 = t.w0 & (kSfRows - 1);      // the tile's lanes: [lane0, lane0 + rt)
       const int row_in_block = quarter * 32 + lane;
       const bool warp_mine = quarter * 32 < lane0 + w_rows && quarter * 32 + 32 > lane0;
+      bool released = false;
+      auto release = [&] {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (PAIR)
+            mbar_arrive_cluster(leader_address(&acc_empty[buf]));
+          else
+            mbar_arrive(&acc_empty[buf]);
+        }
+        released = true;
+      };
       for (int c0 = group * 32; c0 < t.valid; c0 += 32 * kEpiGroups) {
         uint32_t r[2][16];
         if (warp_mine) {
@@ -632,6 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld16(acc + c0 + 16, r[1]);
           tmem_ld_wait();
         }
+        if (c0 + 32 * kEpiGroups >= t.valid) release();     // the warp's last look at the accumulator
         if constexpr (!SWIGLU) {
           uint16_t *ex16 = reinterpret_cast<uint16_t *>(ex);
           if (warp_mine) {
@@ -707,14 +722,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           bar_sync_group(bar);
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if (PAIR)
-          mbar_arrive_cluster(leader_address(&acc_empty[buf]));
-        else
-          mbar_arrive(&acc_empty[buf]);
-      }
+      if (!released) release();
     }
   }
   tc_fence_before();

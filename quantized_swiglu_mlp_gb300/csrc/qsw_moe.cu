@@ -4,6 +4,7 @@
 // equals) and their weights.  Selection looks at the logits themselves -- softmax
 // and sigmoid keep their order -- so it is exact whatever the exponential does.
 // sort_kernel: the stable counting sort of the (token, choice) pairs by expert.
+// route_small_kernel: both, for few tokens.
 // combine_kernel: y[t] = T(sum_j weights[t, j] rows[slots[t, j]] (+ residual[t])),
 // each token summing its own rows in order: no atomics, the same bits every time.
 #include "qsw_fp4.cuh"
@@ -38,18 +39,24 @@ __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k);
 }
 
-// One warp per token; lane l holds experts l, l + 32, ... (PER of them).  Each of
+struct RouteParams {
+  const void *logits;
+  int64_t T;
+  int E, k, scoring, renormalize;
+  float scale;
+  int *ids;
+  float *weights;
+  int *offsets, *slots, *order;
+};
+
+// One warp per token t; lane l holds experts l, l + 32, ... (PER of them).  Each of
 // the k rounds takes the warp's largest key and, among its holders, the lowest
-// index (key 0: taken or past the end).
+// index (key 0: taken or past the end).  Returns lane j's choice j.
 template <class L, int PER>
-__global__ void __launch_bounds__(kTopkWarps * 32)
-    topk_kernel(const L *__restrict__ logits, int64_t T, int E, int k, int scoring, int renormalize, float scale,
-                int *ids, float *weights) {
-  griddep_wait();
-  griddep_launch_dependents();
+__device__ __forceinline__ int topk_row(const RouteParams &p, int64_t t) {
   const int lane = threadIdx.x & 31;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * kTopkWarps + (threadIdx.x >> 5);
-  if (t >= T) return;
+  const int E = p.E, k = p.k, scoring = p.scoring, renormalize = p.renormalize;
+  const L *logits = static_cast<const L *>(p.logits);
   const int wide = static_cast<int>(sizeof(L) == 4 ? 1 : 0);
   const uint8_t *row = reinterpret_cast<const uint8_t *>(logits) + t * E * (wide ? 4 : 2);
   uint32_t key[PER];
@@ -105,8 +112,46 @@ __global__ void __launch_bounds__(kTopkWarps * 32)
   if (lane < k) {
     float w = mine;
     if (scoring == QSW_ROUTE_SOFTMAX || renormalize) w = sum > 0.0f ? mine / sum : 0.0f;
-    ids[t * k + lane] = id;
-    weights[t * k + lane] = w * scale;
+    p.ids[t * k + lane] = id;
+    p.weights[t * k + lane] = w * p.scale;
+  }
+  return id;
+}
+
+template <class L, int PER>
+__global__ void __launch_bounds__(kTopkWarps * 32) topk_kernel(const RouteParams p) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * kTopkWarps + (threadIdx.x >> 5);
+  if (t < p.T) topk_row<L, PER>(p, t);
+}
+
+// Few tokens: choices and sort in one CTA and one launch.  The ids stay in shared
+// memory; thread i places pair i, counting the pairs of smaller experts and those
+// of its own before it.
+constexpr int kSmallPairs = 256;
+template <class L, int PER>
+__global__ void __launch_bounds__(1024) route_small_kernel(const RouteParams p) {
+  __shared__ int ids[kSmallPairs];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31, n = static_cast<int>(p.T) * p.k;
+  for (int t = threadIdx.x >> 5; t < static_cast<int>(p.T); t += blockDim.x >> 5) {
+    const int id = topk_row<L, PER>(p, t);
+    if (lane < p.k) ids[t * p.k + lane] = id;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+    const int e = ids[i];
+    int at = 0;
+    for (int j = 0; j < n; ++j) at += ids[j] < e || (ids[j] == e && j < i);
+    p.slots[i] = at;
+    p.order[at] = i;
+  }
+  for (int e = threadIdx.x; e <= p.E; e += blockDim.x) {
+    int at = 0;
+    for (int j = 0; j < n; ++j) at += ids[j] < e;
+    p.offsets[e] = at;
   }
 }
 
@@ -193,7 +238,8 @@ __global__ void __launch_bounds__(kSortThreads)
   }
 }
 
-// One warp per token and run of 256 columns; 8 columns per lane.
+// One warp per token and run of 256 columns; 8 columns per lane.  The rows of eight
+// choices are on their way before the first is added.
 template <class A>
 __global__ void __launch_bounds__(256)
     combine_kernel(const uint16_t *__restrict__ rows, int64_t n_rows, const int *__restrict__ slots,
@@ -201,13 +247,23 @@ __global__ void __launch_bounds__(256)
                    int chunks, uint16_t *y) {
   griddep_wait();
   griddep_launch_dependents();
+  constexpr int AHEAD = 8;
   const int lane = threadIdx.x & 31;
   const int64_t w = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
   const int64_t t = w / chunks;
   const int64_t h = (w - t * chunks) * 256 + lane * 8;
-  if (t >= T || h >= H) return;
+  if (t >= T) return;
+  // lane j holds choice j
+  int slot = -1;
+  float weight = 0.0f;
+  if (lane < k) {
+    slot = __ldg(slots + t * k + lane);
+    weight = __ldg(weights + t * k + lane);
+    if (slot >= n_rows) slot = -1;
+  }
+  const bool in = h < H;
   float acc[8] = {};
-  if (residual) {
+  if (residual && in) {
     const uint4 v = *reinterpret_cast<const uint4 *>(residual + t * H + h);
     const uint32_t q[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -216,36 +272,56 @@ __global__ void __launch_bounds__(256)
       acc[2 * i + 1] = A::hi(q[i]);
     }
   }
-  for (int j = 0; j < k; ++j) {
-    const int s = __ldg(slots + t * k + j);
-    if (s < 0 || s >= n_rows) continue;
-    const float g = __ldg(weights + t * k + j);
-    const uint4 v = __ldg(reinterpret_cast<const uint4 *>(rows + static_cast<int64_t>(s) * H + h));
-    const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+  for (int j0 = 0; j0 < k; j0 += AHEAD) {
+    uint4 v[AHEAD];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      acc[2 * i] = fmaf(g, A::lo(q[i]), acc[2 * i]);
-      acc[2 * i + 1] = fmaf(g, A::hi(q[i]), acc[2 * i + 1]);
+    for (int a = 0; a < AHEAD; ++a) {
+      const int s = __shfl_sync(0xffffffffu, slot, (j0 + a) & 31);
+      v[a] = j0 + a < k && s >= 0 && in ? __ldg(reinterpret_cast<const uint4 *>(rows + static_cast<int64_t>(s) * H + h))
+                                        : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int a = 0; a < AHEAD; ++a) {
+      const float g = __shfl_sync(0xffffffffu, weight, (j0 + a) & 31);
+      const int s = __shfl_sync(0xffffffffu, slot, (j0 + a) & 31);
+      if (j0 + a >= k || s < 0) continue;
+      const uint32_t q[4] = {v[a].x, v[a].y, v[a].z, v[a].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        acc[2 * i] = fmaf(g, A::lo(q[i]), acc[2 * i]);
+        acc[2 * i + 1] = fmaf(g, A::hi(q[i]), acc[2 * i + 1]);
+      }
     }
   }
-  *reinterpret_cast<uint4 *>(y + t * H + h) = make_uint4(A::pack2(acc[0], acc[1]), A::pack2(acc[2], acc[3]),
-                                                        A::pack2(acc[4], acc[5]), A::pack2(acc[6], acc[7]));
+  if (in)
+    *reinterpret_cast<uint4 *>(y + t * H + h) = make_uint4(A::pack2(acc[0], acc[1]), A::pack2(acc[2], acc[3]),
+                                                          A::pack2(acc[4], acc[5]), A::pack2(acc[6], acc[7]));
+}
+
+template <class L, int PER>
+cudaError_t launch_route(const RouteParams &p, cudaStream_t stream) {
+  const int64_t n = p.T * p.k;
+  if (n <= kSmallPairs) {
+    const int warps = p.T < 1 ? 1 : p.T > 32 ? 32 : static_cast<int>(p.T);
+    const int threads = warps * 32 > p.E ? warps * 32 : (p.E + 31) / 32 * 32;
+    return launch_on(route_small_kernel<L, PER>, dim3(1), threads, 0, stream, false, p);
+  }
+  const dim3 grid(static_cast<unsigned>((p.T + kTopkWarps - 1) / kTopkWarps));
+  const cudaError_t e = launch_on(topk_kernel<L, PER>, grid, kTopkWarps * 32, 0, stream, false, p);
+  if (e != cudaSuccess) return e;
+  const int threads = n >= 8192 ? kSortThreads : 256;
+  return launch_on(sort_kernel, dim3(static_cast<unsigned>(p.E)), threads, 0, stream, true, p.ids, static_cast<int>(n),
+                   p.E, p.offsets, p.slots, p.order);
 }
 
 template <class L>
-cudaError_t launch_topk(const void *logits, int64_t T, int E, int k, int scoring, int renormalize, float scale,
-                        int *ids, float *weights, cudaStream_t stream) {
-  const dim3 grid(static_cast<unsigned>((T + kTopkWarps - 1) / kTopkWarps));
-  const auto *l = static_cast<const L *>(logits);
-#define QSW_TOPK(P) \
-  launch_on(topk_kernel<L, P>, grid, kTopkWarps * 32, 0, stream, false, l, T, E, k, scoring, renormalize, scale, ids, weights)
-  if (E <= 32) return QSW_TOPK(1);
-  if (E <= 64) return QSW_TOPK(2);
-  if (E <= 128) return QSW_TOPK(4);
-  if (E <= 256) return QSW_TOPK(8);
-  if (E <= 512) return QSW_TOPK(16);
-  return QSW_TOPK(32);
-#undef QSW_TOPK
+cudaError_t launch_route_of(const RouteParams &p, cudaStream_t stream) {
+  if (p.E <= 32) return launch_route<L, 1>(p, stream);
+  if (p.E <= 64) return launch_route<L, 2>(p, stream);
+  if (p.E <= 128) return launch_route<L, 4>(p, stream);
+  if (p.E <= 256) return launch_route<L, 8>(p, stream);
+  if (p.E <= 512) return launch_route<L, 16>(p, stream);
+  return launch_route<L, 32>(p, stream);
 }
 
 }  // namespace
@@ -253,34 +329,25 @@ cudaError_t launch_topk(const void *logits, int64_t T, int E, int k, int scoring
 cudaError_t launch_moe_route(const void *logits, int logit_dtype, int64_t T, int E, int k, int scoring,
                              int renormalize, float scale, int *ids, float *weights, int *offsets, int *slots,
                              int *order, cudaStream_t stream) {
-  cudaError_t e;
-  if (T > 0) {
-    if (logit_dtype == QSW_LOGITS_F32)
-      e = launch_topk<float>(logits, T, E, k, scoring, renormalize, scale, ids, weights, stream);
-    else if (logit_dtype == QSW_ACT_BF16)
-      e = launch_topk<ActBf16>(logits, T, E, k, scoring, renormalize, scale, ids, weights, stream);
-    else
-      e = launch_topk<ActF16>(logits, T, E, k, scoring, renormalize, scale, ids, weights, stream);
-    if (e != cudaSuccess) return e;
-  }
-  const int n = static_cast<int>(T * k);
-  const int threads = n >= 8192 ? kSortThreads : n >= 512 ? 256 : 32;
-  return launch_on(sort_kernel, dim3(static_cast<unsigned>(E)), threads, 0, stream, T > 0, ids, n, E, offsets, slots,
-                   order);
+  const RouteParams p = {logits, T, E, k, scoring, renormalize, scale, ids, weights, offsets, slots, order};
+  if (logit_dtype == QSW_LOGITS_F32) return launch_route_of<float>(p, stream);
+  return logit_dtype == QSW_ACT_BF16 ? launch_route_of<ActBf16>(p, stream) : launch_route_of<ActF16>(p, stream);
 }
 
 cudaError_t launch_moe_combine(const void *rows, int64_t n_rows, const int *slots, const float *weights,
                                const void *residual, int64_t T, int k, int64_t H, int act, void *y,
                                cudaStream_t stream, bool dependent) {
   const int chunks = static_cast<int>((H + 255) / 256);
-  const dim3 grid(static_cast<unsigned>((T * chunks + 7) / 8));
+  // few warps: one per CTA, on as many SMs
+  const int threads = T * chunks < 1024 ? 32 : 256;
+  const dim3 grid(static_cast<unsigned>((T * chunks * 32 + threads - 1) / threads));
   const auto *r = static_cast<const uint16_t *>(rows);
   const auto *res = static_cast<const uint16_t *>(residual);
   auto *o = static_cast<uint16_t *>(y);
   if (act == ActF16::kId)
-    return launch_on(combine_kernel<ActF16>, grid, 256, 0, stream, dependent, r, n_rows, slots, weights, res, T, k, H,
+    return launch_on(combine_kernel<ActF16>, grid, threads, 0, stream, dependent, r, n_rows, slots, weights, res, T, k, H,
                      chunks, o);
-  return launch_on(combine_kernel<ActBf16>, grid, 256, 0, stream, dependent, r, n_rows, slots, weights, res, T, k, H,
+  return launch_on(combine_kernel<ActBf16>, grid, threads, 0, stream, dependent, r, n_rows, slots, weights, res, T, k, H,
                    chunks, o);
 }
 
