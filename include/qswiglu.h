@@ -365,8 +365,9 @@ QSW_API qsw_status qsw_moe_route(const void *logits, int64_t T, int E, int k, in
 QSW_API size_t qsw_fp4_moe_workspace_bytes(int64_t T, int k, int64_t H, int64_t I, int E, int fmt);
 QSW_API qsw_status qsw_fp4_moe_mlp(const void *x, int64_t T, int64_t H, int64_t I, int E, int k, int fmt,
                            float x_scale, float h_scale, const int *ids, const float *weights,
-                           const int *offsets, const int *slots, const uint8_t *wgu, const uint8_t *wgu_scales,
-                           const float *gu_scale, const uint8_t *wd, const uint8_t *wd_scales,
+                           const int *offsets, const int *slots, const int *order, const uint8_t *wgu,
+                           const uint8_t *wgu_scales, const float *gu_scale, const uint8_t *wd,
+                           const uint8_t *wd_scales,
                            const float *d_scale, const void *residual, int act_dtype, void *y,
                            void *workspace, size_t workspace_bytes, void *stream);
 

@@ -62,15 +62,21 @@ qsw_status grouped_linear(const void *x, int64_t rows, int64_t K, int64_t N, int
   if (!aligned(x, 16) || !aligned(y, 2) || !aligned(workspace, 256)) return QSW_ERR_UNSUPPORTED;
   if (workspace_bytes < qsw_fp4_workspace_bytes(rows, K, groups, fmt)) return QSW_ERR_INVALID_ARG;
   const int sms = qsw::device_sm_count();
-  auto *codes = static_cast<uint8_t *>(workspace);
-  uint8_t *scales = codes + up256(static_cast<size_t>(rows * (K / 2)));
-  const cudaError_t e =
-      offsets ? qsw::launch_fp4_quantize_ragged(x, rows, K, offsets, groups, fmt, act, x_scale, codes, scales, sms, s)
-              : qsw::launch_fp4_quantize(x, 1, rows, K, fmt, act, x_scale, codes, scales, sms, s);
-  if (e != cudaSuccess) return QSW_ERR_CUDA;
   qsw::Fp4GemmArgs a = {};
-  a.x_codes = codes;
-  a.x_scales = scales;
+  const bool fuse = qsw::fp4_gemm_quantizes(rows, K, fmt);
+  if (fuse) {
+    a.x = x;
+    a.x_tokens = rows;
+  } else {
+    auto *codes = static_cast<uint8_t *>(workspace);
+    uint8_t *scales = codes + up256(static_cast<size_t>(rows * (K / 2)));
+    const cudaError_t e =
+        offsets ? qsw::launch_fp4_quantize_ragged(x, rows, K, offsets, groups, fmt, act, x_scale, codes, scales, sms, s)
+                : qsw::launch_fp4_quantize(x, 1, rows, K, fmt, act, x_scale, codes, scales, sms, s);
+    if (e != cudaSuccess) return QSW_ERR_CUDA;
+    a.x_codes = codes;
+    a.x_scales = scales;
+  }
   a.rows = a.max_group = rows;
   a.offsets = offsets;
   a.groups = groups;
@@ -84,7 +90,7 @@ qsw_status grouped_linear(const void *x, int64_t rows, int64_t K, int64_t N, int
   a.act = act;
   a.out = y;
   a.h_scale = 1.0f;
-  st = from_cuda(qsw::launch_fp4_gemm(a, sms, qsw::wait_timeout_ns(), s, true));
+  st = from_cuda(qsw::launch_fp4_gemm(a, sms, qsw::wait_timeout_ns(), s, !fuse));
   if (st == QSW_OK) qsw::count_call(QSW_CNT_FP4_LINEAR);
   return st;
 }
@@ -191,9 +197,10 @@ size_t qsw_fp4_moe_workspace_bytes(int64_t T, int k, int64_t H, int64_t I, int E
 
 qsw_status qsw_fp4_moe_mlp(const void *x, int64_t T, int64_t H, int64_t I, int E, int k, int fmt, float x_scale,
                            float h_scale, const int *ids, const float *weights, const int *offsets,
-                           const int *slots, const uint8_t *wgu, const uint8_t *wgu_scales, const float *gu_scale,
-                           const uint8_t *wd, const uint8_t *wd_scales, const float *d_scale, const void *residual,
-                           int act_dtype, void *y, void *workspace, size_t workspace_bytes, void *stream) {
+                           const int *slots, const int *order, const uint8_t *wgu, const uint8_t *wgu_scales,
+                           const float *gu_scale, const uint8_t *wd, const uint8_t *wd_scales, const float *d_scale,
+                           const void *residual, int act_dtype, void *y, void *workspace, size_t workspace_bytes,
+                           void *stream) {
   if (T < 0 || E <= 0 || k <= 0 || k > E) return QSW_ERR_INVALID_ARG;
   qsw_status st = check_format(fmt, x_scale);
   if (st != QSW_OK || (st = check_format(fmt, h_scale)) != QSW_OK) return st;
@@ -203,9 +210,9 @@ qsw_status qsw_fp4_moe_mlp(const void *x, int64_t T, int64_t H, int64_t I, int E
   if ((st = check_weights(wgu, wgu_scales, gu_scale, E, 2 * I)) != QSW_OK) return st;
   if ((st = check_weights(wd, wd_scales, d_scale, E, H)) != QSW_OK) return st;
   if (T == 0) return QSW_OK;
-  if (!x || !y || !ids || !weights || !offsets || !slots || !workspace) return QSW_ERR_INVALID_ARG;
+  if (!x || !y || !ids || !weights || !offsets || !slots || !order || !workspace) return QSW_ERR_INVALID_ARG;
   if (!aligned(x, 16) || !aligned(y, 16) || !aligned(residual, 16) || !aligned(workspace, 256) ||
-      !aligned(ids, 4) || !aligned(weights, 4) || !aligned(offsets, 4) || !aligned(slots, 4))
+      !aligned(ids, 4) || !aligned(weights, 4) || !aligned(offsets, 4) || !aligned(slots, 4) || !aligned(order, 4))
     return QSW_ERR_UNSUPPORTED;
   const int64_t R = T * k;
   const MoeWorkspace at(R, H, I, E, fmt);
@@ -217,12 +224,21 @@ qsw_status qsw_fp4_moe_mlp(const void *x, int64_t T, int64_t H, int64_t I, int E
 
   // rows sorted by expert, in 4 bits; gate and up with the SwiGLU, held in
   // 4 bits; down; the tokens' weighted sums
-  cudaError_t e = qsw::launch_fp4_quantize_fan(x, T, H, k, ids, slots, offsets, E, fmt, act_dtype, x_scale,
-                                               ws + at.x_codes, ws + at.x_scales, s);
-  if (e != cudaSuccess) return QSW_ERR_CUDA;
+  cudaError_t e;
   qsw::Fp4GemmArgs a = {};
-  a.x_codes = ws + at.x_codes;
-  a.x_scales = ws + at.x_scales;
+  const bool fuse = qsw::fp4_gemm_quantizes(T, H, fmt);
+  if (fuse) {
+    a.x = x;
+    a.x_tokens = T;
+    a.order = order;
+    a.fan = k;
+  } else {
+    e = qsw::launch_fp4_quantize_fan(x, T, H, k, ids, slots, offsets, E, fmt, act_dtype, x_scale, ws + at.x_codes,
+                                     ws + at.x_scales, s);
+    if (e != cudaSuccess) return QSW_ERR_CUDA;
+    a.x_codes = ws + at.x_codes;
+    a.x_scales = ws + at.x_scales;
+  }
   a.rows = R;
   a.max_group = T;      // a token's experts are distinct
   a.offsets = offsets;
@@ -239,7 +255,8 @@ qsw_status qsw_fp4_moe_mlp(const void *x, int64_t T, int64_t H, int64_t I, int E
   a.h_codes = ws + at.h_codes;
   a.h_scales = ws + at.h_scales;
   a.h_scale = h_scale;
-  if ((e = qsw::launch_fp4_gemm(a, sms, timeout, s, true)) != cudaSuccess) return QSW_ERR_CUDA;
+  if ((e = qsw::launch_fp4_gemm(a, sms, timeout, s, !fuse)) != cudaSuccess) return QSW_ERR_CUDA;
+  a.x = nullptr;
   a.x_codes = ws + at.h_codes;
   a.x_scales = ws + at.h_scales;
   a.w_codes = wd;

@@ -44,6 +44,7 @@ __device__ unsigned int g_fp4_error;
 
 constexpr int kTileTokens = 192;
 constexpr int kMaxStages = 16;
+constexpr int kFuseRows = 16;                // rows of x that a CTA quantises itself
 constexpr int kEpiGroups = 3;                // epilogue groups of four warps
 constexpr int kEpiWarps = 4 * kEpiGroups;
 // Warps: the first producer, the MMA issuer, the epilogue, three more producers.
@@ -79,13 +80,19 @@ struct GemmParams {
   int stages;
   int recs;                 // tiles per CTA at most
   bool wide;                // rows of the output start at 16-byte boundaries
-  int x_off, w_off, sf_off, ex_off, rec_off, table_off;   // byte offsets in shared memory
+  int x_off, w_off, sf_off, fuse_sf_off, ex_off, rec_off, table_off;   // byte offsets in shared memory
   void *out;
   uint8_t *h_codes;
   uint8_t *h_scales;
   int h_k_blocks;
   Fp4Scale hq;
   uint64_t timeout_ns;
+  // few rows: x itself, [<= kFuseRows, K], quantised by every CTA into shared memory
+  const void *x;
+  Fp4Scale xq;
+  int x_f16, x_tokens;      // its type and row count
+  const int *order;         // sorted row r is row order[r] / fan of x; null: row r
+  int fan;
 };
 
 // One tile of a CTA (or of a CTA pair), worked out before the first one starts: the
@@ -134,6 +141,7 @@ __device__ __forceinline__ TileRec make_rec(const GemmParams &p, const int *off,
   t.row = off[e] + t.t0;
   t.valid = min(size, m - t.t0);
   t.n = max(kStep, (t.valid + kStep - 1) & ~(kStep - 1));
+  if (!PAIR && p.x) t.n = kFuseRows;
   t.w0 = wt * p.rt + (PAIR ? static_cast<int>(rank) * kSfRows : 0);
   t.w_block = e * p.w_row_blocks + t.w0 / kSfRows;
   t.x_block = (p.offsets ? static_cast<int>(ragged_row_block(off[e], e)) : 0) + t.t0 / kSfRows;
@@ -283,15 +291,15 @@ __device__ __forceinline__ uint32_t fp4_idesc(int n) {
 // elements of K.  One thread's copies and products run in the order of issue.
 template <int FMT, int XSF, bool PAIR>
 __device__ __forceinline__ void issue_stage(uint32_t d, uint32_t idesc, uint64_t wd, uint64_t xd, uint32_t sf,
-                                            uint64_t sfd, uint32_t x_col, int nkb, int steps, bool first) {
+                                            uint64_t sfw, uint64_t sfx, uint32_t x_col, int nkb, int steps, bool first) {
   constexpr int kSfPerStage = kStageK / Fp4<FMT>::kSfK;
 #pragma unroll
   for (int kb = 0; kb < kSfPerStage; ++kb) {
     if (kb >= nkb) break;
-    scales_to_tmem<PAIR>(sf + kb * 4, sfd + kb * (kSfBytes >> 4));
+    scales_to_tmem<PAIR>(sf + kb * 4, sfw + kb * (kSfBytes >> 4));
 #pragma unroll
     for (int b = 0; b < XSF; ++b)
-      scales_to_tmem<PAIR>(sf + 16 + kb * 8 + b * 4, sfd + (kSfPerStage * (1 + b) + kb) * (kSfBytes >> 4));
+      scales_to_tmem<PAIR>(sf + 16 + kb * 8 + b * 4, sfx + (kSfPerStage * b + kb) * (kSfBytes >> 4));
   }
 #pragma unroll
   for (int kk = 0; kk < kStageK / 64; ++kk) {
@@ -319,19 +327,53 @@ __device__ __forceinline__ bool bar_and_group(int id, bool ok) {
   return r != 0;
 }
 
+// Rows of x into shared memory as the MMA takes them: per stage 16 rows of 128
+// swizzled bytes of codes and the scale blocks.  Elements past K are 0; rows past
+// the last are left as they are (their columns are never read).
+template <class A, int FMT>
+__device__ __forceinline__ void quantize_to_smem(const GemmParams &p, uint8_t *codes, uint8_t *scales, int k_stages,
+                                                 int tid, int threads) {
+  constexpr int B = Fp4<FMT>::kBlock;
+  const int per_row = k_stages * (kStageK / B);       // scales of a row, padding included
+  for (int i = tid; i < per_row * p.x_tokens; i += threads) {
+    const int row = i / per_row, j = i - row * per_row, k0 = j * B;
+    uint32_t byte = 0, c[B / 8] = {};
+    if (k0 < p.K) {
+      const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.x) +
+                                                         static_cast<int64_t>(row) * p.K + k0);
+      uint4 v[B / 8];
+#pragma unroll
+      for (int q = 0; q < B / 8; ++q) v[q] = __ldg(src + q);
+      uint32_t amax = amax_pairs<A>(v[0], v[1]);
+      if (B == 32) amax = max(amax, amax_pairs<A>(v[B / 8 - 2], v[B / 8 - 1]));
+      float inv;
+      byte = fp4_scale_of<FMT>(amax, p.xq, inv);
+#pragma unroll
+      for (int q = 0; q < B / 8; ++q) c[q] = fp4_code8<A>(v[q], inv);
+    }
+    uint8_t *dst = codes + (k0 / kStageK) * (kFuseRows * 128) + row * 128 +
+                   ((((k0 % kStageK) / 32) ^ (row & 7)) << 4) + (k0 % 32) / 2;
+    if (B == 16)
+      *reinterpret_cast<uint2 *>(dst) = make_uint2(c[0], c[1]);
+    else
+      *reinterpret_cast<uint4 *>(dst) = make_uint4(c[0], c[1], c[B / 8 - 2], c[B / 8 - 1]);
+    scales[(j >> 2) * kSfBytes + row * 16 + (j & 3)] = static_cast<uint8_t>(byte);
+  }
+}
+
 // A group's run of `tokens` rows out of the exchange buffer: features [lo, hi) of
-// the 128-row weight block at column n0 of an [.., N] output.  `wide`: rows start
-// at 16-byte boundaries, 16-byte stores; else pairs from each row's first 4-byte
-// boundary on, single values around them.
+// the 128-row weight block at column n0 of an [.., N] output.  `cols`: null, or the buffer row
+// of each.  `wide`: rows start at 16-byte boundaries, 16-byte stores; else pairs
+// from each row's first 4-byte boundary on, single values around them.
 __device__ __forceinline__ void store_rows(const uint16_t *ex, uint16_t *out, int N, int n0, int lo, int hi, int tokens,
-                                           int tid, bool wide) {
+                                           int tid, bool wide, const int *cols) {
   hi = min(hi, N - n0);
   if (wide) {
     const int f = (tid & 15) * 8;
     if (f < lo || f >= hi) return;
     uint4 v[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const uint4 *>(ex + ((tid >> 4) + 8 * i) * kYPitch + f);
+    for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const uint4 *>(ex + (cols ? cols[(tid >> 4) + 8 * i] : (tid >> 4) + 8 * i) * kYPitch + f);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int tok = (tid >> 4) + 8 * i;
@@ -341,7 +383,7 @@ __device__ __forceinline__ void store_rows(const uint16_t *ex, uint16_t *out, in
   }
   for (int tok = tid >> 5; tok < tokens; tok += 4) {
     uint16_t *dst = out + static_cast<int64_t>(tok) * N + n0;
-    const uint16_t *src = ex + tok * kYPitch;
+    const uint16_t *src = ex + (cols ? cols[tok] : tok) * kYPitch;
     const int odd = static_cast<int>(reinterpret_cast<uintptr_t>(dst) >> 1) & 1;
     for (int f = (tid & 31) * 2 - odd; f < hi; f += 64) {
       const bool a = f >= lo, b = f + 1 >= lo && f + 1 < hi;
@@ -371,7 +413,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], mma_done;
   __shared__ uint32_t tmem_slot;
-  __shared__ int abort_word, rec_count;
+  __shared__ uint64_t x_ready;
+  __shared__ int abort_word, rec_count, cols[32];
   volatile int *abort_flag = &abort_word;
   int *table = reinterpret_cast<int *>(smem + p.table_off);
   TileRec *recs = reinterpret_cast<TileRec *>(smem + p.rec_off);
@@ -380,6 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int S = p.stages;
   const uint32_t rank = PAIR ? cluster_rank() : 0;
   const int w_rows = PAIR ? kSfRows : p.rt;      // weight rows of this CTA's part of a tile
+  const bool fuse = !PAIR && p.x != nullptr;     // x is quantised here, and stays for all tiles
 
   if constexpr (kDebugBounds) {
     debug_poison_smem(smem, static_cast<uint32_t>(p.rec_off));
@@ -387,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(&full[s], 4);      // the four producers
+      mbar_init(&full[s], fuse ? 2 : 4);      // the producers
       mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -395,6 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&acc_empty[b], PAIR ? 2 * kEpiWarps : kEpiWarps);
     }
     mbar_init(&mma_done, 1);
+    mbar_init(&x_ready, kEpiWarps);
     abort_word = 0;
     fence_mbar_init();
     prefetch_tensormap(&maps.w);
@@ -464,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the weights' first stages go out before the wait
       if (X) griddep_wait();
       if (ROLE == X_CODES) griddep_launch_dependents();
-      const int stage = SCALES ? kSfPerStage * kSfBytes * (1 + p.x_sf) : (X ? p.x_rows : w_rows) * 128;
+      const int stage = SCALES ? kSfPerStage * kSfBytes * (1 + (fuse ? 0 : p.x_sf)) : (X ? p.x_rows : w_rows) * 128;
       uint8_t *const base = smem + (SCALES ? p.sf_off + (X ? kSfPerStage * kSfBytes : 0) : X ? p.x_off : p.w_off);
       const uint32_t leader_full = PAIR ? leader_address(&full[0]) : 0;
       int s = 0, filled = 0;
@@ -530,7 +575,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     };
-    if (elect_one()) {
+    const bool x_side = warp == kWarpProd1 || warp == kWarpProd1 + 2;
+    if (elect_one() && !(fuse && x_side)) {
       if (warp == 0)
         produce(std::integral_constant<int, W_CODES>());
       else if (warp == kWarpProd1)
@@ -549,7 +595,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // addresses live in uniform registers, as these instructions want them.
     const bool issuer = elect_one();
     const uint32_t x_stage = p.x_rows * 128 >> 4, w_stage = w_rows * 128 >> 4;
-    const uint32_t sf_stage = kSfPerStage * kSfBytes * (1 + p.x_sf) >> 4;
+    const uint32_t sf_stage = kSfPerStage * kSfBytes * (1 + (fuse ? 0 : p.x_sf)) >> 4;
+    const uint64_t sfx0 = scales_desc(smem_u32(smem + p.fuse_sf_off));
     const uint64_t wd_base = umma_desc_sw128(smem_u32(smem + p.w_off));
     const uint64_t xd0 = umma_desc_sw128(smem_u32(smem + p.x_off));
     const uint64_t sfd0 = scales_desc(smem_u32(smem + p.sf_off));
@@ -561,6 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
       return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, p.timeout_ns, err)) != 0;
     };
+    if (fuse && tiles > 0) ok = wait(&x_ready, 0);
     for (int j = 0; ok && rank == 0 && j < tiles; ++j) {
       const int buf = j & 1;
       const int n = __shfl_sync(0xffffffffu, recs[j].n, 0), t0 = __shfl_sync(0xffffffffu, recs[j].t0, 0);
@@ -579,12 +627,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         tc_fence_after();
         const uint32_t sf = tmem + kSfCol + (it & 1) * kSfCols;
-        const uint64_t wd = wd0 + s * w_stage, xd = xd0 + s * x_stage, sfd = sfd0 + s * sf_stage;
+        const uint64_t wd = wd0 + s * w_stage, xd = xd0 + (fuse ? ks : s) * x_stage, sfw = sfd0 + s * sf_stage;
+        constexpr uint32_t kSfStep = kSfPerStage * kSfBytes >> 4;
+        const uint64_t sfx = fuse ? sfx0 + ks * kSfStep : sfw + kSfStep;
         if (issuer) {
           if (x_sf == 1)
-            issue_stage<FMT, 1, PAIR>(d, idesc, wd, xd, sf, sfd, x_col, kb_left, steps_left, ks == 0);
+            issue_stage<FMT, 1, PAIR>(d, idesc, wd, xd, sf, sfw, sfx, x_col, kb_left, steps_left, ks == 0);
           else
-            issue_stage<FMT, 2, PAIR>(d, idesc, wd, xd, sf, sfd, x_col, kb_left, steps_left, ks == 0);
+            issue_stage<FMT, 2, PAIR>(d, idesc, wd, xd, sf, sfw, sfx, x_col, kb_left, steps_left, ks == 0);
           commit_to<PAIR>(&empty[s]);
         }
         __syncwarp();
@@ -615,12 +665,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int bar = 1 + group;
     const int gtid = ((warp - kWarpEpi0) & 3) * 32 + lane;         // thread within the group
     uint8_t *ex = smem + p.ex_off + group * kExBytes;
+    if (fuse) {
+      griddep_wait();
+      griddep_launch_dependents();
+      const int tid = (warp - kWarpEpi0) * 32 + lane;
+      if (p.x_f16)
+        quantize_to_smem<ActF16, FMT>(p, smem + p.x_off, smem + p.fuse_sf_off, k_stages, tid, kEpiWarps * 32);
+      else
+        quantize_to_smem<ActBf16, FMT>(p, smem + p.x_off, smem + p.fuse_sf_off, k_stages, tid, kEpiWarps * 32);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&x_ready);
+    }
     for (int j = 0; j < tiles; ++j) {
       const TileRec t = recs[j];
       const int buf = j & 1;
+      // the column of each of the tile's rows, where all rows of x are columns
+      int col = 0;
+      if (fuse && group == 0 && gtid < 32 && gtid < t.valid) {
+        const int r = p.order ? __ldg(p.order + t.row + gtid) / p.fan : t.row + gtid;
+        col = min(max(r, 0), kFuseRows - 1);
+      }
       bool ok = mbar_wait(&acc_full[buf], (j >> 1) & 1, abort_flag, p.timeout_ns, err);
       ok = bar_and_group(bar, ok);
       if (!ok) break;
+      if (fuse && group == 0 && gtid < 32) cols[gtid] = col;
       tc_fence_after();
       const uint32_t acc = tmem + buf * kTileTokens + (static_cast<uint32_t>(quarter) << 21);
       const float alpha = p.x_scale * (p.w_scale ? __ldg(p.w_scale + t.e) : 1.0f);
@@ -656,7 +725,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           bar_sync_group(bar);
           store_rows(ex16, static_cast<uint16_t *>(p.out) + static_cast<int64_t>(t.row + c0) * p.N,
-                     p.N, t.w0 & ~(kSfRows - 1), lane0, lane0 + w_rows, min(32, t.valid - c0), gtid, p.wide);
+                     p.N, t.w0 & ~(kSfRows - 1), lane0, lane0 + w_rows, min(32, t.valid - c0), gtid, p.wide, fuse ? cols : nullptr);
           bar_sync_group(bar);
         } else {
           if (warp_mine) {
@@ -682,7 +751,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int I = p.N / 2;
           const bool in_tile = fq * 32 >= lane0 && fq * 32 < lane0 + w_rows;
           const bool have = in_tile && c0 + tok < t.valid;
-          const float4 *src = reinterpret_cast<const float4 *>(reinterpret_cast<float *>(ex) + tok * kHPitch + fq * 16);
+          const float4 *src = reinterpret_cast<const float4 *>(reinterpret_cast<float *>(ex) + (fuse ? cols[tok] : tok) * kHPitch + fq * 16);
           float4 v[4];
           uint32_t amax = 0;
           const int rot = (fq >> 1) + 2 * (tok & 1);
@@ -819,16 +888,22 @@ cudaError_t launch_gemm(const Fp4GemmArgs &a, GemmParams p, int num_sms, cudaStr
   if (slots > (1 << 30)) return cudaErrorInvalidValue;
   p.recs = static_cast<int>(ceil_div64(most, slots));
   const int recs = p.recs * static_cast<int>(sizeof(TileRec));
-  const int x_stage = p.x_rows * 128, w_stage = w_rows * 128, sf_stage = kSfPerStage * kSfBytes * (1 + p.x_sf);
-  const int fixed = 1024 + 2 * slack + ex + recs + table;
+  const bool fuse = p.x != nullptr;
+  const int k_stages = ceil_div(p.K, kStageK);
+  const int x_stage = fuse ? 0 : p.x_rows * 128, w_stage = w_rows * 128;
+  const int sf_stage = kSfPerStage * kSfBytes * (1 + (fuse ? 0 : p.x_sf));
+  const int x_all = fuse ? k_stages * kFuseRows * 128 : 0, x_sf_all = fuse ? k_stages * kSfPerStage * kSfBytes : 0;
+  const int fixed = 1024 + 2 * slack + ex + recs + table + x_all + x_sf_all;
   int S = (kSmemLimit - fixed) / (x_stage + w_stage + sf_stage);
   if (S > kMaxStages) S = kMaxStages;
   if (S < 2) return cudaErrorInvalidValue;
   p.stages = S;
   p.x_off = 0;
-  p.w_off = align_up(S * x_stage < slack ? slack : S * x_stage, 1024);
+  const int x_bytes = x_all + S * x_stage;
+  p.w_off = align_up(x_bytes < slack ? slack : x_bytes, 1024);
   p.sf_off = p.w_off + S * w_stage;
-  p.ex_off = align_up(p.sf_off + S * sf_stage, 128);
+  p.fuse_sf_off = p.sf_off + S * sf_stage;
+  p.ex_off = align_up(p.fuse_sf_off + x_sf_all, 128);
   p.rec_off = p.ex_off + ex;
   p.table_off = p.rec_off + recs;
   int bytes = p.table_off + table;
@@ -837,11 +912,11 @@ cudaError_t launch_gemm(const Fp4GemmArgs &a, GemmParams p, int num_sms, cudaStr
   if (bytes > kSmemLimit) return cudaErrorInvalidValue;
 
   GemmMaps maps;
-  if (!encode_codes(&maps.w, a.w_codes, static_cast<int64_t>(p.groups) * p.N, p.K, w_rows) ||
-      !encode_codes(&maps.x, a.x_codes, p.rows, p.K, p.x_rows))
-    return cudaErrorInvalidValue;
+  if (!encode_codes(&maps.w, a.w_codes, static_cast<int64_t>(p.groups) * p.N, p.K, w_rows)) return cudaErrorInvalidValue;
+  maps.x = maps.w;
+  if (!fuse && !encode_codes(&maps.x, a.x_codes, p.rows, p.K, p.x_rows)) return cudaErrorInvalidValue;
   maps.xb = maps.x;
-  if (p.x_box != p.x_rows && !encode_codes(&maps.xb, a.x_codes, p.rows, p.K, p.x_box)) return cudaErrorInvalidValue;
+  if (!fuse && p.x_box != p.x_rows && !encode_codes(&maps.xb, a.x_codes, p.rows, p.K, p.x_box)) return cudaErrorInvalidValue;
   maps.sfw = maps.sfx = maps.x;
   if (PAIR) {
     const int64_t x_blocks = a.offsets ? ragged_row_block(p.rows, p.groups) : ceil_div(p.rows, kSfRows);
@@ -871,6 +946,13 @@ cudaError_t dispatch_gemm(const Fp4GemmArgs &a, const GemmParams &p, int num_sms
 
 }  // namespace
 
+// Whether a CTA quantises `rows` rows of x itself: few rows, and their codes and scales
+// leave most of the shared memory to the weights' stages.  One launch instead of two.
+bool fp4_gemm_quantizes(int64_t rows, int64_t K, int fmt) {
+  const int64_t stages = (K + kStageK - 1) / kStageK;
+  return rows <= kFuseRows && stages * (kFuseRows * 128 + kStageK / (4 * fp4_block(fmt)) * kSfBytes) <= 96 * 1024;
+}
+
 cudaError_t launch_fp4_gemm(const Fp4GemmArgs &a, int num_sms, uint64_t timeout_ns, cudaStream_t stream,
                             bool dependent) {
   if (num_sms <= 0) return cudaErrorInvalidDevice;
@@ -897,6 +979,15 @@ cudaError_t launch_fp4_gemm(const Fp4GemmArgs &a, int num_sms, uint64_t timeout_
   p.hq = make_fp4_scale(a.h_scale);
   p.timeout_ns = timeout_ns;
 
+  if (a.x) {
+    p.x = a.x;
+    p.xq = make_fp4_scale(a.x_scale);
+    p.x_f16 = a.act == ActF16::kId;
+    p.x_tokens = static_cast<int>(a.x_tokens);
+    p.order = a.order;
+    p.fan = a.fan;
+  }
+
   // (group, token tile) pairs there can be at most
   const int64_t groups = p.groups < p.rows ? p.groups : p.rows;
   const int64_t tiles = static_cast<int64_t>(p.rows) / p.bt + groups;
@@ -905,7 +996,7 @@ cudaError_t launch_fp4_gemm(const Fp4GemmArgs &a, int num_sms, uint64_t timeout_
   // half of the tokens, which leaves an SM a quarter less to copy per product.
   // With few tokens per group the weights are all there is to copy, and the tiles
   // are better spread over single CTAs.
-  if (p.rows / groups >= kPairTokens && tiles * ceil_div(p.N, 256) * 2 >= num_sms) {
+  if (!p.x && p.rows / groups >= kPairTokens && tiles * ceil_div(p.N, 256) * 2 >= num_sms) {
     p.bt = align_up(p.bt, 32);
     p.x_rows = p.bt / 2;
     p.x_box = p.x_rows < 32 ? p.x_rows : 32;

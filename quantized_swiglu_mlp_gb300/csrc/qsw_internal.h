@@ -101,7 +101,14 @@ cudaError_t launch_fp4_dequantize(const uint8_t *codes, const uint8_t *scales, i
                                   int64_t K, int fmt, int act, float g, void *out, int num_sms, cudaStream_t stream);
 
 struct Fp4GemmArgs {
-  const uint8_t *x_codes, *x_scales;   // [rows, K] sorted by group, ragged scale blocks
+  // either x in 4 bits, [rows, K] sorted by group, ragged scale blocks
+  const uint8_t *x_codes, *x_scales;
+  // or (fp4_gemm_quantizes) x itself, [x_tokens, K]; sorted row r is its row
+  // order[r] / fan (order null: row r)
+  const void *x;
+  int64_t x_tokens;
+  const int *order;
+  int fan;
   int64_t rows, max_group;             // no group has more than max_group rows
   const int *offsets;                  // [groups + 1] on the device; null: one group
   int groups;
@@ -115,6 +122,7 @@ struct Fp4GemmArgs {
   uint8_t *h_codes, *h_scales;         // swiglu: [rows, I], ragged scale blocks
   float h_scale;
 };
+bool fp4_gemm_quantizes(int64_t rows, int64_t K, int fmt);
 cudaError_t launch_fp4_gemm(const Fp4GemmArgs &a, int num_sms, uint64_t timeout_ns, cudaStream_t stream,
                             bool dependent);
 cudaError_t fp4_gemm_take_errors(unsigned int *out);

@@ -129,7 +129,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.qsw_fp4_moe_workspace_bytes.argtypes = [i64, i32, i64, i64, i32, i32]
         lib.qsw_fp4_moe_workspace_bytes.restype = sz
         lib.qsw_fp4_moe_mlp.argtypes = [p, i64, i64, i64, i32, i32, i32, f32, f32, p, p, p, p, p, p, p, p, p, p, p,
-                                        i32, p, p, sz, p]
+                                        p, i32, p, p, sz, p]
         lib.qsw_fp4_moe_mlp.restype = i32
         lib.qsw_rms_norm.argtypes = [p, p, i64, i64, f32, i32, p, p]
         lib.qsw_rms_norm.restype = i32
@@ -638,16 +638,18 @@ def fp4_moe_mlp(x, route, wgu, wgu_scales, wd, wd_scales, fmt=FP4_NV, x_scale=1.
     """
     lib = _lib or load_library()
     act, dev, shape = _act(x, "x"), x.device, x.shape
-    ids, weights, offsets, slots, _ = route
+    ids, weights, offsets, slots, order = route
     _like(ids, "route.ids", torch.int32, dev)
     _like(weights, "route.weights", torch.float32, dev)
     _like(offsets, "route.offsets", torch.int32, dev)
     _like(slots, "route.slots", torch.int32, dev)
+    _like(order, "route.order", torch.int32, dev)
     if len(shape) != 2 or weights.dim() != 2:
         raise ValueError("x must be [T, H] and route moe_route's result")
     T, H = shape
     E, k = offsets.numel() - 1, weights.shape[1]
-    if weights.shape[0] != T or slots.shape != weights.shape or ids.shape != weights.shape:
+    if weights.shape[0] != T or slots.shape != weights.shape or ids.shape != weights.shape or \
+            order.numel() != T * k:
         raise ValueError("route does not belong to x")
     rows = _fp4_weight(wgu, wgu_scales, gu_scale, H, fmt, "wgu", dev, E)
     if rows % 2:
@@ -664,7 +666,7 @@ def fp4_moe_mlp(x, route, wgu, wgu_scales, wd, wd_scales, fmt=FP4_NV, x_scale=1.
     ws = _scratch(nbytes, dev, stream)
     _check("qsw_fp4_moe_mlp",
            lib.qsw_fp4_moe_mlp(x.data_ptr(), T, H, I, E, k, fmt, x_scale, h_scale, ids.data_ptr(),
-                               weights.data_ptr(), offsets.data_ptr(), slots.data_ptr(), wgu.data_ptr(),
+                               weights.data_ptr(), offsets.data_ptr(), slots.data_ptr(), order.data_ptr(), wgu.data_ptr(),
                                wgu_scales.data_ptr(), _ptr(gu_scale), wd.data_ptr(), wd_scales.data_ptr(),
                                _ptr(d_scale), _ptr(residual), act, out.data_ptr(), ws.data_ptr(), nbytes,
                                _raw_stream(stream, dev)))

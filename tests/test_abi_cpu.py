@@ -287,7 +287,7 @@ def test_moe_route_refuses(lib, kw, code):
 def test_fp4_moe_mlp_refuses(lib, kw, code):
     a = dict(T=4, H=64, I=64, E=8, k=2, fmt=NV, h_scale=1.0, wd=FAKE, residual=None, y=FAKE, ws_bytes=BIG) | kw
     assert lib.qsw_fp4_moe_mlp(FAKE, a["T"], a["H"], a["I"], a["E"], a["k"], a["fmt"], 1.0, a["h_scale"], FAKE, FAKE,
-                               FAKE, FAKE, FAKE, FAKE, None, a["wd"], FAKE, None, a["residual"], 0, a["y"], FAKE,
+                               FAKE, FAKE, FAKE, FAKE, FAKE, None, a["wd"], FAKE, None, a["residual"], 0, a["y"], FAKE,
                                a["ws_bytes"], None) == code
 
 
