@@ -1,14 +1,17 @@
-"""Build libqswiglu.so in-tree with nvcc for sm_103a (GB300).
+"""Build libqswiglu.so in-tree with nvcc for sm_103a (GB300), and the C++ binding of
+the block operators to torch tensors with g++.
 
-Each translation unit compiles in parallel; the shared library lands in
+Each translation unit compiles in parallel; the shared libraries land in
 ``quantized_swiglu_mlp_gb300/lib/``.  No CMake, no torch extension machinery.
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -81,11 +84,43 @@ def _stale(lib: str) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+# The binding of the block operators: a CPython module over torch's C++ headers.
+NATIVE_SOURCE = os.path.join(CSRC, "qsw_torch.cpp")
+NATIVE_PATH = os.path.join(OUT_DIR, "_qsw_torch.so")
+
+
+def _native_stale() -> bool:
+    if not os.path.exists(NATIVE_PATH):
+        return True
+    t = os.path.getmtime(NATIVE_PATH)
+    return any(os.path.getmtime(d) > t for d in (NATIVE_SOURCE, os.path.join(ROOT, "include", "qswiglu.h")))
+
+
+def _build_native() -> None:
+    os.makedirs(OUT_DIR, exist_ok=True)
+    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    tmp = NATIVE_PATH + f".tmp{os.getpid()}"
+    include = [os.path.join(ROOT, "include"), os.path.join(torch_dir, "include"),
+               os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"), os.path.join(cuda, "include"),
+               sysconfig.get_path("include")]
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           *(a for d in include for a in ("-isystem", d)), NATIVE_SOURCE, "-o", tmp,
+           "-L", os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on qsw_torch.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, NATIVE_PATH)
+
+
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
-    """Compile both libraries (every translation unit of both at once) and
-    return the regular one's path."""
+    """Compile both libraries and the binding (every translation unit at once)
+    and return the regular library's path."""
     todo = [v for v in VARIANTS if force or _stale(v[0])]
+    native = force or _native_stale()
     if not todo:
+        if native:
+            _build_native()
         return LIB_PATH
     cc = nvcc()
     flags = _flags(verbose_ptxas)
@@ -104,8 +139,11 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
         return obj
 
     jobs = [(src, objdir, extra) for _, objdir, extra in todo for src in SOURCES]
-    with ThreadPoolExecutor(max_workers=len(jobs)) as ex:
+    with ThreadPoolExecutor(max_workers=len(jobs) + 1) as ex:
+        binding = ex.submit(_build_native) if native else None
         objs = list(ex.map(compile_one, jobs))
+        if binding:
+            binding.result()
     for n, (lib, _, _) in enumerate(todo):
         tmp = lib + f".tmp{os.getpid()}"
         mine = objs[n * len(SOURCES):(n + 1) * len(SOURCES)]

@@ -16,6 +16,7 @@ library's *_ex entry points with that dtype.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import threading
 from typing import NamedTuple
@@ -24,6 +25,7 @@ import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "lib", "libqswiglu.so")
+NATIVE_PATH = os.path.join(_HERE, "lib", "_qsw_torch.so")
 DEBUG_LIB_PATH = os.path.join(_HERE, "lib", "libqswiglu_debug.so")   # built with QSW_DEBUG_BOUNDS
 
 MATCH, F32, DEBUG_GATE, DEBUG_UP = 0, 1, 2, 3
@@ -403,101 +405,55 @@ def unfused_swiglu(x, wg, sg, bg, gs_g, bits_g, wu, su, bu, gs_u, bits_u, varian
 # and formulas: include/qswiglu.h.
 # ------------------------------------------------------------------------
 
-# These calls are small next to a launch, so their binding is kept lean: a
-# check is one expression that goes on to `_need` (which words the error) only
-# where it fails, and scratch memory is kept per stream.
+# The calls go through a small C++ binding (csrc/qsw_torch.cpp), which checks the
+# tensors, allocates and calls the C entry points of the library loaded here:
+# with the checks in Python and ctypes the host took longer than the device.
+# Results and scratch memory belong to the stream of the call.
+
+_native = None
+
+
+def _raise_status(fn: str, code: int) -> None:
+    _check(fn, code)
+
+
+def _load_native():
+    """The C++ binding, bound to the loaded library.  Raises if it is missing."""
+    global _native
+    lib = load_library()
+    with _lock:
+        if _native is None:
+            if not os.path.exists(NATIVE_PATH):
+                raise RuntimeError(f"{NATIVE_PATH} is not built; run quantized_swiglu_mlp_gb300.build.build() "
+                                   "(or __graft_entry__.build())")
+            spec = importlib.util.spec_from_file_location("_qsw_torch", NATIVE_PATH)
+            module = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(module)
+            module.bind({name: ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in EXPORTED},
+                        _raise_status)
+            _native = module
+    return _native
+
 
 def _on(stream):
-    """Context in which buffers belong to `stream`, so that the allocator does
-    not hand them to other streams' work while that stream still uses them."""
+    """Context in which `stream` is the current one."""
     return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream)
                              else torch.cuda.ExternalStream(int(stream)))
 
 
-def _raw_stream(stream, device) -> int:
-    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else _stream_ptr(stream)
-
-
-def _ptr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _act(x, name) -> int:
-    """Activation dtype code of a contiguous CUDA tensor."""
-    act = _ACT.get(getattr(x, "dtype", None))
-    if act is None or not x.is_cuda or not x.is_contiguous():
-        _need(x, name, tuple(_ACT))
-    return act
-
-
-def _like(t, name, dtype, device):
-    """A contiguous tensor of `dtype` on `device`."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == device and t.is_contiguous()):
-        _need(t, name, (dtype,), device)
-    return t
-
-
-def _output(out, name, shape, dtype, device, stream=None):
-    if out is None:
-        if stream is None:
-            return torch.empty(shape, dtype=dtype, device=device)
-        with _on(stream):
-            return torch.empty(shape, dtype=dtype, device=device)
-    _like(out, name, dtype, device)
-    n = 1
-    for d in shape:
-        n *= d
-    if out.numel() != n:
-        raise ValueError(f"{name} has the wrong size")
-    return out
-
-
-_scratches: dict = {}
-
-
-def _scratch(nbytes, device, stream) -> torch.Tensor:
-    """Uninitialised scratch of at least `nbytes` for calls on the current stream
-    (kept per stream and thread -- a call's launches on it must not interleave
-    with another's -- and replaced by a larger one on demand: the allocator reuses
-    the old one's memory in the stream's own order).  A call on another stream,
-    or one that is being captured into a graph, gets memory of its own."""
-    if stream is not None or torch._C._cuda_isCurrentStreamCapturing():
-        return _output(None, "scratch", (nbytes,), torch.uint8, device, stream)
-    key = (device.index, torch._C._cuda_getCurrentRawStream(device.index), threading.get_ident())
-    buf = _scratches.get(key)
-    if buf is None or buf.numel() < nbytes:
-        buf = _scratches[key] = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    return buf
-
-
-def _fp4_format(fmt) -> int:
-    if fmt not in FP4_BLOCK:
-        raise ValueError("fmt must be FP4_MX or FP4_NV")
-    return int(fmt)
+def _call(fn, stream, *args):
+    if stream is None:
+        return fn(*args)
+    with _on(stream):
+        return fn(*args)
 
 
 def fp4_scale_shape(rows: int, K: int, fmt: int) -> tuple[int, int, int]:
     """Shape of the scale blocks of a [rows, K] matrix: row blocks of 128, blocks of 4 scales, 512 bytes."""
-    per = 4 * FP4_BLOCK[_fp4_format(fmt)]
+    if fmt not in FP4_BLOCK:
+        raise ValueError("fmt must be FP4_MX or FP4_NV")
+    per = 4 * FP4_BLOCK[fmt]
     return (rows + 127) // 128, (K + per - 1) // per, 512
-
-
-def _fp4_weight(w, scales, w_scale, K, fmt, name, device, groups=None) -> int:
-    """Checks a 4-bit matrix (or stack of `groups`) with rows of K elements; returns its row count."""
-    _like(w, name, torch.uint8, device)
-    _like(scales, f"{name} scales", torch.uint8, device)
-    shape = w.shape
-    n = shape[-2] if len(shape) >= 2 else 0
-    lead = () if groups is None else (groups,)
-    if shape != (*lead, n, K // 2) or K % 2:
-        raise ValueError(f"{name} must be {[*lead, 'rows', K // 2]} bytes of codes, got {tuple(shape)}")
-    if scales.shape != (*lead, *fp4_scale_shape(n, K, fmt)):
-        raise ValueError(f"{name} scales must be {(*lead, *fp4_scale_shape(n, K, fmt))}, got {tuple(scales.shape)}")
-    if w_scale is not None:
-        _like(w_scale, f"{name} tensor scale", torch.float32, device)
-        if w_scale.numel() != (groups or 1):
-            raise ValueError(f"{name} tensor scale must have one value per matrix")
-    return n
 
 
 def fp4_quantize(x, fmt=FP4_NV, scale=1.0, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
@@ -506,36 +462,14 @@ def fp4_quantize(x, fmt=FP4_NV, scale=1.0, stream=None) -> tuple[torch.Tensor, t
     codes uint8 [..., rows, K/2], scales uint8 [..., row blocks, scale blocks,
     512].  scale: the tensor's f32 scale (FP4_NV only).
     """
-    lib = _lib or load_library()
-    act, dev, shape = _act(x, "x"), x.device, x.shape
-    if len(shape) not in (2, 3):
-        raise ValueError("x must be [rows, K] or [groups, rows, K]")
-    rows, K = shape[-2:]
-    codes = _output(None, "codes", (*shape[:-1], K // 2), torch.uint8, dev, stream)
-    scales = _output(None, "scales", (*shape[:-2], *fp4_scale_shape(rows, K, fmt)), torch.uint8, dev, stream)
-    _check("qsw_fp4_quantize", lib.qsw_fp4_quantize(x.data_ptr(), shape[0] if len(shape) == 3 else 1, rows, K, fmt,
-                                                    scale, act, codes.data_ptr(), scales.data_ptr(),
-                                                    _raw_stream(stream, dev)))
-    return codes, scales
+    return _call((_native or _load_native()).fp4_quantize, stream, x, fmt, scale)
 
 
 def fp4_dequantize(codes, scales, fmt=FP4_NV, scale=1.0, dtype=torch.bfloat16, out=None, stream=None) -> torch.Tensor:
     """The [rows, K] matrix (or stack) that codes and scales stand for, rounded to `dtype`."""
-    lib = _lib or load_library()
     if dtype not in _ACT:
         raise TypeError(f"dtype must be one of {tuple(_ACT)}")
-    _need(codes, "codes", (torch.uint8,))
-    dev, shape = codes.device, codes.shape
-    if len(shape) not in (2, 3):
-        raise ValueError("codes must be [rows, K/2] or [groups, rows, K/2]")
-    groups = shape[0] if len(shape) == 3 else None
-    K = shape[-1] * 2
-    rows = _fp4_weight(codes, scales, None, K, fmt, "codes", dev, groups)
-    out = _output(out, "out", (*shape[:-1], K), dtype, dev, stream)
-    _check("qsw_fp4_dequantize", lib.qsw_fp4_dequantize(codes.data_ptr(), scales.data_ptr(),
-                                                        1 if groups is None else groups, rows, K, fmt, scale,
-                                                        _ACT[dtype], out.data_ptr(), _raw_stream(stream, dev)))
-    return out
+    return _call((_native or _load_native()).fp4_dequantize, stream, codes, scales, fmt, scale, _ACT[dtype], out)
 
 
 def fp4_linear(x, w, w_scales, fmt=FP4_NV, x_scale=1.0, w_scale=None, out=None, stream=None) -> torch.Tensor:
@@ -544,18 +478,7 @@ def fp4_linear(x, w, w_scales, fmt=FP4_NV, x_scale=1.0, w_scale=None, out=None, 
     w uint8 [N, K/2] and w_scales as fp4_quantize returns them; x_scale: the
     f32 scale x is quantised with, w_scale: W's, one f32 on the device (None: 1).
     """
-    lib = _lib or load_library()
-    act, dev, shape = _act(x, "x"), x.device, x.shape
-    K = shape[-1]
-    M = x.numel() // K if K else 0
-    N = _fp4_weight(w, w_scales, w_scale, K, fmt, "w", dev)
-    out = _output(out, "out", (*shape[:-1], N), x.dtype, dev, stream)
-    nbytes = lib.qsw_fp4_workspace_bytes(M, K, 1, fmt)
-    ws = _scratch(nbytes, dev, stream)
-    _check("qsw_fp4_linear", lib.qsw_fp4_linear(x.data_ptr(), M, K, N, fmt, x_scale, w.data_ptr(), w_scales.data_ptr(),
-                                                _ptr(w_scale), act, out.data_ptr(), ws.data_ptr(), nbytes,
-                                                _raw_stream(stream, dev)))
-    return out
+    return _call((_native or _load_native()).fp4_linear, stream, x, w, w_scales, fmt, x_scale, w_scale, out)
 
 
 def fp4_grouped_linear(x, offsets, w, w_scales, fmt=FP4_NV, x_scale=1.0, w_scale=None, out=None,
@@ -565,22 +488,8 @@ def fp4_grouped_linear(x, offsets, w, w_scales, fmt=FP4_NV, x_scale=1.0, w_scale
     offsets int32 [groups + 1] on the device, from 0 to rows; w uint8 [groups,
     N, K/2] with a stack's scales, w_scale f32 [groups] or None.
     """
-    lib = _lib or load_library()
-    act, dev, shape = _act(x, "x"), x.device, x.shape
-    _like(offsets, "offsets", torch.int32, dev)
-    if len(shape) != 2 or offsets.dim() != 1 or offsets.numel() < 2:
-        raise ValueError("x must be [rows, K] and offsets [groups + 1]")
-    rows, K = shape
-    groups = offsets.numel() - 1
-    N = _fp4_weight(w, w_scales, w_scale, K, fmt, "w", dev, groups)
-    out = _output(out, "out", (rows, N), x.dtype, dev, stream)
-    nbytes = lib.qsw_fp4_workspace_bytes(rows, K, groups, fmt)
-    ws = _scratch(nbytes, dev, stream)
-    _check("qsw_fp4_grouped_linear",
-           lib.qsw_fp4_grouped_linear(x.data_ptr(), rows, K, N, groups, offsets.data_ptr(), fmt, x_scale, w.data_ptr(),
-                                      w_scales.data_ptr(), _ptr(w_scale), act, out.data_ptr(), ws.data_ptr(), nbytes,
-                                      _raw_stream(stream, dev)))
-    return out
+    return _call((_native or _load_native()).fp4_grouped_linear, stream, x, offsets, w, w_scales, fmt, x_scale, w_scale,
+                 out)
 
 
 class MoeRoute(NamedTuple):
@@ -594,26 +503,7 @@ class MoeRoute(NamedTuple):
 
 def moe_route(logits, k, scoring=ROUTE_SOFTMAX, renormalize=True, scale=1.0, stream=None) -> MoeRoute:
     """The k largest of each row of logits [T, E] (f32, bf16 or f16), their weights and the expert-sorted order."""
-    lib = _lib or load_library()
-    dtype = _ACT.get(getattr(logits, "dtype", None), LOGITS_F32)
-    if not (isinstance(logits, torch.Tensor) and logits.is_cuda and logits.is_contiguous()) or \
-            (dtype == LOGITS_F32 and logits.dtype is not torch.float32):
-        _need(logits, "logits", (torch.float32, *_ACT))
-    if logits.dim() != 2:
-        raise ValueError("logits must be [T, E]")
-    T, E = logits.shape
-    if not 0 < k <= E:
-        raise ValueError("k must be between 1 and the number of experts")
-    dev, i32 = logits.device, torch.int32
-    ids = _output(None, "ids", (T, k), i32, dev, stream)
-    weights = _output(None, "weights", (T, k), torch.float32, dev, stream)
-    offsets = _output(None, "offsets", (E + 1,), i32, dev, stream)
-    slots = _output(None, "slots", (T, k), i32, dev, stream)
-    order = _output(None, "order", (T * k,), i32, dev, stream)
-    _check("qsw_moe_route", lib.qsw_moe_route(logits.data_ptr(), T, E, k, dtype, scoring, renormalize, scale,
-                                              ids.data_ptr(), weights.data_ptr(), offsets.data_ptr(),
-                                              slots.data_ptr(), order.data_ptr(), _raw_stream(stream, dev)))
-    return MoeRoute(ids, weights, offsets, slots, order)
+    return MoeRoute._make(_call((_native or _load_native()).moe_route, stream, logits, k, scoring, renormalize, scale))
 
 
 def interleave_gate_up(gate, up) -> torch.Tensor:
@@ -636,62 +526,13 @@ def fp4_moe_mlp(x, route, wgu, wgu_scales, wd, wd_scales, fmt=FP4_NV, x_scale=1.
     x_scale, h_scale: the f32 scales that x and the hidden activations are
     quantised with.
     """
-    lib = _lib or load_library()
-    act, dev, shape = _act(x, "x"), x.device, x.shape
-    ids, weights, offsets, slots, order = route
-    _like(ids, "route.ids", torch.int32, dev)
-    _like(weights, "route.weights", torch.float32, dev)
-    _like(offsets, "route.offsets", torch.int32, dev)
-    _like(slots, "route.slots", torch.int32, dev)
-    _like(order, "route.order", torch.int32, dev)
-    if len(shape) != 2 or weights.dim() != 2:
-        raise ValueError("x must be [T, H] and route moe_route's result")
-    T, H = shape
-    E, k = offsets.numel() - 1, weights.shape[1]
-    if weights.shape[0] != T or slots.shape != weights.shape or ids.shape != weights.shape or \
-            order.numel() != T * k:
-        raise ValueError("route does not belong to x")
-    rows = _fp4_weight(wgu, wgu_scales, gu_scale, H, fmt, "wgu", dev, E)
-    if rows % 2:
-        raise ValueError("wgu must have 2 I rows")
-    I = rows // 2
-    if _fp4_weight(wd, wd_scales, d_scale, I, fmt, "wd", dev, E) != H:
-        raise ValueError("wd must have H rows")
-    if residual is not None:
-        _like(residual, "residual", x.dtype, dev)
-        if residual.numel() != T * H:
-            raise ValueError("residual has the wrong size")
-    out = _output(out, "out", (T, H), x.dtype, dev, stream)
-    nbytes = lib.qsw_fp4_moe_workspace_bytes(T, k, H, I, E, fmt)
-    ws = _scratch(nbytes, dev, stream)
-    _check("qsw_fp4_moe_mlp",
-           lib.qsw_fp4_moe_mlp(x.data_ptr(), T, H, I, E, k, fmt, x_scale, h_scale, ids.data_ptr(),
-                               weights.data_ptr(), offsets.data_ptr(), slots.data_ptr(), order.data_ptr(), wgu.data_ptr(),
-                               wgu_scales.data_ptr(), _ptr(gu_scale), wd.data_ptr(), wd_scales.data_ptr(),
-                               _ptr(d_scale), _ptr(residual), act, out.data_ptr(), ws.data_ptr(), nbytes,
-                               _raw_stream(stream, dev)))
-    return out
-
-
-def _norm_vector(w, name, H, dtype, device):
-    if w is None:
-        return None
-    _like(w, name, dtype, device)
-    if w.shape != (H,):
-        raise ValueError(f"{name} must be [{H}]")
-    return w.data_ptr()
+    return _call((_native or _load_native()).fp4_moe_mlp, stream, x, *route, wgu, wgu_scales, wd, wd_scales, fmt,
+                 x_scale, h_scale, gu_scale, d_scale, residual, out)
 
 
 def rms_norm(x, weight=None, eps=1e-6, out=None, stream=None) -> torch.Tensor:
     """T(x * rsqrt(mean(x^2) + eps) * weight) over the last dimension."""
-    lib = _lib or load_library()
-    act, dev, shape = _act(x, "x"), x.device, x.shape
-    H = shape[-1]
-    w = _norm_vector(weight, "weight", H, x.dtype, dev)
-    out = _output(out, "out", shape, x.dtype, dev, stream)
-    _check("qsw_rms_norm", lib.qsw_rms_norm(x.data_ptr(), w, x.numel() // H if H else 0, H, eps, act, out.data_ptr(),
-                                            _raw_stream(stream, dev)))
-    return out
+    return _call((_native or _load_native()).rms_norm, stream, x, weight, eps, out)
 
 
 def post_norm(h, y, weight=None, gate=None, scale=1.0, next_weight=None, eps=1e-6, norm=True, next_norm=True,
@@ -703,30 +544,8 @@ def post_norm(h, y, weight=None, gate=None, scale=1.0, next_weight=None, eps=1e-
     [gate_rows, H] or [gate_rows, 1] with gate_rows dividing the row count.
     `out` may be h, `next_out` may be y.
     """
-    lib = _lib or load_library()
-    act, dev, dt, shape = _act(h, "h"), h.device, h.dtype, h.shape
-    _like(y, "y", dt, dev)
-    if y.shape != shape:
-        raise ValueError("h and y must have the same shape")
-    H = shape[-1]
-    rows = h.numel() // H if H else 0
-    w = _norm_vector(weight, "weight", H, dt, dev)
-    wn = _norm_vector(next_weight, "next_weight", H, dt, dev)
-    gate_rows = gate_cols = 0
-    if gate is not None:
-        _like(gate, "gate", dt, dev)
-        if gate.dim() == 1:
-            gate_rows, gate_cols = 1, gate.shape[0]
-        elif gate.dim() == 2:
-            gate_rows, gate_cols = gate.shape
-        else:
-            raise ValueError("gate must be [H], [gate_rows, H] or [gate_rows, 1]")
-    out = _output(out, "out", shape, dt, dev, stream)
-    n = _output(next_out, "next_out", shape, dt, dev, stream) if next_norm else None
-    _check("qsw_post_norm", lib.qsw_post_norm(h.data_ptr(), y.data_ptr(), 1 if norm else 0, w, _ptr(gate), gate_rows,
-                                              gate_cols, scale, wn, rows, H, eps, act, out.data_ptr(), _ptr(n),
-                                              _raw_stream(stream, dev)))
-    return (out, n) if next_norm else out
+    return _call((_native or _load_native()).post_norm, stream, h, y, weight, gate, scale, next_weight, eps, norm,
+                 next_norm, out, next_out)
 
 
 def qsw_check_device_errors(stream=None) -> None:
