@@ -22,11 +22,17 @@ struct QuantSource {
   int64_t K;
   int64_t k_blocks;        // scale blocks along K
   int groups;
+  bool stream;             // too much to stay in L2
 };
+
+// 16-bit matrices beyond this many bytes are read and written with streaming
+// accesses, so that they do not push the codes out of the 129 MB of L2 (4096 x 14336
+// there and back: 68.1 -> 61.6 us); a smaller one may still be there for its reader.
+constexpr int64_t kStreamBytes = int64_t(64) << 20;
 
 template <class A, int FMT>
 __device__ __forceinline__ void quantize_block(const uint16_t *src, int64_t k0, int64_t K, uint8_t *codes,
-                                               uint8_t *scale, const Fp4Scale &q) {
+                                               uint8_t *scale, const Fp4Scale &q, bool stream) {
   constexpr int B = Fp4<FMT>::kBlock;
   if (k0 >= K) {      // padding of the last scale block
     *scale = 0;
@@ -34,7 +40,10 @@ __device__ __forceinline__ void quantize_block(const uint16_t *src, int64_t k0, 
   }
   uint4 v[B / 8];
 #pragma unroll
-  for (int i = 0; i < B / 8; ++i) v[i] = __ldg(reinterpret_cast<const uint4 *>(src + k0) + i);
+  for (int i = 0; i < B / 8; ++i) {
+    const uint4 *p = reinterpret_cast<const uint4 *>(src + k0) + i;
+    v[i] = stream ? __ldcs(p) : __ldg(p);
+  }
   uint32_t amax = amax_pairs<A>(v[0], v[1]);
   if (B == 32) amax = max(amax, amax_pairs<A>(v[B / 8 - 2], v[B / 8 - 1]));
   float inv;
@@ -90,7 +99,7 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const QuantSour
   const int64_t end = first + run < s.k_blocks ? first + run : s.k_blocks;
 #pragma unroll 2
   for (int64_t kb = first; kb < end; ++kb)
-    quantize_block<A, FMT>(src, (kb * 4 + (lane & 3)) * Fp4<FMT>::kBlock, s.K, codes, scale + kb * kSfBytes, q);
+    quantize_block<A, FMT>(src, (kb * 4 + (lane & 3)) * Fp4<FMT>::kBlock, s.K, codes, scale + kb * kSfBytes, q, s.stream);
 }
 
 // The same unit and mapping as the quantiser: a warp reads 32 consecutive scale
@@ -98,7 +107,7 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const QuantSour
 template <class A, int FMT>
 __global__ void __launch_bounds__(kQuantThreads)
     dequantize_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales, int64_t rows, int64_t K,
-                      int64_t k_blocks, float g, int run, uint16_t *__restrict__ out) {
+                      int64_t k_blocks, float g, int run, bool stream, uint16_t *__restrict__ out) {
   griddep_wait();
   griddep_launch_dependents();
   constexpr int B = Fp4<FMT>::kBlock;
@@ -135,10 +144,14 @@ __global__ void __launch_bounds__(kQuantThreads)
     for (int i = 0; i < B / 8; ++i) {
       uint32_t h[4];
       fp4_unpack8(w[i], h);
-      dst[i] = make_uint4(A::pack2(ActF16::lo(h[0]) * s, ActF16::hi(h[0]) * s),
-                          A::pack2(ActF16::lo(h[1]) * s, ActF16::hi(h[1]) * s),
-                          A::pack2(ActF16::lo(h[2]) * s, ActF16::hi(h[2]) * s),
-                          A::pack2(ActF16::lo(h[3]) * s, ActF16::hi(h[3]) * s));
+      const uint4 o = make_uint4(A::pack2(ActF16::lo(h[0]) * s, ActF16::hi(h[0]) * s),
+                                 A::pack2(ActF16::lo(h[1]) * s, ActF16::hi(h[1]) * s),
+                                 A::pack2(ActF16::lo(h[2]) * s, ActF16::hi(h[2]) * s),
+                                 A::pack2(ActF16::lo(h[3]) * s, ActF16::hi(h[3]) * s));
+      if (stream)
+        __stcs(dst + i, o);
+      else
+        dst[i] = o;
     }
   }
 }
@@ -221,9 +234,9 @@ __global__ void __launch_bounds__(256) quantize_fan_kernel(const FanParams p, co
   }
 }
 
-// Scale blocks per CTA: a grid of a few waves of 4 CTAs per SM (16 loads of 32
-// bytes in flight per thread and SM slot; longer runs with more loads ahead
-// measured the same, at the rate of a device copy of these sizes).
+// Scale blocks per CTA: a grid of a few waves of 4 CTAs per SM.  (Longer runs with
+// more loads in flight per thread measured the same: the kernels run at the rate
+// of a device copy of their sizes.)
 int quant_run(int64_t row_blocks, int64_t k_blocks, int num_sms) {
   const int64_t want = row_blocks * k_blocks / (static_cast<int64_t>(num_sms) * 16);
   return static_cast<int>(want < 1 ? 1 : want > 16 ? 16 : want);
@@ -262,6 +275,7 @@ cudaError_t launch_fp4_quantize(const void *x, int64_t groups, int64_t rows, int
   s.K = K;
   s.k_blocks = fp4_k_blocks(K, fmt);
   s.groups = static_cast<int>(groups);
+  s.stream = groups * rows * K * 2 > kStreamBytes;
   return dispatch_quant<false>(s, fmt, act, g, groups * ((rows + kSfRows - 1) / kSfRows), quant_threads(rows), num_sms,
                                stream, false);
 }
@@ -310,13 +324,14 @@ cudaError_t launch_fp4_quantize_fan(const void *x, int64_t T, int64_t K, int k, 
 }
 
 cudaError_t launch_fp4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t groups, int64_t rows,
-                                  int64_t K, int fmt, int act, float g, void *out, int num_sms, cudaStream_t stream) {
+                                  int64_t K, int fmt, int act, float g, void *out, int num_sms, cudaStream_t cs) {
+  const bool stream = groups * rows * K * 2 > kStreamBytes;
   const int64_t kb = fp4_k_blocks(K, fmt), row_blocks = groups * ((rows + kSfRows - 1) / kSfRows);
   const int threads = quant_threads(rows), run = quant_run(row_blocks, kb, num_sms);
   auto *o = static_cast<uint16_t *>(out);
   const dim3 grid(static_cast<unsigned>(row_blocks), static_cast<unsigned>((kb + run - 1) / run));
 #define QSW_DEQ(A, F) \
-  launch_on(dequantize_kernel<A, F>, grid, threads, 0, stream, false, codes, scales, rows, K, kb, g, run, o)
+  launch_on(dequantize_kernel<A, F>, grid, threads, 0, cs, false, codes, scales, rows, K, kb, g, run, stream, o)
   if (act == ActBf16::kId) return fmt == FP4_MX ? QSW_DEQ(ActBf16, FP4_MX) : QSW_DEQ(ActBf16, FP4_NV);
   return fmt == FP4_MX ? QSW_DEQ(ActF16, FP4_MX) : QSW_DEQ(ActF16, FP4_NV);
 #undef QSW_DEQ

@@ -21,6 +21,7 @@ struct NormParams {
   int H;
   int gate_cols;           // H, or 1: one gate value per gate row
   int norm_y;
+  int stream;              // more rows than stay in L2
   float scale, eps, inv_h;
 };
 
@@ -30,11 +31,12 @@ struct Raw {
   uint32_t w[(VEC + 1) / 2];
 };
 
+// `once`: a row's value, which is not read again (evicted first from L2).
 template <int VEC>
-__device__ __forceinline__ Raw<VEC> load_raw(const uint16_t *p) {
+__device__ __forceinline__ Raw<VEC> load_raw(const uint16_t *p, bool once = false) {
   Raw<VEC> r;
   if constexpr (VEC == 8) {
-    const uint4 q = *reinterpret_cast<const uint4 *>(p);
+    const uint4 q = once ? __ldcs(reinterpret_cast<const uint4 *>(p)) : *reinterpret_cast<const uint4 *>(p);
     r.w[0] = q.x;
     r.w[1] = q.y;
     r.w[2] = q.z;
@@ -53,11 +55,14 @@ __device__ __forceinline__ float value(const Raw<VEC> &r, int j) {
 }
 
 template <class A, int VEC>
-__device__ __forceinline__ void store_vec(uint16_t *p, const float (&v)[VEC]) {
-  if constexpr (VEC == 8)
-    *reinterpret_cast<uint4 *>(p) = make_uint4(A::pack2(v[0], v[1]), A::pack2(v[2], v[3]), A::pack2(v[4], v[5]),
-                                               A::pack2(v[6], v[7]));
-  else if constexpr (VEC == 2)
+__device__ __forceinline__ void store_vec(uint16_t *p, const float (&v)[VEC], bool stream) {
+  if constexpr (VEC == 8) {
+    const uint4 q = make_uint4(A::pack2(v[0], v[1]), A::pack2(v[2], v[3]), A::pack2(v[4], v[5]), A::pack2(v[6], v[7]));
+    if (stream)
+      __stcs(reinterpret_cast<uint4 *>(p), q);
+    else
+      *reinterpret_cast<uint4 *>(p) = q;
+  } else if constexpr (VEC == 2)
     *reinterpret_cast<uint32_t *>(p) = A::pack2(v[0], v[1]);
   else
     *p = A::store(v[0]);
@@ -82,7 +87,8 @@ __device__ __forceinline__ float block_sum(float v, float *buf) {
 // with a stride of the grid; while it works on one, the next one's h and y are on
 // their way, and the weights stay in registers.  (With a CTA per row, the row's
 // loads, two block sums and stores came one after the other and each row read the
-// weights again: 57.4 us for 8192 rows of 4096, against 40.2 us of copying.)
+// weights again: 57.4 us for 8192 rows of 4096; a device copy of as many bytes takes
+// 47 us.)
 template <class A, int VEC, int EPT>
 __global__ void __launch_bounds__(1024) norm_kernel(const NormParams p) {
   constexpr int RUNS = EPT / VEC;
@@ -96,7 +102,7 @@ __global__ void __launch_bounds__(1024) norm_kernel(const NormParams p) {
 #pragma unroll
     for (int i = 0; i < RUNS; ++i) {
       const int c = first + i * step;
-      r[i] = c < p.H ? load_raw<VEC>(base + row * p.H + c) : zero;
+      r[i] = c < p.H ? load_raw<VEC>(base + row * p.H + c, p.stream) : zero;
     }
   };
   Raw<VEC> wp[kAhead ? RUNS : 1], wn[kAhead ? RUNS : 1];
@@ -157,7 +163,7 @@ __global__ void __launch_bounds__(1024) norm_kernel(const NormParams p) {
         }
 #pragma unroll
         for (int j = 0; j < VEC; ++j) hv[i][j] = fmaf(f[j], value<A, VEC>(y[i], j), hv[i][j]);
-        if (p.h_out) store_vec<A, VEC>(p.h_out + row * p.H + c, hv[i]);
+        if (p.h_out) store_vec<A, VEC>(p.h_out + row * p.H + c, hv[i], p.stream);
       }
     }
     if (!p.n_out) continue;
@@ -179,17 +185,18 @@ __global__ void __launch_bounds__(1024) norm_kernel(const NormParams p) {
 #pragma unroll
         for (int j = 0; j < VEC; ++j) q[j] *= value<A, VEC>(w, j);
       }
-      store_vec<A, VEC>(p.n_out + row * p.H + c, q);
+      store_vec<A, VEC>(p.n_out + row * p.H + c, q, p.stream);
     }
   }
 }
 
 template <class A, int VEC>
 cudaError_t launch_vec(const NormParams &p, int num_sms, cudaStream_t stream) {
-  // 8 elements per thread up to 256 threads, then 16, and 32 where 1024 threads
-  // need them; as many CTAs as 64 registers a thread let run at once
+  // 8 elements per thread, 16 and 32 where 1024 threads need them (rows of 4096:
+  // 512 threads of 8 take 51.5 us for 8192 of them, 256 threads of 16 take 53.0);
+  // as many CTAs as 64 registers a thread let run at once
   const int need8 = (p.H + 7) / 8;
-  const int ept = need8 <= 256 ? 8 : need8 <= 2048 ? 16 : 32;
+  const int ept = need8 <= 1024 ? 8 : need8 <= 2048 ? 16 : 32;
   const int threads = ((p.H + ept - 1) / ept + 31) / 32 * 32;
   const int64_t most = static_cast<int64_t>(num_sms) * (1024 / threads);
   const dim3 grid(static_cast<unsigned>(p.rows < most ? p.rows : most));
@@ -232,6 +239,9 @@ cudaError_t launch_norm(const NormArgs &a, int num_sms, cudaStream_t stream) {
   p.scale = a.scale;
   p.eps = a.eps;
   p.inv_h = 1.0f / static_cast<float>(a.H);
+  // rows, twice in and twice out, against the L2's 129 MB: streaming accesses take 8192
+  // rows of 4096 from 53.4 to 51.5 us; what fits stays for its reader
+  p.stream = a.rows * a.H * 8 > int64_t(128) << 20;
   return a.act == ActF16::kId ? launch_act<ActF16>(p, num_sms, stream) : launch_act<ActBf16>(p, num_sms, stream);
 }
 
