@@ -291,7 +291,7 @@ typedef enum {
 QSW_API size_t qsw_fp4_scale_bytes(int64_t groups, int64_t rows, int64_t K, int fmt);
 
 /* Quantise x [groups, rows, K] (act_dtype) to codes and scales, and back.
- * K a multiple of 32; all pointers 16-byte aligned. */
+ * K a multiple of 32, at most 2^22; all pointers 16-byte aligned. */
 QSW_API qsw_status qsw_fp4_quantize(const void *x, int64_t groups, int64_t rows, int64_t K, int fmt, float scale,
                            int act_dtype, uint8_t *codes, uint8_t *scales, void *stream);
 QSW_API qsw_status qsw_fp4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t groups, int64_t rows,
@@ -451,6 +451,10 @@ QSW_API void qsw_set_wait_timeout_ns(uint64_t ns);
  * QSW_ERR_TIMEOUT.  Later calls are unaffected.  Nothing traps and nothing
  * waits without a limit. */
 QSW_API void qsw_debug_withhold_next_fill(void);
+
+/* The same for the next 4-bit product (qsw_fp4_linear, qsw_fp4_grouped_linear or the
+ * first of qsw_fp4_moe_mlp): it never requests its weights, so its waits run out. */
+QSW_API void qsw_debug_withhold_next_product(void);
 
 /* Dispatch counters (process-wide, monotonically increasing). `out` receives
  * min(n, QSW_NUM_COUNTERS) values. */

@@ -12,6 +12,7 @@ namespace {
 constexpr int64_t kMaxRows = int64_t(1) << 30;
 constexpr int kMaxGroups = 1024;
 constexpr int kMaxTopK = 32;
+constexpr int64_t kMaxK = int64_t(1) << 22;      // elements of a row
 constexpr int64_t kMaxNorm = 32768;
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -31,7 +32,7 @@ qsw_status check_format(int fmt, float g) {
 // Rows of `K` elements: whole MX blocks, 16-byte code rows.
 qsw_status check_k(int64_t K) {
   if (K <= 0) return QSW_ERR_INVALID_ARG;
-  return K % 32 != 0 || K > kMaxRows ? QSW_ERR_UNSUPPORTED : QSW_OK;
+  return K % 32 != 0 || K > kMaxK ? QSW_ERR_UNSUPPORTED : QSW_OK;
 }
 
 size_t scale_bytes(int64_t row_blocks, int64_t K, int fmt) {
@@ -272,6 +273,8 @@ qsw_status qsw_fp4_moe_mlp(const void *x, int64_t T, int64_t H, int64_t I, int E
   if (st == QSW_OK) qsw::count_call(QSW_CNT_FP4_MOE);
   return st;
 }
+
+void qsw_debug_withhold_next_product(void) { qsw::fp4_gemm_withhold_next(); }
 
 qsw_status qsw_rms_norm(const void *x, const void *weight, int64_t rows, int64_t H, float eps, int act_dtype,
                         void *out, void *stream) {

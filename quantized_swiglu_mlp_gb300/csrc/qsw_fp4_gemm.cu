@@ -31,6 +31,7 @@
 // the group table, the weights of its first stages -- reads only what was
 // complete before the launch in front of this one began (each kernel of a chain
 // lets the next one start only after its own wait).
+#include <atomic>
 #include <mutex>
 #include <type_traits>
 
@@ -41,6 +42,7 @@ namespace qsw {
 namespace {
 
 __device__ unsigned int g_fp4_error;
+std::atomic<int> g_withhold{0};
 
 constexpr int kTileTokens = 192;
 constexpr int kMaxStages = 16;
@@ -87,6 +89,7 @@ struct GemmParams {
   int h_k_blocks;
   Fp4Scale hq;
   uint64_t timeout_ns;
+  int withhold;             // test hook: the weights' codes are never requested
   // few rows: x itself, [<= kFuseRows, K], quantised by every CTA into shared memory
   const void *x;
   Fp4Scale xq;
@@ -414,6 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], mma_done;
   __shared__ uint32_t tmem_slot;
   __shared__ uint64_t x_ready;
+  __shared__ int fills[4];      // stages that each producer has requested
   __shared__ int abort_word, rec_count, cols[32];
   volatile int *abort_flag = &abort_word;
   int *table = reinterpret_cast<int *>(smem + p.table_off);
@@ -441,6 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&mma_done, 1);
     mbar_init(&x_ready, kEpiWarps);
     abort_word = 0;
+    for (int r = 0; r < 4; ++r) fills[r] = 0;
     fence_mbar_init();
     prefetch_tensormap(&maps.w);
     prefetch_tensormap(&maps.x);
@@ -498,6 +503,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
   const int k_stages = ceil_div(p.K, kStageK);
   const int tiles = rec_count;
+  if constexpr (kDebugBounds) {
+    // every column := NaN before the first product (a warp per lane quarter)
+    if (warp >= kWarpEpi0 && warp < kWarpEpi0 + 4) {
+      uint32_t nan16[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) nan16[i] = ~0u;
+      for (uint32_t col = 0; col < 512; col += 16)
+        tmem_st16(tmem + (static_cast<uint32_t>(warp & 3) << 21) + col, nan16);
+      tmem_st_wait();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (PAIR) cluster_sync();
+    tc_fence_after();
+  }
 
   // Ring positions are counted, not divided: a division by the run-time stage
   // count in every iteration cost the issuing thread more than its products.
@@ -566,17 +586,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (!ok && rank == 0) {
-        // let the copies already issued land before the CTA's memory goes away
-        // (a pair's leader waits for both; the partner stays until it has)
-        for (int i = 0; i < S && i < filled; ++i) {
-          const int last = i + ((filled - 1 - i) / S) * S;
-          mbar_wait_drain(&full[i], (last / S) & 1, 100000000ull);
-        }
-      }
+      fills[ROLE] = filled;
     };
     const bool x_side = warp == kWarpProd1 || warp == kWarpProd1 + 2;
-    if (elect_one() && !(fuse && x_side)) {
+    if (elect_one() && !(fuse && x_side) && !(p.withhold && warp == 0)) {
       if (warp == 0)
         produce(std::integral_constant<int, W_CODES>());
       else if (warp == kWarpProd1)
@@ -648,10 +661,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (ok && issuer) commit_to<PAIR>(&acc_full[buf]);
     }
-    if (!ok && issuer) {
-      commit_to<PAIR>(&mma_done);
-      mbar_wait_drain(&mma_done, 0, 100000000ull);
-    }
     __syncwarp();
   } else {
     // ------------------------------------------------------------ epilogue --
@@ -680,6 +689,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int j = 0; j < tiles; ++j) {
       const TileRec t = recs[j];
       const int buf = j & 1;
+      debug_check(t.row >= 0 && t.row + t.valid <= p.rows && t.w0 >= 0 && t.e < p.groups, err);
       // the column of each of the tile's rows, where all rows of x are columns
       int col = 0;
       if (fuse && group == 0 && gtid < 32 && gtid < t.valid) {
@@ -796,6 +806,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if (*abort_flag && rank == 0) {
+    // Given up: let the products and copies already issued finish before tensor and
+    // shared memory go away, each wait with a limit.  (A pair's leader waits for
+    // both CTAs'; the partner stays until it has.)
+    if (warp == kWarpMma && elect_one()) {
+      commit_to<PAIR>(&mma_done);
+      mbar_wait_drain(&mma_done, 0, 100000000ull);
+    }
+    if (warp == 0 && lane < 4) {
+      const int filled = fills[lane];
+      for (int i = 0; i < S && i < filled; ++i) {
+        const int last = i + ((filled - 1 - i) / S) * S;
+        mbar_wait_drain(&full[i], (last / S) & 1, 100000000ull);
+      }
+    }
+    __syncthreads();
+  }
   if (PAIR) cluster_sync();      // nothing of the partner's reaches this CTA any more
   tc_fence_after();
   if (warp == kWarpMma) tmem_free_all<PAIR>(tmem);
@@ -978,6 +1005,7 @@ cudaError_t launch_fp4_gemm(const Fp4GemmArgs &a, int num_sms, uint64_t timeout_
   p.h_k_blocks = a.swiglu ? static_cast<int>(fp4_k_blocks(a.N / 2, a.fmt)) : 0;
   p.hq = make_fp4_scale(a.h_scale);
   p.timeout_ns = timeout_ns;
+  p.withhold = g_withhold.exchange(0, std::memory_order_relaxed);
 
   if (a.x) {
     p.x = a.x;
@@ -1024,6 +1052,8 @@ cudaError_t launch_fp4_gemm(const Fp4GemmArgs &a, int num_sms, uint64_t timeout_
   p.n_tiles = ceil_div(p.N, p.rt);
   return dispatch_gemm<false>(a, p, num_sms, stream, dependent);
 }
+
+void fp4_gemm_withhold_next() { g_withhold.store(1); }
 
 // Read and clear the device error word of this translation unit's kernels.
 cudaError_t fp4_gemm_take_errors(unsigned int *out) {

@@ -126,6 +126,7 @@ bool fp4_gemm_quantizes(int64_t rows, int64_t K, int fmt);
 cudaError_t launch_fp4_gemm(const Fp4GemmArgs &a, int num_sms, uint64_t timeout_ns, cudaStream_t stream,
                             bool dependent);
 cudaError_t fp4_gemm_take_errors(unsigned int *out);
+void fp4_gemm_withhold_next();   // test hook: the next product's waits run out
 
 cudaError_t launch_moe_route(const void *logits, int logit_dtype, int64_t T, int E, int k, int scoring,
                              int renormalize, float scale, int *ids, float *weights, int *offsets, int *slots,

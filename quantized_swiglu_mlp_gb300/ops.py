@@ -51,7 +51,7 @@ EXPORTED = ("qswiglu_forward", "affine_qmm", "qswiglu_forward_ws", "affine_qmm_w
             "qsw_get_counters", "qsw_reset_counters", "qsw_status_string", "qsw_version",
             "qsw_fp4_scale_bytes", "qsw_fp4_quantize", "qsw_fp4_dequantize", "qsw_fp4_workspace_bytes",
             "qsw_fp4_linear", "qsw_fp4_grouped_linear", "qsw_moe_route", "qsw_fp4_moe_workspace_bytes",
-            "qsw_fp4_moe_mlp", "qsw_rms_norm", "qsw_post_norm")
+            "qsw_fp4_moe_mlp", "qsw_rms_norm", "qsw_post_norm", "qsw_debug_withhold_next_product")
 
 _lock = threading.Lock()
 _lib = None
@@ -568,6 +568,11 @@ def qsw_debug_withhold_next_fill() -> None:
     """Test hook: the next small-M call leaves its first units unrequested, so
     its waits run out (see include/qswiglu.h)."""
     load_library().qsw_debug_withhold_next_fill()
+
+
+def qsw_debug_withhold_next_product() -> None:
+    """Test hook: the next 4-bit product never requests its weights, so its waits run out."""
+    load_library().qsw_debug_withhold_next_product()
 
 
 def qsw_debug_build() -> bool:

@@ -230,6 +230,7 @@ def test_fp4_sizes(lib):
 
 @pytest.mark.parametrize("kw,code", [
     (dict(rows=0), OK), (dict(groups=0), OK), (dict(rows=-1), INVALID), (dict(K=0), INVALID), (dict(K=48), UNSUPPORTED),
+    (dict(K=(1 << 22) + 32), UNSUPPORTED),
     (dict(fmt=2), INVALID), (dict(scale=0.0), INVALID), (dict(scale=float("nan")), INVALID),
     (dict(scale=float("inf")), INVALID), (dict(fmt=MX, scale=2.0), INVALID), (dict(act=2), INVALID),
     (dict(x=0), INVALID), (dict(codes=FAKE + 8), UNSUPPORTED), (dict(scales=FAKE + 4), UNSUPPORTED),
