@@ -13,11 +13,8 @@
 // every token count: N is a run-time operand of the instruction (a multiple of
 // 16 up to 192), so one token and a ragged group of 150 waste no more than 15
 // columns, and a single token streams its weights through TMA at HBM rate
-// without a second kernel.  Where the 128-row tiles would not fill the SMs, a tile
-// is 64, 32 or 16 rows (`rt`): only those rows are copied, the MMA still reads 128
-// -- the others hold whatever shared memory holds, and their accumulator lanes
-// are never read.  The rows keep their place r mod 128, so that the scale block's
-// lanes fit: the A descriptor starts that many rows before the copied ones.
+// without a second kernel.  (Tiles of 64, 32 or 16 weight rows, to have more CTAs for
+// few rows, gained nothing: a tile's time is that of its chain of stages.)
 //
 // One persistent CTA per SM, 17 warps: warps 0 and 14-16 issue the copies of the
 // weights' and activations' codes and scales (a ring of stages of 256 elements of
@@ -46,7 +43,8 @@ std::atomic<int> g_withhold{0};
 
 constexpr int kTileTokens = 192;
 constexpr int kMaxStages = 16;
-constexpr int kFuseRows = 16;                // rows of x that a CTA quantises itself
+constexpr int kFuseRows = 16;                // rows of x that a CTA quantises itself, at most
+constexpr int64_t kFuseElements = 8192;      // and elements
 constexpr int kEpiGroups = 3;                // epilogue groups of four warps
 constexpr int kEpiWarps = 4 * kEpiGroups;
 // Warps: the first producer, the MMA issuer, the epilogue, three more producers.
@@ -73,10 +71,11 @@ struct GemmParams {
   int rows;                 // rows of x
   int max_group;            // no group has more rows
   int N, K;
-  int n_tiles;              // weight tiles of `rt` rows per group
+  int n_tiles;              // weight tiles per group
   int k_blocks;             // scale blocks along K
   int w_row_blocks;         // scale row blocks of a group's weights
-  int rt, bt;               // weight rows and most tokens of a tile
+  int bt;                   // most tokens of a tile
+  int split;                // CTAs (a cluster) that share a tile's K: 1, 2 or 4
   int x_box, x_rows;        // rows of the small TMA box of x, and of a stage (the large box)
   int x_sf;                 // scale row blocks of x in a stage
   int stages;
@@ -145,7 +144,7 @@ __device__ __forceinline__ TileRec make_rec(const GemmParams &p, const int *off,
   t.valid = min(size, m - t.t0);
   t.n = max(kStep, (t.valid + kStep - 1) & ~(kStep - 1));
   if (!PAIR && p.x) t.n = kFuseRows;
-  t.w0 = wt * p.rt + (PAIR ? static_cast<int>(rank) * kSfRows : 0);
+  t.w0 = wt * (PAIR ? 2 * kSfRows : kSfRows) + (PAIR ? static_cast<int>(rank) * kSfRows : 0);
   t.w_block = e * p.w_row_blocks + t.w0 / kSfRows;
   t.x_block = (p.offsets ? static_cast<int>(ragged_row_block(off[e], e)) : 0) + t.t0 / kSfRows;
   return t;
@@ -191,6 +190,44 @@ __device__ __forceinline__ uint32_t leader_address(const void *p) {
   uint32_t a;
   asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_u32(p)));
   return a;
+}
+__device__ __forceinline__ uint32_t peer_address(const void *p, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ float load_peer(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+// Hands the thread's shared memory over to the waiting CTA.
+__device__ __forceinline__ void mbar_arrive_release_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// mbar_wait for what other CTAs of the cluster handed over.
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity, volatile int *abort,
+                                                  uint64_t timeout_ns, unsigned int *err) {
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t it = 1;; ++it) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if ((it & 63u) == 0) {
+      if (*abort) return false;
+      if (globaltimer_ns() - t0 > timeout_ns) {
+        *abort = 1;
+        atomicOr(err, DEVERR_TIMEOUT);
+        return false;
+      }
+    }
+  }
 }
 // Relaxed: nothing in memory is handed over (a releasing arrival would wait for the
 // thread's global stores to be performed).
@@ -331,49 +368,57 @@ __device__ __forceinline__ bool bar_and_group(int id, bool ok) {
 }
 
 // Rows of x into shared memory as the MMA takes them: per stage 16 rows of 128
-// swizzled bytes of codes and the scale blocks.  Elements past K are 0; rows past
-// the last are left as they are (their columns are never read).
+// swizzled bytes of codes and the scale blocks, stages [k_first, k_end).  Elements
+// past K are 0; rows past the last are left as they are (their columns are never read).
 template <class A, int FMT>
-__device__ __forceinline__ void quantize_to_smem(const GemmParams &p, uint8_t *codes, uint8_t *scales, int k_stages,
-                                                 int tid, int threads) {
-  constexpr int B = Fp4<FMT>::kBlock;
-  const int per_row = k_stages * (kStageK / B);       // scales of a row, padding included
-  for (int i = tid; i < per_row * p.x_tokens; i += threads) {
-    const int row = i / per_row, j = i - row * per_row, k0 = j * B;
-    uint32_t byte = 0, c[B / 8] = {};
-    if (k0 < p.K) {
+__device__ __forceinline__ void quantize_to_smem(const GemmParams &p, uint8_t *codes, uint8_t *scales, int k_first,
+                                                 int k_end, int tid, int threads) {
+  constexpr int B = Fp4<FMT>::kBlock, AHEAD = 64 / B;   // 128 bytes in flight per thread
+  const int per_row = (k_end - k_first) * (kStageK / B);   // scales of a row's stages, padding included
+  const int n = per_row * p.x_tokens;
+  for (int i0 = tid; i0 < n; i0 += AHEAD * threads) {
+    uint4 v[AHEAD][B / 8];
+#pragma unroll
+    for (int a = 0; a < AHEAD; ++a) {
+      const int i = i0 + a * threads, row = i / per_row, k0 = (i - row * per_row) * B + k_first * kStageK;
+      const bool in = i < n && k0 < p.K;
       const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.x) +
                                                          static_cast<int64_t>(row) * p.K + k0);
-      uint4 v[B / 8];
 #pragma unroll
-      for (int q = 0; q < B / 8; ++q) v[q] = __ldg(src + q);
-      uint32_t amax = amax_pairs<A>(v[0], v[1]);
-      if (B == 32) amax = max(amax, amax_pairs<A>(v[B / 8 - 2], v[B / 8 - 1]));
-      float inv;
-      byte = fp4_scale_of<FMT>(amax, p.xq, inv);
-#pragma unroll
-      for (int q = 0; q < B / 8; ++q) c[q] = fp4_code8<A>(v[q], inv);
+      for (int q = 0; q < B / 8; ++q) v[a][q] = in ? __ldg(src + q) : make_uint4(0, 0, 0, 0);
     }
-    uint8_t *dst = codes + (k0 / kStageK) * (kFuseRows * 128) + row * 128 +
-                   ((((k0 % kStageK) / 32) ^ (row & 7)) << 4) + (k0 % 32) / 2;
-    if (B == 16)
-      *reinterpret_cast<uint2 *>(dst) = make_uint2(c[0], c[1]);
-    else
-      *reinterpret_cast<uint4 *>(dst) = make_uint4(c[0], c[1], c[B / 8 - 2], c[B / 8 - 1]);
-    scales[(j >> 2) * kSfBytes + row * 16 + (j & 3)] = static_cast<uint8_t>(byte);
+#pragma unroll
+    for (int a = 0; a < AHEAD; ++a) {
+      const int i = i0 + a * threads, row = i / per_row, j = i - row * per_row + k_first * (kStageK / B), k0 = j * B;
+      if (i >= n) break;
+      uint32_t amax = amax_pairs<A>(v[a][0], v[a][1]);
+      if (B == 32) amax = max(amax, amax_pairs<A>(v[a][B / 8 - 2], v[a][B / 8 - 1]));
+      float inv;
+      const uint32_t byte = fp4_scale_of<FMT>(amax, p.xq, inv);
+      uint32_t c[B / 8];
+#pragma unroll
+      for (int q = 0; q < B / 8; ++q) c[q] = fp4_code8<A>(v[a][q], inv);
+      uint8_t *dst = codes + (k0 / kStageK) * (kFuseRows * 128) + row * 128 +
+                     ((((k0 % kStageK) / 32) ^ (row & 7)) << 4) + (k0 % 32) / 2;
+      if (B == 16)
+        *reinterpret_cast<uint2 *>(dst) = make_uint2(c[0], c[1]);
+      else
+        *reinterpret_cast<uint4 *>(dst) = make_uint4(c[0], c[1], c[B / 8 - 2], c[B / 8 - 1]);
+      scales[(j >> 2) * kSfBytes + row * 16 + (j & 3)] = k0 < p.K ? static_cast<uint8_t>(byte) : 0;
+    }
   }
 }
 
-// A group's run of `tokens` rows out of the exchange buffer: features [lo, hi) of
-// the 128-row weight block at column n0 of an [.., N] output.  `cols`: null, or the buffer row
+// A group's run of `tokens` rows out of the exchange buffer: features of the
+// weight tile at column n0 of an [.., N] output.  `cols`: null, or the buffer row
 // of each.  `wide`: rows start at 16-byte boundaries, 16-byte stores; else pairs
 // from each row's first 4-byte boundary on, single values around them.
-__device__ __forceinline__ void store_rows(const uint16_t *ex, uint16_t *out, int N, int n0, int lo, int hi, int tokens,
+__device__ __forceinline__ void store_rows(const uint16_t *ex, uint16_t *out, int N, int n0, int tokens,
                                            int tid, bool wide, const int *cols) {
-  hi = min(hi, N - n0);
+  const int hi = min(kSfRows, N - n0);
   if (wide) {
     const int f = (tid & 15) * 8;
-    if (f < lo || f >= hi) return;
+    if (f >= hi) return;
     uint4 v[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const uint4 *>(ex + (cols ? cols[(tid >> 4) + 8 * i] : (tid >> 4) + 8 * i) * kYPitch + f);
@@ -389,7 +434,7 @@ __device__ __forceinline__ void store_rows(const uint16_t *ex, uint16_t *out, in
     const uint16_t *src = ex + (cols ? cols[tok] : tok) * kYPitch;
     const int odd = static_cast<int>(reinterpret_cast<uintptr_t>(dst) >> 1) & 1;
     for (int f = (tid & 31) * 2 - odd; f < hi; f += 64) {
-      const bool a = f >= lo, b = f + 1 >= lo && f + 1 < hi;
+      const bool a = f >= 0, b = f + 1 < hi;
       if (a && b)
         *reinterpret_cast<uint32_t *>(dst + f) = src[f] | static_cast<uint32_t>(src[f + 1]) << 16;
       else if (a)
@@ -408,15 +453,21 @@ struct GemmMaps {
   CUtensorMap w, x, xb, sfw, sfx;
 };
 
-template <class A, int FMT, bool SWIGLU, bool PAIR>
+// How a tile's work is shared: one CTA, a cluster that splits K, a CTA pair.  (A
+// template: the code of the others in a lone CTA's kernel cost a 1 x 2048 x 8192 product
+// half a microsecond.)
+enum Mode : int { LONE = 0, SPLIT = 1, PAIRED = 2 };
+
+template <class A, int FMT, bool SWIGLU, int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
     fp4_gemm_kernel(const __grid_constant__ GemmParams p, const __grid_constant__ GemmMaps maps) {
+  constexpr bool PAIR = MODE == PAIRED;
   constexpr int kSfPerStage = kStageK / Fp4<FMT>::kSfK;   // scale blocks per stage: 2 (MX), 4 (NV)
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], mma_done;
   __shared__ uint32_t tmem_slot;
-  __shared__ uint64_t x_ready;
+  __shared__ uint64_t x_ready, part_ready;
   __shared__ int fills[4];      // stages that each producer has requested
   __shared__ int abort_word, rec_count, cols[32];
   volatile int *abort_flag = &abort_word;
@@ -426,7 +477,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   unsigned int *err = &g_fp4_error;
   const int S = p.stages;
   const uint32_t rank = PAIR ? cluster_rank() : 0;
-  const int w_rows = PAIR ? kSfRows : p.rt;      // weight rows of this CTA's part of a tile
+  const int split = MODE == SPLIT ? p.split : 1, unit = PAIR ? 2 : split;   // CTAs that share a tile
+  const int k_rank = MODE == SPLIT ? static_cast<int>(cluster_rank()) : 0;
   const bool fuse = !PAIR && p.x != nullptr;     // x is quantised here, and stays for all tiles
 
   if constexpr (kDebugBounds) {
@@ -444,6 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(&mma_done, 1);
     mbar_init(&x_ready, kEpiWarps);
+    mbar_init(&part_ready, split * kEpiWarps);
     abort_word = 0;
     for (int r = 0; r < 4; ++r) fills[r] = 0;
     fence_mbar_init();
@@ -490,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
     // this CTA's tiles: every gridDim-th from its own index on
-    const int start = static_cast<int>(blockIdx.x) >> (PAIR ? 1 : 0), step = static_cast<int>(gridDim.x) >> (PAIR ? 1 : 0);
+    const int start = static_cast<int>(blockIdx.x) / unit, step = static_cast<int>(gridDim.x) / unit;
     const int count = total > start ? ceil_div(total - start, step) : 0;
     debug_check(count <= p.recs, err);
     for (int j = lane; j < count; j += 32) recs[j] = make_rec<PAIR>(p, table, first, start + j * step, rank);
@@ -498,10 +551,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (PAIR) cluster_sync();      // the partner's barriers are ready too
+  if (MODE != LONE) cluster_sync();      // the partners' barriers are ready too
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
+  // this CTA's stages of K: all, or its part of a split tile's
   const int k_stages = ceil_div(p.K, kStageK);
+  const int k_first = k_stages * k_rank / split, k_end = k_stages * (k_rank + 1) / split;
   const int tiles = rec_count;
   if constexpr (kDebugBounds) {
     // every column := NaN before the first product (a warp per lane quarter)
@@ -529,11 +584,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the weights' first stages go out before the wait
       if (X) griddep_wait();
       if (ROLE == X_CODES) griddep_launch_dependents();
-      const int stage = SCALES ? kSfPerStage * kSfBytes * (1 + (fuse ? 0 : p.x_sf)) : (X ? p.x_rows : w_rows) * 128;
+      const int stage = SCALES ? kSfPerStage * kSfBytes * (1 + (fuse ? 0 : p.x_sf)) : (X ? p.x_rows : kSfRows) * 128;
       uint8_t *const base = smem + (SCALES ? p.sf_off + (X ? kSfPerStage * kSfBytes : 0) : X ? p.x_off : p.w_off);
       const uint32_t leader_full = PAIR ? leader_address(&full[0]) : 0;
       int s = 0, filled = 0;
-      uint32_t phase = 1;      // parity that a free slot's barrier shows: the first round passes at once
+      uint32_t phase = 1;      // of the wait for a free slot; the first round has none
       bool ok = true;
       for (int j = 0; ok && j < tiles; ++j) {
         const TileRec t = recs[j];
@@ -550,8 +605,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint8_t *src = (X ? p.x_scales : p.w_scales) + static_cast<int64_t>(block) * p.k_blocks * kSfBytes;
         const uint32_t bytes = SCALES ? blocks * kSfPerStage * kSfBytes : whole ? stage : boxes * p.x_box * 128;
         debug_check(blocks <= p.x_sf && (!X || SCALES || n * 128 <= static_cast<int>(bytes)), err);
-        for (int ks = 0; ks < k_stages; ++ks) {
-          if (!mbar_wait(&empty[s], phase, abort_flag, p.timeout_ns, err)) {
+        for (int ks = k_first; ks < k_end; ++ks) {
+          if (filled >= S && !mbar_wait(&empty[s], phase, abort_flag, p.timeout_ns, err)) {
             ok = false;
             break;
           }
@@ -607,10 +662,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // control flow and operands the same in all lanes, descriptors and
     // addresses live in uniform registers, as these instructions want them.
     const bool issuer = elect_one();
-    const uint32_t x_stage = p.x_rows * 128 >> 4, w_stage = w_rows * 128 >> 4;
+    const uint32_t x_stage = p.x_rows * 128 >> 4, w_stage = kSfRows * 128 >> 4;
     const uint32_t sf_stage = kSfPerStage * kSfBytes * (1 + (fuse ? 0 : p.x_sf)) >> 4;
     const uint64_t sfx0 = scales_desc(smem_u32(smem + p.fuse_sf_off));
-    const uint64_t wd_base = umma_desc_sw128(smem_u32(smem + p.w_off));
+    const uint64_t wd0 = umma_desc_sw128(smem_u32(smem + p.w_off));
     const uint64_t xd0 = umma_desc_sw128(smem_u32(smem + p.x_off));
     const uint64_t sfd0 = scales_desc(smem_u32(smem + p.sf_off));
     const int steps_all = ceil_div(p.K, 64);
@@ -625,17 +680,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int j = 0; ok && rank == 0 && j < tiles; ++j) {
       const int buf = j & 1;
       const int n = __shfl_sync(0xffffffffu, recs[j].n, 0), t0 = __shfl_sync(0xffffffffu, recs[j].t0, 0);
-      const int w0 = __shfl_sync(0xffffffffu, recs[j].w0, 0);
       ok = wait(&acc_empty[buf], ((j >> 1) & 1) ^ 1u);
       if (!ok) break;
       const uint32_t d = tmem + buf * kTileTokens;
       const uint32_t idesc = fp4_idesc<FMT, PAIR>(n);
       const uint32_t x_col = (t0 & 64) ? 2u : 0u;        // scale column of the tile's first token
       const int x_sf = ceil_div((t0 & (kSfRows - 1)) + n, kSfRows);
-      // the descriptor starts w0 mod 128 rows before the tile's first weight row
-      const uint64_t wd0 = wd_base - ((w0 & (kSfRows - 1)) * 128 >> 4);
-      int kb_left = p.k_blocks, steps_left = steps_all;
-      for (int ks = 0; ks < k_stages; ++ks) {
+      int kb_left = p.k_blocks - k_first * kSfPerStage, steps_left = steps_all - k_first * (kStageK / 64);
+      for (int ks = k_first; ks < k_end; ++ks) {
         ok = wait(&full[s], phase);
         if (!ok) break;
         tc_fence_after();
@@ -645,9 +697,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t sfx = fuse ? sfx0 + ks * kSfStep : sfw + kSfStep;
         if (issuer) {
           if (x_sf == 1)
-            issue_stage<FMT, 1, PAIR>(d, idesc, wd, xd, sf, sfw, sfx, x_col, kb_left, steps_left, ks == 0);
+            issue_stage<FMT, 1, PAIR>(d, idesc, wd, xd, sf, sfw, sfx, x_col, kb_left, steps_left, ks == k_first);
           else
-            issue_stage<FMT, 2, PAIR>(d, idesc, wd, xd, sf, sfw, sfx, x_col, kb_left, steps_left, ks == 0);
+            issue_stage<FMT, 2, PAIR>(d, idesc, wd, xd, sf, sfw, sfx, x_col, kb_left, steps_left, ks == k_first);
           commit_to<PAIR>(&empty[s]);
         }
         __syncwarp();
@@ -679,9 +731,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       griddep_launch_dependents();
       const int tid = (warp - kWarpEpi0) * 32 + lane;
       if (p.x_f16)
-        quantize_to_smem<ActF16, FMT>(p, smem + p.x_off, smem + p.fuse_sf_off, k_stages, tid, kEpiWarps * 32);
+        quantize_to_smem<ActF16, FMT>(p, smem + p.x_off, smem + p.fuse_sf_off, k_first, k_end, tid, kEpiWarps * 32);
       else
-        quantize_to_smem<ActBf16, FMT>(p, smem + p.x_off, smem + p.fuse_sf_off, k_stages, tid, kEpiWarps * 32);
+        quantize_to_smem<ActBf16, FMT>(p, smem + p.x_off, smem + p.fuse_sf_off, k_first, k_end, tid, kEpiWarps * 32);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&x_ready);
@@ -702,10 +754,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (fuse && group == 0 && gtid < 32) cols[gtid] = col;
       tc_fence_after();
       const uint32_t acc = tmem + buf * kTileTokens + (static_cast<uint32_t>(quarter) << 21);
-      const float alpha = p.x_scale * (p.w_scale ? __ldg(p.w_scale + t.e) : 1.0f);
-      const int lane0 = t.w0 & (kSfRows - 1);      // the tile's lanes: [lane0, lane0 + rt)
       const int row_in_block = quarter * 32 + lane;
-      const bool warp_mine = quarter * 32 < lane0 + w_rows && quarter * 32 + 32 > lane0;
+      // The tokens this CTA finishes.  A split tile: every CTA of the cluster lays its
+      // partial sums out in shared memory (the stages' space: all of its products
+      // are done), and adds all of them up, in rank order, for its share of the tokens.
+      int first = 0, count = t.valid;
+      float *part = reinterpret_cast<float *>(smem);
+      if constexpr (MODE == SPLIT) {
+        const int share = ceil_div(t.valid, split);
+        first = min(t.valid, k_rank * share);
+        count = min(t.valid, first + share) - first;
+        for (int c0 = group * 32; c0 < t.n; c0 += 32 * kEpiGroups) {
+          uint32_t r[2][16];
+          tmem_ld16(acc + c0, r[0]);
+          tmem_ld16(acc + c0 + 16, r[1]);
+          tmem_ld_wait();
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            if (c0 + c < t.n) part[(c0 + c) * kSfRows + row_in_block] = __uint_as_float(r[c >> 4][c & 15]);
+        }
+        __syncwarp();
+        if (lane < split) mbar_arrive_release_cluster(peer_address(&part_ready, lane));
+        ok = mbar_wait_cluster(&part_ready, j & 1, abort_flag, p.timeout_ns, err);
+        ok = bar_and_group(bar, ok);
+        if (!ok) break;
+      }
+      const float alpha = p.x_scale * (p.w_scale ? __ldg(p.w_scale + t.e) : 1.0f);
       bool released = false;
       auto release = [&] {
         tc_fence_before();
@@ -718,50 +792,60 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         released = true;
       };
-      for (int c0 = group * 32; c0 < t.valid; c0 += 32 * kEpiGroups) {
+      for (int c0 = group * 32; c0 < count; c0 += 32 * kEpiGroups) {
         uint32_t r[2][16];
-        if (warp_mine) {
+        if constexpr (MODE == SPLIT) {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) r[c >> 4][c & 15] = 0;
+          for (int q = 0; q < split; ++q) {
+            const uint32_t from = peer_address(part + row_in_block, q);
+            float v[32];
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+              const int i = first + c0 + c;
+              v[c] = c0 + c < count ? load_peer(from + (fuse ? cols[i] : i) * (kSfRows * 4)) : 0.0f;
+            }
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              r[c >> 4][c & 15] = __float_as_uint(__uint_as_float(r[c >> 4][c & 15]) + v[c]);
+          }
+        } else {
           tmem_ld16(acc + c0, r[0]);
           tmem_ld16(acc + c0 + 16, r[1]);
           tmem_ld_wait();
         }
-        if (c0 + 32 * kEpiGroups >= t.valid) release();     // the warp's last look at the accumulator
+        if (c0 + 32 * kEpiGroups >= count) release();     // the warp's last look at the accumulator
         if constexpr (!SWIGLU) {
           uint16_t *ex16 = reinterpret_cast<uint16_t *>(ex);
-          if (warp_mine) {
 #pragma unroll
-            for (int c = 0; c < 32; ++c)
-              ex16[c * kYPitch + row_in_block] = A::store(__uint_as_float(r[c >> 4][c & 15]) * alpha);
-          }
+          for (int c = 0; c < 32; ++c)
+            ex16[c * kYPitch + row_in_block] = A::store(__uint_as_float(r[c >> 4][c & 15]) * alpha);
           bar_sync_group(bar);
-          store_rows(ex16, static_cast<uint16_t *>(p.out) + static_cast<int64_t>(t.row + c0) * p.N,
-                     p.N, t.w0 & ~(kSfRows - 1), lane0, lane0 + w_rows, min(32, t.valid - c0), gtid, p.wide, fuse ? cols : nullptr);
+          store_rows(ex16, static_cast<uint16_t *>(p.out) + static_cast<int64_t>(t.row + first + c0) * p.N, p.N, t.w0,
+                     min(32, count - c0), gtid, p.wide, fuse && MODE != SPLIT ? cols : nullptr);
           bar_sync_group(bar);
         } else {
-          if (warp_mine) {
-            // lanes 0-15 hold gate rows, 16-31 the same features' up rows: a
-            // swap across the half warps gives the lower half the even
-            // tokens' pairs and the upper half the odd tokens'
-            const bool upper = lane >= 16;
-            float *dst = reinterpret_cast<float *>(ex) + (lane >> 4) * kHPitch + quarter * 16 + (lane & 15);
+          // lanes 0-15 hold gate rows, 16-31 the same features' up rows: a
+          // swap across the half warps gives the lower half the even
+          // tokens' pairs and the upper half the odd tokens'
+          const bool upper = lane >= 16;
+          float *dst = reinterpret_cast<float *>(ex) + (lane >> 4) * kHPitch + quarter * 16 + (lane & 15);
 #pragma unroll
-            for (int c = 0; c < 32; c += 2) {
-              const float a = __uint_as_float(r[c >> 4][c & 15]) * alpha;
-              const float b = __uint_as_float(r[c >> 4][(c & 15) + 1]) * alpha;
-              const float other = __shfl_xor_sync(0xffffffffu, upper ? a : b, 16);
-              const float g = upper ? other : a, u = upper ? b : other;
-              dst[c * kHPitch] = g * sigmoid_fast(g) * u;
-            }
+          for (int c = 0; c < 32; c += 2) {
+            const float a = __uint_as_float(r[c >> 4][c & 15]) * alpha;
+            const float b = __uint_as_float(r[c >> 4][(c & 15) + 1]) * alpha;
+            const float other = __shfl_xor_sync(0xffffffffu, upper ? a : b, 16);
+            const float g = upper ? other : a, u = upper ? b : other;
+            dst[c * kHPitch] = g * sigmoid_fast(g) * u;
           }
           bar_sync_group(bar);
           // one token's 16 features per thread: the four loads go in an order
           // that keeps the eight threads of a phase on different banks
           const int tok = gtid >> 2, fq = gtid & 3;
-          const int f0 = (t.w0 & ~(kSfRows - 1)) / 2 + fq * 16;      // first feature
+          const int f0 = t.w0 / 2 + fq * 16;      // first feature
           const int I = p.N / 2;
-          const bool in_tile = fq * 32 >= lane0 && fq * 32 < lane0 + w_rows;
-          const bool have = in_tile && c0 + tok < t.valid;
-          const float4 *src = reinterpret_cast<const float4 *>(reinterpret_cast<float *>(ex) + (fuse ? cols[tok] : tok) * kHPitch + fq * 16);
+          const bool have = c0 + tok < count;
+          const float4 *src = reinterpret_cast<const float4 *>(reinterpret_cast<float *>(ex) + (fuse && MODE != SPLIT ? cols[tok] : tok) * kHPitch + fq * 16);
           float4 v[4];
           uint32_t amax = 0;
           const int rot = (fq >> 1) + 2 * (tok & 1);
@@ -774,7 +858,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (FMT == FP4_MX) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
           float inv;
           uint32_t byte = fp4_scale_of<FMT>(amax, p.hq, inv);
-          const int tl = t.t0 + c0 + tok;       // token within the group
+          const int tl = t.t0 + first + c0 + tok;       // token within the group
           if (have) {
             const int64_t blk = t.x_block - t.t0 / kSfRows + tl / kSfRows;
             const int j = f0 / Fp4<FMT>::kBlock;
@@ -795,7 +879,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 codes |= static_cast<uint64_t>(c8 & 0xFFFFu) << (16 * ((i + rot) & 3));
                 codes |= static_cast<uint64_t>(c8 >> 16) << (16 * ((i + 1 + rot) & 3));
               }
-              *reinterpret_cast<uint64_t *>(p.h_codes + static_cast<int64_t>(t.row + c0 + tok) * (I / 2) + f0 / 2) = codes;
+              *reinterpret_cast<uint64_t *>(p.h_codes + static_cast<int64_t>(t.row + first + c0 + tok) * (I / 2) + f0 / 2) = codes;
             }
           }
           bar_sync_group(bar);
@@ -823,7 +907,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncthreads();
   }
-  if (PAIR) cluster_sync();      // nothing of the partner's reaches this CTA any more
+  if (MODE != LONE) cluster_sync();      // nothing of a partner's reaches this CTA any more
   tc_fence_after();
   if (warp == kWarpMma) tmem_free_all<PAIR>(tmem);
 }
@@ -861,8 +945,12 @@ bool encode_codes(CUtensorMap *map, const void *base, int64_t rows, int64_t K, i
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Tokens per group from which CTA pairs are taken.
-constexpr int kPairTokens = 64;
+// Tokens per group from which CTA pairs are taken (K = 2048, N = 2048, 16 groups: 128
+// tokens 13.9 us without and 14.6 with, 192 17.0 and 17.5, 320 26.3 both; 64 groups of
+// 512 110 and 104; 4096 x 4096 x 14336 111 and 105).
+constexpr int kPairTokens = 192;
+// Stages of K from which a tile is split.
+constexpr int kSplitStages = 24;
 
 constexpr int kSmemLimit = 227 * 1024 - 1024;   // less the static part
 
@@ -883,10 +971,11 @@ bool encode_scales(CUtensorMap *map, const void *base, int64_t row_blocks, int64
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <class A, int FMT, bool SWIGLU, bool PAIR>
+template <class A, int FMT, bool SWIGLU, int MODE>
 cudaError_t launch_gemm(const Fp4GemmArgs &a, GemmParams p, int num_sms, cudaStream_t stream, bool dependent) {
   constexpr int kSfPerStage = kStageK / Fp4<FMT>::kSfK;
-  auto *kernel = fp4_gemm_kernel<A, FMT, SWIGLU, PAIR>;
+  constexpr bool PAIR = MODE == PAIRED;
+  auto *kernel = fp4_gemm_kernel<A, FMT, SWIGLU, MODE>;
   static std::once_flag once[64];
   static cudaError_t attr[64];
   int dev = 0;
@@ -899,17 +988,14 @@ cudaError_t launch_gemm(const Fp4GemmArgs &a, GemmParams p, int num_sms, cudaStr
   if (attr[dev] != cudaSuccess) return attr[dev];
 
   // shared memory: x stages, weight stages, scale stages, exchange buffers,
-  // group table; around the weight stages at least the 128 - rt rows that an
-  // MMA reads beyond a short tile
-  const int w_rows = PAIR ? kSfRows : p.rt;
-  const int slack = (kSfRows - w_rows) * 128;
+  // tile records, group table
   const int ex = kEpiGroups * kExBytes;
   const int table = align_up(2 * (p.groups + 1) * 4, 16);
   // CTAs (pairs): one per SM (two SMs), no more than tiles can exist, and no more
   // tiles each than there are records
   const int64_t groups = p.groups < p.rows ? p.groups : p.rows;
   const int64_t most = (static_cast<int64_t>(p.rows) / p.bt + groups) * p.n_tiles;
-  int64_t slots = PAIR ? num_sms / 2 : num_sms;
+  int64_t slots = num_sms / (PAIR ? 2 : p.split);
   if (most < slots) slots = most;
   if (ceil_div64(most, slots) > kMaxRecs) slots = ceil_div64(most, kMaxRecs);
   if (slots > (1 << 30)) return cudaErrorInvalidValue;
@@ -917,29 +1003,27 @@ cudaError_t launch_gemm(const Fp4GemmArgs &a, GemmParams p, int num_sms, cudaStr
   const int recs = p.recs * static_cast<int>(sizeof(TileRec));
   const bool fuse = p.x != nullptr;
   const int k_stages = ceil_div(p.K, kStageK);
-  const int x_stage = fuse ? 0 : p.x_rows * 128, w_stage = w_rows * 128;
+  const int x_stage = fuse ? 0 : p.x_rows * 128, w_stage = kSfRows * 128;
   const int sf_stage = kSfPerStage * kSfBytes * (1 + (fuse ? 0 : p.x_sf));
   const int x_all = fuse ? k_stages * kFuseRows * 128 : 0, x_sf_all = fuse ? k_stages * kSfPerStage * kSfBytes : 0;
-  const int fixed = 1024 + 2 * slack + ex + recs + table + x_all + x_sf_all;
+  const int fixed = 1024 + ex + recs + table + x_all + x_sf_all;
   int S = (kSmemLimit - fixed) / (x_stage + w_stage + sf_stage);
   if (S > kMaxStages) S = kMaxStages;
   if (S < 2) return cudaErrorInvalidValue;
   p.stages = S;
   p.x_off = 0;
   const int x_bytes = x_all + S * x_stage;
-  p.w_off = align_up(x_bytes < slack ? slack : x_bytes, 1024);
+  p.w_off = align_up(x_bytes, 1024);
   p.sf_off = p.w_off + S * w_stage;
   p.fuse_sf_off = p.sf_off + S * sf_stage;
   p.ex_off = align_up(p.fuse_sf_off + x_sf_all, 128);
   p.rec_off = p.ex_off + ex;
   p.table_off = p.rec_off + recs;
-  int bytes = p.table_off + table;
-  if (bytes < p.sf_off + slack) bytes = p.sf_off + slack;
-  bytes += 1024;   // base alignment
+  const int bytes = p.table_off + table + 1024;   // and the base's alignment
   if (bytes > kSmemLimit) return cudaErrorInvalidValue;
 
   GemmMaps maps;
-  if (!encode_codes(&maps.w, a.w_codes, static_cast<int64_t>(p.groups) * p.N, p.K, w_rows)) return cudaErrorInvalidValue;
+  if (!encode_codes(&maps.w, a.w_codes, static_cast<int64_t>(p.groups) * p.N, p.K, kSfRows)) return cudaErrorInvalidValue;
   maps.x = maps.w;
   if (!fuse && !encode_codes(&maps.x, a.x_codes, p.rows, p.K, p.x_rows)) return cudaErrorInvalidValue;
   maps.xb = maps.x;
@@ -952,32 +1036,36 @@ cudaError_t launch_gemm(const Fp4GemmArgs &a, GemmParams p, int num_sms, cudaStr
         !encode_scales(&maps.sfx, a.x_scales, x_blocks, p.k_blocks, kSfPerStage, p.x_sf))
       return cudaErrorInvalidValue;
   }
-  const int grid = static_cast<int>(slots) * (PAIR ? 2 : 1);
-  return launch_clusters(kernel, dim3(static_cast<unsigned>(grid)), PAIR ? 2 : 1, kThreads, static_cast<size_t>(bytes),
+  const int unit = PAIR ? 2 : p.split;
+  const int grid = static_cast<int>(slots) * unit;
+  if (p.split > 1 && p.bt * kSfRows * 4 > p.ex_off) return cudaErrorInvalidValue;   // the partial sums' space
+  return launch_clusters(kernel, dim3(static_cast<unsigned>(grid)), unit, kThreads, static_cast<size_t>(bytes),
                          stream, dependent, p, maps);
 }
 
-template <bool PAIR>
+template <int MODE>
 cudaError_t dispatch_gemm(const Fp4GemmArgs &a, const GemmParams &p, int num_sms, cudaStream_t stream,
                           bool dependent) {
   const bool mx = a.fmt == FP4_MX;
   if (a.swiglu)
-    return mx ? launch_gemm<ActBf16, FP4_MX, true, PAIR>(a, p, num_sms, stream, dependent)
-              : launch_gemm<ActBf16, FP4_NV, true, PAIR>(a, p, num_sms, stream, dependent);
+    return mx ? launch_gemm<ActBf16, FP4_MX, true, MODE>(a, p, num_sms, stream, dependent)
+              : launch_gemm<ActBf16, FP4_NV, true, MODE>(a, p, num_sms, stream, dependent);
   if (a.act == ActF16::kId)
-    return mx ? launch_gemm<ActF16, FP4_MX, false, PAIR>(a, p, num_sms, stream, dependent)
-              : launch_gemm<ActF16, FP4_NV, false, PAIR>(a, p, num_sms, stream, dependent);
-  return mx ? launch_gemm<ActBf16, FP4_MX, false, PAIR>(a, p, num_sms, stream, dependent)
-            : launch_gemm<ActBf16, FP4_NV, false, PAIR>(a, p, num_sms, stream, dependent);
+    return mx ? launch_gemm<ActF16, FP4_MX, false, MODE>(a, p, num_sms, stream, dependent)
+              : launch_gemm<ActF16, FP4_NV, false, MODE>(a, p, num_sms, stream, dependent);
+  return mx ? launch_gemm<ActBf16, FP4_MX, false, MODE>(a, p, num_sms, stream, dependent)
+            : launch_gemm<ActBf16, FP4_NV, false, MODE>(a, p, num_sms, stream, dependent);
 }
 
 }  // namespace
 
-// Whether a CTA quantises `rows` rows of x itself: few rows, and their codes and scales
-// leave most of the shared memory to the weights' stages.  One launch instead of two.
+// Whether every CTA quantises `rows` rows of x itself: one launch instead of two, as
+// long as there is little of it (N = 8192: 1 x 2048 6.55 us against 6.94 with a launch
+// of its own, 4 x 2048 6.78 and 6.95, 8 x 2048 7.20 and 6.94) and its codes and scales
+// leave most of the shared memory to the weights' stages.
 bool fp4_gemm_quantizes(int64_t rows, int64_t K, int fmt) {
   const int64_t stages = (K + kStageK - 1) / kStageK;
-  return rows <= kFuseRows && stages * (kFuseRows * 128 + kStageK / (4 * fp4_block(fmt)) * kSfBytes) <= 96 * 1024;
+  return rows <= kFuseRows && rows * K <= kFuseElements && stages * (kFuseRows * 128 + kStageK / (4 * fp4_block(fmt)) * kSfBytes) <= 96 * 1024;
 }
 
 cudaError_t launch_fp4_gemm(const Fp4GemmArgs &a, int num_sms, uint64_t timeout_ns, cudaStream_t stream,
@@ -1029,28 +1117,29 @@ cudaError_t launch_fp4_gemm(const Fp4GemmArgs &a, int num_sms, uint64_t timeout_
     p.x_rows = p.bt / 2;
     p.x_box = p.x_rows < 32 ? p.x_rows : 32;
     p.x_rows = align_up(p.x_rows, p.x_box);
-    p.rt = 2 * kSfRows;
-    p.n_tiles = ceil_div(p.N, p.rt);
-    return dispatch_gemm<true>(a, p, num_sms, stream, dependent);
+    p.n_tiles = ceil_div(p.N, 2 * kSfRows);
+    p.split = 1;
+    return dispatch_gemm<PAIRED>(a, p, num_sms, stream, dependent);
   }
 
-  // Rows of a weight tile: the fewest rounds of the SMs, counted in rows plus a
-  // fixed cost per tile.
   p.x_box = p.bt < 64 ? p.bt : 64;
   p.x_rows = align_up(p.bt, p.x_box);
-  const int least = !a.swiglu ? 16 : a.fmt == FP4_MX ? 64 : 32;   // a hidden block's features within one tile
-  int64_t best = -1;
-  p.rt = kSfRows;
-  for (int rt = kSfRows; rt >= least; rt /= 2) {
-    const int64_t rounds = (tiles * ceil_div(p.N, rt) + num_sms - 1) / num_sms;
-    const int64_t cost = rounds * (rt + 16);
-    if (best < 0 || cost < best) {
-      best = cost;
-      p.rt = rt;
-    }
+  p.n_tiles = ceil_div(p.N, kSfRows);
+
+  // Few tiles and a long K: a cluster of 4 or 2 CTAs shares a tile's K.  A tile's time
+  // is 4.5 us and 0.28 us per stage of its chain, the cluster's barriers and the
+  // sum cost about 1.5 us, more with many tokens (N = 2048, M = 1: K = 8192 13.6 -> 10.6
+  // us with 4, K = 4096 9.2 -> 9.0, K = 2048 7.2 -> 8.2; M = 128, K = 8192: 14.6 us,
+  // with 2 13.7, with 4 14.9).  Clusters of 4 fill 128 of the SMs.
+  p.split = 1;
+  if (ceil_div(p.K, kStageK) >= kSplitStages) {
+    if (p.bt <= 64 && tiles * p.n_tiles * 4 <= num_sms * 27 / 32)
+      p.split = 4;
+    else if (tiles * p.n_tiles * 2 <= num_sms)
+      p.split = 2;
   }
-  p.n_tiles = ceil_div(p.N, p.rt);
-  return dispatch_gemm<false>(a, p, num_sms, stream, dependent);
+  return p.split > 1 ? dispatch_gemm<SPLIT>(a, p, num_sms, stream, dependent)
+                     : dispatch_gemm<LONE>(a, p, num_sms, stream, dependent);
 }
 
 void fp4_gemm_withhold_next() { g_withhold.store(1); }

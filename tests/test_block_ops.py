@@ -155,6 +155,16 @@ def test_linear_on_cta_pairs(dev, fmt, M, N, K):
 
 
 @formats
+@dtypes
+@pytest.mark.parametrize("M,N,K", [(1, 130, 5920), (1, 128, 7168), (2, 2048, 8192), (3, 1000, 6176), (16, 256, 9216),
+                                   (17, 700, 8224), (33, 513, 7200), (64, 128, 10240), (65, 200, 6400), (100, 2047, 6144),
+                                   (192, 1024, 6432), (200, 300, 8000), (1, 9000, 6240)])
+def test_linear_split_over_a_cluster(dev, fmt, dt, M, N, K):
+    """Few tiles and a long K: 2 or 4 CTAs share a tile, uneven parts among them."""
+    test_linear(dev, fmt, dt, M, N, K)
+
+
+@formats
 def test_linear_is_deterministic_and_flattens(dev, fmt):
     x = randn(1, 3, 5, 512)
     w, ws, wg, _ = weight(4, 1, 320, 512, fmt)
@@ -178,6 +188,12 @@ def test_linear_propagates_nonfinite_rows_only(dev, fmt):
     assert torch.isnan(z[7]).all()
     keep = torch.arange(40, device="cuda") != 7
     assert torch.equal(y[keep], z[keep])
+
+
+@formats
+@pytest.mark.parametrize("sizes", [[3], [0, 1, 0], [7, 2], [0, 40, 0, 9]], ids=str)
+def test_grouped_linear_split_over_a_cluster(dev, fmt, sizes):
+    test_grouped_linear(dev, fmt, sizes, 200, 6240)
 
 
 SIZES = [
@@ -317,7 +333,8 @@ def moe_reference(x, r, k, vals_gu, vals_d, fmt, dt, residual):
 @formats
 @dtypes
 @pytest.mark.parametrize("T,E,k,H,I", [(1, 4, 2, 64, 32), (1, 16, 8, 256, 128), (3, 2, 2, 96, 160), (5, 8, 1, 288, 96),
-                                       (16, 8, 3, 256, 64), (40, 3, 2, 128, 224)])
+                                       (16, 8, 3, 256, 64), (40, 3, 2, 128, 224), (1, 2, 1, 6176, 96),
+                                       (2, 3, 2, 96, 6240), (5, 2, 2, 6208, 64)])
 @pytest.mark.parametrize("with_residual", [False, True], ids=["plain", "residual"])
 def test_moe_mlp(dev, fmt, dt, T, E, k, H, I, with_residual):
     x = randn(T + H, T, H, dt=dt)
