@@ -42,7 +42,7 @@ __device__ unsigned int g_fp4_error;
 std::atomic<int> g_withhold{0};
 
 constexpr int kTileTokens = 192;
-constexpr int kMaxStages = 16;
+constexpr int kMaxStages = 16;               // (and at most 28: a lane initialises each)
 constexpr int kFuseRows = 16;                // rows of x that a CTA quantises itself, at most
 constexpr int64_t kFuseElements = 8192;      // and elements
 constexpr int kEpiGroups = 3;                // epilogue groups of four warps
@@ -485,27 +485,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     debug_poison_smem(smem, static_cast<uint32_t>(p.rec_off));
     __syncthreads();
   }
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < S; ++s) {
-      mbar_init(&full[s], fuse ? 2 : 4);      // the producers
-      mbar_init(&empty[s], 1);
+  if (warp == 0) {
+    // a lane per barrier pair
+    if (lane < S) {
+      mbar_init(&full[lane], fuse ? 2 : 4);      // the producers
+      mbar_init(&empty[lane], 1);
+    } else if (lane >= kMaxStages && lane < kMaxStages + 2) {
+      mbar_init(&acc_full[lane - kMaxStages], 1);
+      mbar_init(&acc_empty[lane - kMaxStages], PAIR ? 2 * kEpiWarps : kEpiWarps);
+    } else if (lane == kMaxStages + 2) {
+      mbar_init(&mma_done, 1);
+      mbar_init(&x_ready, kEpiWarps);
+      mbar_init(&part_ready, split * kEpiWarps);
+    } else if (lane == kMaxStages + 3) {
+      abort_word = 0;
+      for (int r = 0; r < 4; ++r) fills[r] = 0;
     }
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], PAIR ? 2 * kEpiWarps : kEpiWarps);
-    }
-    mbar_init(&mma_done, 1);
-    mbar_init(&x_ready, kEpiWarps);
-    mbar_init(&part_ready, split * kEpiWarps);
-    abort_word = 0;
-    for (int r = 0; r < 4; ++r) fills[r] = 0;
     fence_mbar_init();
-    prefetch_tensormap(&maps.w);
-    prefetch_tensormap(&maps.x);
-    prefetch_tensormap(&maps.xb);
-    if (PAIR) {
-      prefetch_tensormap(&maps.sfw);
-      prefetch_tensormap(&maps.sfx);
+    if (lane == 0) {
+      prefetch_tensormap(&maps.w);
+      prefetch_tensormap(&maps.x);
+      prefetch_tensormap(&maps.xb);
+      if (PAIR) {
+        prefetch_tensormap(&maps.sfw);
+        prefetch_tensormap(&maps.sfx);
+      }
     }
   }
   if (warp == kWarpMma) {
