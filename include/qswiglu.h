@@ -352,24 +352,24 @@ QSW_API qsw_status qsw_moe_route(const void *logits, int64_t T, int E, int k, in
 /*
  * The MLP of a mixture of experts, with the routing of qsw_moe_route:
  *     hidden = silu(Q(x) . Wg[e]^T) * (Q(x) . Wu[e]^T)          in f32
- *     y[t]   = T( residual[t] + sum_j weights[t, j] T(Q(hidden) . Wd[e]^T) )
+ *     y[t]   = T( residual[t] + sum_j weights[t, j] Q(hidden) . Wd[e]^T )
  * with x [T, H] quantised with the tensor scale x_scale and hidden with h_scale.
  * wgu is [E, 2 I, H/2] with gate and up rows in alternating runs of 16 (rows
  * 32 i .. 32 i + 15 are gate features 16 i .. 16 i + 15, the next 16 the same
  * features' up rows), wd [E, H, I/2]; gu_scale and d_scale [E] or NULL.  H and
  * I multiples of 32.  residual [T, H] or NULL; it may be y.  A token's experts
- * must be distinct, as qsw_moe_route's are.  Each expert's row is rounded to T
- * before the weighted sum, which is one f32 sum per token in the order of its
- * choices: the same bits every time.
+ * must be distinct, as qsw_moe_route's are.  The weighted sum is one f32 sum per
+ * token in the order of its choices: the same bits every time.  Where the
+ * experts' rows come to more than 8 MB in f32 (4 T k H bytes), each is rounded
+ * to T before that sum.
  */
 QSW_API size_t qsw_fp4_moe_workspace_bytes(int64_t T, int k, int64_t H, int64_t I, int E, int fmt);
 QSW_API qsw_status qsw_fp4_moe_mlp(const void *x, int64_t T, int64_t H, int64_t I, int E, int k, int fmt,
                            float x_scale, float h_scale, const int *ids, const float *weights,
                            const int *offsets, const int *slots, const int *order, const uint8_t *wgu,
                            const uint8_t *wgu_scales, const float *gu_scale, const uint8_t *wd,
-                           const uint8_t *wd_scales,
-                           const float *d_scale, const void *residual, int act_dtype, void *y,
-                           void *workspace, size_t workspace_bytes, void *stream);
+                           const uint8_t *wd_scales, const float *d_scale, const void *residual,
+                           int act_dtype, void *y, void *workspace, size_t workspace_bytes, void *stream);
 
 /* out = T( x * rsqrt(mean(x^2) + eps) * weight ), weight [H] or NULL (1).
  * Any H up to 32768; statistics in f32. */

@@ -81,6 +81,7 @@ struct GemmParams {
   int stages;
   int recs;                 // tiles per CTA at most
   bool wide;                // rows of the output start at 16-byte boundaries
+  bool out_f32;             // the output is f32
   int x_off, w_off, sf_off, fuse_sf_off, ex_off, rec_off, table_off;   // byte offsets in shared memory
   void *out;
   uint8_t *h_codes;
@@ -819,7 +820,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld_wait();
         }
         if (c0 + 32 * kEpiGroups >= count) release();     // the warp's last look at the accumulator
-        if constexpr (!SWIGLU) {
+        if (!SWIGLU && p.out_f32) {
+          // 32 lanes store 128 contiguous bytes: no need to turn the run around
+          const int n = t.w0 + row_in_block;
+          float *out = static_cast<float *>(p.out) + static_cast<int64_t>(t.row + first + c0) * p.N + n;
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            if (c0 + c < count && n < p.N) out[static_cast<int64_t>(c) * p.N] = __uint_as_float(r[c >> 4][c & 15]) * alpha;
+        } else if constexpr (!SWIGLU) {
           uint16_t *ex16 = reinterpret_cast<uint16_t *>(ex);
 #pragma unroll
           for (int c = 0; c < 32; ++c)
@@ -1091,6 +1099,7 @@ cudaError_t launch_fp4_gemm(const Fp4GemmArgs &a, int num_sms, uint64_t timeout_
   p.bt = p.max_group >= kTileTokens ? kTileTokens : align_up(p.max_group, 16);
   p.x_sf = p.max_group > 128 ? 2 : 1;
   p.out = a.out;
+  p.out_f32 = a.out_f32;
   p.wide = a.N % 8 == 0 && reinterpret_cast<uintptr_t>(a.out) % 16 == 0;
   p.h_codes = a.h_codes;
   p.h_scales = a.h_scales;

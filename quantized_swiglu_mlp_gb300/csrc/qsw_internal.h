@@ -118,7 +118,8 @@ struct Fp4GemmArgs {
   float x_scale;
   int fmt, act;
   bool swiglu;                         // N = 2 I interleaved gate and up rows, result held in 4 bits
-  void *out;                           // linear: [rows, N] in the activation dtype
+  void *out;                           // linear: [rows, N] in the activation dtype, or
+  bool out_f32;                        // f32 (then x comes in 4 bits)
   uint8_t *h_codes, *h_scales;         // swiglu: [rows, I], ragged scale blocks
   float h_scale;
 };
@@ -131,7 +132,7 @@ void fp4_gemm_withhold_next();   // test hook: the next product's waits run out
 cudaError_t launch_moe_route(const void *logits, int logit_dtype, int64_t T, int E, int k, int scoring,
                              int renormalize, float scale, int *ids, float *weights, int *offsets, int *slots,
                              int *order, cudaStream_t stream);
-cudaError_t launch_moe_combine(const void *rows, int64_t n_rows, const int *slots, const float *weights,
+cudaError_t launch_moe_combine(const void *rows, bool rows_f32, int64_t n_rows, const int *slots, const float *weights,
                                const void *residual, int64_t T, int k, int64_t H, int act, void *y,
                                cudaStream_t stream, bool dependent);
 

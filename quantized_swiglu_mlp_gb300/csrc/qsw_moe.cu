@@ -238,11 +238,28 @@ __global__ void __launch_bounds__(kSortThreads)
   }
 }
 
+// Eight columns of a row: f32, or pairs of an activation type.
+template <class A, bool F32>
+struct Eight {
+  uint4 v[F32 ? 2 : 1];
+  __device__ __forceinline__ void load(const void *rows, int64_t at) {
+    const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(rows) + at * (F32 ? 4 : 2));
+    v[0] = __ldg(p);
+    if (F32) v[F32 ? 1 : 0] = __ldg(p + 1);
+  }
+  __device__ __forceinline__ float value(int i) const {
+    const uint4 &q = v[F32 ? i >> 2 : 0];
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    if (F32) return __uint_as_float(w[i & 3]);
+    return (i & 1) ? A::hi(w[i >> 1]) : A::lo(w[i >> 1]);
+  }
+};
+
 // One warp per token and run of 256 columns; 8 columns per lane.  The rows of eight
 // choices are on their way before the first is added.
-template <class A>
+template <class A, bool F32>
 __global__ void __launch_bounds__(256)
-    combine_kernel(const uint16_t *__restrict__ rows, int64_t n_rows, const int *__restrict__ slots,
+    combine_kernel(const void *__restrict__ rows, int64_t n_rows, const int *__restrict__ slots,
                    const float *__restrict__ weights, const uint16_t *residual, int64_t T, int k, int64_t H,
                    int chunks, uint16_t *y) {
   griddep_wait();
@@ -273,24 +290,19 @@ __global__ void __launch_bounds__(256)
     }
   }
   for (int j0 = 0; j0 < k; j0 += AHEAD) {
-    uint4 v[AHEAD];
+    Eight<A, F32> v[AHEAD] = {};
 #pragma unroll
     for (int a = 0; a < AHEAD; ++a) {
       const int s = __shfl_sync(0xffffffffu, slot, (j0 + a) & 31);
-      v[a] = j0 + a < k && s >= 0 && in ? __ldg(reinterpret_cast<const uint4 *>(rows + static_cast<int64_t>(s) * H + h))
-                                        : make_uint4(0, 0, 0, 0);
+      if (j0 + a < k && s >= 0 && in) v[a].load(rows, static_cast<int64_t>(s) * H + h);
     }
 #pragma unroll
     for (int a = 0; a < AHEAD; ++a) {
       const float g = __shfl_sync(0xffffffffu, weight, (j0 + a) & 31);
       const int s = __shfl_sync(0xffffffffu, slot, (j0 + a) & 31);
       if (j0 + a >= k || s < 0) continue;
-      const uint32_t q[4] = {v[a].x, v[a].y, v[a].z, v[a].w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        acc[2 * i] = fmaf(g, A::lo(q[i]), acc[2 * i]);
-        acc[2 * i + 1] = fmaf(g, A::hi(q[i]), acc[2 * i + 1]);
-      }
+      for (int i = 0; i < 8; ++i) acc[i] = fmaf(g, v[a].value(i), acc[i]);
     }
   }
   if (in)
@@ -334,21 +346,21 @@ cudaError_t launch_moe_route(const void *logits, int logit_dtype, int64_t T, int
   return logit_dtype == QSW_ACT_BF16 ? launch_route_of<ActBf16>(p, stream) : launch_route_of<ActF16>(p, stream);
 }
 
-cudaError_t launch_moe_combine(const void *rows, int64_t n_rows, const int *slots, const float *weights,
+cudaError_t launch_moe_combine(const void *rows, bool rows_f32, int64_t n_rows, const int *slots, const float *weights,
                                const void *residual, int64_t T, int k, int64_t H, int act, void *y,
                                cudaStream_t stream, bool dependent) {
   const int chunks = static_cast<int>((H + 255) / 256);
   // few warps: one per CTA, on as many SMs
   const int threads = T * chunks < 1024 ? 32 : 256;
   const dim3 grid(static_cast<unsigned>((T * chunks * 32 + threads - 1) / threads));
-  const auto *r = static_cast<const uint16_t *>(rows);
   const auto *res = static_cast<const uint16_t *>(residual);
   auto *o = static_cast<uint16_t *>(y);
-  if (act == ActF16::kId)
-    return launch_on(combine_kernel<ActF16>, grid, threads, 0, stream, dependent, r, n_rows, slots, weights, res, T, k, H,
-                     chunks, o);
-  return launch_on(combine_kernel<ActBf16>, grid, threads, 0, stream, dependent, r, n_rows, slots, weights, res, T, k, H,
-                   chunks, o);
+#define QSW_COMBINE(A, F)                                                                                           \
+  launch_on(combine_kernel<A, F>, grid, threads, 0, stream, dependent, rows, n_rows, slots, weights, res, T, k, H, \
+            chunks, o)
+  if (act == ActF16::kId) return rows_f32 ? QSW_COMBINE(ActF16, true) : QSW_COMBINE(ActF16, false);
+  return rows_f32 ? QSW_COMBINE(ActBf16, true) : QSW_COMBINE(ActBf16, false);
+#undef QSW_COMBINE
 }
 
 }  // namespace qsw

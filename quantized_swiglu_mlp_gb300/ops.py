@@ -417,7 +417,7 @@ def _raise_status(fn: str, code: int) -> None:
     _check(fn, code)
 
 
-def _load_native():
+def load_native():
     """The C++ binding, bound to the loaded library.  Raises if it is missing."""
     global _native
     lib = load_library()
@@ -462,14 +462,14 @@ def fp4_quantize(x, fmt=FP4_NV, scale=1.0, stream=None) -> tuple[torch.Tensor, t
     codes uint8 [..., rows, K/2], scales uint8 [..., row blocks, scale blocks,
     512].  scale: the tensor's f32 scale (FP4_NV only).
     """
-    return _call((_native or _load_native()).fp4_quantize, stream, x, fmt, scale)
+    return _call((_native or load_native()).fp4_quantize, stream, x, fmt, scale)
 
 
 def fp4_dequantize(codes, scales, fmt=FP4_NV, scale=1.0, dtype=torch.bfloat16, out=None, stream=None) -> torch.Tensor:
     """The [rows, K] matrix (or stack) that codes and scales stand for, rounded to `dtype`."""
     if dtype not in _ACT:
         raise TypeError(f"dtype must be one of {tuple(_ACT)}")
-    return _call((_native or _load_native()).fp4_dequantize, stream, codes, scales, fmt, scale, _ACT[dtype], out)
+    return _call((_native or load_native()).fp4_dequantize, stream, codes, scales, fmt, scale, _ACT[dtype], out)
 
 
 def fp4_linear(x, w, w_scales, fmt=FP4_NV, x_scale=1.0, w_scale=None, out=None, stream=None) -> torch.Tensor:
@@ -478,7 +478,7 @@ def fp4_linear(x, w, w_scales, fmt=FP4_NV, x_scale=1.0, w_scale=None, out=None, 
     w uint8 [N, K/2] and w_scales as fp4_quantize returns them; x_scale: the
     f32 scale x is quantised with, w_scale: W's, one f32 on the device (None: 1).
     """
-    return _call((_native or _load_native()).fp4_linear, stream, x, w, w_scales, fmt, x_scale, w_scale, out)
+    return _call((_native or load_native()).fp4_linear, stream, x, w, w_scales, fmt, x_scale, w_scale, out)
 
 
 def fp4_grouped_linear(x, offsets, w, w_scales, fmt=FP4_NV, x_scale=1.0, w_scale=None, out=None,
@@ -488,7 +488,7 @@ def fp4_grouped_linear(x, offsets, w, w_scales, fmt=FP4_NV, x_scale=1.0, w_scale
     offsets int32 [groups + 1] on the device, from 0 to rows; w uint8 [groups,
     N, K/2] with a stack's scales, w_scale f32 [groups] or None.
     """
-    return _call((_native or _load_native()).fp4_grouped_linear, stream, x, offsets, w, w_scales, fmt, x_scale, w_scale,
+    return _call((_native or load_native()).fp4_grouped_linear, stream, x, offsets, w, w_scales, fmt, x_scale, w_scale,
                  out)
 
 
@@ -503,7 +503,7 @@ class MoeRoute(NamedTuple):
 
 def moe_route(logits, k, scoring=ROUTE_SOFTMAX, renormalize=True, scale=1.0, stream=None) -> MoeRoute:
     """The k largest of each row of logits [T, E] (f32, bf16 or f16), their weights and the expert-sorted order."""
-    return MoeRoute._make(_call((_native or _load_native()).moe_route, stream, logits, k, scoring, renormalize, scale))
+    return MoeRoute._make(_call((_native or load_native()).moe_route, stream, logits, k, scoring, renormalize, scale))
 
 
 def interleave_gate_up(gate, up) -> torch.Tensor:
@@ -526,13 +526,13 @@ def fp4_moe_mlp(x, route, wgu, wgu_scales, wd, wd_scales, fmt=FP4_NV, x_scale=1.
     x_scale, h_scale: the f32 scales that x and the hidden activations are
     quantised with.
     """
-    return _call((_native or _load_native()).fp4_moe_mlp, stream, x, *route, wgu, wgu_scales, wd, wd_scales, fmt,
+    return _call((_native or load_native()).fp4_moe_mlp, stream, x, *route, wgu, wgu_scales, wd, wd_scales, fmt,
                  x_scale, h_scale, gu_scale, d_scale, residual, out)
 
 
 def rms_norm(x, weight=None, eps=1e-6, out=None, stream=None) -> torch.Tensor:
     """T(x * rsqrt(mean(x^2) + eps) * weight) over the last dimension."""
-    return _call((_native or _load_native()).rms_norm, stream, x, weight, eps, out)
+    return _call((_native or load_native()).rms_norm, stream, x, weight, eps, out)
 
 
 def post_norm(h, y, weight=None, gate=None, scale=1.0, next_weight=None, eps=1e-6, norm=True, next_norm=True,
@@ -544,7 +544,7 @@ def post_norm(h, y, weight=None, gate=None, scale=1.0, next_weight=None, eps=1e-
     [gate_rows, H] or [gate_rows, 1] with gate_rows dividing the row count.
     `out` may be h, `next_out` may be y.
     """
-    return _call((_native or _load_native()).post_norm, stream, h, y, weight, gate, scale, next_weight, eps, norm,
+    return _call((_native or load_native()).post_norm, stream, h, y, weight, gate, scale, next_weight, eps, norm,
                  next_norm, out, next_out)
 
 

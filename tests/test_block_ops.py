@@ -469,6 +469,21 @@ def test_norm_of_zero_and_of_nonfinite_rows(dev):
     assert ops.rms_norm(x[:0]).shape == (0, 256)
 
 
+# ------------------------------------------------------------------ example --
+
+@pytest.mark.parametrize("tokens,hidden,inner,experts,k", [(1, 512, 256, 8, 2), (70, 256, 512, 6, 3)])
+def test_example_block(dev, tokens, hidden, inner, experts, k, capsys):
+    """The example's block is near the same block with unrounded activations: an
+    e2m1 value is within 1/6 of its block's scaled magnitude, errors of many
+    elements average out, so a quarter of the MLP's share (about half of the
+    residual stream's) bounds both outputs."""
+    from examples.expert_block import main
+    off = main(["--tokens", str(tokens), "--hidden", str(hidden), "--inner", str(inner), "--experts", str(experts),
+                "--top-k", str(k)])
+    assert off < 0.125
+    assert "tokens through the block" in capsys.readouterr().out
+
+
 # ----------------------------------------------- streams, graphs, refusals ---
 
 def test_on_another_stream(dev):
