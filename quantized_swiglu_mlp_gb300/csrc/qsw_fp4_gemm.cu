@@ -22,7 +22,16 @@
 // warp each, since a copy takes its issuer over 100 cycles), warp 1 moves the
 // scales into tensor memory and issues the MMAs, warps 2-13 run the epilogue.
 // Tensor memory: two accumulators of 192 columns, so that a tile's epilogue runs
-// under the next tile's products, and two scale buffers of 48 columns.
+// under the next tile's products, and two scale buffers of 48 columns.  A tile is
+// the work of one CTA, of a CTA pair (256 weight rows, many tokens) or of a
+// cluster that splits K (few tiles, long K); little x is quantised in the kernel.
+//
+// What bounds it (GB300): few rows, the weights' bytes -- 8 experts of 4096 x 16384
+// at 5.8 TB/s -- or, below about 30 MB, the launch and one tile's chain of stages
+// (1 x 2048 x 8192, 9.5 MB: 7.2 us, of which launch and set-up 2, stages 2.5).  Many
+// rows, the tensor pipe: 4096 x 4096 x 14336 takes 97 us, 5.0 PFLOP/s, and 12 scale
+// copies per 4 products (192 tokens) are a quarter of that: 85 us without an epilogue, 63
+// also without the scale copies, 54 with the loads alone.
 //
 // Programmatic dependent launch: everything a CTA does before griddep_wait --
 // the group table, the weights of its first stages -- reads only what was
@@ -296,8 +305,8 @@ __device__ __forceinline__ void umma_fp4(uint32_t d, uint64_t a, uint64_t b, uin
   if constexpr (FMT == FP4_MX && !PAIR)
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::
+            "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
         : "memory");
   else if constexpr (FMT == FP4_MX)
     asm volatile(
@@ -348,8 +357,8 @@ __device__ __forceinline__ void issue_stage(uint32_t d, uint32_t idesc, uint64_t
     const int kb = FMT == FP4_MX ? kk >> 1 : kk;
     // MX: an MMA takes two of a scale block's four scales
     const uint32_t sel = FMT == FP4_MX ? static_cast<uint32_t>(kk & 1) * 2u : 0u;
-    umma_fp4<FMT, PAIR>(d, wd + 2 * kk, xd + 2 * kk, idesc | (sel << 4) | (sel << 29), sf + kb * 4, sf + 16 + kb * 8 + x_col,
-                  first && kk == 0 ? 0u : 1u);
+    umma_fp4<FMT, PAIR>(d, wd + 2 * kk, xd + 2 * kk, idesc | (sel << 4) | (sel << 29), sf + kb * 4,
+                        sf + 16 + kb * 8 + x_col, first && kk == 0 ? 0u : 1u);
   }
 }
 
@@ -422,7 +431,10 @@ __device__ __forceinline__ void store_rows(const uint16_t *ex, uint16_t *out, in
     if (f >= hi) return;
     uint4 v[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const uint4 *>(ex + (cols ? cols[(tid >> 4) + 8 * i] : (tid >> 4) + 8 * i) * kYPitch + f);
+    for (int i = 0; i < 4; ++i) {
+      const int tok = (tid >> 4) + 8 * i;
+      v[i] = *reinterpret_cast<const uint4 *>(ex + (cols ? cols[tok] : tok) * kYPitch + f);
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int tok = (tid >> 4) + 8 * i;
@@ -591,14 +603,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ROLE == X_CODES) griddep_launch_dependents();
       const int stage = SCALES ? kSfPerStage * kSfBytes * (1 + (fuse ? 0 : p.x_sf)) : (X ? p.x_rows : kSfRows) * 128;
       uint8_t *const base = smem + (SCALES ? p.sf_off + (X ? kSfPerStage * kSfBytes : 0) : X ? p.x_off : p.w_off);
-      const uint32_t leader_full = PAIR ? leader_address(&full[0]) : 0;
+      [[maybe_unused]] const uint32_t leader_full = PAIR ? leader_address(&full[0]) : 0;
       int s = 0, filled = 0;
       uint32_t phase = 1;      // of the wait for a free slot; the first round has none
       bool ok = true;
       for (int j = 0; ok && j < tiles; ++j) {
         const TileRec t = recs[j];
         // codes of x: each CTA of a pair copies half of the tokens; one box of a
-        // stage's rows, or small boxes where they come to less
+        // stage's rows, or small boxes where they come to less (256 experts of
+        // 2048 x 2048, 20000 rows unevenly: 144.3 us with large boxes alone, 143.5)
         const int n = PAIR ? t.n / 2 : t.n;
         const bool whole = !X || n > p.x_rows - p.x_box;
         const int boxes = whole ? 1 : ceil_div(n, p.x_box);
@@ -607,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // scale row blocks: a pair's box always holds x_sf of x
         const int block = X ? t.x_block : t.w_block;
         const int blocks = !X ? 1 : PAIR ? p.x_sf : ceil_div((t.t0 & (kSfRows - 1)) + t.n, kSfRows);
-        const uint8_t *src = (X ? p.x_scales : p.w_scales) + static_cast<int64_t>(block) * p.k_blocks * kSfBytes;
+        [[maybe_unused]] const uint8_t *src = (X ? p.x_scales : p.w_scales) + static_cast<int64_t>(block) * p.k_blocks * kSfBytes;
         const uint32_t bytes = SCALES ? blocks * kSfPerStage * kSfBytes : whole ? stage : boxes * p.x_box * 128;
         debug_check(blocks <= p.x_sf && (!X || SCALES || n * 128 <= static_cast<int>(bytes)), err);
         for (int ks = k_first; ks < k_end; ++ks) {
@@ -826,7 +839,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           float *out = static_cast<float *>(p.out) + static_cast<int64_t>(t.row + first + c0) * p.N + n;
 #pragma unroll
           for (int c = 0; c < 32; ++c)
-            if (c0 + c < count && n < p.N) out[static_cast<int64_t>(c) * p.N] = __uint_as_float(r[c >> 4][c & 15]) * alpha;
+            if (c0 + c < count && n < p.N)
+              out[static_cast<int64_t>(c) * p.N] = __uint_as_float(r[c >> 4][c & 15]) * alpha;
         } else if constexpr (!SWIGLU) {
           uint16_t *ex16 = reinterpret_cast<uint16_t *>(ex);
 #pragma unroll
@@ -857,7 +871,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int f0 = t.w0 / 2 + fq * 16;      // first feature
           const int I = p.N / 2;
           const bool have = c0 + tok < count;
-          const float4 *src = reinterpret_cast<const float4 *>(reinterpret_cast<float *>(ex) + (fuse && MODE != SPLIT ? cols[tok] : tok) * kHPitch + fq * 16);
+          const float4 *src = reinterpret_cast<const float4 *>(
+              reinterpret_cast<float *>(ex) + (fuse && MODE != SPLIT ? cols[tok] : tok) * kHPitch + fq * 16);
           float4 v[4];
           uint32_t amax = 0;
           const int rot = (fq >> 1) + 2 * (tok & 1);
@@ -891,7 +906,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 codes |= static_cast<uint64_t>(c8 & 0xFFFFu) << (16 * ((i + rot) & 3));
                 codes |= static_cast<uint64_t>(c8 >> 16) << (16 * ((i + 1 + rot) & 3));
               }
-              *reinterpret_cast<uint64_t *>(p.h_codes + static_cast<int64_t>(t.row + first + c0 + tok) * (I / 2) + f0 / 2) = codes;
+              const int64_t at = static_cast<int64_t>(t.row + first + c0 + tok);
+              *reinterpret_cast<uint64_t *>(p.h_codes + at * (I / 2) + f0 / 2) = codes;
             }
           }
           bar_sync_group(bar);
@@ -1035,11 +1051,13 @@ cudaError_t launch_gemm(const Fp4GemmArgs &a, GemmParams p, int num_sms, cudaStr
   if (bytes > kSmemLimit) return cudaErrorInvalidValue;
 
   GemmMaps maps;
-  if (!encode_codes(&maps.w, a.w_codes, static_cast<int64_t>(p.groups) * p.N, p.K, kSfRows)) return cudaErrorInvalidValue;
+  if (!encode_codes(&maps.w, a.w_codes, static_cast<int64_t>(p.groups) * p.N, p.K, kSfRows))
+    return cudaErrorInvalidValue;
   maps.x = maps.w;
   if (!fuse && !encode_codes(&maps.x, a.x_codes, p.rows, p.K, p.x_rows)) return cudaErrorInvalidValue;
   maps.xb = maps.x;
-  if (!fuse && p.x_box != p.x_rows && !encode_codes(&maps.xb, a.x_codes, p.rows, p.K, p.x_box)) return cudaErrorInvalidValue;
+  if (!fuse && p.x_box != p.x_rows && !encode_codes(&maps.xb, a.x_codes, p.rows, p.K, p.x_box))
+    return cudaErrorInvalidValue;
   maps.sfw = maps.sfx = maps.x;
   if (PAIR) {
     const int64_t x_blocks = a.offsets ? ragged_row_block(p.rows, p.groups) : ceil_div(p.rows, kSfRows);
@@ -1077,7 +1095,8 @@ cudaError_t dispatch_gemm(const Fp4GemmArgs &a, const GemmParams &p, int num_sms
 // leave most of the shared memory to the weights' stages.
 bool fp4_gemm_quantizes(int64_t rows, int64_t K, int fmt) {
   const int64_t stages = (K + kStageK - 1) / kStageK;
-  return rows <= kFuseRows && rows * K <= kFuseElements && stages * (kFuseRows * 128 + kStageK / (4 * fp4_block(fmt)) * kSfBytes) <= 96 * 1024;
+  const int64_t bytes = stages * (kFuseRows * 128 + kStageK / (4 * fp4_block(fmt)) * kSfBytes);
+  return rows <= kFuseRows && rows * K <= kFuseElements && bytes <= 96 * 1024;
 }
 
 cudaError_t launch_fp4_gemm(const Fp4GemmArgs &a, int num_sms, uint64_t timeout_ns, cudaStream_t stream,

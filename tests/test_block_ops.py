@@ -251,7 +251,7 @@ def test_grouped_linear_clamps_offsets(dev):
 
 @pytest.mark.parametrize("dt", [torch.float32, BF16, F16], ids=["f32", "bf16", "f16"])
 @pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 8, 2), (3, 5, 5), (9, 32, 4), (64, 33, 8), (200, 64, 6), (513, 128, 8),
-                                   (77, 257, 32), (40, 600, 3), (31, 1024, 17), (5000, 16, 1)])
+                                   (77, 257, 32), (40, 600, 3), (31, 1024, 17), (5000, 16, 1), (4100, 64, 8), (17001, 9, 8)])
 @pytest.mark.parametrize("sigmoid,renormalize", [(False, True), (False, False), (True, True), (True, False)])
 def test_route(dev, dt, T, E, k, sigmoid, renormalize):
     logits = randn(T + E, T, E, dt=dt, std=2.0)     # 16-bit logits tie often
@@ -286,6 +286,23 @@ def test_route_masked_rows(dev):
             assert torch.equal(r.slots.long(), slots) and torch.equal(r.offsets.long(), offsets)
             check(r.weights, w, w * 104 * 2.0 ** -23 + 1e-37)
     assert not ops.moe_route(x, 5).weights[0].any()
+
+
+def test_route_ids_at_any_word(dev):
+    """The C entry takes ids at any 4-byte boundary."""
+    lib = ops.load_library()
+    T, E, k = 301, 20, 3
+    logits = randn(5, T, E, dt=torch.float32)
+    want = ops.moe_route(logits, k)
+    ids = torch.empty(T * k + 1, dtype=torch.int32, device="cuda")[1:]
+    w = torch.empty(T * k, device="cuda")
+    offsets, slots, order = (torch.empty(n, dtype=torch.int32, device="cuda") for n in (E + 1, T * k, T * k))
+    st = lib.qsw_moe_route(logits.data_ptr(), T, E, k, 2, ops.ROUTE_SOFTMAX, 1, 1.0, ids.data_ptr(), w.data_ptr(),
+                           offsets.data_ptr(), slots.data_ptr(), order.data_ptr(),
+                           torch.cuda.current_stream().cuda_stream)
+    assert st == 0
+    assert torch.equal(ids.view(T, k), want.ids) and torch.equal(offsets, want.offsets)
+    assert torch.equal(slots.view(T, k), want.slots.view(T, k)) and torch.equal(order, want.order)
 
 
 def test_route_without_tokens(dev):
