@@ -316,9 +316,10 @@ QSW_API qsw_status qsw_fp4_linear(const void *x, int64_t M, int64_t K, int64_t N
  * offsets[e] .. offsets[e+1] - 1 are multiplied with W[e] (codes [groups, N,
  * K/2], a stack's scale blocks, w_scale [groups] or NULL).  offsets is
  * [groups + 1] int32 on the device, not decreasing from 0 to rows; a group may
- * be empty.  Offsets outside that are clamped to it (nothing is read or written
- * out of range); rows that no group covers are left unwritten.  At most 1024
- * groups.
+ * be empty.  Any other table is taken as the nearest such one from below: an
+ * entry counts as no less than 0 or than any entry before it, and as no more
+ * than rows (nothing is read or written out of range, and no row belongs to two
+ * groups).  Rows that no group covers are left unwritten.  At most 1024 groups.
  */
 QSW_API qsw_status qsw_fp4_grouped_linear(const void *x, int64_t rows, int64_t K, int64_t N, int groups,
                            const int *offsets, int fmt, float x_scale, const uint8_t *w,
@@ -358,7 +359,9 @@ QSW_API qsw_status qsw_moe_route(const void *logits, int64_t T, int E, int k, in
  * 32 i .. 32 i + 15 are gate features 16 i .. 16 i + 15, the next 16 the same
  * features' up rows), wd [E, H, I/2]; gu_scale and d_scale [E] or NULL.  H and
  * I multiples of 32.  residual [T, H] or NULL; it may be y.  A token's experts
- * must be distinct, as qsw_moe_route's are.  The weighted sum is one f32 sum per
+ * must be distinct, as qsw_moe_route's are; with a routing that is not one of
+ * qsw_moe_route's the values are unspecified, but nothing is read or written out
+ * of range.  The weighted sum is one f32 sum per
  * token in the order of its choices: the same bits every time.  Where the
  * experts' rows come to more than 8 MB in f32 (4 T k H bytes), each is rounded
  * to T before that sum.

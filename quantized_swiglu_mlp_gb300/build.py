@@ -21,7 +21,7 @@ OUT_DIR = os.path.join(HERE, "lib")
 LIB_PATH = os.path.join(OUT_DIR, "libqswiglu.so")
 SOURCES = ["qsw_api.cu", "qsw_gemv.cu", "qsw_gemv_stream.cu", "qsw_prefill.cu", "qsw_elementwise.cu",
            "qsw_block_api.cu", "qsw_fp4.cu", "qsw_fp4_gemm.cu", "qsw_moe.cu", "qsw_norm.cu"]
-HEADERS = ["qsw_device.cuh", "qsw_smallm.cuh", "qsw_fp4.cuh", "qsw_internal.h"]
+HEADERS = ["qsw_device.cuh", "qsw_smallm.cuh", "qsw_fp4.cuh", "qsw_tiles.h", "qsw_internal.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

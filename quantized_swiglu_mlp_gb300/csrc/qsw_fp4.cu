@@ -9,6 +9,7 @@
 // crosses a lane.
 #include "qsw_fp4.cuh"
 #include "qsw_internal.h"
+#include "qsw_tiles.h"
 
 namespace qsw {
 namespace {
@@ -69,21 +70,38 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const QuantSour
   const int64_t block = blockIdx.x;
   int64_t dst;            // row of the result, -1: none
   if (RAGGED) {
-    // the group whose padded row blocks hold this one: one thread per group looks
-    __shared__ int found;
+    // the group whose padded row blocks hold this one: a thread looks at each.  Its
+    // rows are the product's (raised_offset), which in an ascending table are its own
+    // two entries'; a thread walks any other table from the start.  (With the walk as
+    // a scan in every CTA, for all tables: 8192 rows of 4096 in 32 groups 3 us longer.)
+    __shared__ int found, found_lo, found_hi;
     if (threadIdx.x == 0) found = -1;
     __syncthreads();
     const int rows = static_cast<int>(s.rows);
-    int lo, hi;
-    for (int e = threadIdx.x; e < s.groups; e += blockDim.x) {
-      ragged_range(s.offsets, e, rows, lo, hi);
+    auto look = [&](int e, int top) {
+      const int lo = raised_offset(__ldg(s.offsets + e), top, rows);
+      const int hi = raised_offset(__ldg(s.offsets + e + 1), lo, rows);
       const int64_t base = ragged_row_block(lo, e);
-      if (base <= block && block < base + (hi - lo + kSfRows - 1) / kSfRows) found = e;
+      if (base <= block && block < base + ceil_div(hi - lo, kSfRows)) {
+        found = e;
+        found_lo = lo;
+        found_hi = hi;
+      }
+      return lo;
+    };
+    bool backward = false;
+    for (int e = threadIdx.x; e < s.groups; e += blockDim.x)
+      backward |= raised_offset(__ldg(s.offsets + e + 1), 0, rows) < look(e, 0);
+    if (__syncthreads_or(backward)) {
+      if (threadIdx.x == 0) {
+        found = -1;
+        for (int e = 0, top = 0; e < s.groups; ++e) top = look(e, top);
+      }
+      __syncthreads();
     }
-    __syncthreads();
     const int e = found;
     if (e < 0) return;
-    ragged_range(s.offsets, e, rows, lo, hi);
+    const int lo = found_lo, hi = found_hi;
     dst = lo + (block - ragged_row_block(lo, e)) * kSfRows + row;
     if (dst >= hi) return;
   } else {

@@ -44,7 +44,8 @@ __host__ __device__ __forceinline__ int64_t ragged_row_block(int64_t off, int e)
   return (off + kSfRows - 1) / kSfRows + e;
 }
 
-// Rows [lo, hi) of group e, clamped so that no table leads outside the rows.
+// Rows [lo, hi) of group e of an ascending table, clamped so that no other one leads
+// outside the rows.
 __device__ __forceinline__ void ragged_range(const int *offsets, int e, int rows, int &lo, int &hi) {
   lo = min(max(__ldg(offsets + e), 0), rows);
   hi = min(max(__ldg(offsets + e + 1), lo), rows);

@@ -43,6 +43,7 @@
 
 #include "qsw_fp4.cuh"
 #include "qsw_internal.h"
+#include "qsw_tiles.h"
 
 namespace qsw {
 namespace {
@@ -120,16 +121,11 @@ struct alignas(16) TileRec {
   int x_block;  // scale row block of the first token's 128 rows
   int t0;       // first token within the group
 };
-constexpr int kMaxRecs = 256;     // per CTA; more tiles launch more CTAs
-
-__host__ __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
-
-// Token tiles of a group of m rows; more than one tile: equal sizes, multiples
-// of 64 (the scale lanes of a tile then start at column 0 or 2 of a block).
-__device__ __forceinline__ int token_tiles(int m, int bt) { return ceil_div(m, bt); }
 
 // Tile `id` (< the number of tiles): token tiles fastest, then weight tiles, then
-// groups.  off, first: first row and first tile of each group.
+// groups.  off, first: first row and first tile of each group.  More than one token
+// tile in a group: equal sizes, multiples of 64 (the scale lanes of a tile then start
+// at column 0 or 2 of a block).
 template <bool PAIR>
 __device__ __forceinline__ TileRec make_rec(const GemmParams &p, const int *off, const int *first, int id,
                                             uint32_t rank) {
@@ -530,18 +526,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc_all<PAIR>(&tmem_slot);
   }
   if (warp == kWarpEpi0) {
-    // group table: offsets (clamped, so that no table of the caller leads
-    // outside the buffers) and the first tile id of each group
+    // group table: the offsets as they are used (raised_offset: the records below
+    // hold the tiles of any table) and the first tile id of each group
     int *first = table + p.groups + 1;
     int total = 0;
+    bool backward = false;
     for (int e0 = 0; e0 < p.groups; e0 += 32) {
       const int e = e0 + lane;
       int lo = 0, hi = 0;
       if (e < p.groups) {
         hi = p.rows;
-        if (p.offsets) ragged_range(p.offsets, e, p.rows, lo, hi);
+        if (p.offsets) {
+          lo = raised_offset(__ldg(p.offsets + e), 0, p.rows);
+          hi = raised_offset(__ldg(p.offsets + e + 1), 0, p.rows);
+        }
       }
-      int tiles = token_tiles(min(hi - lo, p.max_group), p.bt) * p.n_tiles;
+      backward |= hi < lo;
+      const int tiles = token_tiles(min(hi - lo, p.max_group), p.bt) * p.n_tiles;
       int sum = tiles;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
@@ -558,11 +559,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       total += __shfl_sync(0xffffffffu, sum, 31);
     }
+    if (__any_sync(0xffffffffu, backward)) {
+      // not ascending: from the start, entry by entry.  (One token through 8 of 64 experts
+      // takes 19.5 us; with every table's entries raised in the loop above 19.8 to 20.0.)
+      __syncwarp();
+      if (lane == 0) {
+        total = 0;
+        for (int e = 0, top = 0; e < p.groups; ++e) {
+          top = raised_offset(__ldg(p.offsets + e), top, p.rows);
+          const int end = raised_offset(__ldg(p.offsets + e + 1), top, p.rows);
+          table[e] = top;
+          table[e + 1] = end;
+          first[e] = total;
+          total += token_tiles(min(end - top, p.max_group), p.bt) * p.n_tiles;
+        }
+        first[p.groups] = total;
+      }
+      total = __shfl_sync(0xffffffffu, total, 0);
+    }
     __syncwarp();
     // this CTA's tiles: every gridDim-th from its own index on
     const int start = static_cast<int>(blockIdx.x) / unit, step = static_cast<int>(gridDim.x) / unit;
-    const int count = total > start ? ceil_div(total - start, step) : 0;
-    debug_check(count <= p.recs, err);
+    const int count = min(tiles_of(total, start, step), p.recs);
+    debug_check(tiles_of(total, start, step) <= p.recs, err);
     for (int j = lane; j < count; j += 32) recs[j] = make_rec<PAIR>(p, table, first, start + j * step, rank);
     if (lane == 0) rec_count = count;
   }
@@ -982,7 +1001,6 @@ constexpr int kSplitStages = 24;
 
 constexpr int kSmemLimit = 227 * 1024 - 1024;   // less the static part
 
-int64_t ceil_div64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int align_up(int v, int a) { return (v + a - 1) / a * a; }
 
 // Scale blocks [row blocks, k blocks] of 512 bytes as 128 words each; a box is a
@@ -1021,13 +1039,9 @@ cudaError_t launch_gemm(const Fp4GemmArgs &a, GemmParams p, int num_sms, cudaStr
   const int table = align_up(2 * (p.groups + 1) * 4, 16);
   // CTAs (pairs): one per SM (two SMs), no more than tiles can exist, and no more
   // tiles each than there are records
-  const int64_t groups = p.groups < p.rows ? p.groups : p.rows;
-  const int64_t most = (static_cast<int64_t>(p.rows) / p.bt + groups) * p.n_tiles;
-  int64_t slots = num_sms / (PAIR ? 2 : p.split);
-  if (most < slots) slots = most;
-  if (ceil_div64(most, slots) > kMaxRecs) slots = ceil_div64(most, kMaxRecs);
-  if (slots > (1 << 30)) return cudaErrorInvalidValue;
-  p.recs = static_cast<int>(ceil_div64(most, slots));
+  const TilePlan plan = plan_tiles(most_tiles(p.rows, p.groups, p.bt, p.n_tiles), num_sms, PAIR ? 2 : p.split);
+  if (plan.slots > (1 << 30)) return cudaErrorInvalidValue;
+  p.recs = static_cast<int>(plan.recs);
   const int recs = p.recs * static_cast<int>(sizeof(TileRec));
   const bool fuse = p.x != nullptr;
   const int k_stages = ceil_div(p.K, kStageK);
@@ -1067,7 +1081,7 @@ cudaError_t launch_gemm(const Fp4GemmArgs &a, GemmParams p, int num_sms, cudaStr
       return cudaErrorInvalidValue;
   }
   const int unit = PAIR ? 2 : p.split;
-  const int grid = static_cast<int>(slots) * unit;
+  const int grid = static_cast<int>(plan.slots) * unit;
   if (p.split > 1 && p.bt * kSfRows * 4 > p.ex_off) return cudaErrorInvalidValue;   // the partial sums' space
   return launch_clusters(kernel, dim3(static_cast<unsigned>(grid)), unit, kThreads, static_cast<size_t>(bytes),
                          stream, dependent, p, maps);
@@ -1138,7 +1152,7 @@ cudaError_t launch_fp4_gemm(const Fp4GemmArgs &a, int num_sms, uint64_t timeout_
 
   // (group, token tile) pairs there can be at most
   const int64_t groups = p.groups < p.rows ? p.groups : p.rows;
-  const int64_t tiles = static_cast<int64_t>(p.rows) / p.bt + groups;
+  const int64_t tiles = most_tiles(p.rows, p.groups, p.bt, 1);
 
   // CTA pairs share a tile of 256 weight rows: each copies its own 128 rows and
   // half of the tokens, which leaves an SM a quarter less to copy per product.
