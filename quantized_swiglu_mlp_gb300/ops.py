@@ -435,17 +435,21 @@ def load_native():
     return _native
 
 
-def _on(stream):
-    """Context in which `stream` is the current one."""
-    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream)
-                             else torch.cuda.ExternalStream(int(stream)))
+def _on(stream, device):
+    """Context in which `stream` is the current one of `device`; a pointer is a stream of that device."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    elif stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
+    return torch.cuda.stream(stream)
 
 
-def _call(fn, stream, *args):
-    if stream is None:
-        return fn(*args)
-    with _on(stream):
-        return fn(*args)
+def _call(fn, stream, first, *args):
+    """fn(first, *args) on `stream`: it takes the current stream of its first tensor's device."""
+    if stream is None or not getattr(first, "is_cuda", False):      # without a CUDA tensor, fn refuses
+        return fn(first, *args)
+    with _on(stream, first.device):
+        return fn(first, *args)
 
 
 def fp4_scale_shape(rows: int, K: int, fmt: int) -> tuple[int, int, int]:
