@@ -361,10 +361,8 @@ QSW_API qsw_status qsw_moe_route(const void *logits, int64_t T, int E, int k, in
  * I multiples of 32.  residual [T, H] or NULL; it may be y.  A token's experts
  * must be distinct, as qsw_moe_route's are; with a routing that is not one of
  * qsw_moe_route's the values are unspecified, but nothing is read or written out
- * of range.  The weighted sum is one f32 sum per
- * token in the order of its choices: the same bits every time.  Where the
- * experts' rows come to more than 8 MB in f32 (4 T k H bytes), each is rounded
- * to T before that sum.
+ * of range.  The weighted sum is one f32 sum of f32 rows per token in the order
+ * of its choices, rounded once: the same bits every time.
  */
 QSW_API size_t qsw_fp4_moe_workspace_bytes(int64_t T, int k, int64_t H, int64_t I, int E, int fmt);
 QSW_API qsw_status qsw_fp4_moe_mlp(const void *x, int64_t T, int64_t H, int64_t I, int E, int k, int fmt,

@@ -96,15 +96,12 @@ qsw_status grouped_linear(const void *x, int64_t rows, int64_t K, int64_t N, int
   return st;
 }
 
-// The experts' rows stay f32 until the weighted sum where there are few; beyond,
-// they are rounded to T, which halves what the down projection writes and the sum
-// reads (64 experts, H = 2048, I = 1024, k = 8: 64 tokens 47.7 us with T, 48.2 with
-// f32; 512 tokens 55.7 and 61.2; 4096 tokens 163 and 212).
-constexpr int64_t kRowsF32Bytes = int64_t(8) << 20;
-
-// Byte offsets of the parts of the expert MLP's workspace.
+// Byte offsets of the parts of the expert MLP's workspace.  The experts' rows are f32
+// until the weighted sum, at every size: rounded to T they overflow in f16 where the
+// sum does not, and a token's result depends on how many others are in the batch.
+// (Rows of T would halve what the down projection writes and the sum reads: 4096 tokens
+// through 8 of 64 experts, H = 2048, I = 1024, take 217 us, with T 174.)
 struct MoeWorkspace {
-  bool rows_f32;
   size_t x_codes, x_scales, h_codes, h_scales, rows, total;
   MoeWorkspace(int64_t R, int64_t H, int64_t I, int E, int fmt) {
     x_codes = 0;
@@ -112,8 +109,7 @@ struct MoeWorkspace {
     h_codes = x_scales + up256(ragged_scale_bytes(R, E, H, fmt));
     h_scales = h_codes + up256(static_cast<size_t>(R * (I / 2)));
     rows = h_scales + up256(ragged_scale_bytes(R, E, I, fmt));
-    rows_f32 = R * H * 4 <= kRowsF32Bytes;
-    total = rows + up256(static_cast<size_t>(R * H * (rows_f32 ? 4 : 2)));
+    total = rows + up256(static_cast<size_t>(R * H * 4));
   }
 };
 
@@ -276,9 +272,10 @@ qsw_status qsw_fp4_moe_mlp(const void *x, int64_t T, int64_t H, int64_t I, int E
   a.x_scale = h_scale;
   a.swiglu = false;
   a.out = ws + at.rows;
-  a.out_f32 = at.rows_f32;
+  a.out_f32 = true;
   if ((e = qsw::launch_fp4_gemm(a, sms, timeout, s, true)) != cudaSuccess) return QSW_ERR_CUDA;
-  st = from_cuda(qsw::launch_moe_combine(ws + at.rows, at.rows_f32, R, slots, weights, residual, T, k, H, act_dtype, y, s, true));
+  st = from_cuda(qsw::launch_moe_combine(reinterpret_cast<const float *>(ws + at.rows), R, slots, weights, residual, T,
+                                         k, H, act_dtype, y, s, true));
   if (st == QSW_OK) qsw::count_call(QSW_CNT_FP4_MOE);
   return st;
 }

@@ -132,7 +132,7 @@ void fp4_gemm_withhold_next();   // test hook: the next product's waits run out
 cudaError_t launch_moe_route(const void *logits, int logit_dtype, int64_t T, int E, int k, int scoring,
                              int renormalize, float scale, int *ids, float *weights, int *offsets, int *slots,
                              int *order, cudaStream_t stream);
-cudaError_t launch_moe_combine(const void *rows, bool rows_f32, int64_t n_rows, const int *slots, const float *weights,
+cudaError_t launch_moe_combine(const float *rows, int64_t n_rows, const int *slots, const float *weights,
                                const void *residual, int64_t T, int k, int64_t H, int act, void *y,
                                cudaStream_t stream, bool dependent);
 
