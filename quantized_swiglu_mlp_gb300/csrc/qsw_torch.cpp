@@ -346,6 +346,8 @@ PyObject *post_norm(Args a) {
     if (g.dim() != 1 && g.dim() != 2) fail(PyExc_ValueError, "%s must be [H], [gate_rows, H] or [gate_rows, 1]", "gate");
     gate_rows = g.dim() == 1 ? 1 : g.size(0);
     gate_cols = g.size(-1);
+    // (its pointer would be null, which is no gate)
+    if (rows > 0 && g.numel() == 0) fail(PyExc_ValueError, "%s must not be empty", "gate");
     gate = data(g);
   }
   const bool norm = truth(a[7]), next_norm = truth(a[8]);
