@@ -304,7 +304,8 @@ QSW_API qsw_status qsw_fp4_dequantize(const uint8_t *codes, const uint8_t *scale
  * blocks, w_scale a device pointer to its f32 tensor scale (NULL: 1).  K a
  * multiple of 32; x, w, w_scales 16-byte aligned, workspace 256-byte aligned
  * with at least qsw_fp4_workspace_bytes(M, K, 1, fmt) bytes.  The workspace
- * need not be cleared; calls that can run concurrently must not share it.
+ * need not be cleared; calls that can run concurrently must not share it.  y may
+ * lie over x.
  */
 QSW_API size_t qsw_fp4_workspace_bytes(int64_t rows, int64_t K, int groups, int fmt);
 QSW_API qsw_status qsw_fp4_linear(const void *x, int64_t M, int64_t K, int64_t N, int fmt, float x_scale,

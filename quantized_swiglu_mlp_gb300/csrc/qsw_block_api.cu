@@ -19,6 +19,12 @@ bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 qsw_status from_cuda(cudaError_t e) { return e == cudaSuccess ? QSW_OK : QSW_ERR_CUDA; }
 size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 
+// Whether [a, a + n) and [b, b + m) have a byte in common.
+bool overlap(const void *a, int64_t n, const void *b, int64_t m) {
+  const auto p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
+  return p < q + static_cast<uintptr_t>(m) && q < p + static_cast<uintptr_t>(n);
+}
+
 bool act_ok(int act) { return act == QSW_ACT_BF16 || act == QSW_ACT_F16; }
 
 // Format and tensor scale: the E8M0 format has no tensor scale.
@@ -64,7 +70,9 @@ qsw_status grouped_linear(const void *x, int64_t rows, int64_t K, int64_t N, int
   if (workspace_bytes < qsw_fp4_workspace_bytes(rows, K, groups, fmt)) return QSW_ERR_INVALID_ARG;
   const int sms = qsw::device_sm_count();
   qsw::Fp4GemmArgs a = {};
-  const bool fuse = qsw::fp4_gemm_quantizes(rows, K, fmt);
+  // Every CTA of the form without a quantiser reads x for itself, while others may be
+  // writing y already: not where y lies over x.
+  const bool fuse = qsw::fp4_gemm_quantizes(rows, K, fmt) && !overlap(x, rows * K * 2, y, rows * N * 2);
   if (fuse) {
     a.x = x;
     a.x_tokens = rows;
