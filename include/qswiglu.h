@@ -339,7 +339,7 @@ typedef enum {
  * equals; NaN counts as -infinity) and their weights, largest logit first.
  * renormalize: the chosen weights are divided by their sum; then all are
  * multiplied by `scale`.  A row without any logit above -infinity gets the
- * weights 0.
+ * weights 0; the sigmoid of logits up to -700 counts as 0.
  *   ids      int32 [T, k]  experts        weights  f32 [T, k]
  *   offsets  int32 [E + 1] first row of each expert in the expert-sorted order
  *   slots    int32 [T, k]  row of (token, choice) in that order

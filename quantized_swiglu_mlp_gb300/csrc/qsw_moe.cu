@@ -14,6 +14,7 @@ namespace qsw {
 namespace {
 
 constexpr int kTopkWarps = 8;
+constexpr float kNoScore = -700.0f;   // logits up to this one have the sigmoid 0: masks of any type's lowest value
 
 template <class L>
 __device__ __forceinline__ float load_logit(const L *p);
@@ -81,6 +82,9 @@ __device__ __forceinline__ int topk_row(const RouteParams &p, int64_t t) {
 #pragma unroll
     for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
   }
+  // sigmoid scores that are only looked at for their ratios, all below 1/2: e^-peak
+  // times as large, so that none that counts is lost below f32's range
+  const float far = renormalize && peak < 0.0f ? peak : 0.0f;
   // round j's choice stays with lane j
   float mine = 0.0f;
   int id = 0;
@@ -100,7 +104,7 @@ __device__ __forceinline__ int topk_row(const RouteParams &p, int64_t t) {
     const float v = key_value(best);
     float p;
     if (scoring == QSW_ROUTE_SIGMOID)
-      p = 1.0f / (1.0f + expf(-v));
+      p = v > 0.0f ? 1.0f / (1.0f + expf(-v)) : v > kNoScore ? expf(v - far) / (1.0f + expf(v)) : 0.0f;
     else
       p = none ? 0.0f : v == peak ? 1.0f : expf(v - peak);
     if (lane == j) {
