@@ -268,8 +268,8 @@ QSW_API qsw_status qsw_silu_mul(const void *g, const void *u, int64_t n, int var
  * nibble, and one scale per block of consecutive elements of a row.
  *   QSW_FP4_MX  blocks of 32, scale 2^(floor(log2 amax) - 2) held as E8M0
  *   QSW_FP4_NV  blocks of 16, scale E4M3(amax / (6 g)) times g, one positive
- *               f32 g for the whole tensor (the `scale` arguments below; they
- *               must be 1 for QSW_FP4_MX)
+ *               f32 g for the whole tensor (the `scale` arguments below; 1 / (6 g)
+ *               must be within f32's range, and g 1 for QSW_FP4_MX)
  * A code is the e2m1 value nearest to x / scale, ties to even, saturating at 6.
  * A block that holds an infinity or a NaN gets the scale NaN.
  *

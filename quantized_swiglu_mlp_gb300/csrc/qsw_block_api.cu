@@ -1,6 +1,7 @@
 // C entry points of the operators around the MLP block: microscaled 4-bit
 // quantisation and products, products grouped by expert, routing and norms
 // (include/qswiglu.h).  Arguments are checked before anything is enqueued.
+#include <cfloat>
 #include <cmath>
 
 #include "qsw_fp4.cuh"
@@ -27,10 +28,12 @@ bool overlap(const void *a, int64_t n, const void *b, int64_t m) {
 
 bool act_ok(int act) { return act == QSW_ACT_BF16 || act == QSW_ACT_F16; }
 
-// Format and tensor scale: the E8M0 format has no tensor scale.
+// Format and tensor scale: the E8M0 format has no tensor scale, the other's needs a
+// reciprocal within f32 (make_fp4_scale; a block of zeros would become NaN).
 qsw_status check_format(int fmt, float g) {
   if (fmt != QSW_FP4_MX && fmt != QSW_FP4_NV) return QSW_ERR_INVALID_ARG;
   if (!(g > 0.0f) || !std::isfinite(g)) return QSW_ERR_INVALID_ARG;
+  if (1.0 / (6.0 * static_cast<double>(g)) > static_cast<double>(FLT_MAX)) return QSW_ERR_INVALID_ARG;
   if (fmt == QSW_FP4_MX && g != 1.0f) return QSW_ERR_INVALID_ARG;
   return QSW_OK;
 }
