@@ -271,6 +271,7 @@ cudaError_t launch_quant(const QuantSource &s, const Fp4Scale &q, int64_t row_bl
 template <bool RAGGED>
 cudaError_t dispatch_quant(const QuantSource &s, int fmt, int act, float g, int64_t row_blocks,
                            int num_sms, cudaStream_t stream) {
+  if (num_sms <= 0) return cudaErrorInvalidDevice;
   const Fp4Scale q = make_fp4_scale(g);
   if (act == ActBf16::kId)
     return fmt == FP4_MX ? launch_quant<ActBf16, FP4_MX, RAGGED>(s, q, row_blocks, num_sms, stream)
@@ -341,6 +342,7 @@ cudaError_t launch_fp4_quantize_fan(const void *x, int64_t T, int64_t K, int k, 
 
 cudaError_t launch_fp4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t groups, int64_t rows,
                                   int64_t K, int fmt, int act, float g, void *out, int num_sms, cudaStream_t cs) {
+  if (num_sms <= 0) return cudaErrorInvalidDevice;
   const bool stream = groups * rows * K * 2 > kStreamBytes;
   const int64_t kb = fp4_k_blocks(K, fmt), row_blocks = groups * ((rows + kSfRows - 1) / kSfRows);
   const int run = quant_run(row_blocks, kb, num_sms);

@@ -3,8 +3,11 @@ accepts, on the CPU."""
 from __future__ import annotations
 
 import pytest
+import torch
 
 from tests.test_abi_cpu import BIG, FAKE, INVALID, MX, NV, OK, lib  # noqa: F401
+
+CUDA = 3
 
 
 @pytest.mark.parametrize("scale,code", [(1e-45, INVALID), (1e-40, INVALID), (4.8e-40, INVALID), (5e-40, OK), (1e-30, OK),
@@ -18,3 +21,21 @@ def test_tensor_scales_without_a_reciprocal(lib, scale, code):  # noqa: F811
     for x_scale, h_scale in ((scale, 1.0), (1.0, scale)):
         assert lib.qsw_fp4_moe_mlp(FAKE, rows, 64, 64, 8, 2, NV, x_scale, h_scale, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE,
                                    FAKE, None, FAKE, FAKE, None, None, 0, FAKE, FAKE, BIG, None) == code
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the arguments are valid: with a device these would be launched")
+def test_without_a_device(lib):  # noqa: F811
+    """Valid calls on a machine without a GPU return an error."""
+    rest = (FAKE, FAKE, None, 0, FAKE, FAKE, BIG, None)
+    for fmt in (MX, NV):
+        assert lib.qsw_fp4_quantize(FAKE, 1, 4, 64, fmt, 1.0, 0, FAKE, FAKE, None) == CUDA
+        assert lib.qsw_fp4_dequantize(FAKE, FAKE, 1, 4, 64, fmt, 1.0, 0, FAKE, None) == CUDA
+        for rows in (1, 1000):
+            assert lib.qsw_fp4_linear(FAKE, rows, 64, 32, fmt, 1.0, *rest) == CUDA
+            assert lib.qsw_fp4_grouped_linear(FAKE, rows, 64, 32, 3, FAKE, fmt, 1.0, *rest) == CUDA
+            assert lib.qsw_fp4_moe_mlp(FAKE, rows, 64, 64, 8, 2, fmt, 1.0, 1.0, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE,
+                                       None, FAKE, FAKE, None, None, 0, FAKE, FAKE, BIG, None) == CUDA
+    for T in (0, 1, 1000):
+        assert lib.qsw_moe_route(FAKE, T, 8, 2, 2, 0, 1, 1.0, FAKE, FAKE, FAKE, FAKE, FAKE, None) == CUDA
+    assert lib.qsw_rms_norm(FAKE, None, 4, 64, 1e-6, 0, FAKE, None) == CUDA
+    assert lib.qsw_post_norm(FAKE, FAKE, 1, None, None, 0, 0, 1.0, None, 4, 64, 1e-6, 0, FAKE, None, None) == CUDA
