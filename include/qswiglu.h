@@ -303,7 +303,8 @@ QSW_API qsw_status qsw_fp4_dequantize(const uint8_t *codes, const uint8_t *scale
  * block-scaled tensor core with f32 accumulation.  W: codes [N, K/2] and scale
  * blocks, w_scale a device pointer to its f32 tensor scale (NULL: 1).  K a
  * multiple of 32; x, w, w_scales 16-byte aligned, workspace 256-byte aligned
- * with at least qsw_fp4_workspace_bytes(M, K, 1, fmt) bytes.  The workspace
+ * with at least qsw_fp4_workspace_bytes(M, K, 1, fmt) bytes (0: no call accepts
+ * such arguments, as for all sizes of these operators).  The workspace
  * need not be cleared; calls that can run concurrently must not share it.  y may
  * lie over x.
  */

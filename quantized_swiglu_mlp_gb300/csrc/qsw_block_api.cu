@@ -130,6 +130,7 @@ extern "C" {
 
 size_t qsw_fp4_scale_bytes(int64_t groups, int64_t rows, int64_t K, int fmt) {
   if (groups < 0 || rows < 0 || check_format(fmt, 1.0f) != QSW_OK || check_k(K) != QSW_OK) return 0;
+  if (groups == 0 || rows > kMaxRows || groups > kMaxRows / (rows > 0 ? rows : 1)) return 0;
   return scale_bytes(groups * ((rows + qsw::kSfRows - 1) / qsw::kSfRows), K, fmt);
 }
 
@@ -167,6 +168,7 @@ qsw_status qsw_fp4_dequantize(const uint8_t *codes, const uint8_t *scales, int64
 
 size_t qsw_fp4_workspace_bytes(int64_t rows, int64_t K, int groups, int fmt) {
   if (rows < 0 || groups <= 0 || check_format(fmt, 1.0f) != QSW_OK || check_k(K) != QSW_OK) return 0;
+  if (rows > kMaxRows || groups > kMaxGroups) return 0;
   return up256(static_cast<size_t>(rows * (K / 2))) + up256(ragged_scale_bytes(rows, groups, K, fmt));
 }
 
@@ -208,6 +210,7 @@ qsw_status qsw_moe_route(const void *logits, int64_t T, int E, int k, int logit_
 size_t qsw_fp4_moe_workspace_bytes(int64_t T, int k, int64_t H, int64_t I, int E, int fmt) {
   if (T < 0 || k <= 0 || E <= 0 || check_format(fmt, 1.0f) != QSW_OK || check_k(H) != QSW_OK || check_k(I) != QSW_OK)
     return 0;
+  if (k > E || E > kMaxGroups || k > kMaxTopK || T > kMaxRows / k) return 0;
   return MoeWorkspace(T * k, H, I, E, fmt).total;
 }
 

@@ -39,3 +39,18 @@ def test_without_a_device(lib):  # noqa: F811
         assert lib.qsw_moe_route(FAKE, T, 8, 2, 2, 0, 1, 1.0, FAKE, FAKE, FAKE, FAKE, FAKE, None) == CUDA
     assert lib.qsw_rms_norm(FAKE, None, 4, 64, 1e-6, 0, FAKE, None) == CUDA
     assert lib.qsw_post_norm(FAKE, FAKE, 1, None, None, 0, 0, 1.0, None, 4, 64, 1e-6, 0, FAKE, None, None) == CUDA
+
+
+def test_sizes_that_no_call_accepts(lib):  # noqa: F811
+    """0, as documented, not a product that passed 64 bits."""
+    top, more = 1 << 30, (1 << 30) + 1
+    assert lib.qsw_fp4_scale_bytes(1, top, 32, MX) == top // 128 * 512
+    assert lib.qsw_fp4_scale_bytes(1, more, 32, MX) == lib.qsw_fp4_scale_bytes(more, 1, 32, MX) == 0
+    assert lib.qsw_fp4_scale_bytes(1 << 62, 1 << 62, 64, NV) == lib.qsw_fp4_scale_bytes(3, 1 << 62, 64, NV) == 0
+    assert lib.qsw_fp4_scale_bytes(0, 1 << 62, 64, NV) == lib.qsw_fp4_scale_bytes(1 << 62, 0, 64, NV) == 0
+    assert lib.qsw_fp4_workspace_bytes(top, 32, 1024, NV) == top * 16 + (top // 128 + 1024) * 512
+    assert lib.qsw_fp4_workspace_bytes(more, 32, 1, NV) == lib.qsw_fp4_workspace_bytes(1 << 62, 64, 3, NV) == 0
+    assert lib.qsw_fp4_workspace_bytes(4, 64, 1025, NV) == 0
+    assert lib.qsw_fp4_moe_workspace_bytes(4, 2, 64, 64, 8, NV) > 0
+    for T, k, E in ((1 << 62, 2, 8), ((1 << 29) + 1, 2, 8), (4, 33, 64), (4, 2, 1025), (4, 9, 8)):
+        assert lib.qsw_fp4_moe_workspace_bytes(T, k, 64, 64, E, NV) == 0
