@@ -6,6 +6,7 @@ Each translation unit compiles in parallel; the shared libraries land in
 """
 from __future__ import annotations
 
+import importlib.metadata
 import importlib.util
 import os
 import shutil
@@ -87,11 +88,20 @@ def _stale(lib: str) -> bool:
 # The binding of the block operators: a CPython module over torch's C++ headers.
 NATIVE_SOURCE = os.path.join(CSRC, "qsw_torch.cpp")
 NATIVE_PATH = os.path.join(OUT_DIR, "_qsw_torch.so")
+NATIVE_STAMP = NATIVE_PATH + ".built_for"
+
+
+def _native_target() -> str:
+    """What the binding is built for: another torch or Python needs another one."""
+    return f"torch {importlib.metadata.version('torch')}, {sys.implementation.cache_tag}"
 
 
 def _native_stale() -> bool:
-    if not os.path.exists(NATIVE_PATH):
+    if not os.path.exists(NATIVE_PATH) or not os.path.exists(NATIVE_STAMP):
         return True
+    with open(NATIVE_STAMP) as f:
+        if f.read() != _native_target():
+            return True
     t = os.path.getmtime(NATIVE_PATH)
     return any(os.path.getmtime(d) > t for d in (NATIVE_SOURCE, os.path.join(ROOT, "include", "qswiglu.h")))
 
@@ -111,6 +121,8 @@ def _build_native() -> None:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on qsw_torch.cpp:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, NATIVE_PATH)
+    with open(NATIVE_STAMP, "w") as f:
+        f.write(_native_target())
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
