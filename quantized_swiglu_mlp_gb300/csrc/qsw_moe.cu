@@ -169,9 +169,10 @@ constexpr int kSortThreads = 1024;
 // the pairs.  The ballots of up to 32 groups stay in registers of the lane of that
 // number (n <= 131072); longer runs are read a second time.  Ids outside [0, E) are
 // ignored (their slot is -1).  Bound by the latency of the loads, so 8 of 16 bytes are
-// in flight.  `wide`: ids starts at a 16-byte boundary.
+// in flight.  `wide`: ids starts at a 16-byte boundary.  The ids are not read through
+// the read-only path: the kernel that writes them may still run when this one starts.
 __global__ void __launch_bounds__(kSortThreads)
-    sort_kernel(const int *__restrict__ ids, int n, int E, bool wide, int *offsets, int *slots, int *order) {
+    sort_kernel(const int *ids, int n, int E, bool wide, int *offsets, int *slots, int *order) {
   griddep_wait();
   griddep_launch_dependents();
   __shared__ int warp_eq[32], warp_lt[32];
@@ -181,10 +182,10 @@ __global__ void __launch_bounds__(kSortThreads)
   const int g0 = min(warp * per, groups), g1 = min(g0 + per, groups);
   auto load = [&](int g) {
     const int i = g * 128 + lane * 4;
-    if (wide && g < g1 && i + 4 <= n) return __ldg(reinterpret_cast<const int4 *>(ids + i));
+    if (wide && g < g1 && i + 4 <= n) return *reinterpret_cast<const int4 *>(ids + i);
     int v[4];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) v[c] = g < g1 && i + c < n ? __ldg(ids + i + c) : E;   // neither equal nor below
+    for (int c = 0; c < 4; ++c) v[c] = g < g1 && i + c < n ? ids[i + c] : E;   // neither equal nor below
     return make_int4(v[0], v[1], v[2], v[3]);
   };
   constexpr int AHEAD = 8;      // loads in flight: a ballot waits for its own

@@ -30,3 +30,31 @@ def test_sigmoid_of_far_logits(dev, dt, mean, renormalize):  # noqa: F811
     if renormalize:
         rest = torch.arange(T, device="cuda") > 5
         assert (r.weights[rest].sum(1) - 1).abs().max() < 1e-5
+
+
+def test_routings_one_after_another(dev):  # noqa: F811
+    """Many routings in a row over the same memory, choices and sort overlapping: each reads its own ids."""
+    T, E, k = 3000, 24, 4
+    logits = [randn(s, T, E, dt=torch.float32) for s in range(3)]
+    want = [ref.route(v, k) for v in logits]
+    x, got = torch.empty_like(logits[0]), []
+
+    def round_trip():
+        for v in logits:
+            x.copy_(v)
+            r = ops.moe_route(x, k)
+            got.append([t.clone() for t in (r.ids, r.offsets, r.slots, r.order)])
+            del r        # the next routing takes the same memory
+    round_trip()
+    got.clear()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(5):
+            round_trip()
+    for _ in range(4):
+        graph.replay()
+        torch.cuda.synchronize()
+        for i, parts in enumerate(got):
+            ids, _, offsets, slots, order = want[i % 3]
+            for a, b in zip(parts, (ids, offsets, slots, order)):
+                assert torch.equal(a.long(), b)
