@@ -992,9 +992,15 @@ bool encode_codes(CUtensorMap *map, const void *base, int64_t rows, int64_t K, i
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Tokens per group from which CTA pairs are taken (K = 2048, N = 2048, 16 groups: 128
-// tokens 13.9 us without and 14.6 with, 192 17.0 and 17.5, 320 26.3 both; 64 groups of
-// 512 110 and 104; 4096 x 4096 x 14336 111 and 105).
+// Tokens per group from which CTA pairs are taken.  Where the weights pass L2 pairs gain
+// from there on, where they stay in it only from about 320 (us on pairs / on single CTAs,
+// at 128, 192, 256, 320, 512 tokens per group; NV):
+//   32 x 2048 x 4096    47.1/47.1  53.5/54.1  63.0/65.5  72.5/75.1  96.8/102.5
+//   64 x 2048 x 2048    47.7/46.9  54.3/54.6  67.4/69.4  77.2/80.1  102.9/108.7
+//    8 x 4096 x 7168    35.8/35.9  41.4/41.8  52.0/54.7  58.4/61.1  77.7/81.9
+//   16 x 2048 x 2048    14.6/13.9  17.4/17.0  22.0/21.9  26.2/26.2  34.9/35.9
+//    1 x 14336 x 4096   12.0/11.0  12.8/12.2  16.4/16.1  18.1/18.1  22.8/23.1
+//    1 x 10240 x 2560    9.5/9.0   10.5/10.0  12.4/12.1  13.8/13.4  14.6/14.5
 constexpr int kPairTokens = 192;
 // Stages of K from which a tile is split.
 constexpr int kSplitStages = 24;
