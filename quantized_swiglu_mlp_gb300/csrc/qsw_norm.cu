@@ -92,7 +92,11 @@ __device__ __forceinline__ float block_sum(float v, float *buf) {
 template <class A, int VEC, int EPT>
 __global__ void __launch_bounds__(1024) norm_kernel(const NormParams p) {
   constexpr int RUNS = EPT / VEC;
-  constexpr bool kAhead = EPT <= 16;      // more does not fit in 64 registers
+  // The next row and the weights in registers, where 64 hold them or spill little: 16 elements
+  // spill up to 100 bytes a thread and still gain over many rows (2048 rows, bf16: H = 16384 58.8 us,
+  // without 63.1; 12288 49.7 and 52.4; 8200 44.7 and 42.5), but not as single values, a
+  // register each (H = 12001: 329 us and 928 bytes, without 114).
+  constexpr bool kAhead = EPT <= 8 || (EPT <= 16 && VEC > 1);
   __shared__ float sums[4][32];
   griddep_wait();
   griddep_launch_dependents();

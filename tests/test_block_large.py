@@ -143,7 +143,7 @@ def norm_case(rows, H, dt, gates):
 
 @dtypes
 @pytest.mark.parametrize("rows,H,gates", [(1000, 4096, 4), (2600, 512, 1), (5000, 100, 5000), (700, 8200, 7), (400, 8191, 2),
-                                          (320, 16390, 4), (310, 20001, 1), (8192, 4096, 4)])
+                                          (320, 16390, 4), (310, 20001, 1), (330, 10002, 2), (330, 12001, 1), (8192, 4096, 4)])
 def test_norms_over_many_rows(dev, dt, rows, H, gates):  # noqa: F811
     """Several rows per CTA, of each width; the last with streaming accesses.  In place the same bits."""
     h, y, w, wn, gate = norm_case(rows, H, dt, gates)
