@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(kSortThreads)
 }
 
 // Eight columns of an expert's row.  Read once, so evicted first (4096 tokens of 2048, k = 8:
-// the expert MLP 224.5 us with ordinary loads, 216.6).  Not through the read-only path: the
+// the expert MLP took 224.5 us with ordinary loads, 216.6 so).  Not through the read-only path: the
 // products that write the rows may still run when this kernel starts.
 struct Eight {
   float4 v[2];
@@ -284,20 +284,18 @@ struct Eight {
   }
 };
 
-// One warp per token and run of 256 columns; 8 columns per lane.  The rows of eight
-// choices are on their way before the first is added.
+// One warp, a CTA, per token and run of 256 columns; 8 columns per lane.  The rows of
+// eight choices are on their way before the first is added.
 template <class A>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(32)
     combine_kernel(const float *rows, int64_t n_rows, const int *__restrict__ slots, const float *__restrict__ weights,
-                   const uint16_t *residual, int64_t T, int k, int64_t H, int chunks, uint16_t *y) {
+                   const uint16_t *residual, int k, int64_t H, int chunks, uint16_t *y) {
   griddep_wait();
   griddep_launch_dependents();
   constexpr int AHEAD = 8;
-  const int lane = threadIdx.x & 31;
-  const int64_t w = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-  const int64_t t = w / chunks;
-  const int64_t h = (w - t * chunks) * 256 + lane * 8;
-  if (t >= T) return;
+  const int lane = threadIdx.x;
+  const int64_t t = blockIdx.x / chunks;
+  const int64_t h = (blockIdx.x - t * chunks) * 256 + lane * 8;
   // lane j holds choice j
   int slot = -1;
   float weight = 0.0f;
@@ -381,14 +379,14 @@ cudaError_t launch_moe_combine(const float *rows, int64_t n_rows, const int *slo
                                const void *residual, int64_t T, int k, int64_t H, int act, void *y,
                                cudaStream_t stream, bool dependent) {
   const int chunks = static_cast<int>((H + 255) / 256);
-  // few warps: one per CTA, on as many SMs (the expert MLP of 64 tokens, 64 experts of
-  // 2048 x 1024: 48.2 us with CTAs of a warp, 49.5 with 8; of 1024 tokens 66.4 and 65.1)
-  const int threads = T * chunks < 1024 ? 32 : 256;
-  const dim3 grid(static_cast<unsigned>((T * chunks * 32 + threads - 1) / threads));
+  // CTAs of a warp, on as many SMs as there are (the expert MLP of 64 tokens, 8 of 64 experts
+  // of 2048 x 1024: 46.7 us, with CTAs of 8 warps 47.8; of 1024 tokens 75.3 and 77.6, of 16384
+  // 706 and 738)
+  const dim3 grid(static_cast<unsigned>(T * chunks));
   const auto *res = static_cast<const uint16_t *>(residual);
   auto *o = static_cast<uint16_t *>(y);
-  return launch_on(act == ActF16::kId ? combine_kernel<ActF16> : combine_kernel<ActBf16>, grid, threads, 0, stream,
-                   dependent, rows, n_rows, slots, weights, res, T, k, H, chunks, o);
+  return launch_on(act == ActF16::kId ? combine_kernel<ActF16> : combine_kernel<ActBf16>, grid, 32, 0, stream,
+                   dependent, rows, n_rows, slots, weights, res, k, H, chunks, o);
 }
 
 }  // namespace qsw
