@@ -462,6 +462,30 @@ struct GemmMaps {
   CUtensorMap w, x, xb, sfw, sfx;
 };
 
+// The group table of offsets that go backwards, entry by entry, by one lane of a warp;
+// returns the number of tiles.  (A function of its own, not unrolled: inline it cost
+// ascending tables 0.2 to 0.4 us, and so did raising every table's entries in the loop
+// that fills it; one token through 8 of 64 experts takes 19.0 us.)
+__device__ __noinline__ int raise_table(const int *offsets, int groups, int rows, int max_group, int bt, int n_tiles,
+                                        int *table) {
+  int *first = table + groups + 1;
+  int total = 0;
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) {
+#pragma unroll 1
+    for (int e = 0, top = 0; e < groups; ++e) {
+      top = raised_offset(__ldg(offsets + e), top, rows);
+      const int end = raised_offset(__ldg(offsets + e + 1), top, rows);
+      table[e] = top;
+      table[e + 1] = end;
+      first[e] = total;
+      total += token_tiles(min(end - top, max_group), bt) * n_tiles;
+    }
+    first[groups] = total;
+  }
+  return __shfl_sync(0xffffffffu, total, 0);
+}
+
 // How a tile's work is shared: one CTA, a cluster that splits K, a CTA pair.  (A
 // template: the code of the others in a lone CTA's kernel cost a 1 x 2048 x 8192 product
 // half a microsecond.)
@@ -559,24 +583,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       total += __shfl_sync(0xffffffffu, sum, 31);
     }
-    if (__any_sync(0xffffffffu, backward)) {
-      // not ascending: from the start, entry by entry.  (One token through 8 of 64 experts
-      // takes 19.5 us; with every table's entries raised in the loop above 19.8 to 20.0.)
-      __syncwarp();
-      if (lane == 0) {
-        total = 0;
-        for (int e = 0, top = 0; e < p.groups; ++e) {
-          top = raised_offset(__ldg(p.offsets + e), top, p.rows);
-          const int end = raised_offset(__ldg(p.offsets + e + 1), top, p.rows);
-          table[e] = top;
-          table[e + 1] = end;
-          first[e] = total;
-          total += token_tiles(min(end - top, p.max_group), p.bt) * p.n_tiles;
-        }
-        first[p.groups] = total;
-      }
-      total = __shfl_sync(0xffffffffu, total, 0);
-    }
+    if (__any_sync(0xffffffffu, backward))
+      total = raise_table(p.offsets, p.groups, p.rows, p.max_group, p.bt, p.n_tiles, table);
     __syncwarp();
     // this CTA's tiles: every gridDim-th from its own index on
     const int start = static_cast<int>(blockIdx.x) / unit, step = static_cast<int>(gridDim.x) / unit;
