@@ -259,7 +259,8 @@ QSW_API qsw_status qsw_silu_mul(const void *g, const void *u, int64_t n, int var
  * Operators around the MLP block: microscaled 4-bit floating point, products
  * grouped by expert, routing, norms.  Inference only, like the rest of the
  * library (the weights are codes).  Same ownership, execution and error rules
- * as above.
+ * as above.  An output must not overlap an input or another output except where
+ * it is said that it may.
  * ------------------------------------------------------------------------ */
 
 /*
@@ -300,13 +301,13 @@ QSW_API qsw_status qsw_fp4_dequantize(const uint8_t *codes, const uint8_t *scale
 /*
  * y[M, N] = T( Q(x) . W^T ): x [M, K] is quantised to the weights' format (with
  * the tensor scale x_scale) into the workspace, then multiplied on the
- * block-scaled tensor core with f32 accumulation.  W: codes [N, K/2] and scale
- * blocks, w_scale a device pointer to its f32 tensor scale (NULL: 1).  K a
- * multiple of 32; x, w, w_scales 16-byte aligned, workspace 256-byte aligned
- * with at least qsw_fp4_workspace_bytes(M, K, 1, fmt) bytes (0: no call accepts
- * such arguments, as for all sizes of these operators).  The workspace
- * need not be cleared; calls that can run concurrently must not share it.  y may
- * lie over x.
+ * block-scaled tensor core with f32 accumulation, in an order that depends on
+ * the sizes alone.  W: codes [N, K/2] and scale blocks, w_scale a device pointer
+ * to its f32 tensor scale (NULL: 1).  K a multiple of 32; x, w, w_scales 16-byte
+ * aligned, workspace 256-byte aligned with at least qsw_fp4_workspace_bytes(M,
+ * K, 1, fmt) bytes (0: no call accepts such arguments, as for all sizes of these
+ * operators).  The workspace need not be cleared; calls that can run
+ * concurrently must not share it.  y may lie over x.
  */
 QSW_API size_t qsw_fp4_workspace_bytes(int64_t rows, int64_t K, int groups, int fmt);
 QSW_API qsw_status qsw_fp4_linear(const void *x, int64_t M, int64_t K, int64_t N, int fmt, float x_scale,
@@ -364,7 +365,9 @@ QSW_API qsw_status qsw_moe_route(const void *logits, int64_t T, int E, int k, in
  * must be distinct, as qsw_moe_route's are; with a routing that is not one of
  * qsw_moe_route's the values are unspecified, but nothing is read or written out
  * of range.  The weighted sum is one f32 sum of f32 rows per token in the order
- * of its choices, rounded once: the same bits every time.
+ * of its choices, rounded once: the same bits every time.  (Among how many
+ * others a token stands matters to them only where H or I passes 5888: the
+ * products of few tokens may then add up K in parts.)
  */
 QSW_API size_t qsw_fp4_moe_workspace_bytes(int64_t T, int k, int64_t H, int64_t I, int E, int fmt);
 QSW_API qsw_status qsw_fp4_moe_mlp(const void *x, int64_t T, int64_t H, int64_t I, int E, int k, int fmt,
@@ -375,7 +378,7 @@ QSW_API qsw_status qsw_fp4_moe_mlp(const void *x, int64_t T, int64_t H, int64_t 
                            int act_dtype, void *y, void *workspace, size_t workspace_bytes, void *stream);
 
 /* out = T( x * rsqrt(mean(x^2) + eps) * weight ), weight [H] or NULL (1).
- * Any H up to 32768; statistics in f32. */
+ * Any H up to 32768; statistics in f32.  out may be x. */
 QSW_API qsw_status qsw_rms_norm(const void *x, const void *weight, int64_t rows, int64_t H, float eps,
                            int act_dtype, void *out, void *stream);
 

@@ -354,6 +354,6 @@ const char *qsw_status_string(qsw_status s) {
   }
 }
 
-int qsw_version(void) { return 106; }
+int qsw_version(void) { return 107; }
 
 }  // extern "C"

@@ -408,7 +408,8 @@ def unfused_swiglu(x, wg, sg, bg, gs_g, bits_g, wu, su, bu, gs_u, bits_u, varian
 # The calls go through a small C++ binding (csrc/qsw_torch.cpp), which checks the
 # tensors, allocates and calls the C entry points of the library loaded here:
 # with the checks in Python and ctypes the host took longer than the device.
-# Results and scratch memory belong to the stream of the call.
+# Results and scratch memory belong to the stream of the call: `stream`, a torch stream
+# of the tensors' device or the pointer of one, or the current stream.
 
 _native = None
 
@@ -481,6 +482,7 @@ def fp4_linear(x, w, w_scales, fmt=FP4_NV, x_scale=1.0, w_scale=None, out=None, 
 
     w uint8 [N, K/2] and w_scales as fp4_quantize returns them; x_scale: the
     f32 scale x is quantised with, w_scale: W's, one f32 on the device (None: 1).
+    `out` may lie over x.
     """
     return _call((_native or load_native()).fp4_linear, stream, x, w, w_scales, fmt, x_scale, w_scale, out)
 
@@ -489,8 +491,9 @@ def fp4_grouped_linear(x, offsets, w, w_scales, fmt=FP4_NV, x_scale=1.0, w_scale
                        stream=None) -> torch.Tensor:
     """y[r] = T(Q(x[r]) . W[e]^T) for the rows offsets[e] <= r < offsets[e+1]; returns [rows, N].
 
-    offsets int32 [groups + 1] on the device, from 0 to rows; w uint8 [groups,
-    N, K/2] with a stack's scales, w_scale f32 [groups] or None.
+    offsets int32 [groups + 1] on the device, ascending from 0 to rows (an entry
+    below one before it counts as that one); w uint8 [groups, N, K/2] with a
+    stack's scales, w_scale f32 [groups] or None.
     """
     return _call((_native or load_native()).fp4_grouped_linear, stream, x, offsets, w, w_scales, fmt, x_scale, w_scale,
                  out)
