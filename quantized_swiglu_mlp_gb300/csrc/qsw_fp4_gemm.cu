@@ -28,7 +28,7 @@
 //
 // What bounds it (GB300): few rows, the weights' bytes -- 8 experts of 4096 x 16384
 // at 5.8 TB/s -- or, below about 30 MB, the launch and one tile's chain of stages
-// (1 x 2048 x 8192, 9.5 MB: 7.2 us, of which launch and set-up 2, stages 2.5).  Many
+// (1 x 2048 x 8192, 9.5 MB: 7.4 us, of which launch and set-up 2, stages 2.5).  Many
 // rows, the tensor pipe: 4096 x 4096 x 14336 takes 97 us, 5.0 PFLOP/s, and 12 scale
 // copies per 4 products (192 tokens) are a quarter of that: 85 us without an epilogue, 63
 // also without the scale copies, 54 with the loads alone.
