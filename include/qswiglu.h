@@ -96,7 +96,11 @@ enum {
     QSW_CNT_MOE_ROUTE = 9,
     QSW_CNT_FP4_MOE = 10,     /* qsw_fp4_moe_mlp */
     QSW_CNT_NORM = 11,        /* qsw_rms_norm and qsw_post_norm */
-    QSW_NUM_COUNTERS = 12
+    QSW_CNT_ROPE = 12,
+    QSW_CNT_KV_APPEND = 13,
+    QSW_CNT_PAGED_PLAN = 14,
+    QSW_CNT_PAGED_ATTENTION = 15,
+    QSW_NUM_COUNTERS = 16
 };
 
 /*
@@ -395,6 +399,100 @@ QSW_API qsw_status qsw_rms_norm(const void *x, const void *weight, int64_t rows,
 QSW_API qsw_status qsw_post_norm(const void *h, const void *y, int norm_y, const void *w_post, const void *gate,
                            int64_t gate_rows, int64_t gate_cols, float scale, const void *w_next, int64_t rows,
                            int64_t H, float eps, int act_dtype, void *h_out, void *n_out, void *stream);
+
+/* ------------------------------------------------------------------------
+ * The attention half of a decoder block: rotary positions, a paged cache of
+ * keys and values, attention of new tokens over it.  Inference only.  Same
+ * ownership, execution and error rules as above.
+ * ------------------------------------------------------------------------ */
+
+/* Heads of tokens: [T, heads, D] in the activation dtype, elements of a head
+ * contiguous; strides in elements. */
+typedef struct {
+    const void *data;
+    int64_t token_stride, head_stride;
+} qsw_heads;
+
+/* A paged cache: k and v [pages, kv_heads, page_size, D] in the activation dtype,
+ * elements of a row contiguous, strides (page, head, row) in elements.  Token p of a
+ * sequence is row p % page_size of page page_table[sequence][p / page_size].
+ * page_size a multiple of 8, D a multiple of 8 from 8 to 128; pages * page_size
+ * below 2^31.  k, v and all strides are multiples of 16 bytes. */
+typedef struct {
+    void *k, *v;
+    int64_t pages, kv_heads, page_size;
+    int64_t k_strides[3], v_strides[3];
+} qsw_kv_cache;
+
+/*
+ * Rotary positions: out[t, h] = x[t, h] with the pairs of its first `rot` elements
+ * turned by the angle positions[t] * f_i and multiplied by `scale`; the others are
+ * copied.  Pairs are (i, i + rot / 2), or (2 i, 2 i + 1) with `interleaved`.
+ * table[i] (int64 [rot / 2] on the device) is f_i in turns per position times 2^64,
+ * modulo 2^64: positions (int32, of either sign; NULL: all 0) of any size keep their
+ * angle to 2^-24.  rot is even, from 0 to D; D at most 1024, heads at most 4096.  Any
+ * strides; 2-byte alignment (16-byte alignment of everything is faster).  out may be
+ * x with the same strides.
+ */
+QSW_API qsw_status qsw_rope(const qsw_heads *x, int64_t T, int64_t heads, int64_t D, const int *positions,
+                           const int64_t *table, int64_t rot, int interleaved, float scale, int act_dtype,
+                           void *out, int64_t out_token_stride, int64_t out_head_stride, void *stream);
+
+/*
+ * Appends keys and values [T, kv_heads, D] to the cache: token t goes to row
+ * slots[t] % page_size of page slots[t] / page_size, k turned as in qsw_rope (rot 0:
+ * as it is).  q [T, heads, D], if not NULL, is turned into q_out in the same launch.  A slot
+ * below 0 or past the cache is not written; a token at a negative position is left
+ * out altogether, its row of q_out included.  Slots of two tokens should differ (else
+ * the row is of either, or of parts of both).  The cache's alignment as stated there;
+ * q, k, v and q_out as in qsw_rope; q_out may be q with the same strides.
+ */
+QSW_API qsw_status qsw_kv_append(const qsw_heads *q, const qsw_heads *k, const qsw_heads *v, int64_t T, int64_t heads,
+                                int64_t D, const int *slots, const int *positions, const int64_t *table,
+                                int64_t rot, int interleaved, float scale, int act_dtype,
+                                const qsw_kv_cache *cache, void *q_out, int64_t q_out_token_stride,
+                                int64_t q_out_head_stride, void *stream);
+
+/*
+ * The plan of a step, which every layer's append and attention of that step share: the
+ * new tokens of sequence b are rows offsets[b] .. offsets[b + 1] - 1 (int32 [B + 1] on
+ * the device, not decreasing, from 0 to at most T), its last ones; lengths[b] (int32)
+ * counts all its tokens, the new ones among them; page_table is int32 [B, max_pages]
+ * with rows table_stride apart.  Writes positions and slots int32 [T] (-1: no
+ * sequence's row, a position before the first, a page outside the cache) and the plan,
+ * qsw_paged_plan_bytes(B, T) bytes, 16-byte aligned.  `window`: 0, or a token at
+ * position p sees the keys p - window + 1 .. p.  A length counts as no less than 0 and
+ * no more than max_pages * page_size; with offsets that decrease or pass T the values are
+ * unspecified, but nothing is read or written out of range.  The plan holds
+ * for calls with the same B, T, heads, D, window and cache geometry; it is only read by them, so that
+ * calls on several streams may share it.  B at most 65536, T at most 2^22, heads at
+ * most 1024 and a multiple of kv_heads.
+ */
+QSW_API size_t qsw_paged_plan_bytes(int64_t B, int64_t T);
+QSW_API qsw_status qsw_paged_plan(const int *offsets, const int *lengths, int64_t B, const int *page_table,
+                                 int64_t table_stride, int64_t max_pages, int64_t T, int64_t heads, int64_t D,
+                                 int64_t window, const qsw_kv_cache *cache, int *positions, int *slots, void *plan,
+                                 void *stream);
+
+/*
+ * out[t, h] = sum_j softmax_j(scale q[t, h] . k_j) v_j over the keys j that token t
+ * sees: those of its sequence up to its own position (and within the window), of kv
+ * head h / (heads / kv_heads).  out is [T, heads, D], contiguous.  A token that sees no key gets 0; rows
+ * of no sequence are left as they were.  A page that is not in the cache counts as
+ * zeros; what a row does not see has no effect on it, infinities and NaN among them (a row
+ * that comes out infinite or NaN is computed again key by key, with f32 weights).
+ * Statistics and sums in f32, the weights rounded to the activation dtype before they
+ * meet v; long histories are split over CTAs and joined in f32 in a fixed order: the same bits
+ * every time.  scale > 0.  workspace: qsw_paged_attention_workspace_bytes(...) bytes,
+ * 256-byte aligned (0 bytes: may be NULL); it need not be cleared, and calls that can
+ * run concurrently must not share it.  q, out: 16-byte aligned, as are q's strides.
+ */
+QSW_API size_t qsw_paged_attention_workspace_bytes(int64_t B, int64_t T, int64_t heads, int64_t kv_heads, int64_t D);
+QSW_API qsw_status qsw_paged_attention(const qsw_heads *q, const qsw_kv_cache *cache, const int *page_table,
+                                      int64_t table_stride, int64_t max_pages, const void *plan, int64_t B,
+                                      int64_t T, int64_t heads, int64_t D, int64_t window, float scale,
+                                      int act_dtype, void *out, void *workspace, size_t workspace_bytes,
+                                      void *stream);
 
 /* Synchronise `stream`, then read and clear the device error word.
  * Returns QSW_ERR_BOUNDS if a debug-build check failed (libqswiglu_debug.so

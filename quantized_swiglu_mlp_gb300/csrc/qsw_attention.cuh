@@ -1,0 +1,221 @@
+// Attention over a paged cache: what the plan, the two kernels and the join share.
+//
+//   o = sum_j softmax_j(scale q . k_j) v_j      over the keys j that the token sees
+//
+// Query rows of one kv head are numbered token * group + (head in the group): the heads
+// that share a kv head are rows of one tile, and K and V are read once for all of them.
+// A tile of rows over a range of keys is an item; a sequence whose history is long
+// against the number of rows is cut into splits, whose normalised results and
+// log-sum-exps are joined by a second kernel.
+#pragma once
+
+#include "qsw_fp4.cuh"
+#include "qsw_internal.h"
+
+namespace qsw {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// One sequence of a plan.
+struct alignas(16) SeqRec {
+  int row;       // its first new token
+  int n;         // new tokens
+  int len;       // tokens in the cache, the new ones among them
+  int blocks;    // row tiles per kv head
+  int splits;
+  int chunk;     // keys per split
+  int pad[2];
+};
+
+// The plan in device memory: words 0 (items) and 1 (whether any sequence is split), the
+// first item of each sequence, the records, the sequence of each token (-1: none).
+struct PlanView {
+  int *head;
+  int *first;        // [B + 1]
+  SeqRec *rec;       // [B]
+  int *seq_of;       // [T]
+};
+constexpr int kPlanHead = 8;
+__host__ __device__ inline PlanView plan_view(void *base, int64_t B) {
+  PlanView v;
+  v.head = static_cast<int *>(base);
+  v.first = v.head + kPlanHead;
+  v.rec = reinterpret_cast<SeqRec *>(v.first + ((B + 1 + 7) / 8) * 8);
+  v.seq_of = reinterpret_cast<int *>(v.rec + B);
+  return v;
+}
+
+struct AttnParams {
+  const uint16_t *q;
+  uint16_t *out;                   // [T, heads, D]
+  const uint16_t *k, *v;
+  int64_t q_t, q_h;                // strides in elements
+  int64_t k_page, k_head, k_row, v_page, v_head, v_row;
+  const int *page_table;
+  int64_t table_stride;
+  PlanView plan;
+  int B, T, heads, kv_heads, group, D;
+  int pages, page_size, max_pages;
+  int window;                      // 0: none
+  int tile_rows, tile_keys;
+  float scale_log2;                // scale log2(e)
+  float *part;                     // [splits][T][heads][D], normalised
+  float *part_lse;                 // [splits][T][heads], log2
+  uint64_t timeout_ns;
+};
+
+// One item: rows [row0, row0 + rows) (token * group + head in the group) of a sequence's
+// kv head, keys [k0, k1), of which no row sees those before `first`.
+struct Item {
+  SeqRec s;
+  int b, head, row0, rows, k0, k1, first, split;
+};
+
+// First and last + 1 key that the tokens [a, b) of a sequence see.
+__device__ __forceinline__ void seen_keys(const SeqRec &s, int a, int b, int window, int &lo, int &hi) {
+  hi = min(max(s.len - s.n + b, 0), s.len);
+  lo = window ? max(s.len - s.n + a - window + 1, 0) : 0;
+}
+
+// Item `id` of the plan, by a converged warp: the sequence by a search 32 wide.
+__device__ __forceinline__ Item find_item(const AttnParams &p, int id) {
+  const int lane = static_cast<int>(lane_id());
+  int lo = 0, n = p.B;                 // the last sequence of [lo, lo + n) whose first item is at most id
+  while (n > 1) {
+    const int step = (n + 31) / 32;
+    const int at = lane * step;
+    const bool le = at < n && __ldg(p.plan.first + lo + at) <= id;
+    const int last = 31 - __clz(__ballot_sync(0xffffffffu, le) | 1u);
+    lo += last * step;
+    n = min(step, n - last * step);
+  }
+  Item t;
+  t.b = lo;
+  const int4 *r = reinterpret_cast<const int4 *>(p.plan.rec + lo);
+  const int4 a = __ldg(r), c = __ldg(r + 1);
+  t.s.row = a.x, t.s.n = a.y, t.s.len = a.z, t.s.blocks = a.w, t.s.splits = c.x, t.s.chunk = c.y;
+  const int local = id - __ldg(p.plan.first + lo);
+  // the last rows first (they see the most keys), then splits, kv heads innermost: CTAs
+  // that run together read the same keys of a head
+  const int per = p.kv_heads * t.s.splits;
+  const int up = local / per, r2 = local - up * per;
+  const int block = t.s.blocks - 1 - up;
+  t.split = r2 / p.kv_heads;
+  t.head = r2 - t.split * p.kv_heads;
+  t.row0 = block * p.tile_rows;
+  t.rows = min(p.tile_rows, t.s.n * p.group - t.row0);
+  int end;
+  seen_keys(t.s, t.row0 / p.group, (t.row0 + t.rows - 1) / p.group + 1, p.window, t.first, end);
+  const int start = t.first / p.tile_keys * p.tile_keys;
+  // (64 bits: the last split's end)
+  t.k0 = static_cast<int>(min(static_cast<int64_t>(start) + static_cast<int64_t>(t.split) * t.s.chunk,
+                              static_cast<int64_t>(end)));
+  t.k1 = static_cast<int>(min(static_cast<int64_t>(t.k0) + t.s.chunk, static_cast<int64_t>(end)));
+  // the last split takes what is left
+  if (t.split == t.s.splits - 1) t.k1 = max(end, t.k0);
+  return t;
+}
+
+// Token and head of row r of an item.
+__device__ __forceinline__ void row_of(const AttnParams &p, const Item &t, int r, int64_t &token, int &head, int &pos) {
+  const int row = t.row0 + r, i = row / p.group;
+  token = t.s.row + i;
+  head = t.head * p.group + row - i * p.group;
+  pos = t.s.len - t.s.n + i;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Page of a sequence's tokens [page * page_size, ..), -1 for one that no cache row belongs to.
+__device__ __forceinline__ int page_of(const AttnParams &p, int b, int page) {
+  if (page >= p.max_pages) return -1;
+  const int id = __ldg(p.page_table + b * p.table_stride + page);
+  return id >= 0 && id < p.pages ? id : -1;
+}
+
+// Row r of an item by one warp, key by key with what the row does not see left out, for
+// rows that came out infinite or NaN: in the tiles a masked key has the weight 0, and
+// 0 * inf is NaN.  Slow (a key at a time), and only ever run for such rows.
+template <class A>
+__device__ __noinline__ void exact_row(const AttnParams &p, const Item &t, int r) {
+  const int lane = static_cast<int>(lane_id());
+  int64_t token;
+  int head, pos;
+  row_of(p, t, r, token, head, pos);
+  const int lo = max(t.k0, p.window ? pos - p.window + 1 : 0), hi = min(t.k1, pos + 1);
+  const uint16_t *q = p.q + token * p.q_t + head * p.q_h;
+  auto score = [&](int j) {
+    const int page = page_of(p, t.b, j / p.page_size);
+    if (page < 0) return 0.0f;
+    const uint16_t *k = p.k + page * p.k_page + t.head * p.k_head + (j % p.page_size) * p.k_row;
+    float s = 0.0f;
+    for (int d = 0; d < p.D; d += 2) {
+      const uint32_t a = *reinterpret_cast<const uint32_t *>(q + d), b = *reinterpret_cast<const uint32_t *>(k + d);
+      s = fmaf(A::lo(a), A::lo(b), s);
+      s = fmaf(A::hi(a), A::hi(b), s);
+    }
+    return s * p.scale_log2;
+  };
+  float m = -INFINITY;
+  for (int j = lo + lane; j < hi; j += 32) m = fmaxf(m, score(j));
+#pragma unroll
+  for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  const float base = m == -INFINITY ? 0.0f : m;
+  float sum = 0.0f;
+  for (int j = lo + lane; j < hi; j += 32) sum += ex2(score(j) - base);
+#pragma unroll
+  for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int j0 = lo; j0 < hi; j0 += 32) {
+    const float mine = j0 + lane < hi ? ex2(score(j0 + lane) - base) * inv : 0.0f;
+    const int end = min(32, hi - j0);
+    for (int i = 0; i < end; ++i) {
+      const float w = __shfl_sync(0xffffffffu, mine, i);
+      const int page = page_of(p, t.b, (j0 + i) / p.page_size);
+      if (page < 0) continue;
+      const uint16_t *v = p.v + page * p.v_page + t.head * p.v_head + ((j0 + i) % p.page_size) * p.v_row;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int d = 2 * lane + 64 * x;
+        if (d >= p.D) continue;
+        const uint32_t c = *reinterpret_cast<const uint32_t *>(v + d);
+        o[2 * x] = fmaf(w, A::lo(c), o[2 * x]);
+        o[2 * x + 1] = fmaf(w, A::hi(c), o[2 * x + 1]);
+      }
+    }
+  }
+  const int64_t at = token * p.heads + head;
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const int d = 2 * lane + 64 * x;
+    if (d >= p.D) continue;
+    if (t.s.splits > 1) {
+      float *dst = p.part + (t.split * static_cast<int64_t>(p.T) * p.heads + at) * p.D + d;
+      dst[0] = o[2 * x];
+      dst[1] = o[2 * x + 1];
+    } else {
+      *reinterpret_cast<uint32_t *>(p.out + at * p.D + d) = A::pack2(o[2 * x], o[2 * x + 1]);
+    }
+  }
+  if (t.s.splits > 1 && lane == 0)
+    p.part_lse[t.split * static_cast<int64_t>(p.T) * p.heads + at] = sum == 0.0f ? -INFINITY : base + __log2f(sum);
+}
+
+// The form of a call, a function of its sizes alone: the plan and the attention work it
+// out for themselves and agree.
+struct AttnForm {
+  int tile_rows, tile_keys;
+  int slots;              // CTAs that run at once
+  int max_splits;         // 1: no history is split
+  int64_t items;          // at most
+};
+
+cudaError_t launch_attention_tiles(const AttnParams &p, const AttnForm &f, int act, const qsw_kv_cache &cache,
+                                   cudaStream_t stream);
+
+}  // namespace qsw

@@ -146,6 +146,47 @@ struct NormArgs {
 };
 cudaError_t launch_norm(const NormArgs &a, int num_sms, cudaStream_t stream);
 
+// ------------------------------------------------- attention ---------------
+// Rotary positions, the paged cache and attention over it (qsw_rope.cu,
+// qsw_attention*.cu).
+
+struct RopeArgs {
+  qsw_heads q, k, v;             // q.data null: none; k and v only with `slots`
+  int64_t T, heads, D, rot;
+  const int *positions, *slots;  // slots null: no cache
+  const int64_t *table;
+  int interleaved, act;
+  float scale;
+  void *out;                     // of q
+  int64_t out_token_stride, out_head_stride;
+  qsw_kv_cache cache;
+};
+cudaError_t launch_rope(const RopeArgs &a, int num_sms, cudaStream_t stream);
+
+struct PlanArgs {
+  const int *offsets, *lengths, *page_table;
+  int64_t B, T, table_stride, max_pages, heads, D, window;
+  qsw_kv_cache cache;
+  int *positions, *slots;
+  void *plan;
+};
+int64_t paged_plan_bytes(int64_t B, int64_t T);
+cudaError_t launch_paged_plan(const PlanArgs &a, int num_sms, cudaStream_t stream);
+
+struct AttentionArgs {
+  qsw_heads q;
+  qsw_kv_cache cache;
+  int64_t B, T, table_stride, max_pages, heads, D, window;
+  const int *page_table;
+  const void *plan;
+  float scale;
+  int act;
+  void *out, *workspace;
+};
+// Bytes of split results (0: no history is split).
+size_t attention_workspace_bytes(int64_t T, int64_t B, int64_t heads, int64_t kv_heads, int64_t D, int num_sms);
+cudaError_t launch_paged_attention(const AttentionArgs &a, int num_sms, uint64_t timeout_ns, cudaStream_t stream);
+
 // Shared state of the C entry points (qsw_api.cu).
 int device_sm_count();
 uint64_t wait_timeout_ns();

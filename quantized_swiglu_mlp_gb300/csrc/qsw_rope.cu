@@ -1,0 +1,277 @@
+// Rotary positions, and appending keys and values to a paged cache with the
+// rotation on the way (HBM-bound):
+//
+//   angle a = position f_i,  f_i the angle per position of pair i < rot / 2
+//   y0 = s (x0 cos a - x1 sin a),  y1 = s (x1 cos a + x0 sin a)
+//
+// with (x0, x1) the elements (i, i + rot/2) of a head or (2i, 2i + 1); elements from
+// `rot` on are copied.  Far positions: an angle of 10^5 rad in f32 is off by 0.004.
+// Here f_i is held as a fraction of a turn in 64 fractional bits, so that position *
+// f_i modulo 2^64 is the fraction of a turn exactly, and its upper 32 bits go through
+// sincospif: the angle is within 2^-24 of the exact one at any position.
+//
+// A CTA takes a few tokens: first a thread per (token, pair) puts cos and sin in
+// shared memory, where all heads of q and k find them, then the threads walk the
+// tokens' units: 8 pairs (two 16-byte runs half a rotation apart) or 8 elements.
+#include "qsw_fp4.cuh"
+#include "qsw_internal.h"
+
+namespace qsw {
+namespace {
+
+// n / d for n < 2^31 and 1 <= d < 2^31 as one multiplication: (n m) >> 32 >> shift with
+// m = ceil(2^(32 + shift) / d) (Granlund and Montgomery).
+struct FastDiv {
+  uint32_t d, m, shift;
+};
+FastDiv make_div(uint32_t d) {
+  uint32_t s = 0;
+  while ((uint64_t(1) << s) < d) ++s;          // 2^s >= d
+  // 2^(32 + s - 1) / d fits in 32 bits and serves n < 2^31
+  const uint32_t shift = s ? s - 1 : 0;
+  const uint64_t m = ((uint64_t(1) << (32 + shift)) + d - 1) / d;
+  return FastDiv{d, d == 1 ? 0u : static_cast<uint32_t>(m), shift};
+}
+__device__ __forceinline__ uint32_t div_by(uint32_t n, const FastDiv &f) {
+  return f.d == 1 ? n : __umulhi(n, f.m) >> f.shift;
+}
+
+// Heads of one tensor: where they come from and go to.
+struct Segment {
+  const uint16_t *src;
+  uint16_t *dst;
+  int64_t src_t, src_h;          // strides in elements
+  int64_t dst_t, dst_h;          // strides; of a cache, page (dst_t), head and row strides
+  int64_t dst_r;
+  int heads;
+  int rotate;
+  int paged;
+  FastDiv per_head;              // units of a head
+};
+
+struct RopeParams {
+  Segment seg[3];
+  int segments;
+  int first_unit[4];             // of each segment within a token, and their number
+  const int *positions;          // null: all 0
+  const int *slots;
+  const int64_t *table;
+  int T, D, half;                // half: pairs
+  int tokens;                    // per CTA
+  int interleaved;
+  int skip_negative;             // tokens at negative positions are left out
+  int pages;
+  float scale;
+  FastDiv per_token, page_size, halves;
+};
+
+template <class A, int VEC>
+struct Unit {
+  uint32_t w[2][VEC == 8 ? 4 : 1];
+};
+
+// One unit: `pairs` 8 (or 1) pairs half a rotation apart, else 8 (1) elements, of which
+// interleaved pairs may turn.
+template <class A, int VEC>
+__device__ __forceinline__ void load_unit(const uint16_t *p, int first, int second, bool both, Unit<A, VEC> &u) {
+  if constexpr (VEC == 8) {
+    const uint4 a = *reinterpret_cast<const uint4 *>(p + first);
+    u.w[0][0] = a.x, u.w[0][1] = a.y, u.w[0][2] = a.z, u.w[0][3] = a.w;
+    if (both) {
+      const uint4 b = *reinterpret_cast<const uint4 *>(p + second);
+      u.w[1][0] = b.x, u.w[1][1] = b.y, u.w[1][2] = b.z, u.w[1][3] = b.w;
+    }
+  } else {
+    u.w[0][0] = p[first];
+    if (both) u.w[1][0] = p[second];
+  }
+}
+
+template <class A, int VEC>
+__global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeParams p) {
+  extern __shared__ float2 turn[];       // [tokens][half]: cos, sin
+  griddep_wait();
+  griddep_launch_dependents();
+  const int t0 = static_cast<int>(blockIdx.x) * p.tokens;
+  const int count = min(p.tokens, p.T - t0);
+  if (p.half) {
+    for (uint32_t i = threadIdx.x; i < static_cast<uint32_t>(count * p.half); i += blockDim.x) {
+      const uint32_t t = div_by(i, p.halves), pair = i - t * p.half;
+      const uint64_t at = static_cast<uint64_t>(static_cast<int64_t>(p.positions ? __ldg(p.positions + t0 + t) : 0)) *
+                          static_cast<uint64_t>(__ldg(p.table + pair));
+      float s, c;
+      sincospif(static_cast<float>(static_cast<int32_t>(at >> 32)) * 0x1p-31f, &s, &c);
+      turn[i] = make_float2(c * p.scale, s * p.scale);
+    }
+    __syncthreads();
+  }
+  const uint32_t units = static_cast<uint32_t>(count) * p.per_token.d;
+  const int rot = 2 * p.half;
+  constexpr int kAhead = VEC == 8 ? 4 : 2;
+  for (uint32_t u0 = threadIdx.x; u0 < units; u0 += blockDim.x * kAhead) {
+    Unit<A, VEC> in[kAhead];
+    uint16_t *dst[kAhead];
+    const float2 *cs[kAhead];
+    int e0[kAhead], e1[kAhead];          // elements; e1 < 0: one run
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+      const uint32_t u = u0 + a * blockDim.x;
+      dst[a] = nullptr;
+      if (u >= units) continue;
+      const uint32_t tl = div_by(u, p.per_token);
+      const int t = t0 + static_cast<int>(tl);
+      int r = static_cast<int>(u - tl * p.per_token.d);
+      const int g = (p.segments > 1 && r >= p.first_unit[1]) + (p.segments > 2 && r >= p.first_unit[2]);
+      const Segment &s = p.seg[g];
+      r -= p.first_unit[g];
+      if (p.skip_negative && p.positions && __ldg(p.positions + t) < 0) continue;
+      const uint32_t h = div_by(static_cast<uint32_t>(r), s.per_head);
+      const int c = r - static_cast<int>(h * s.per_head.d);
+      uint16_t *d;
+      if (s.paged) {
+        const int slot = __ldg(p.slots + t);
+        if (slot < 0) continue;
+        const uint32_t page = div_by(static_cast<uint32_t>(slot), p.page_size);
+        if (page >= static_cast<uint32_t>(p.pages)) continue;
+        d = s.dst + page * s.dst_t + (slot - page * p.page_size.d) * s.dst_r + h * s.dst_h;
+      } else {
+        d = s.dst + t * s.dst_t + h * s.dst_h;
+      }
+      dst[a] = d;
+      cs[a] = nullptr;
+      e1[a] = -1;
+      if (s.rotate && !p.interleaved) {
+        // units of pairs first, then what is copied
+        const int pair = c * VEC;
+        if (pair < p.half) {
+          e0[a] = pair;
+          e1[a] = pair + p.half;
+          cs[a] = turn + tl * p.half + pair;
+        } else {
+          e0[a] = pair + p.half;
+        }
+      } else if (VEC == 1 && s.rotate) {
+        if (c < p.half) {
+          e0[a] = 2 * c;
+          e1[a] = 2 * c + 1;
+          cs[a] = turn + tl * p.half + c;
+        } else {
+          e0[a] = c + p.half;
+        }
+      } else {
+        e0[a] = c * VEC;
+        if (s.rotate && e0[a] < rot) cs[a] = turn + tl * p.half + e0[a] / 2;
+      }
+      load_unit<A, VEC>(s.src + t * s.src_t + h * s.src_h, e0[a], e1[a], e1[a] >= 0, in[a]);
+    }
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+      if (!dst[a]) continue;
+      if constexpr (VEC == 8) {
+        uint4 o0 = make_uint4(in[a].w[0][0], in[a].w[0][1], in[a].w[0][2], in[a].w[0][3]);
+        if (cs[a] && e1[a] >= 0) {
+          uint32_t y0[4], y1[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float4 f = reinterpret_cast<const float4 *>(cs[a])[j];     // cos, sin, cos, sin
+            const float a0 = A::lo(in[a].w[0][j]), a1 = A::hi(in[a].w[0][j]);
+            const float b0 = A::lo(in[a].w[1][j]), b1 = A::hi(in[a].w[1][j]);
+            y0[j] = A::pack2(a0 * f.x - b0 * f.y, a1 * f.z - b1 * f.w);
+            y1[j] = A::pack2(b0 * f.x + a0 * f.y, b1 * f.z + a1 * f.w);
+          }
+          o0 = make_uint4(y0[0], y0[1], y0[2], y0[3]);
+          *reinterpret_cast<uint4 *>(dst[a] + e1[a]) = make_uint4(y1[0], y1[1], y1[2], y1[3]);
+        } else if (cs[a]) {
+          uint32_t y[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 f = cs[a][j];
+            const float x0 = A::lo(in[a].w[0][j]), x1 = A::hi(in[a].w[0][j]);
+            y[j] = A::pack2(x0 * f.x - x1 * f.y, x1 * f.x + x0 * f.y);
+          }
+          o0 = make_uint4(y[0], y[1], y[2], y[3]);
+        }
+        *reinterpret_cast<uint4 *>(dst[a] + e0[a]) = o0;
+      } else {
+        if (cs[a]) {
+          const float2 f = *cs[a];
+          const float x0 = A::lo(in[a].w[0][0]), x1 = A::lo(in[a].w[1][0]);
+          dst[a][e0[a]] = A::store(x0 * f.x - x1 * f.y);
+          dst[a][e1[a]] = A::store(x1 * f.x + x0 * f.y);
+        } else {
+          dst[a][e0[a]] = static_cast<uint16_t>(in[a].w[0][0]);
+        }
+      }
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_rope(const RopeArgs &a, int num_sms, cudaStream_t stream) {
+  if (num_sms <= 0) return cudaErrorInvalidDevice;
+  RopeParams p = {};
+  p.positions = a.positions;
+  p.slots = a.slots;
+  p.table = a.table;
+  p.T = static_cast<int>(a.T);
+  p.D = static_cast<int>(a.D);
+  p.half = static_cast<int>(a.rot / 2);
+  p.interleaved = a.interleaved;
+  p.skip_negative = a.slots != nullptr;
+  p.pages = static_cast<int>(a.cache.pages);
+  p.scale = a.scale;
+  // 16-byte runs where every row, run and half allows
+  uintptr_t bits = static_cast<uintptr_t>(a.D) * 2;
+  if (p.half) bits |= static_cast<uintptr_t>(a.interleaved ? a.rot : p.half) * 2;
+  auto add = [&](const void *src, int64_t st, int64_t sh, void *dst, int64_t dt, int64_t dh, int64_t dr, int64_t heads,
+                 int rotate, int paged) {
+    Segment &s = p.seg[p.segments++];
+    s.src = static_cast<const uint16_t *>(src);
+    s.dst = static_cast<uint16_t *>(dst);
+    s.src_t = st, s.src_h = sh, s.dst_t = dt, s.dst_h = dh, s.dst_r = dr;
+    s.heads = static_cast<int>(heads);
+    s.rotate = rotate && p.half;
+    s.paged = paged;
+    bits |= reinterpret_cast<uintptr_t>(src) | reinterpret_cast<uintptr_t>(dst) |
+            static_cast<uintptr_t>((st | sh | dt | dh | dr) * 2);
+  };
+  if (a.q.data)
+    add(a.q.data, a.q.token_stride, a.q.head_stride, a.out, a.out_token_stride, a.out_head_stride, 0, a.heads, 1, 0);
+  if (a.slots) {
+    const qsw_kv_cache &c = a.cache;
+    add(a.k.data, a.k.token_stride, a.k.head_stride, c.k, c.k_strides[0], c.k_strides[1], c.k_strides[2], c.kv_heads, 1,
+        1);
+    add(a.v.data, a.v.token_stride, a.v.head_stride, c.v, c.v_strides[0], c.v_strides[1], c.v_strides[2], c.kv_heads, 0,
+        1);
+    p.page_size = make_div(static_cast<uint32_t>(c.page_size));
+  }
+  const bool wide = bits % 16 == 0;
+  const int vec = wide ? 8 : 1;
+  int units = 0;
+  for (int i = 0; i < p.segments; ++i) {
+    Segment &s = p.seg[i];
+    // a unit holds two runs where halves turn (or, element by element, any pair)
+    const int two = s.rotate && (!p.interleaved || !wide) ? p.half : 0;
+    const int per = (p.D - two) / vec;
+    s.per_head = make_div(static_cast<uint32_t>(per));
+    p.first_unit[i] = units;
+    units += per * s.heads;
+  }
+  p.per_token = make_div(static_cast<uint32_t>(units));
+  p.halves = make_div(static_cast<uint32_t>(p.half ? p.half : 1));
+  // four tokens a CTA where there are CTAs enough, so that its threads have a few units each
+  int64_t tokens = a.T / (2 * static_cast<int64_t>(num_sms));
+  tokens = tokens < 1 ? 1 : tokens > 4 ? 4 : tokens;
+  p.tokens = static_cast<int>(tokens);
+  const dim3 grid(static_cast<unsigned>((a.T + tokens - 1) / tokens));
+  const size_t smem = static_cast<size_t>(tokens) * p.half * sizeof(float2);
+  const bool f16 = a.act == ActF16::kId;
+  if (wide)
+    return f16 ? launch_on(rope_kernel<ActF16, 8>, grid, 256, smem, stream, false, p)
+               : launch_on(rope_kernel<ActBf16, 8>, grid, 256, smem, stream, false, p);
+  return f16 ? launch_on(rope_kernel<ActF16, 1>, grid, 256, smem, stream, false, p)
+             : launch_on(rope_kernel<ActBf16, 1>, grid, 256, smem, stream, false, p);
+}
+
+}  // namespace qsw

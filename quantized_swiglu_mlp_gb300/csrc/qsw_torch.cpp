@@ -1,5 +1,5 @@
 // Python binding of the block operators (qsw_fp4_*, qsw_moe_*, qsw_rms_norm,
-// qsw_post_norm) for torch tensors: checks device, dtype, shape and contiguity,
+// qsw_post_norm, qsw_rope, qsw_kv_append, qsw_paged_*) for torch tensors: checks device, dtype, shape and contiguity,
 // allocates results and scratch memory on the current stream, and calls the C entry
 // points, whose addresses ops.py hands over from the library it loaded.
 //
@@ -24,7 +24,9 @@ namespace {
 
 #define QSW_ENTRIES(X)                                                                                       \
   X(qsw_fp4_quantize) X(qsw_fp4_dequantize) X(qsw_fp4_workspace_bytes) X(qsw_fp4_linear) X(qsw_fp4_grouped_linear) \
-  X(qsw_moe_route) X(qsw_fp4_moe_workspace_bytes) X(qsw_fp4_moe_mlp) X(qsw_rms_norm) X(qsw_post_norm)
+  X(qsw_moe_route) X(qsw_fp4_moe_workspace_bytes) X(qsw_fp4_moe_mlp) X(qsw_rms_norm) X(qsw_post_norm) \
+  X(qsw_rope) X(qsw_kv_append) X(qsw_paged_plan_bytes) X(qsw_paged_plan) X(qsw_paged_attention_workspace_bytes)    \
+  X(qsw_paged_attention)
 
 struct Entries {
 #define X(name) decltype(&::name) name##_;
@@ -366,6 +368,184 @@ PyObject *post_norm(Args a) {
   return r;
 }
 
+// Heads [T, heads, D] of an activation type, a head's elements contiguous.
+const at::Tensor &heads_of(PyObject *o, const char *name, const at::Tensor *like) {
+  const at::Tensor &t = tensor(o, name);
+  if (like ? t.scalar_type() != like->scalar_type() : !is_act(t.scalar_type()))
+    fail(PyExc_TypeError, like ? "%s has the wrong dtype" : "%s must be bfloat16 or float16", name);
+  if (like && t.device() != like->device()) fail(PyExc_ValueError, "%s is on another device", name);
+  if (t.dim() != 3) fail(PyExc_ValueError, "%s must be [tokens, heads, head_dim]", name);
+  if (t.size(2) > 1 && t.stride(2) != 1) fail(PyExc_ValueError, "%s must have contiguous heads", name);
+  return t;
+}
+// The stride of dimension d, for one of a single element that of a dense tensor.
+int64_t step_of(const at::Tensor &t, int64_t d) {
+  if (t.size(d) > 1) return t.stride(d);
+  int64_t s = 1;
+  for (int64_t i = d + 1; i < t.dim(); ++i) s *= t.size(i);
+  return s;
+}
+qsw_heads heads_arg(const at::Tensor &t) { return qsw_heads{data(t), step_of(t, 0), step_of(t, 1)}; }
+
+// k and v [pages, kv_heads, page_size, D] of the same type, shape and device as `like`'s.
+qsw_kv_cache cache_arg(PyObject *ko, PyObject *vo, const at::Tensor *like) {
+  const at::Tensor &k = tensor(ko, "k_cache"), &v = tensor(vo, "v_cache");
+  if (like ? k.scalar_type() != like->scalar_type() : !is_act(k.scalar_type()))
+    fail(PyExc_TypeError, like ? "%s has the wrong dtype" : "%s must be bfloat16 or float16", "k_cache");
+  if (v.scalar_type() != k.scalar_type()) fail(PyExc_TypeError, "%s has the wrong dtype", "v_cache");
+  if (like && k.device() != like->device()) fail(PyExc_ValueError, "%s is on another device", "k_cache");
+  if (v.device() != k.device()) fail(PyExc_ValueError, "%s is on another device", "v_cache");
+  if (k.dim() != 4 || v.sizes() != k.sizes())
+    fail(PyExc_ValueError, "%s and v_cache must be [pages, kv_heads, page_size, head_dim]", "k_cache");
+  if (k.size(3) > 1 && (k.stride(3) != 1 || v.stride(3) != 1))
+    fail(PyExc_ValueError, "%s and v_cache must have contiguous rows", "k_cache");
+  qsw_kv_cache c = {data(k), data(v), k.size(0), k.size(1), k.size(2), {}, {}};
+  for (int i = 0; i < 3; ++i) {
+    c.k_strides[i] = step_of(k, i);
+    c.v_strides[i] = step_of(v, i);
+  }
+  return c;
+}
+const int *indices(PyObject *o, const char *name, int64_t n, const at::Tensor &like) {
+  const at::Tensor &t = operand(o, name, at::kInt, like);
+  if (t.dim() != 1 || t.size(0) != n) fail(PyExc_ValueError, "%s has the wrong size", name);
+  return static_cast<const int *>(data(t));
+}
+// The caller's output for heads like `x`, of any strides, or a new one.
+at::Tensor heads_output(PyObject *o, const char *name, const at::Tensor &x) {
+  if (o == Py_None) return empty(x.sizes(), x.scalar_type(), x);
+  const at::Tensor &t = heads_of(o, name, &x);
+  if (t.sizes() != x.sizes()) fail(PyExc_ValueError, "%s has the wrong size", name);
+  return t;
+}
+struct Rotation {
+  const int *positions = nullptr;
+  const int64_t *table = nullptr;
+  int64_t rot = 0;
+  Rotation(PyObject *pos, PyObject *tab, int64_t T, const at::Tensor &like) {
+    if (pos != Py_None) positions = indices(pos, "positions", T, like);
+    if (tab == Py_None) return;
+    const at::Tensor &t = operand(tab, "table", at::kLong, like);
+    if (t.dim() != 1 || 2 * t.size(0) > like.size(2)) fail(PyExc_ValueError, "%s must have at most half as many values as a head", "table");
+    if (T > 0 && t.size(0) && !positions) fail(PyExc_ValueError, "%s must be given where heads turn", "positions");
+    table = static_cast<const int64_t *>(data(t));
+    rot = 2 * t.size(0);
+  }
+};
+
+// x, positions, table, interleaved, scale, out
+PyObject *rope(Args a) {
+  const at::Tensor &x = heads_of(a[0], "x", nullptr);
+  const int64_t T = x.size(0), heads = x.size(1), D = x.size(2);
+  const Rotation r(a[1], a[2], T, x);
+  c10::cuda::CUDAGuard guard(x.device());
+  at::Tensor out = heads_output(a[5], "out", x);
+  const qsw_heads in = heads_arg(x);
+  check_status("qsw_rope",
+               g_fn.qsw_rope_(&in, heads ? T : 0, heads ? heads : 1, D, r.positions, r.table, r.rot, truth(a[3]),
+                              number(a[4]), act_code(x.scalar_type()), data(out), step_of(out, 0), step_of(out, 1),
+                              current_stream(x)));
+  return wrap(std::move(out));
+}
+
+// k, v, k_cache, v_cache, slots, positions, table, q, interleaved, scale, q_out
+PyObject *kv_append(Args a) {
+  const at::Tensor &k = heads_of(a[0], "k", nullptr), &v = heads_of(a[1], "v", &k);
+  const qsw_kv_cache cache = cache_arg(a[2], a[3], &k);
+  const at::Tensor &kc = THPVariable_Unpack(a[2]);
+  const int64_t T = k.size(0), D = k.size(2);
+  if (v.sizes() != k.sizes()) fail(PyExc_ValueError, "%s and v must have the same shape", "k");
+  if (k.size(1) != cache.kv_heads || D != kc.size(3)) fail(PyExc_ValueError, "%s does not fit the cache", "k");
+  const int *slots = indices(a[4], "slots", T, k);
+  const Rotation r(a[5], a[6], T, k);
+  c10::cuda::CUDAGuard guard(k.device());
+  const qsw_heads ka = heads_arg(k), va = heads_arg(v);
+  qsw_heads qa = {};
+  at::Tensor q_out;
+  int64_t heads = 0;
+  if (a[7] != Py_None) {
+    const at::Tensor &q = heads_of(a[7], "q", &k);
+    heads = q.size(1);
+    if (q.size(0) != T || q.size(2) != D || heads < 1) fail(PyExc_ValueError, "%s does not fit k", "q");
+    qa = heads_arg(q);
+    q_out = heads_output(a[10], "q_out", q);
+  } else if (a[10] != Py_None) {
+    fail(PyExc_ValueError, "%s is given without q", "q_out");
+  }
+  check_status("qsw_kv_append",
+               g_fn.qsw_kv_append_(heads ? &qa : nullptr, &ka, &va, T, heads, D, slots, r.positions, r.table, r.rot,
+                                   truth(a[8]), number(a[9]), act_code(k.scalar_type()), &cache,
+                                   heads ? data(q_out) : nullptr, heads ? step_of(q_out, 0) : 0,
+                                   heads ? step_of(q_out, 1) : 0, current_stream(k)));
+  if (!heads) Py_RETURN_NONE;
+  return wrap(std::move(q_out));
+}
+
+// A page table [B, max_pages], a sequence's pages contiguous.
+const at::Tensor &page_table_of(PyObject *o, const at::Tensor &like) {
+  const at::Tensor &t = tensor(o, "page_table");
+  if (t.scalar_type() != at::kInt) fail(PyExc_TypeError, "%s has the wrong dtype", "page_table");
+  if (t.device() != like.device()) fail(PyExc_ValueError, "%s is on another device", "page_table");
+  if (t.dim() != 2) fail(PyExc_ValueError, "%s must be [sequences, pages]", "page_table");
+  if (t.size(1) > 1 && t.stride(1) != 1) fail(PyExc_ValueError, "%s must have contiguous rows", "page_table");
+  return t;
+}
+
+// offsets, lengths, page_table, k_cache, tokens, heads, window -> positions, slots, plan
+PyObject *paged_plan(Args a) {
+  const qsw_kv_cache cache = cache_arg(a[3], a[3], nullptr);
+  const at::Tensor &kc = THPVariable_Unpack(a[3]);
+  const at::Tensor &table = page_table_of(a[2], kc), &offsets = operand(a[0], "offsets", at::kInt, kc);
+  const int64_t B = table.size(0), T = integer(a[4]), heads = integer(a[5]), D = kc.size(3);
+  if (offsets.dim() != 1 || offsets.size(0) != B + 1 || B < 1)
+    fail(PyExc_ValueError, "%s must have one value more than there are sequences", "offsets");
+  const int *lengths = indices(a[1], "lengths", B, kc);
+  if (T < 0) fail(PyExc_ValueError, "%s must not be negative", "tokens");
+  c10::cuda::CUDAGuard guard(kc.device());
+  const size_t bytes = g_fn.qsw_paged_plan_bytes_(B, T);
+  const int64_t rows = bytes ? T : 0;     // (sizes that the call below refuses)
+  at::Tensor positions = empty({rows}, at::kInt, kc), slots = empty({rows}, at::kInt, kc),
+             plan = empty({static_cast<int64_t>(bytes)}, at::kByte, kc);
+  check_status("qsw_paged_plan",
+               g_fn.qsw_paged_plan_(offsets.const_data_ptr<int>(), lengths, B, static_cast<int *>(data(table)),
+                                    step_of(table, 0), table.size(1), T, heads, D, integer(a[6]), &cache,
+                                    static_cast<int *>(data(positions)), static_cast<int *>(data(slots)), data(plan),
+                                    current_stream(kc)));
+  PyObject *r = PyTuple_New(3);
+  if (!r) throw PyError();
+  at::Tensor *parts[3] = {&positions, &slots, &plan};
+  for (int i = 0; i < 3; ++i) PyTuple_SET_ITEM(r, i, wrap(std::move(*parts[i])));
+  return r;
+}
+
+// q, k_cache, v_cache, page_table, plan, plan's (tokens, heads, window, pages, kv_heads, page_size, head_dim), scale, out
+PyObject *paged_attention(Args a) {
+  const at::Tensor &q = heads_of(a[0], "q", nullptr);
+  const qsw_kv_cache cache = cache_arg(a[1], a[2], &q);
+  const at::Tensor &kc = THPVariable_Unpack(a[1]);
+  const at::Tensor &table = page_table_of(a[3], q), &plan = operand(a[4], "plan", at::kByte, q);
+  const int64_t T = q.size(0), heads = q.size(1), D = q.size(2), B = table.size(0);
+  if (D != kc.size(3)) fail(PyExc_ValueError, "%s does not fit the cache", "q");
+  const int64_t made[6] = {T, heads, cache.pages, cache.kv_heads, cache.page_size, D};
+  const int at_arg[6] = {5, 6, 8, 9, 10, 11};
+  for (int i = 0; i < 6; ++i)
+    if (integer(a[at_arg[i]]) != made[i]) fail(PyExc_ValueError, "%s was made for other sizes", "plan");
+  if (static_cast<size_t>(plan.numel()) != g_fn.qsw_paged_plan_bytes_(B, T))
+    fail(PyExc_ValueError, "%s was made for other sizes", "plan");
+  c10::cuda::CUDAGuard guard(q.device());
+  at::Tensor out = output(a[13], "out", q.sizes(), q.scalar_type(), q);
+  const size_t bytes = g_fn.qsw_paged_attention_workspace_bytes_(B, T, heads, cache.kv_heads, D);
+  at::Tensor ws;
+  if (bytes) ws = empty({static_cast<int64_t>(bytes)}, at::kByte, q);
+  const qsw_heads in = heads_arg(q);
+  check_status("qsw_paged_attention",
+               g_fn.qsw_paged_attention_(&in, &cache, static_cast<int *>(data(table)), step_of(table, 0), table.size(1),
+                                         data(plan), B, T, heads, D, integer(a[7]), number(a[12]),
+                                         act_code(q.scalar_type()), data(out), bytes ? data(ws) : nullptr, bytes,
+                                         current_stream(q)));
+  return wrap(std::move(out));
+}
+
 // {name: address}, raise_status
 PyObject *bind(Args a) {
 #define X(name)                                                        \
@@ -401,6 +581,8 @@ PyObject *guarded(PyObject *, PyObject *const *a, Py_ssize_t n) {
 PyMethodDef g_methods[] = {METHOD(bind, 2),        METHOD(fp4_quantize, 3),       METHOD(fp4_dequantize, 6),
                            METHOD(fp4_linear, 7),  METHOD(fp4_grouped_linear, 8), METHOD(moe_route, 5),
                            METHOD(fp4_moe_mlp, 17), METHOD(rms_norm, 4),          METHOD(post_norm, 11),
+                           METHOD(rope, 6),        METHOD(kv_append, 11),         METHOD(paged_plan, 7),
+                           METHOD(paged_attention, 14),
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_qsw_torch", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -17,6 +17,7 @@ from __future__ import annotations
 
 import ctypes
 import importlib.util
+import math
 import os
 import threading
 from typing import NamedTuple
@@ -32,7 +33,8 @@ MATCH, F32, DEBUG_GATE, DEBUG_UP = 0, 1, 2, 3
 VARIANTS = {"match": MATCH, "f32": F32, "debug_gate": DEBUG_GATE, "debug_up": DEBUG_UP}
 CNT_FUSED_TC, CNT_FUSED_GEMV, CNT_QMM_TC, CNT_QMM_GEMV, CNT_SILU_MUL, CNT_GEMV_STREAM = range(6)
 CNT_FP4_QUANTIZE, CNT_FP4_DEQUANTIZE, CNT_FP4_LINEAR, CNT_MOE_ROUTE, CNT_FP4_MOE, CNT_NORM = range(6, 12)
-NUM_COUNTERS = 12
+CNT_ROPE, CNT_KV_APPEND, CNT_PAGED_PLAN, CNT_PAGED_ATTENTION = range(12, 16)
+NUM_COUNTERS = 16
 STATUS = {0: "QSW_OK", 1: "QSW_ERR_INVALID_ARG", 2: "QSW_ERR_UNSUPPORTED", 3: "QSW_ERR_CUDA",
           4: "QSW_ERR_TIMEOUT", 5: "QSW_ERR_BOUNDS"}
 STREAM_K_OFF, STREAM_K_AUTO, STREAM_K_ALWAYS = 0, 1, 2
@@ -51,10 +53,24 @@ EXPORTED = ("qswiglu_forward", "affine_qmm", "qswiglu_forward_ws", "affine_qmm_w
             "qsw_get_counters", "qsw_reset_counters", "qsw_status_string", "qsw_version",
             "qsw_fp4_scale_bytes", "qsw_fp4_quantize", "qsw_fp4_dequantize", "qsw_fp4_workspace_bytes",
             "qsw_fp4_linear", "qsw_fp4_grouped_linear", "qsw_moe_route", "qsw_fp4_moe_workspace_bytes",
-            "qsw_fp4_moe_mlp", "qsw_rms_norm", "qsw_post_norm", "qsw_debug_withhold_next_product")
+            "qsw_fp4_moe_mlp", "qsw_rms_norm", "qsw_post_norm", "qsw_debug_withhold_next_product",
+            "qsw_rope", "qsw_kv_append", "qsw_paged_plan_bytes", "qsw_paged_plan",
+            "qsw_paged_attention_workspace_bytes", "qsw_paged_attention")
 
 _lock = threading.Lock()
 _lib = None
+
+
+class Heads(ctypes.Structure):
+    """qsw_heads"""
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class KvCache(ctypes.Structure):
+    """qsw_kv_cache"""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("pages", ctypes.c_int64),
+                ("kv_heads", ctypes.c_int64), ("page_size", ctypes.c_int64), ("k_strides", ctypes.c_int64 * 3),
+                ("v_strides", ctypes.c_int64 * 3)]
 
 
 class QswError(RuntimeError):
@@ -137,6 +153,19 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.qsw_rms_norm.restype = i32
         lib.qsw_post_norm.argtypes = [p, p, i32, p, p, i64, i64, f32, p, i64, i64, f32, i32, p, p, p]
         lib.qsw_post_norm.restype = i32
+        h, c = ctypes.POINTER(Heads), ctypes.POINTER(KvCache)
+        lib.qsw_rope.argtypes = [h, i64, i64, i64, p, p, i64, i32, f32, i32, p, i64, i64, p]
+        lib.qsw_rope.restype = i32
+        lib.qsw_kv_append.argtypes = [h, h, h, i64, i64, i64, p, p, p, i64, i32, f32, i32, c, p, i64, i64, p]
+        lib.qsw_kv_append.restype = i32
+        lib.qsw_paged_plan_bytes.argtypes = [i64, i64]
+        lib.qsw_paged_plan_bytes.restype = sz
+        lib.qsw_paged_plan.argtypes = [p, p, i64, p, i64, i64, i64, i64, i64, i64, c, p, p, p, p]
+        lib.qsw_paged_plan.restype = i32
+        lib.qsw_paged_attention_workspace_bytes.argtypes = [i64, i64, i64, i64, i64]
+        lib.qsw_paged_attention_workspace_bytes.restype = sz
+        lib.qsw_paged_attention.argtypes = [h, c, p, i64, i64, p, i64, i64, i64, i64, i64, f32, i32, p, p, sz, p]
+        lib.qsw_paged_attention.restype = i32
         _lib = lib
         return lib
 
@@ -453,6 +482,14 @@ def _call(fn, stream, first, *args):
         return fn(first, *args)
 
 
+def _call_on(like, fn, stream, *args):
+    """_call for functions that take the current stream of another argument's device."""
+    if stream is None or not getattr(like, "is_cuda", False):
+        return fn(*args)
+    with _on(stream, like.device):
+        return fn(*args)
+
+
 def fp4_scale_shape(rows: int, K: int, fmt: int) -> tuple[int, int, int]:
     """Shape of the scale blocks of a [rows, K] matrix: row blocks of 128, blocks of 4 scales, 512 bytes."""
     if fmt not in FP4_BLOCK:
@@ -553,6 +590,136 @@ def post_norm(h, y, weight=None, gate=None, scale=1.0, next_weight=None, eps=1e-
     """
     return _call((_native or load_native()).post_norm, stream, h, y, weight, gate, scale, next_weight, eps, norm,
                  next_norm, out, next_out)
+
+
+# ------------------------------------------------------------------------
+# The attention half of a block: rotary positions, a paged cache, attention of new
+# tokens over it.  Layouts and formulas: include/qswiglu.h.
+# ------------------------------------------------------------------------
+
+def rope_frequencies(dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                     original_length: int = 0, fast: float = 32.0, slow: float = 1.0) -> torch.Tensor:
+    """Angle per position of each pair of a rotation over `dim` elements: base^(-2 i / dim), f64 [dim / 2].
+
+    For contexts `factor` times as long as those trained on, `scaling` is
+      "linear"  every frequency over the factor (positions interpolated);
+      "base"    the base times factor^(dim / (dim - 2)): the slowest pair is interpolated
+                by the factor, the fastest not at all;
+      "ramp"    pairs that turn over `fast` times within original_length positions are left, those
+                that turn less than `slow` times interpolated, a linear ramp over the pair's
+                index between.
+    """
+    if dim < 2 or dim % 2:
+        raise ValueError("dim must be even and positive")
+    if not (base > 0 and factor > 0) or not math.isfinite(base * factor):
+        raise ValueError("base and factor must be positive")
+    i = torch.arange(dim // 2, dtype=torch.float64)
+    if scaling == "base":
+        if dim == 2:
+            raise ValueError('"base" scaling needs more than one pair')
+        base = base * factor ** (dim / (dim - 2))
+    f = base ** (-2.0 * i / dim)
+    if scaling in ("none", "base"):
+        return f
+    if scaling == "linear":
+        return f / factor
+    if scaling != "ramp":
+        raise ValueError('scaling must be "none", "linear", "base" or "ramp"')
+    if original_length < 1 or not fast > slow > 0 or base <= 1:
+        raise ValueError('"ramp" scaling needs original_length, fast above slow above 0 and a base above 1')
+
+    def pair_of(turns):      # the pair that turns so often within original_length
+        return dim * math.log(original_length / (turns * 2 * math.pi)) / (2 * math.log(base))
+    first = min(max(math.floor(pair_of(fast)), 0), dim // 2 - 1)
+    last = min(max(math.ceil(pair_of(slow)), 0), dim // 2 - 1)
+    ramp = ((i - first) / max(last - first, 0.001)).clamp(0, 1)
+    return f / factor * ramp + f * (1 - ramp)
+
+
+def rope_table(frequencies, device=None) -> torch.Tensor:
+    """Frequencies (angle per position, f64, one per pair) as rope and kv_append take
+    them: int64, turns per position times 2^64 modulo 2^64.  On the frequencies' device, or
+    the given one, or the current CUDA device."""
+    if isinstance(frequencies, torch.Tensor):
+        if device is None and frequencies.is_cuda:
+            device = frequencies.device
+        frequencies = frequencies.double().tolist()
+    values = []
+    for f in frequencies:
+        if not math.isfinite(f):
+            raise ValueError("frequencies must be finite")
+        # (the remainder of a float is exact; 2^64 turns as an integer, wrapped to a signed one)
+        turns = int(math.ldexp(math.fmod(f / (2.0 * math.pi), 1.0), 64)) % (1 << 64)
+        values.append(turns - (1 << 64) if turns >> 63 else turns)
+    return torch.tensor(values, dtype=torch.int64, device="cuda" if device is None else device)
+
+
+def rope(x, positions, table, interleaved=False, scale=1.0, out=None, stream=None) -> torch.Tensor:
+    """x [T, heads, D] with the first 2 * len(table) elements of each head turned by positions.
+
+    positions int32 [T] of either sign (the rotation's inverse: the negative positions), table
+    as rope_table returns it.  Pairs are half a rotation apart, or adjacent
+    with `interleaved`; `scale` multiplies what is turned.  x may have any strides
+    between tokens and heads; `out` likewise, and it may be x.
+    """
+    return _call((_native or load_native()).rope, stream, x, positions, table, interleaved, scale, out)
+
+
+class PagedPlan(NamedTuple):
+    """What paged_plan returns and paged_attention takes, for every layer of a step."""
+    positions: torch.Tensor    # int32 [T] position of each new token in its sequence; -1: none
+    slots: torch.Tensor        # int32 [T] its row in the cache, page * page_size + row; -1: none
+    page_table: torch.Tensor   # as given
+    work: torch.Tensor         # how the attention is divided (uint8)
+    tokens: int
+    heads: int
+    window: int
+    pages: int
+    kv_heads: int
+    page_size: int
+    head_dim: int
+
+
+def paged_plan(offsets, lengths, page_table, k_cache, tokens, heads, window=0, stream=None) -> PagedPlan:
+    """The plan of a step over a paged cache (qsw_paged_plan): made once, used by every
+    layer's kv_append and paged_attention with caches of k_cache's shape.
+
+    offsets int32 [B + 1]: sequence b's new tokens are rows offsets[b] .. offsets[b + 1] - 1
+    of the step's `tokens` rows; lengths int32 [B]: its tokens in all; page_table int32
+    [B, max_pages].  window: 0, or how many keys a token sees, itself among them.
+    Nothing is read back: in a CUDA graph the plan is captured with the step and follows
+    new contents of offsets, lengths and page_table.
+    """
+    got = _call_on(k_cache, (_native or load_native()).paged_plan, stream, offsets, lengths, page_table, k_cache, tokens,
+                   heads, window)
+    return PagedPlan(got[0], got[1], page_table, got[2], int(tokens), int(heads), int(window), k_cache.shape[0],
+                     k_cache.shape[1], k_cache.shape[2], k_cache.shape[3])
+
+
+def kv_append(k, v, k_cache, v_cache, slots, positions=None, table=None, q=None, interleaved=False, scale=1.0,
+              q_out=None, stream=None):
+    """Writes k, turned by positions, and v [T, kv_heads, D] to the cache rows slots; returns q [T, heads, D] turned, if given.
+
+    k_cache, v_cache [pages, kv_heads, page_size, D]; slots and positions int32 [T], as paged_plan returns them (tokens
+    with a negative slot are not written, those at a negative position left out
+    altogether).  table None: nothing turns.  `q_out` may be q.
+    """
+    return _call((_native or load_native()).kv_append, stream, k, v, k_cache, v_cache, slots, positions, table, q,
+                 interleaved, scale, q_out)
+
+
+def paged_attention(q, k_cache, v_cache, plan, scale=None, out=None, stream=None) -> torch.Tensor:
+    """Causal attention of new tokens q [T, heads, D] over their sequences in the cache; returns [T, heads, D].
+
+    plan: paged_plan's result, made after the lengths and for caches of this shape.  Heads
+    of q share kv heads in runs of heads / kv_heads.  scale: of the scores, D^-0.5 by
+    default.  Rows of no sequence are left as they are.
+    """
+    if not isinstance(plan, PagedPlan):
+        raise TypeError("plan must be a PagedPlan")
+    if scale is None:
+        scale = plan.head_dim ** -0.5
+    return _call((_native or load_native()).paged_attention, stream, q, k_cache, v_cache, *plan[2:], scale, out)
 
 
 def qsw_check_device_errors(stream=None) -> None:
