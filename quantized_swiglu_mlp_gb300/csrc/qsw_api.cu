@@ -294,13 +294,14 @@ qsw_status qsw_silu_mul(const void *g, const void *u, int64_t n, int variant, vo
 
 qsw_status qsw_check_device_errors(void *stream) {
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return QSW_ERR_CUDA;
-  unsigned int a = 0, b = 0, c = 0, d = 0;
+  unsigned int a = 0, b = 0, c = 0, d = 0, e = 0;
   if (qsw::prefill_take_errors(&a) != cudaSuccess) return QSW_ERR_CUDA;
   if (qsw::gemv_take_errors(&b) != cudaSuccess) return QSW_ERR_CUDA;
   if (qsw::gemv_stream_take_errors(&c) != cudaSuccess) return QSW_ERR_CUDA;
   if (qsw::fp4_gemm_take_errors(&d) != cudaSuccess) return QSW_ERR_CUDA;
-  if ((a | b | c | d) & qsw::DEVERR_BOUNDS) return QSW_ERR_BOUNDS;
-  return (a | b | c | d) ? QSW_ERR_TIMEOUT : QSW_OK;
+  if (qsw::attention_take_errors(&e) != cudaSuccess) return QSW_ERR_CUDA;
+  if ((a | b | c | d | e) & qsw::DEVERR_BOUNDS) return QSW_ERR_BOUNDS;
+  return (a | b | c | d | e) ? QSW_ERR_TIMEOUT : QSW_OK;
 }
 
 void qsw_set_gemv_max_m(int m) {

@@ -529,9 +529,17 @@ constexpr int kMaxSplits = 128;
 AttnForm attention_form(int64_t T, int64_t B, int64_t heads, int64_t kv_heads, int64_t D, int num_sms) {
   AttnForm f = {};
   const int64_t group = heads / kv_heads, seqs = T < B ? T : B;
-  f.tile_rows = 16;
-  f.tile_keys = kRowWarps * kSubKeys;
-  f.slots = 2 * num_sms;
+  // rows of a sequence and kv head, on average: as many as a warp's products take, or the
+  // tensor-core form
+  if ((T + seqs - 1) / seqs * group <= 16) {
+    f.tile_rows = 16;
+    f.tile_keys = kRowWarps * kSubKeys;
+    f.slots = 2 * num_sms;
+  } else {
+    f.tile_rows = 256;
+    f.tile_keys = 128;
+    f.slots = num_sms;
+  }
   const int64_t blocks = (T * group + f.tile_rows - 1) / f.tile_rows;       // at least
   int64_t splits = kPartBytes / (T * heads * D * 4 + 1);
   // where the unsplit items alone are many waves there is nothing to gain
@@ -612,7 +620,9 @@ cudaError_t launch_paged_attention(const AttentionArgs &a, int num_sms, uint64_t
   p.part = static_cast<float *>(a.workspace);
   p.part_lse = p.part + static_cast<int64_t>(f.max_splits) * a.T * a.heads * a.D;
   const bool f16 = a.act == ActF16::kId;
-  cudaError_t e = f16 ? launch_rows<ActF16>(p, f, stream) : launch_rows<ActBf16>(p, f, stream);
+  cudaError_t e = f.tile_rows > 16 ? launch_attention_tiles(p, f, a.act, c, stream)
+                  : f16            ? launch_rows<ActF16>(p, f, stream)
+                                   : launch_rows<ActBf16>(p, f, stream);
   if (e != cudaSuccess || f.max_splits == 1) return e;
   const dim3 grid(static_cast<unsigned>((a.T * a.heads + 7) / 8));
   return f16 ? launch_on(join_kernel<ActF16>, grid, 256, 0, stream, true, p)

@@ -1,0 +1,560 @@
+// Attention over a paged cache for many rows per kv head, on the tensor core
+// (qsw_attention.cuh):
+//
+//   S = Q K^T      tile of 128 rows by 128 keys, f32 in tensor memory
+//   P = 2^(scale log2(e) S - base)     one pass with a running base per row, in registers,
+//                                      back to tensor memory in the activation type
+//   O = O + P V    f32 in tensor memory
+//
+// An item is 256 rows: two tiles of 128 rows that share K and V and take turns, so that one
+// tile's softmax runs under the other's products.  12 warps: warps 0-3 and 4-7 each own a
+// row tile (a thread per row: row maximum and sum need no exchange), warp 8 issues the
+// products, warps 9 and 10 copy K and V pages by TMA (a box per page, or per 8 to 128 rows
+// of one; a page outside the cache is a coordinate outside the tensor and reads zeros).
+// P lies where S was: the products that read P and overwrite S run in the order of issue.
+//
+// The base of a row is raised (and O rescaled in tensor memory) only when a score passes
+// it by 8, so that weights reach 256 at most and most tiles leave O alone.
+#include <mutex>
+
+#include "qsw_attention.cuh"
+
+namespace qsw {
+
+namespace {
+
+__device__ unsigned int g_attn_error;
+
+constexpr int kRows = 128;            // of a tile
+constexpr int kKeys = 128;
+constexpr int kThreads = 384;
+constexpr int kWarpMma = 8, kWarpK = 9, kWarpV = 10;
+constexpr float kRaise = 8.0f;
+
+template <int DP>
+struct Shape {
+  static constexpr int kHalves = DP / 64;                    // 128-byte columns of a tile
+  static constexpr int kHalfBytes = 128 * 128;
+  static constexpr int kTileBytes = kHalves * kHalfBytes;    // 128 rows of K, V or Q
+  static constexpr int kKStages = DP == 128 ? 2 : 4;
+  static constexpr int kVStages = DP == 128 ? 3 : 4;
+  static constexpr int kStages = kKStages + kVStages;
+  static constexpr int kSmem = (2 + kStages) * kTileBytes + 1024;
+};
+
+struct TcMaps {
+  CUtensorMap k, v;
+  int box;               // rows of a box
+  int k_head_first, v_head_first;   // order of the maps' dimensions
+};
+
+__device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, uint64_t *bar, int c0, int c1, int c2,
+                                            int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], "
+      "[%2];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
+// D[tmem] (+)= A[tmem] . B[smem]
+__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                        uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Descriptor of V as the B operand with the columns contiguous (keys are the product's
+// K): blocks of 64 columns by 8 keys, 128-byte swizzle; the next 8 keys 1024 bytes on, the
+// next 64 columns a half on.
+__device__ __forceinline__ uint64_t v_desc(uint32_t smem_addr, uint32_t half_bytes) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((smem_addr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(half_bytes >> 4) << 16;
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t *r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,"
+      "%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+
+// (a, b) * (c, c) + (d, d), and sums, two at a time.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float &lo, float &hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// The item of a CTA's step: every second wave in reverse, since items come longest first.
+__device__ __forceinline__ int item_of(int step) {
+  const int G = static_cast<int>(gridDim.x), c = static_cast<int>(blockIdx.x);
+  return step * G + ((step & 1) ? G - 1 - c : c);
+}
+
+struct Barriers {
+  uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
+  uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
+  uint64_t mma_done;
+};
+
+template <class A, int DP>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_tiles_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ TcMaps maps) {
+  using S = Shape<DP>;
+  constexpr int KS = S::kKStages, VS = S::kVStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t *q_smem = smem, *k_smem = smem + 2 * S::kTileBytes, *v_smem = k_smem + KS * S::kTileBytes;
+  __shared__ Barriers bar;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_word;
+  volatile int *abort_flag = &abort_word;
+  unsigned int *err = &g_attn_error;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+
+  if constexpr (kDebugBounds) debug_poison_smem(smem, (2 + S::kStages) * S::kTileBytes);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&bar.k_full[i], 1);
+      mbar_init(&bar.k_empty[i], 1);
+      mbar_init(&bar.v_full[i], 1);
+      mbar_init(&bar.v_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar.q_full[i], 4);
+      mbar_init(&bar.s_full[i], 1);
+      mbar_init(&bar.p_full[i], 4);
+      mbar_init(&bar.o_full[i], 1);
+    }
+    mbar_init(&bar.mma_done, 1);
+    abort_word = 0;
+    fence_mbar_init();
+    prefetch_tensormap(&maps.k);
+    prefetch_tensormap(&maps.v);
+  }
+  if (warp == kWarpMma) {
+    __syncwarp();
+    tmem_alloc(&tmem_slot, 512);
+    tmem_relinquish();
+  }
+  fence_proxy_async_smem();      // (debug build: the fill, before the copies)
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
+  griddep_wait();
+  griddep_launch_dependents();
+  const int total = __ldg(p.plan.head);
+  // Tensor memory: S (and P) of the two row tiles, then O of both.
+  const uint32_t o_col = 256;
+
+  if (warp < 8) {
+    // ------------------------------------------------------------- softmax --
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    const int tile = warp >> 2;
+    const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;      // this warp's 32 lanes
+    const uint32_t s_addr = tmem + lanes + tile * 128, o_addr = tmem + lanes + o_col + tile * DP;
+    const int r = (warp & 3) * 32 + lane;                              // row of the tile
+    uint8_t *q_tile = q_smem + tile * S::kTileBytes;
+    uint32_t s_count = 0, o_count = 0, v_count = 0;
+    for (int step = 0, id; (id = item_of(step)) < total; ++step) {
+      const Item t = find_item(p, id);
+      const int n = (t.k1 - t.k0 + kKeys - 1) / kKeys;
+      const int mine = t.rows - tile * kRows;                          // live rows of the tile
+      if (mine <= 0) {
+        v_count += n;
+        continue;
+      }
+      const bool live = r < mine;
+      int64_t token;
+      int head, pos;
+      row_of(p, t, live ? tile * kRows + r : 0, token, head, pos);
+      float base = -INFINITY, sum = 0.0f;
+      bool ok = true;
+      if (n > 0) {
+        // the row of q into shared memory, as the products take it
+        const uint16_t *src = p.q + token * p.q_t + head * p.q_h;
+        uint4 x[DP / 8];
+#pragma unroll
+        for (int c = 0; c < DP / 8; ++c)
+          x[c] = live && c * 8 < p.D ? __ldg(reinterpret_cast<const uint4 *>(src) + c) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int c = 0; c < DP / 8; ++c)
+          *reinterpret_cast<uint4 *>(q_tile + (c >> 3) * S::kHalfBytes + r * 128 + (((c ^ r) & 7) << 4)) = x[c];
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.q_full[tile]);
+      }
+      const bool warp_live = (warp & 3) * 32 < mine;
+      const float scale = p.scale_log2;
+      for (int i = 0; i < n; ++i, ++s_count) {
+        const int key0 = t.k0 + i * kKeys;
+        if (!(ok = warp_wait(&bar.s_full[tile], s_count & 1, abort_flag, p.timeout_ns, err))) break;
+        tc_fence_after();
+        if (tile == 0 && (key0 + kKeys > t.k1 || key0 < t.first)) {
+          // rows of V that no row of the item sees may hold anything: a weight of 0 does
+          // not take out infinities or NaN.  (Before both tiles' products: tile 0's go
+          // first.)
+          const uint32_t at = v_count + i;
+          if (!(ok = warp_wait(&bar.v_full[at % VS], (at / VS) & 1, abort_flag, p.timeout_ns, err))) break;
+          if (key0 + r >= t.k1 || key0 + r < t.first) {
+            uint8_t *v = v_smem + (at % VS) * S::kTileBytes + r * 128;
+#pragma unroll
+            for (int c = 0; c < DP / 8; ++c)
+              *reinterpret_cast<uint4 *>(v + (c >> 3) * S::kHalfBytes + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+        }
+        if (warp_live) {
+          float s[128];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + c * 32, reinterpret_cast<uint32_t *>(s) + c * 32);
+          tmem_ld_wait();
+          // keys of the tile that the row sees: columns [lo, hi)
+          const int hi = live ? min(pos + 1, t.k1) - key0 : 0;
+          const int lo = p.window ? pos - p.window + 1 - key0 : 0;
+          if (!__all_sync(0xffffffffu, hi >= kKeys && lo <= 0)) {
+#pragma unroll
+            for (int c = 0; c < 128; ++c) s[c] = c < hi && c >= lo ? s[c] : -INFINITY;
+          }
+          float top[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+          for (int c = 4; c < 128; c += 4)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) top[x] = fmaxf(top[x], s[c + x]);
+          const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
+          const bool raise = most > base + kRaise || (base == -INFINITY && most > -INFINITY);
+          if (__any_sync(0xffffffffu, raise)) {
+            const float now = raise ? most : base;
+            const float shrink = raise ? ex2(base - now) : 1.0f;
+            base = now;
+            sum *= shrink;
+            if (i > 0) {
+#pragma unroll
+              for (int c = 0; c < DP; c += 16) {
+                uint32_t o[16];
+                tmem_ld16(o_addr + c, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * shrink);
+                tmem_st16(o_addr + c, o);
+              }
+            }
+          }
+          const float off = base == -INFINITY ? 0.0f : -base;
+          const uint64_t scale2 = pair(scale, scale), off2 = pair(off, off);
+          uint64_t sums[2] = {0, 0};
+#pragma unroll
+          for (int c = 0; c < 128; c += 32) {
+            uint32_t w[16];
+#pragma unroll
+            for (int x = 0; x < 16; ++x) {
+              float a, b;
+              unpair(fma2(pair(s[c + 2 * x], s[c + 2 * x + 1]), scale2, off2), a, b);
+              a = ex2(a);
+              b = ex2(b);
+              sums[x & 1] = add2(sums[x & 1], pair(a, b));
+              w[x] = A::pack2(a, b);     // the weights as the products take them
+            }
+            tmem_st16(s_addr + c / 2, w);
+          }
+          float a, b, c, d;
+          unpair(sums[0], a, b);
+          unpair(sums[1], c, d);
+          sum += (a + b) + (c + d);
+          tmem_st_wait();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.p_full[tile]);
+      }
+      v_count += n;
+      if (ok && n > 0) {
+        ok = warp_wait(&bar.o_full[tile], o_count & 1, abort_flag, p.timeout_ns, err);
+        ++o_count;
+        tc_fence_after();
+      }
+      if (!ok) break;
+      if (!warp_live) continue;
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+      const int64_t at = token * p.heads + head, rows = static_cast<int64_t>(p.T) * p.heads;
+      bool finite = true;
+#pragma unroll
+      for (int c = 0; c < DP; c += 16) {
+        uint32_t o[16];
+        if (n > 0) {
+          tmem_ld16(o_addr + c, o);
+          tmem_ld_wait();
+        }
+        float y[16];
+#pragma unroll
+        for (int x = 0; x < 16; ++x) {
+          y[x] = n > 0 && sum != 0.0f ? __uint_as_float(o[x]) * inv : 0.0f;
+          finite &= !(fabsf(y[x]) >= INFINITY) && y[x] == y[x];
+        }
+        if (!live) continue;
+#pragma unroll
+        for (int x = 0; x < 16; x += 8) {
+          if (c + x >= p.D) continue;
+          if (t.s.splits > 1) {
+            float4 *dst = reinterpret_cast<float4 *>(p.part + (t.split * rows + at) * p.D + c + x);
+            dst[0] = make_float4(y[x], y[x + 1], y[x + 2], y[x + 3]);
+            dst[1] = make_float4(y[x + 4], y[x + 5], y[x + 6], y[x + 7]);
+          } else {
+            *reinterpret_cast<uint4 *>(p.out + at * p.D + c + x) =
+                make_uint4(A::pack2(y[x], y[x + 1]), A::pack2(y[x + 2], y[x + 3]), A::pack2(y[x + 4], y[x + 5]),
+                           A::pack2(y[x + 6], y[x + 7]));
+          }
+        }
+      }
+      if (t.s.splits > 1 && live) p.part_lse[t.split * rows + at] = sum == 0.0f ? -INFINITY : base + __log2f(sum);
+      tc_fence_before();
+      for (unsigned again = __ballot_sync(0xffffffffu, live && !finite); again; again &= again - 1)
+        exact_row<A>(p, t, tile * kRows + (warp & 3) * 32 + __ffs(again) - 1);
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp == kWarpMma) {
+      // ---------------------------------------------------------- products --
+      const uint32_t idesc_s = umma_idesc_f16kind(kRows, kKeys, A::kUmmaFormat);
+      const uint32_t idesc_o = umma_idesc_f16kind(kRows, DP, A::kUmmaFormat) | (1u << 16);     // B: columns contiguous
+      uint32_t k_count = 0, v_count = 0, q_count[2] = {0, 0}, p_count[2] = {0, 0};
+      bool ok = true;
+      auto wait = [&](uint64_t *b, uint32_t parity) {
+        ok = ok && warp_wait(b, parity & 1, abort_flag, p.timeout_ns, err);
+        return ok;
+      };
+      auto scores = [&](int x, uint32_t slot) {
+        if (elect_one()) {
+          const uint64_t a = umma_desc_sw128(smem_u32(q_smem + x * S::kTileBytes));
+          const uint64_t b = umma_desc_sw128(smem_u32(k_smem + slot * S::kTileBytes));
+#pragma unroll
+          for (int k = 0; k < DP / 16; ++k) {
+            const uint64_t at = (k >> 2) * (S::kHalfBytes >> 4) + (k & 3) * 2;
+            umma_bf16(tmem + x * 128, a + at, b + at, idesc_s, k > 0);
+          }
+          umma_commit(&bar.s_full[x]);
+        }
+        __syncwarp();
+      };
+      auto values = [&](int x, uint32_t slot, bool first) {
+        if (elect_one()) {
+          const uint64_t b = v_desc(smem_u32(v_smem + slot * S::kTileBytes), S::kHalfBytes);
+#pragma unroll
+          for (int k = 0; k < kKeys / 16; ++k)
+            umma_ts(tmem + o_col + x * DP, tmem + x * 128 + k * 8, b + k * (2048 >> 4), idesc_o, !first || k > 0);
+        }
+        __syncwarp();
+      };
+      auto commit = [&](uint64_t *b) {
+        if (elect_one()) umma_commit(b);
+        __syncwarp();
+      };
+      for (int step = 0, id; ok && (id = item_of(step)) < total; ++step) {
+        const Item t = find_item(p, id);
+        const int n = (t.k1 - t.k0 + kKeys - 1) / kKeys;
+        if (n <= 0) continue;
+        const int tiles = t.rows > kRows ? 2 : 1;
+        if (!wait(&bar.k_full[k_count % KS], k_count / KS)) break;
+        for (int x = 0; x < tiles; ++x) {
+          if (!wait(&bar.q_full[x], q_count[x]++)) break;
+          tc_fence_after();
+          scores(x, k_count % KS);
+        }
+        if (!ok) break;
+        commit(&bar.k_empty[k_count % KS]);
+        ++k_count;
+        for (int i = 0; i < n && ok; ++i, ++v_count) {
+          if (!wait(&bar.v_full[v_count % VS], v_count / VS)) break;
+          for (int x = 0; x < tiles; ++x) {
+            if (!wait(&bar.p_full[x], p_count[x]++)) break;
+            tc_fence_after();
+            values(x, v_count % VS, i == 0);
+            if (x == tiles - 1) commit(&bar.v_empty[v_count % VS]);
+            if (i + 1 < n) {
+              if (x == 0 && !wait(&bar.k_full[k_count % KS], k_count / KS)) break;
+              scores(x, k_count % KS);
+            } else {
+              commit(&bar.o_full[x]);
+            }
+          }
+          if (ok && i + 1 < n) {
+            commit(&bar.k_empty[k_count % KS]);
+            ++k_count;
+          }
+        }
+      }
+      // given up: the products in flight
+      if (*abort_flag) {
+        commit(&bar.mma_done);
+        mbar_wait_drain(&bar.mma_done, 0, p.timeout_ns);
+      }
+    } else if (warp == kWarpK || warp == kWarpV) {
+      // ------------------------------------------------------------ copies --
+      const bool is_k = warp == kWarpK;
+      const uint32_t stages = is_k ? KS : VS;
+      uint64_t *full = is_k ? bar.k_full : bar.v_full, *empty = is_k ? bar.k_empty : bar.v_empty;
+      uint8_t *ring = is_k ? k_smem : v_smem;
+      const CUtensorMap *map = is_k ? &maps.k : &maps.v;
+      const bool head_first = is_k ? maps.k_head_first : maps.v_head_first;
+      // a lane per box
+      const int per_half = kKeys / maps.box, half = lane / per_half, j = lane - half * per_half;
+      const bool has_box = half < S::kHalves;
+      uint32_t count = 0;
+      for (int step = 0, id; (id = item_of(step)) < total; ++step) {
+        const Item t = find_item(p, id);
+        const int n = (t.k1 - t.k0 + kKeys - 1) / kKeys;
+        int page = -1, row = 0;
+        auto look_up = [&](int i) {
+          const int64_t key = static_cast<int64_t>(t.k0) + static_cast<int64_t>(i) * kKeys + j * maps.box;
+          page = -1;
+          row = 0;
+          if (has_box && key < t.k1 && key + maps.box > t.first) {
+            const int x = static_cast<int>(key) / p.page_size;
+            row = static_cast<int>(key) - x * p.page_size;
+            page = page_of(p, t.b, x);
+          }
+        };
+        look_up(0);
+        bool ok = true;
+        for (int i = 0; i < n; ++i, ++count) {
+          const uint32_t slot = count % stages;
+          if (!(ok = warp_wait(&empty[slot], ((count / stages) & 1) ^ 1, abort_flag, p.timeout_ns, err))) break;
+          if (lane == 0) mbar_arrive_expect_tx(&full[slot], S::kTileBytes);
+          __syncwarp();
+          if (has_box) {
+            uint8_t *dst = ring + slot * S::kTileBytes + half * S::kHalfBytes + j * maps.box * 128;
+            tma_load_4d(dst, map, &full[slot], half * 64, head_first ? t.head : row, head_first ? row : t.head, page);
+          }
+          __syncwarp();
+          if (i + 1 < n) look_up(i + 1);
+        }
+        if (!ok) break;
+      }
+      // given up: the copies in flight
+      if (*abort_flag)
+        for (uint32_t c = count > stages ? count - stages : 0; c < count; ++c)
+          mbar_wait_drain(&full[c % stages], (c / stages) & 1, p.timeout_ns);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWarpMma) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                   const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static EncodeTiledFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void *ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(ptr);
+  });
+  return fn;
+}
+
+// A cache as a tensor of (D, rows, heads, pages), rows and heads in the order of their
+// strides; boxes of 64 columns by `box` rows of a page.
+bool encode_cache(CUtensorMap *map, int *head_first, const void *base, const int64_t (&strides)[3],
+                  const qsw_kv_cache &c, int64_t D, int box, bool f16) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const bool hf = strides[1] < strides[2];
+  const cuuint64_t rows = static_cast<cuuint64_t>(c.page_size), heads = static_cast<cuuint64_t>(c.kv_heads);
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), hf ? heads : rows, hf ? rows : heads,
+                              static_cast<cuuint64_t>(c.pages)};
+  const cuuint64_t bytes[3] = {static_cast<cuuint64_t>(hf ? strides[1] : strides[2]) * 2,
+                               static_cast<cuuint64_t>(hf ? strides[2] : strides[1]) * 2,
+                               static_cast<cuuint64_t>(strides[0]) * 2};
+  const cuuint32_t b = static_cast<cuuint32_t>(box);
+  const cuuint32_t boxes[4] = {64, hf ? 1 : b, hf ? b : 1, 1};
+  const cuuint32_t one[4] = {1, 1, 1, 1};
+  *head_first = hf;
+  return fn(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base),
+            dims, bytes, boxes, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <class A, int DP>
+cudaError_t launch_shape(const AttnParams &p, const TcMaps &maps, int grid, cudaStream_t stream) {
+  auto kernel = attn_tiles_kernel<A, DP>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<DP>::kSmem);
+  return e != cudaSuccess ? e : launch_on(kernel, dim3(static_cast<unsigned>(grid)), kThreads, Shape<DP>::kSmem, stream,
+                                          false, p, maps);
+}
+
+}  // namespace
+
+cudaError_t launch_attention_tiles(const AttnParams &p, const AttnForm &f, int act, const qsw_kv_cache &cache,
+                                   cudaStream_t stream) {
+  const bool f16 = act == ActF16::kId;
+  TcMaps maps = {};
+  // the largest power of two of a page's rows, at most a tile: no box leaves a page
+  maps.box = static_cast<int>(cache.page_size & -cache.page_size);
+  if (maps.box > kKeys) maps.box = kKeys;
+  if (!encode_cache(&maps.k, &maps.k_head_first, cache.k, cache.k_strides, cache, p.D, maps.box, f16) ||
+      !encode_cache(&maps.v, &maps.v_head_first, cache.v, cache.v_strides, cache, p.D, maps.box, f16))
+    return cudaErrorInvalidValue;
+  const int grid = static_cast<int>(f.items < f.slots ? f.items : f.slots);
+  if (p.D <= 64)
+    return f16 ? launch_shape<ActF16, 64>(p, maps, grid, stream) : launch_shape<ActBf16, 64>(p, maps, grid, stream);
+  return f16 ? launch_shape<ActF16, 128>(p, maps, grid, stream) : launch_shape<ActBf16, 128>(p, maps, grid, stream);
+}
+
+cudaError_t attention_take_errors(unsigned int *out) {
+  unsigned int v = 0, zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, g_attn_error, sizeof v);
+  if (e != cudaSuccess) return e;
+  if (v) {
+    e = cudaMemcpyToSymbol(g_attn_error, &zero, sizeof zero);
+    if (e != cudaSuccess) return e;
+  }
+  *out = v;
+  return cudaSuccess;
+}
+
+}  // namespace qsw

@@ -185,6 +185,7 @@ struct AttentionArgs {
 };
 // Bytes of split results (0: no history is split).
 size_t attention_workspace_bytes(int64_t T, int64_t B, int64_t heads, int64_t kv_heads, int64_t D, int num_sms);
+cudaError_t attention_take_errors(unsigned int *out);
 cudaError_t launch_paged_attention(const AttentionArgs &a, int num_sms, uint64_t timeout_ns, cudaStream_t stream);
 
 // Shared state of the C entry points (qsw_api.cu).

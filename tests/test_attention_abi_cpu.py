@@ -58,7 +58,7 @@ def test_no_tokens_is_a_noop(lib):  # noqa: F811
     (dict(table=None), INVALID), (dict(table=FAKE + 4), UNSUPPORTED), (dict(D=1026), UNSUPPORTED),
     (dict(H=4097), UNSUPPORTED), (dict(T=(1 << 30) + 1), UNSUPPORTED), (dict(T=1, x=heads(0)), INVALID),
     (dict(T=1, out=0), INVALID), (dict(T=1, x=heads(FAKE + 1)), UNSUPPORTED), (dict(T=1, out=FAKE + 1), UNSUPPORTED),
-    (dict(T=1, positions=FAKE + 2), UNSUPPORTED)], ids=str)
+    (dict(T=1, positions=FAKE + 2), UNSUPPORTED)])
 def test_rope_rejects(lib, kw, code):  # noqa: F811
     assert rope(lib, **kw) == code
 
@@ -71,7 +71,7 @@ BAD_CACHES = [
     (dict(v_strides=(2044, 1024, 64)), UNSUPPORTED), (dict(v_strides=(2048, -1024, 64)), INVALID)]
 
 
-@pytest.mark.parametrize("kw,code", BAD_CACHES, ids=str)
+@pytest.mark.parametrize("kw,code", BAD_CACHES)
 def test_bad_caches(lib, kw, code):  # noqa: F811
     assert append(lib, c=cache(**kw)) == plan(lib, c=cache(**kw)) == attend(lib, c=cache(**kw)) == code
 
@@ -85,7 +85,7 @@ def test_head_sizes(lib, D, code):  # noqa: F811
     (dict(T=-1), INVALID), (dict(H=0), INVALID), (dict(rot=66), INVALID), (dict(act=2), INVALID),
     (dict(T=1, slots=0), INVALID), (dict(T=1, k=heads(0)), INVALID), (dict(T=1, v=heads(0)), INVALID),
     (dict(T=1, q=heads(0)), INVALID), (dict(T=1, q_out=0), INVALID), (dict(T=1, slots=FAKE + 1), UNSUPPORTED),
-    (dict(T=1, k=heads(FAKE + 1)), UNSUPPORTED), (dict(q=None, H=0), OK)], ids=str)
+    (dict(T=1, k=heads(FAKE + 1)), UNSUPPORTED), (dict(q=None, H=0), OK)])
 def test_append_rejects(lib, kw, code):  # noqa: F811
     assert append(lib, **kw) == code
 
@@ -98,7 +98,7 @@ BAD_STEPS = [
     (dict(T=1, work=FAKE + 8), UNSUPPORTED), (dict(T=1, table=FAKE + 2), UNSUPPORTED)]
 
 
-@pytest.mark.parametrize("kw,code", BAD_STEPS, ids=str)
+@pytest.mark.parametrize("kw,code", BAD_STEPS)
 def test_bad_steps(lib, kw, code):  # noqa: F811
     assert plan(lib, **kw) == attend(lib, **kw) == code
 
@@ -108,7 +108,7 @@ def test_bad_steps(lib, kw, code):  # noqa: F811
     (dict(act=3), INVALID), (dict(T=1, q=heads(0)), INVALID), (dict(T=1, out=0), INVALID),
     (dict(T=1, q=heads(FAKE + 8)), UNSUPPORTED), (dict(T=1, out=FAKE + 8), UNSUPPORTED),
     (dict(T=1, q=heads(token=516)), UNSUPPORTED), (dict(T=1, q=heads(head=68)), UNSUPPORTED),
-    (dict(T=1, ws=FAKE + 128), UNSUPPORTED)], ids=str)
+    (dict(T=1, ws=FAKE + 128), UNSUPPORTED)])
 def test_attention_rejects(lib, kw, code):  # noqa: F811
     assert attend(lib, **kw) == code
 
