@@ -10,12 +10,15 @@
 // tile's softmax runs under the other's products.  12 warps: warps 0-3 and 4-7 each own a
 // row tile (a thread per row: row maximum and sum need no exchange), warp 8 issues the
 // products, warps 9 and 10 copy K and V pages by TMA (a box per page, or per 8 to 128 rows
-// of one; a page outside the cache is a coordinate outside the tensor and reads zeros).
+// of one; a page outside the cache is a coordinate outside the tensor and reads zeros), warp
+// 11 works out the items ahead.
 // P lies where S was: the products that read P and overwrite S run in the order of issue.
 //
 // The base of a row is raised (and O rescaled in tensor memory) only when a score passes
 // it by 8, so that weights reach 256 at most and most tiles leave O alone.
+#include <climits>
 #include <mutex>
+#include <type_traits>
 
 #include "qsw_attention.cuh"
 
@@ -28,7 +31,9 @@ __device__ unsigned int g_attn_error;
 constexpr int kRows = 128;            // of a tile
 constexpr int kKeys = 128;
 constexpr int kThreads = 384;
-constexpr int kWarpMma = 8, kWarpK = 9, kWarpV = 10;
+constexpr int kWarpMma = 8, kWarpK = 9, kWarpV = 10, kWarpItems = 11;
+constexpr int kItems = 4;             // items worked out ahead
+constexpr int kItemReaders = 11;      // warps that read them
 constexpr float kRaise = 8.0f;
 
 template <int DP>
@@ -120,6 +125,20 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// A wait of a whole warp, one vote where the phase is complete (the products' issuer waits
+// four times a tile, and beside eight busy warps every instruction of it counts).
+__device__ __forceinline__ bool wait_all(uint64_t *bar, uint32_t parity, volatile int *abort, uint64_t timeout_ns,
+                                         unsigned int *err) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, timeout_ns, err));
+}
+
 // The item of a CTA's step: every second wave in reverse, since items come longest first.
 __device__ __forceinline__ int item_of(int step) {
   const int G = static_cast<int>(gridDim.x), c = static_cast<int>(blockIdx.x);
@@ -128,9 +147,30 @@ __device__ __forceinline__ int item_of(int step) {
 
 struct Barriers {
   uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
-  uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
+  uint64_t q_full[2], s_full[2], p_half[2], p_full[2], o_full[2];
+  uint64_t item_full[kItems], item_empty[kItems];
   uint64_t mma_done;
 };
+
+// A reader's place in the ring of items; the item it is at stays until it moves on.
+struct ItemCursor {
+  uint32_t at = 0;
+  // Waits for the next item; null at the end, or when given up.
+  __device__ __forceinline__ const Item *next(Barriers &bar, const Item *items, volatile int *abort, uint64_t timeout_ns,
+                                              unsigned int *err) {
+    const uint32_t slot = at % kItems;
+    if (!wait_all(&bar.item_full[slot], (at / kItems) & 1, abort, timeout_ns, err)) return nullptr;
+    ++at;
+    return items[slot].rows > 0 ? items + slot : nullptr;
+  }
+  // The item before the last `ahead` ones is no longer needed.
+  __device__ __forceinline__ void done(Barriers &bar, uint32_t ahead) {
+    __syncwarp();
+    if (lane_id() == 0) mbar_arrive(&bar.item_empty[(at - 1 - ahead) % kItems]);
+  }
+};
+
+__device__ __forceinline__ int tiles_of_item(const Item *t) { return (t->k1 - t->k0 + kKeys - 1) / kKeys; }
 
 template <class A, int DP>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -141,6 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t *q_smem = smem, *k_smem = smem + 2 * S::kTileBytes, *v_smem = k_smem + KS * S::kTileBytes;
   __shared__ Barriers bar;
+  __shared__ Item items[kItems];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_word;
   volatile int *abort_flag = &abort_word;
@@ -158,8 +199,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar.q_full[i], 4);
       mbar_init(&bar.s_full[i], 1);
+      mbar_init(&bar.p_half[i], 4);
       mbar_init(&bar.p_full[i], 4);
       mbar_init(&bar.o_full[i], 1);
+    }
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(&bar.item_full[i], 1);
+      mbar_init(&bar.item_empty[i], kItemReaders);
     }
     mbar_init(&bar.mma_done, 1);
     abort_word = 0;
@@ -179,7 +225,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
   griddep_wait();
   griddep_launch_dependents();
-  const int total = __ldg(p.plan.head);
   // Tensor memory: S (and P) of the two row tiles, then O of both.
   const uint32_t o_col = 256;
 
@@ -192,47 +237,84 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r = (warp & 3) * 32 + lane;                              // row of the tile
     uint8_t *q_tile = q_smem + tile * S::kTileBytes;
     uint32_t s_count = 0, o_count = 0, v_count = 0;
-    for (int step = 0, id; (id = item_of(step)) < total; ++step) {
-      const Item t = find_item(p, id);
-      const int n = (t.k1 - t.k0 + kKeys - 1) / kKeys;
-      const int mine = t.rows - tile * kRows;                          // live rows of the tile
-      if (mine <= 0) {
-        v_count += n;
-        continue;
-      }
-      const bool live = r < mine;
+    const float scale = p.scale_log2;
+    const bool first_half = tile == 0;
+
+    // The tile's rows of an item, from q into shared memory as the products take them: this
+    // warp's 32, a row to 16 (8) lanes.
+    auto load_q = [&](const Item *t) {
+      constexpr int CH = DP / 8, PER = 32 / CH;      // lanes of a row, rows at once
+      const int x = tile * kRows + r;
       int64_t token;
       int head, pos;
-      row_of(p, t, live ? tile * kRows + r : 0, token, head, pos);
-      float base = -INFINITY, sum = 0.0f;
-      bool ok = true;
-      if (n > 0) {
-        // the row of q into shared memory, as the products take it
-        const uint16_t *src = p.q + token * p.q_t + head * p.q_h;
-        uint4 x[DP / 8];
+      row_of(p, *t, x < t->rows ? x : 0, token, head, pos);
+      const uint64_t row = x < t->rows ? reinterpret_cast<uint64_t>(p.q + token * p.q_t + head * p.q_h) : 0;
+      const int c = lane % CH;
 #pragma unroll
-        for (int c = 0; c < DP / 8; ++c)
-          x[c] = live && c * 8 < p.D ? __ldg(reinterpret_cast<const uint4 *>(src) + c) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int c = 0; c < DP / 8; ++c)
-          *reinterpret_cast<uint4 *>(q_tile + (c >> 3) * S::kHalfBytes + r * 128 + (((c ^ r) & 7) << 4)) = x[c];
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.q_full[tile]);
+      for (int i = 0; i < 32 / PER; ++i) {
+        const int from = i * PER + lane / CH, y = (warp & 3) * 32 + from;
+        const uint64_t src = __shfl_sync(0xffffffffu, row, from);
+        const bool ok = src != 0 && c * 8 < p.D;
+        const uint32_t dst = smem_u32(q_tile + (c >> 3) * S::kHalfBytes + y * 128 + (((c ^ y) & 7) << 4));
+        const void *at = ok ? reinterpret_cast<const uint16_t *>(src) + c * 8 : p.q;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(at), "r"(ok ? 16u : 0u) : "memory");
       }
-      const bool warp_live = (warp & 3) * 32 < mine;
-      const float scale = p.scale_log2;
+    };
+    auto q_loaded = [&] {
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.q_full[tile]);
+    };
+    auto needs_q = [&](const Item *t) { return t->rows > tile * kRows && t->k1 > t->k0; };
+
+    ItemCursor cursor;
+    const Item *t = cursor.next(bar, items, abort_flag, p.timeout_ns, err);
+    if (t && needs_q(t)) {
+      load_q(t);
+      q_loaded();
+    }
+    bool ok = true;
+    while (t) {
+      const int n = tiles_of_item(t);
+      const int mine = t->rows - tile * kRows;                          // live rows of the tile
+      const Item *after = nullptr;
+      if (mine <= 0) {
+        v_count += n;
+        after = cursor.next(bar, items, abort_flag, p.timeout_ns, err);
+        if (after && needs_q(after)) {
+          load_q(after);
+          q_loaded();
+        }
+        cursor.done(bar, 1);
+        t = after;
+        continue;
+      }
+      const bool live = r < mine, warp_live = (warp & 3) * 32 < mine;
+      int64_t token;
+      int head, pos;
+      row_of(p, *t, live ? tile * kRows + r : 0, token, head, pos);
+      // keys that the row sees, from the item's first on: [lo, hi); a row of nobody all, so that
+      // it asks for no mask
+      const int hi = live ? min(pos + 1, t->k1) - t->k0 : INT_MAX;
+      const int lo = live && p.window ? pos - p.window + 1 - t->k0 : 0;
+      float base = live ? -INFINITY : 0.0f, sum = 0.0f;
       for (int i = 0; i < n; ++i, ++s_count) {
-        const int key0 = t.k0 + i * kKeys;
-        if (!(ok = warp_wait(&bar.s_full[tile], s_count & 1, abort_flag, p.timeout_ns, err))) break;
+        const int key0 = t->k0 + i * kKeys;
+        if (!(ok = wait_all(&bar.s_full[tile], s_count & 1, abort_flag, p.timeout_ns, err))) break;
         tc_fence_after();
-        if (tile == 0 && (key0 + kKeys > t.k1 || key0 < t.first)) {
+        if (i == n - 1) {
+          // the last scores are out: the next item's rows of q take the place of these
+          after = cursor.next(bar, items, abort_flag, p.timeout_ns, err);
+          if (after && needs_q(after)) load_q(after);
+        }
+        if (first_half && (key0 + kKeys > t->k1 || key0 < t->first)) {
           // rows of V that no row of the item sees may hold anything: a weight of 0 does
           // not take out infinities or NaN.  (Before both tiles' products: tile 0's go
           // first.)
           const uint32_t at = v_count + i;
-          if (!(ok = warp_wait(&bar.v_full[at % VS], (at / VS) & 1, abort_flag, p.timeout_ns, err))) break;
-          if (key0 + r >= t.k1 || key0 + r < t.first) {
+          if (!(ok = wait_all(&bar.v_full[at % VS], (at / VS) & 1, abort_flag, p.timeout_ns, err))) break;
+          if (key0 + r >= t->k1 || key0 + r < t->first) {
             uint8_t *v = v_smem + (at % VS) * S::kTileBytes + r * 128;
 #pragma unroll
             for (int c = 0; c < DP / 8; ++c)
@@ -245,20 +327,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + c * 32, reinterpret_cast<uint32_t *>(s) + c * 32);
           tmem_ld_wait();
-          // keys of the tile that the row sees: columns [lo, hi)
-          const int hi = live ? min(pos + 1, t.k1) - key0 : 0;
-          const int lo = p.window ? pos - p.window + 1 - key0 : 0;
-          if (!__all_sync(0xffffffffu, hi >= kKeys && lo <= 0)) {
+          const int h = hi - i * kKeys, l = lo - i * kKeys;
+          if (!__all_sync(0xffffffffu, h >= kKeys && l <= 0)) {
 #pragma unroll
-            for (int c = 0; c < 128; ++c) s[c] = c < hi && c >= lo ? s[c] : -INFINITY;
+            for (int c = 0; c < 128; ++c) s[c] = c < h && c >= l ? s[c] : -INFINITY;
           }
           float top[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-          for (int c = 4; c < 128; c += 4)
+          for (int c = 4; c < 124; c += 8)
 #pragma unroll
-            for (int x = 0; x < 4; ++x) top[x] = fmaxf(top[x], s[c + x]);
-          const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
-          const bool raise = most > base + kRaise || (base == -INFINITY && most > -INFINITY);
+            for (int x = 0; x < 4; ++x) top[x] = max3(top[x], s[c + 2 * x], s[c + 2 * x + 1]);
+          top[0] = max3(top[0], s[124], s[125]);
+          top[1] = max3(top[1], s[126], s[127]);
+          const float most = fmaxf(max3(top[0], top[1], top[2]), top[3]) * scale;
+          const bool raise = most > base + kRaise;
           if (__any_sync(0xffffffffu, raise)) {
             const float now = raise ? most : base;
             const float shrink = raise ? ex2(base - now) : 1.0f;
@@ -292,132 +374,177 @@ __global__ void __launch_bounds__(kThreads, 1)
               w[x] = A::pack2(a, b);     // the weights as the products take them
             }
             tmem_st16(s_addr + c / 2, w);
+            if (c == 32) {
+              // half of the weights: their products start under the other half's exponentials
+              tmem_st_wait();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&bar.p_half[tile]);
+            }
           }
           float a, b, c, d;
           unpair(sums[0], a, b);
           unpair(sums[1], c, d);
           sum += (a + b) + (c + d);
           tmem_st_wait();
+        } else if (lane == 0) {
+          mbar_arrive(&bar.p_half[tile]);
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.p_full[tile]);
       }
+      if (!ok) break;
       v_count += n;
-      if (ok && n > 0) {
-        ok = warp_wait(&bar.o_full[tile], o_count & 1, abort_flag, p.timeout_ns, err);
+      if (n == 0) {
+        after = cursor.next(bar, items, abort_flag, p.timeout_ns, err);
+        if (after && needs_q(after)) load_q(after);
+      }
+      // the next item's scores run under this one's last steps
+      if (after && needs_q(after)) q_loaded();
+      if (n > 0) {
+        if (!(ok = wait_all(&bar.o_full[tile], o_count & 1, abort_flag, p.timeout_ns, err))) break;
         ++o_count;
         tc_fence_after();
       }
-      if (!ok) break;
-      if (!warp_live) continue;
-      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-      const int64_t at = token * p.heads + head, rows = static_cast<int64_t>(p.T) * p.heads;
-      bool finite = true;
+      if (warp_live) {
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        const int64_t at = token * p.heads + head, rows = static_cast<int64_t>(p.T) * p.heads;
+        const bool split = t->s.splits > 1;
+        const int64_t part_at = t->split * rows + at;
+        float odd = 0.0f;             // 0 times every value: NaN if one is not finite
 #pragma unroll
-      for (int c = 0; c < DP; c += 16) {
-        uint32_t o[16];
-        if (n > 0) {
-          tmem_ld16(o_addr + c, o);
-          tmem_ld_wait();
-        }
-        float y[16];
+        for (int c = 0; c < DP; c += 32) {
+          uint32_t o[32];
+          if (n > 0) {
+            tmem_ld32(o_addr + c, o);
+            tmem_ld_wait();
+          }
 #pragma unroll
-        for (int x = 0; x < 16; ++x) {
-          y[x] = n > 0 && sum != 0.0f ? __uint_as_float(o[x]) * inv : 0.0f;
-          finite &= !(fabsf(y[x]) >= INFINITY) && y[x] == y[x];
-        }
-        if (!live) continue;
+          for (int x = 0; x < 32; x += 8) {
+            float y[8];
 #pragma unroll
-        for (int x = 0; x < 16; x += 8) {
-          if (c + x >= p.D) continue;
-          if (t.s.splits > 1) {
-            float4 *dst = reinterpret_cast<float4 *>(p.part + (t.split * rows + at) * p.D + c + x);
-            dst[0] = make_float4(y[x], y[x + 1], y[x + 2], y[x + 3]);
-            dst[1] = make_float4(y[x + 4], y[x + 5], y[x + 6], y[x + 7]);
-          } else {
-            *reinterpret_cast<uint4 *>(p.out + at * p.D + c + x) =
-                make_uint4(A::pack2(y[x], y[x + 1]), A::pack2(y[x + 2], y[x + 3]), A::pack2(y[x + 4], y[x + 5]),
-                           A::pack2(y[x + 6], y[x + 7]));
+            for (int z = 0; z < 8; ++z) {
+              y[z] = sum == 0.0f ? 0.0f : __uint_as_float(o[x + z]) * inv;
+              odd = fmaf(y[z], 0.0f, odd);
+            }
+            if (!live || c + x >= p.D) continue;
+            if (split) {
+              float4 *dst = reinterpret_cast<float4 *>(p.part + part_at * p.D + c + x);
+              dst[0] = make_float4(y[0], y[1], y[2], y[3]);
+              dst[1] = make_float4(y[4], y[5], y[6], y[7]);
+            } else {
+              *reinterpret_cast<uint4 *>(p.out + at * p.D + c + x) =
+                  make_uint4(A::pack2(y[0], y[1]), A::pack2(y[2], y[3]), A::pack2(y[4], y[5]), A::pack2(y[6], y[7]));
+            }
           }
         }
+        if (split && live) p.part_lse[part_at] = sum == 0.0f ? -INFINITY : base + __log2f(sum);
+        tc_fence_before();
+        for (unsigned x = __ballot_sync(0xffffffffu, live && odd != 0.0f); x; x &= x - 1)
+          exact_row<A>(p, *t, tile * kRows + (warp & 3) * 32 + __ffs(x) - 1);
       }
-      if (t.s.splits > 1 && live) p.part_lse[t.split * rows + at] = sum == 0.0f ? -INFINITY : base + __log2f(sum);
-      tc_fence_before();
-      for (unsigned again = __ballot_sync(0xffffffffu, live && !finite); again; again &= again - 1)
-        exact_row<A>(p, t, tile * kRows + (warp & 3) * 32 + __ffs(again) - 1);
+      cursor.done(bar, 1);
+      t = after;
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == kWarpMma) {
       // ---------------------------------------------------------- products --
       const uint32_t idesc_s = umma_idesc_f16kind(kRows, kKeys, A::kUmmaFormat);
       const uint32_t idesc_o = umma_idesc_f16kind(kRows, DP, A::kUmmaFormat) | (1u << 16);     // B: columns contiguous
-      uint32_t k_count = 0, v_count = 0, q_count[2] = {0, 0}, p_count[2] = {0, 0};
+      uint32_t q_count[2] = {0, 0}, p_count[2] = {0, 0};
       bool ok = true;
-      auto wait = [&](uint64_t *b, uint32_t parity) {
-        ok = ok && warp_wait(b, parity & 1, abort_flag, p.timeout_ns, err);
-        return ok;
-      };
-      auto scores = [&](int x, uint32_t slot) {
-        if (elect_one()) {
-          const uint64_t a = umma_desc_sw128(smem_u32(q_smem + x * S::kTileBytes));
-          const uint64_t b = umma_desc_sw128(smem_u32(k_smem + slot * S::kTileBytes));
-#pragma unroll
-          for (int k = 0; k < DP / 16; ++k) {
-            const uint64_t at = (k >> 2) * (S::kHalfBytes >> 4) + (k & 3) * 2;
-            umma_bf16(tmem + x * 128, a + at, b + at, idesc_s, k > 0);
-          }
-          umma_commit(&bar.s_full[x]);
-        }
-        __syncwarp();
-      };
-      auto values = [&](int x, uint32_t slot, bool first) {
-        if (elect_one()) {
-          const uint64_t b = v_desc(smem_u32(v_smem + slot * S::kTileBytes), S::kHalfBytes);
-#pragma unroll
-          for (int k = 0; k < kKeys / 16; ++k)
-            umma_ts(tmem + o_col + x * DP, tmem + x * 128 + k * 8, b + k * (2048 >> 4), idesc_o, !first || k > 0);
-        }
-        __syncwarp();
-      };
       auto commit = [&](uint64_t *b) {
         if (elect_one()) umma_commit(b);
         __syncwarp();
       };
-      for (int step = 0, id; ok && (id = item_of(step)) < total; ++step) {
-        const Item t = find_item(p, id);
-        const int n = (t.k1 - t.k0 + kKeys - 1) / kKeys;
-        if (n <= 0) continue;
-        const int tiles = t.rows > kRows ? 2 : 1;
-        if (!wait(&bar.k_full[k_count % KS], k_count / KS)) break;
-        for (int x = 0; x < tiles; ++x) {
-          if (!wait(&bar.q_full[x], q_count[x]++)) break;
+      auto wait = [&](uint64_t *b, uint32_t parity) {
+        ok = ok && wait_all(b, parity & 1, abort_flag, p.timeout_ns, err);
+        return ok;
+      };
+      // (a tile's number and the loop bodies are fixed at compile time: with either left to
+      // run time the operands were no longer uniform registers, and an instruction took
+      // over 100 cycles to issue instead of 40)
+      const uint64_t q_desc = umma_desc_sw128(smem_u32(q_smem)), k_desc = umma_desc_sw128(smem_u32(k_smem));
+      const uint64_t v_desc0 = v_desc(smem_u32(v_smem), S::kHalfBytes);
+      auto scores = [&](auto x, uint32_t slot, uint64_t *done) {
+        if (elect_one()) {
+          const uint64_t a = q_desc + x.value * (S::kTileBytes >> 4), b = k_desc + slot * (S::kTileBytes >> 4);
+#pragma unroll
+          for (int k = 0; k < DP / 16; ++k) {
+            const uint64_t at = (k >> 2) * (S::kHalfBytes >> 4) + (k & 3) * 2;
+            umma_bf16(tmem + x.value * 128, a + at, b + at, idesc_s, k > 0);
+          }
+          umma_commit(&bar.s_full[x.value]);
+          if (done) umma_commit(done);
+        }
+        __syncwarp();
+      };
+      // the products of a tile's weights, half by half; false when given up
+      auto values = [&](auto x, uint32_t slot, uint32_t first, uint64_t *done) {
+        const uint64_t b = v_desc0 + slot * (S::kTileBytes >> 4);
+        auto half = [&](auto from) {
           tc_fence_after();
-          scores(x, k_count % KS);
-        }
-        if (!ok) break;
-        commit(&bar.k_empty[k_count % KS]);
-        ++k_count;
-        for (int i = 0; i < n && ok; ++i, ++v_count) {
-          if (!wait(&bar.v_full[v_count % VS], v_count / VS)) break;
-          for (int x = 0; x < tiles; ++x) {
-            if (!wait(&bar.p_full[x], p_count[x]++)) break;
-            tc_fence_after();
-            values(x, v_count % VS, i == 0);
-            if (x == tiles - 1) commit(&bar.v_empty[v_count % VS]);
-            if (i + 1 < n) {
-              if (x == 0 && !wait(&bar.k_full[k_count % KS], k_count / KS)) break;
-              scores(x, k_count % KS);
-            } else {
-              commit(&bar.o_full[x]);
-            }
+          if (elect_one()) {
+#pragma unroll
+            for (int k = from.value; k < from.value + kKeys / 32; ++k)
+              umma_ts(tmem + o_col + x.value * DP, tmem + x.value * 128 + k * 8, b + k * (2048 >> 4), idesc_o,
+                      k > 0 ? 1u : first ^ 1u);
+            if (from.value > 0 && done) umma_commit(done);
           }
-          if (ok && i + 1 < n) {
-            commit(&bar.k_empty[k_count % KS]);
-            ++k_count;
-          }
+          __syncwarp();
+        };
+        const uint32_t parity = p_count[x.value]++;
+        if (!wait(&bar.p_half[x.value], parity)) return false;
+        half(std::integral_constant<int, 0>{});
+        if (!wait(&bar.p_full[x.value], parity)) return false;
+        half(std::integral_constant<int, kKeys / 32>{});
+        return true;
+      };
+      constexpr std::integral_constant<int, 0> X0{};
+      constexpr std::integral_constant<int, 1> X1{};
+      uint32_t k_slot = 0, k_turn = 0, v_slot = 0, v_turn = 0;
+      auto next_k = [&] { k_slot = k_slot + 1 == KS ? (k_turn ^= 1, 0) : k_slot + 1; };
+      auto next_v = [&] { v_slot = v_slot + 1 == VS ? (v_turn ^= 1, 0) : v_slot + 1; };
+      ItemCursor cursor;
+#pragma unroll 1
+      for (const Item *t; ok && (t = cursor.next(bar, items, abort_flag, p.timeout_ns, err));) {
+        // (from one lane: the compiler then knows them, and what the loop carries, as uniform)
+        const int n = __shfl_sync(0xffffffffu, tiles_of_item(t), 0);
+        const bool two = __shfl_sync(0xffffffffu, t->rows, 0) > kRows;
+        cursor.done(bar, 0);
+        if (n <= 0) continue;
+        if (!wait(&bar.k_full[k_slot], k_turn) || !wait(&bar.q_full[0], q_count[0]++)) break;
+        tc_fence_after();
+        scores(X0, k_slot, two ? nullptr : &bar.k_empty[k_slot]);
+        if (two) {
+          if (!wait(&bar.q_full[1], q_count[1]++)) break;
+          tc_fence_after();
+          scores(X1, k_slot, &bar.k_empty[k_slot]);
         }
+        next_k();
+#pragma unroll 1
+        for (int i = 0; i < n - 1; ++i) {
+          if (!wait(&bar.k_full[k_slot], k_turn) || !wait(&bar.v_full[v_slot], v_turn)) break;
+          if (!values(X0, v_slot, i == 0, two ? nullptr : &bar.v_empty[v_slot])) break;
+          scores(X0, k_slot, two ? nullptr : &bar.k_empty[k_slot]);
+          if (two) {
+            if (!values(X1, v_slot, i == 0, &bar.v_empty[v_slot])) break;
+            scores(X1, k_slot, &bar.k_empty[k_slot]);
+          }
+          next_v();
+          next_k();
+        }
+        if (!ok || !wait(&bar.v_full[v_slot], v_turn)) break;
+        if (!values(X0, v_slot, n == 1, two ? nullptr : &bar.v_empty[v_slot])) break;
+        commit(&bar.o_full[0]);
+        if (two) {
+          if (!values(X1, v_slot, n == 1, &bar.v_empty[v_slot])) break;
+          commit(&bar.o_full[1]);
+        }
+        next_v();
       }
       // given up: the products in flight
       if (*abort_flag) {
@@ -436,9 +563,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int per_half = kKeys / maps.box, half = lane / per_half, j = lane - half * per_half;
       const bool has_box = half < S::kHalves;
       uint32_t count = 0;
-      for (int step = 0, id; (id = item_of(step)) < total; ++step) {
-        const Item t = find_item(p, id);
-        const int n = (t.k1 - t.k0 + kKeys - 1) / kKeys;
+      ItemCursor cursor;
+      for (const Item *next; (next = cursor.next(bar, items, abort_flag, p.timeout_ns, err));) {
+        const Item t = *next;
+        const int n = tiles_of_item(next);
+        cursor.done(bar, 0);
         int page = -1, row = 0;
         auto look_up = [&](int i) {
           const int64_t key = static_cast<int64_t>(t.k0) + static_cast<int64_t>(i) * kKeys + j * maps.box;
@@ -454,7 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         for (int i = 0; i < n; ++i, ++count) {
           const uint32_t slot = count % stages;
-          if (!(ok = warp_wait(&empty[slot], ((count / stages) & 1) ^ 1, abort_flag, p.timeout_ns, err))) break;
+          if (!(ok = wait_all(&empty[slot], ((count / stages) & 1) ^ 1, abort_flag, p.timeout_ns, err))) break;
           if (lane == 0) mbar_arrive_expect_tx(&full[slot], S::kTileBytes);
           __syncwarp();
           if (has_box) {
@@ -470,6 +599,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (*abort_flag)
         for (uint32_t c = count > stages ? count - stages : 0; c < count; ++c)
           mbar_wait_drain(&full[c % stages], (c / stages) & 1, p.timeout_ns);
+    } else if (warp == kWarpItems) {
+      // ------------------------------------------------------------- items --
+      const int total = __ldg(p.plan.head);
+      for (int step = 0;; ++step) {
+        const int slot = step % kItems, id = item_of(step);
+        Item t;
+        t.rows = 0;
+        if (id < total) t = find_item(p, id);
+        if (!wait_all(&bar.item_empty[slot], ((step / kItems) & 1) ^ 1, abort_flag, p.timeout_ns, err)) break;
+        if (lane == 0) {
+          items[slot] = t;
+          mbar_arrive(&bar.item_full[slot]);
+        }
+        __syncwarp();
+        if (id >= total) break;
+      }
     }
   }
   tc_fence_before();
