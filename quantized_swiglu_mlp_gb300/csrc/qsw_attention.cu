@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     }
     s.splits = 1;
     s.chunk = (keys + p.tile_keys - 1) / p.tile_keys;       // tiles, for now
-    s.pad[0] = (mean + p.tile_keys - 1) / p.tile_keys;
+    s.pad = (mean + p.tile_keys - 1) / p.tile_keys;
     if (s.blocks) longest = max(longest, s.chunk);
     p.out.rec[b] = s;
   }
@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
       const int splits = max(1, min(p.max_splits, (s.chunk + c - 1) / c));
       const float n = static_cast<float>(s.blocks) * p.kv_heads;
       items += n * splits;
-      work += n * (s.pad[0] + kItemCost * splits);
+      work += n * (s.pad + kItemCost * splits);
       most = fmaxf(most, static_cast<float>((s.chunk + splits - 1) / splits));
     }
 #pragma unroll
@@ -135,10 +135,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
       items += __shfl_xor_sync(0xffffffffu, items, d);
       most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
     }
-    // items that do not run at once end unevenly: half an item more
-    const float tail = items > p.cta_slots ? 0.5f : 0.0f;
-    const float cost =
-        fmaxf(most + kItemCost, work / p.cta_slots + tail * (most + kItemCost)) + (parts > 1 ? 1.0f : 0.0f);
+    // whole waves of items (exact for equal ones)
+    const float waves = items / p.cta_slots;
+    const float cost = fmaxf(most + kItemCost, work / p.cta_slots * (ceilf(waves) / waves)) + (parts > 1 ? 1.0f : 0.0f);
     // the cheapest, the fewest splits among equals
     if (lane == 0)
       atomicMin(&best, static_cast<unsigned long long>(__float_as_uint(cost)) << 32 | static_cast<unsigned>(warp));
@@ -151,14 +150,13 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
   for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
     const int b = b0 + tid;
     int items = 0;
+    SeqRec s;
     if (b < p.B) {
-      SeqRec s = p.out.rec[b];
+      s = p.out.rec[b];
       if (s.blocks && p.max_splits > 1)
         s.splits = max(1, min(p.max_splits, (s.chunk + chunk - 1) / chunk));
       any |= s.splits > 1;
       s.chunk = max(1, (s.chunk + s.splits - 1) / s.splits) * p.tile_keys;
-      s.pad[0] = 0;
-      p.out.rec[b] = s;
       items = s.blocks * s.splits * p.kv_heads;
     }
     int sum = items;
@@ -172,13 +170,16 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     int before = lane < warp ? sums[lane] : 0, all = sums[lane];
     before = __reduce_add_sync(0xffffffffu, before);
     all = __reduce_add_sync(0xffffffffu, all);
-    if (b < p.B) p.out.first[b] = total + before + sum - items;
+    if (b < p.B) {
+      s.first = total + before + sum - items;
+      s.pad = 0;
+      p.out.rec[b] = s;
+    }
     total += all;
     __syncthreads();
   }
   any = __syncthreads_or(any);
   if (tid == 0) {
-    p.out.first[p.B] = total;
     p.out.head[0] = total;
     p.out.head[1] = any;
   }
@@ -241,8 +242,9 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2) attn_rows_kernel(const __gr
   const int ch = lane % CH, sub = lane / CH;
   const uint32_t mine = smem_u32(ring) + warp * kRowStages * STAGE;
 
-  for (int id = static_cast<int>(blockIdx.x); id < total; id += static_cast<int>(gridDim.x)) {
+  for (int id = static_cast<int>(blockIdx.x);; id += static_cast<int>(gridDim.x)) {
     const Item t = find_item(p, id);
+    if (id >= total) break;
     __syncthreads();      // the ring of the item before is free, its flags have been read
     if (tid == 0) redo = 0;
     const int runs = (t.k1 - t.k0 + kSubKeys - 1) / kSubKeys;       // of the item
@@ -467,45 +469,58 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2) attn_rows_kernel(const __gr
 // -------------------------------------------------------------------- join --
 
 // Rows of split sequences: o = sum_s 2^(lse_s - top) o_s / sum_s 2^(lse_s - top), in the
-// order of the splits.  A warp per row.
+// order of the splits.  A warp per row; a split without a key the row sees holds zeros
+// and -infinity.  What the plan says is read before the attention has ended: it was
+// complete before that began.
 template <class A>
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ AttnParams p) {
-  griddep_wait();
-  griddep_launch_dependents();
-  if (!__ldg(p.plan.head + 1)) return;
-  const int lane = static_cast<int>(lane_id());
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5), rows = static_cast<int64_t>(p.T) * p.heads;
-  if (row >= rows) return;
-  const int b = __ldg(p.plan.seq_of + row / p.heads);
-  if (b < 0) return;
-  const int splits = __ldg(&p.plan.rec[b].splits);
-  if (splits <= 1) return;
-  float top = -INFINITY;
-  for (int s = lane; s < splits; s += 32) top = fmaxf(top, p.part_lse[s * rows + row]);
+  constexpr int kStep = 8;       // splits in flight
+  const int lane = static_cast<int>(lane_id()), c = lane * 4;
+  const int64_t rows = static_cast<int64_t>(p.T) * p.heads;
+  const int any = __ldg(p.plan.head + 1);
+  int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  bool waited = false;
+  for (; any && row < rows; row += static_cast<int64_t>(gridDim.x) * 8) {
+    const int b = __ldg(p.plan.seq_of + row / p.heads);
+    const int splits = b < 0 ? 1 : __ldg(&p.plan.rec[b].splits);
+    if (!waited) griddep_wait();
+    waited = true;
+    if (splits <= 1) continue;
+    float top = -INFINITY, all = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int s0 = 0; s0 < splits; s0 += kStep) {
+      float lse[kStep];
+      float4 v[kStep];
 #pragma unroll
-  for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-  const float base = top == -INFINITY ? 0.0f : top;
-  const int c = lane * 4;
-  float o[4] = {0.0f, 0.0f, 0.0f, 0.0f}, all = 0.0f;
-  for (int s0 = 0; s0 < splits; s0 += 32) {
-    const float mine = s0 + lane < splits ? ex2(p.part_lse[(s0 + lane) * rows + row] - base) : 0.0f;
-    const int n = min(32, splits - s0);
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-      const float w = __shfl_sync(0xffffffffu, mine, i);
-      all += w;
-      if (w == 0.0f || c >= p.D) continue;      // a split without a key the row sees
-      const float4 v = *reinterpret_cast<const float4 *>(p.part + ((s0 + i) * rows + row) * p.D + c);
-      o[0] = fmaf(w, v.x, o[0]);
-      o[1] = fmaf(w, v.y, o[1]);
-      o[2] = fmaf(w, v.z, o[2]);
-      o[3] = fmaf(w, v.w, o[3]);
+      for (int i = 0; i < kStep; ++i) {
+        const int64_t at = (s0 + i) * rows + row;
+        lse[i] = s0 + i < splits ? p.part_lse[at] : -INFINITY;
+        v[i] = s0 + i < splits && c < p.D ? *reinterpret_cast<const float4 *>(p.part + at * p.D + c)
+                                          : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      }
+      float now = top;
+#pragma unroll
+      for (int i = 0; i < kStep; ++i) now = fmaxf(now, lse[i]);
+      const float base = now == -INFINITY ? 0.0f : now, shrink = ex2(top - base);
+      top = now;
+      all *= shrink;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) o[x] *= shrink;
+#pragma unroll
+      for (int i = 0; i < kStep; ++i) {
+        const float w = ex2(lse[i] - base);
+        all += w;
+        o[0] = fmaf(w, v[i].x, o[0]);
+        o[1] = fmaf(w, v[i].y, o[1]);
+        o[2] = fmaf(w, v[i].z, o[2]);
+        o[3] = fmaf(w, v[i].w, o[3]);
+      }
     }
+    const float inv = all == 0.0f ? 0.0f : 1.0f / all;
+    if (c < p.D)
+      *reinterpret_cast<uint2 *>(p.out + row * p.D + c) =
+          make_uint2(A::pack2(o[0] * inv, o[1] * inv), A::pack2(o[2] * inv, o[3] * inv));
   }
-  const float inv = all == 0.0f ? 0.0f : 1.0f / all;
-  if (c < p.D)
-    *reinterpret_cast<uint2 *>(p.out + row * p.D + c) =
-        make_uint2(A::pack2(o[0] * inv, o[1] * inv), A::pack2(o[2] * inv, o[3] * inv));
+  if (!waited) griddep_wait();
 }
 
 template <class A>
@@ -624,7 +639,9 @@ cudaError_t launch_paged_attention(const AttentionArgs &a, int num_sms, uint64_t
                   : f16            ? launch_rows<ActF16>(p, f, stream)
                                    : launch_rows<ActBf16>(p, f, stream);
   if (e != cudaSuccess || f.max_splits == 1) return e;
-  const dim3 grid(static_cast<unsigned>((a.T * a.heads + 7) / 8));
+  // (few CTAs: often no sequence is split, and they only begin and end)
+  const int64_t ctas = (a.T * a.heads + 7) / 8, most = 8 * static_cast<int64_t>(num_sms);
+  const dim3 grid(static_cast<unsigned>(ctas < most ? ctas : most));
   return f16 ? launch_on(join_kernel<ActF16>, grid, 256, 0, stream, true, p)
              : launch_on(join_kernel<ActBf16>, grid, 256, 0, stream, true, p);
 }

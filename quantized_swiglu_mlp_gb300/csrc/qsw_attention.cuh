@@ -9,6 +9,8 @@
 // log-sum-exps are joined by a second kernel.
 #pragma once
 
+#include <climits>
+
 #include "qsw_fp4.cuh"
 #include "qsw_internal.h"
 
@@ -24,14 +26,14 @@ struct alignas(16) SeqRec {
   int blocks;    // row tiles per kv head
   int splits;
   int chunk;     // keys per split
-  int pad[2];
+  int first;     // its first item
+  int pad;
 };
 
 // The plan in device memory: words 0 (items) and 1 (whether any sequence is split), the
-// first item of each sequence, the records, the sequence of each token (-1: none).
+// records, the sequence of each token (-1: none).
 struct PlanView {
   int *head;
-  int *first;        // [B + 1]
   SeqRec *rec;       // [B]
   int *seq_of;       // [T]
 };
@@ -39,8 +41,7 @@ constexpr int kPlanHead = 8;
 __host__ __device__ inline PlanView plan_view(void *base, int64_t B) {
   PlanView v;
   v.head = static_cast<int *>(base);
-  v.first = v.head + kPlanHead;
-  v.rec = reinterpret_cast<SeqRec *>(v.first + ((B + 1 + 7) / 8) * 8);
+  v.rec = reinterpret_cast<SeqRec *>(v.head + kPlanHead);
   v.seq_of = reinterpret_cast<int *>(v.rec + B);
   return v;
 }
@@ -77,24 +78,37 @@ __device__ __forceinline__ void seen_keys(const SeqRec &s, int a, int b, int win
   lo = window ? max(s.len - s.n + a - window + 1, 0) : 0;
 }
 
-// Item `id` of the plan, by a converged warp: the sequence by a search 32 wide.
+// Item `id` of the plan, by a converged warp: the sequence by a search 32 wide, whose last
+// step holds the records themselves.  (An id past the last item gives an item that must
+// not be run: its loads need not wait for the number of items.)
 __device__ __forceinline__ Item find_item(const AttnParams &p, int id) {
   const int lane = static_cast<int>(lane_id());
   int lo = 0, n = p.B;                 // the last sequence of [lo, lo + n) whose first item is at most id
-  while (n > 1) {
+  while (n > 32) {
     const int step = (n + 31) / 32;
     const int at = lane * step;
-    const bool le = at < n && __ldg(p.plan.first + lo + at) <= id;
+    const bool le = at < n && __ldg(&p.plan.rec[lo + at].first) <= id;
     const int last = 31 - __clz(__ballot_sync(0xffffffffu, le) | 1u);
     lo += last * step;
     n = min(step, n - last * step);
   }
+  int4 a = make_int4(0, 0, 0, 0), c = make_int4(1, 1, INT_MAX, 0);
+  if (lane < n) {
+    const int4 *r = reinterpret_cast<const int4 *>(p.plan.rec + lo + lane);
+    a = __ldg(r);
+    c = __ldg(r + 1);
+  }
+  const int last = 31 - __clz(__ballot_sync(0xffffffffu, c.z <= id) | 1u);
   Item t;
-  t.b = lo;
-  const int4 *r = reinterpret_cast<const int4 *>(p.plan.rec + lo);
-  const int4 a = __ldg(r), c = __ldg(r + 1);
-  t.s.row = a.x, t.s.n = a.y, t.s.len = a.z, t.s.blocks = a.w, t.s.splits = c.x, t.s.chunk = c.y;
-  const int local = id - __ldg(p.plan.first + lo);
+  t.b = lo + last;
+  t.s.row = __shfl_sync(0xffffffffu, a.x, last);
+  t.s.n = __shfl_sync(0xffffffffu, a.y, last);
+  t.s.len = __shfl_sync(0xffffffffu, a.z, last);
+  t.s.blocks = __shfl_sync(0xffffffffu, a.w, last);
+  t.s.splits = __shfl_sync(0xffffffffu, c.x, last);
+  t.s.chunk = __shfl_sync(0xffffffffu, c.y, last);
+  t.s.first = __shfl_sync(0xffffffffu, c.z, last);
+  const int local = id - t.s.first;
   // the last rows first (they see the most keys), then splits, kv heads innermost: CTAs
   // that run together read the same keys of a head
   const int per = p.kv_heads * t.s.splits;

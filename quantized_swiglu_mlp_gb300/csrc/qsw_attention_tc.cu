@@ -16,7 +16,6 @@
 //
 // The base of a row is raised (and O rescaled in tensor memory) only when a score passes
 // it by 8, so that weights reach 256 at most and most tiles leave O alone.
-#include <climits>
 #include <mutex>
 #include <type_traits>
 
@@ -143,6 +142,29 @@ __device__ __forceinline__ bool wait_all(uint64_t *bar, uint32_t parity, volatil
 __device__ __forceinline__ int item_of(int step) {
   const int G = static_cast<int>(gridDim.x), c = static_cast<int>(blockIdx.x);
   return step * G + ((step & 1) ? G - 1 - c : c);
+}
+
+// Of N consecutive lanes with N pieces each, lane i gets piece i of all (pieces in the
+// lanes' order).
+template <int N>
+__device__ __forceinline__ void turn_rows(uint4 (&v)[N], int lane) {
+#pragma unroll
+  for (int m = N / 2; m; m >>= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (i & m) continue;
+      const bool up = lane & m;
+      const uint4 give = up ? v[i] : v[i | m];
+      uint4 got;
+      got.x = __shfl_xor_sync(0xffffffffu, give.x, m);
+      got.y = __shfl_xor_sync(0xffffffffu, give.y, m);
+      got.z = __shfl_xor_sync(0xffffffffu, give.z, m);
+      got.w = __shfl_xor_sync(0xffffffffu, give.w, m);
+      if (up)
+        v[i] = got;
+      else
+        v[i | m] = got;
+    }
 }
 
 struct Barriers {
@@ -409,9 +431,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (warp_live) {
         const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-        const int64_t at = token * p.heads + head, rows = static_cast<int64_t>(p.T) * p.heads;
+        const int64_t at = token * p.heads + head;
         const bool split = t->s.splits > 1;
-        const int64_t part_at = t->split * rows + at;
+        const int64_t part_at = t->split * static_cast<int64_t>(p.T) * p.heads + at;
+        // where this lane's row goes, in bytes from the first row; and the rows of its 8 lanes
+        uint8_t *const to = split ? reinterpret_cast<uint8_t *>(p.part) : reinterpret_cast<uint8_t *>(p.out);
+        const int size = split ? 4 : 2;
+        const int64_t mine_at = live ? (split ? part_at : at) * p.D * size : -1;
         float odd = 0.0f;             // 0 times every value: NaN if one is not finite
 #pragma unroll
         for (int c = 0; c < DP; c += 32) {
@@ -420,22 +446,39 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld32(o_addr + c, o);
             tmem_ld_wait();
           }
+          float y[32];
 #pragma unroll
-          for (int x = 0; x < 32; x += 8) {
-            float y[8];
+          for (int x = 0; x < 32; ++x) {
+            y[x] = sum == 0.0f ? 0.0f : __uint_as_float(o[x]) * inv;
+            odd = fmaf(y[x], 0.0f, odd);
+          }
+          // 8 lanes turn their rows so that a store covers runs of each row: 128 bytes of f32, or 64
+          // of the type, 4 lanes to a row
+          if (split) {
+            uint4 v[8];
 #pragma unroll
-            for (int z = 0; z < 8; ++z) {
-              y[z] = sum == 0.0f ? 0.0f : __uint_as_float(o[x + z]) * inv;
-              odd = fmaf(y[z], 0.0f, odd);
+            for (int x = 0; x < 8; ++x)
+              v[x] = make_uint4(__float_as_uint(y[4 * x]), __float_as_uint(y[4 * x + 1]), __float_as_uint(y[4 * x + 2]),
+                                __float_as_uint(y[4 * x + 3]));
+            turn_rows<8>(v, lane);
+            const int col = c + (lane & 7) * 4;
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+              const int64_t row = __shfl_sync(0xffffffffu, mine_at, (lane & ~7) + x);
+              if (row >= 0 && col < p.D) *reinterpret_cast<uint4 *>(to + row + col * 4) = v[x];
             }
-            if (!live || c + x >= p.D) continue;
-            if (split) {
-              float4 *dst = reinterpret_cast<float4 *>(p.part + part_at * p.D + c + x);
-              dst[0] = make_float4(y[0], y[1], y[2], y[3]);
-              dst[1] = make_float4(y[4], y[5], y[6], y[7]);
-            } else {
-              *reinterpret_cast<uint4 *>(p.out + at * p.D + c + x) =
-                  make_uint4(A::pack2(y[0], y[1]), A::pack2(y[2], y[3]), A::pack2(y[4], y[5]), A::pack2(y[6], y[7]));
+          } else {
+            uint4 v[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              v[x] = make_uint4(A::pack2(y[8 * x], y[8 * x + 1]), A::pack2(y[8 * x + 2], y[8 * x + 3]),
+                                A::pack2(y[8 * x + 4], y[8 * x + 5]), A::pack2(y[8 * x + 6], y[8 * x + 7]));
+            turn_rows<4>(v, lane);
+            const int col = c + (lane & 3) * 8;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const int64_t row = __shfl_sync(0xffffffffu, mine_at, (lane & ~3) + x);
+              if (row >= 0 && col < p.D) *reinterpret_cast<uint4 *>(to + row + col * 2) = v[x];
             }
           }
         }
@@ -604,9 +647,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int total = __ldg(p.plan.head);
       for (int step = 0;; ++step) {
         const int slot = step % kItems, id = item_of(step);
-        Item t;
-        t.rows = 0;
-        if (id < total) t = find_item(p, id);
+        Item t = find_item(p, id);
+        if (id >= total) t.rows = 0;
         if (!wait_all(&bar.item_empty[slot], ((step / kItems) & 1) ^ 1, abort_flag, p.timeout_ns, err)) break;
         if (lane == 0) {
           items[slot] = t;

@@ -10,9 +10,9 @@
 // f_i modulo 2^64 is the fraction of a turn exactly, and its upper 32 bits go through
 // sincospif: the angle is within 2^-24 of the exact one at any position.
 //
-// A CTA takes a few tokens: first a thread per (token, pair) puts cos and sin in
-// shared memory, where all heads of q and k find them, then the threads walk the
-// tokens' units: 8 pairs (two 16-byte runs half a rotation apart) or 8 elements.
+// A CTA takes a few tokens, whose units its threads walk: 8 pairs as two 16-byte runs half a
+// rotation apart, or two runs of 8 elements.  cos and sin are worked out once per token
+// and pair, while the first units are on their way, and all heads find them in shared memory.
 #include "qsw_fp4.cuh"
 #include "qsw_internal.h"
 
@@ -65,37 +65,135 @@ struct RopeParams {
   FastDiv per_token, page_size, halves;
 };
 
-template <class A, int VEC>
+constexpr int kThreads = 256;
+constexpr int kAhead = 4;          // units of a thread in flight
+
+// Two runs of VEC elements.
+template <int VEC>
 struct Unit {
-  uint32_t w[2][VEC == 8 ? 4 : 1];
+  uint32_t w[2][VEC == 8 ? 4 : 1];   // as they are stored
+  uint16_t *dst;                     // the head's first element; null: nothing to do
+  int turn;                          // of the first run's first pair in shared memory; -1: both copied
+  int e0, e1;                        // elements of the runs; e1 < 0: one run
+  int kind;                          // 0: copied; 1: pairs across the runs; 2, 3: adjacent pairs in the first, in both
 };
 
-// One unit: `pairs` 8 (or 1) pairs half a rotation apart, else 8 (1) elements, of which
-// interleaved pairs may turn.
-template <class A, int VEC>
-__device__ __forceinline__ void load_unit(const uint16_t *p, int first, int second, bool both, Unit<A, VEC> &u) {
+// Unit u of the CTA's tokens [t0, ..): where it goes, and the loads of what it holds.
+template <int VEC>
+__device__ __forceinline__ void fetch_unit(const RopeParams &p, int t0, uint32_t u, uint32_t units, Unit<VEC> &x) {
+  x.dst = nullptr;
+  if (u >= units) return;
+  const uint32_t tl = div_by(u, p.per_token);
+  const int t = t0 + static_cast<int>(tl);
+  int r = static_cast<int>(u - tl * p.per_token.d);
+  const int g = (p.segments > 1 && r >= p.first_unit[1]) + (p.segments > 2 && r >= p.first_unit[2]);
+  const Segment &s = p.seg[g];
+  r -= p.first_unit[g];
+  const uint32_t h = div_by(static_cast<uint32_t>(r), s.per_head);
+  const int c = r - static_cast<int>(h * s.per_head.d);
+  x.kind = 0;
+  x.turn = static_cast<int>(tl) * p.half;
+  // across: pairs half a rotation apart, and element by element any pairs
+  const bool across = s.rotate && (VEC == 1 || !p.interleaved);
+  if (across && c * VEC < p.half) {
+    const int pair = c * VEC;
+    x.e0 = p.interleaved ? 2 * pair : pair;
+    x.e1 = p.interleaved ? 2 * pair + 1 : pair + p.half;
+    x.turn += pair;
+    x.kind = 1;
+  } else {
+    // (behind the rotation, if there are units across)
+    x.e0 = across ? 2 * p.half + (c * VEC - p.half) * 2 : c * VEC * 2;
+    x.e1 = x.e0 + VEC < p.D ? x.e0 + VEC : -1;
+    if (s.rotate && !across && x.e0 < 2 * p.half) {
+      x.turn += x.e0 / 2;
+      x.kind = x.e0 + VEC < 2 * p.half ? 3 : 2;
+    }
+  }
+  // (before the token's slot is looked at: the loads need not wait for it)
+  const uint16_t *src = s.src + t * s.src_t + h * s.src_h;
   if constexpr (VEC == 8) {
-    const uint4 a = *reinterpret_cast<const uint4 *>(p + first);
-    u.w[0][0] = a.x, u.w[0][1] = a.y, u.w[0][2] = a.z, u.w[0][3] = a.w;
-    if (both) {
-      const uint4 b = *reinterpret_cast<const uint4 *>(p + second);
-      u.w[1][0] = b.x, u.w[1][1] = b.y, u.w[1][2] = b.z, u.w[1][3] = b.w;
+    const uint4 a = __ldcs(reinterpret_cast<const uint4 *>(src + x.e0));
+    x.w[0][0] = a.x, x.w[0][1] = a.y, x.w[0][2] = a.z, x.w[0][3] = a.w;
+    if (x.e1 >= 0) {
+      const uint4 b = __ldcs(reinterpret_cast<const uint4 *>(src + x.e1));
+      x.w[1][0] = b.x, x.w[1][1] = b.y, x.w[1][2] = b.z, x.w[1][3] = b.w;
     }
   } else {
-    u.w[0][0] = p[first];
-    if (both) u.w[1][0] = p[second];
+    x.w[0][0] = src[x.e0];
+    if (x.e1 >= 0) x.w[1][0] = src[x.e1];
+  }
+  const bool left_out = p.skip_negative && p.positions && __ldg(p.positions + t) < 0;
+  uint16_t *d;
+  if (s.paged) {
+    const int slot = __ldg(p.slots + t);
+    const uint32_t page = div_by(static_cast<uint32_t>(max(slot, 0)), p.page_size);
+    d = slot < 0 || page >= static_cast<uint32_t>(p.pages)
+            ? nullptr
+            : s.dst + page * s.dst_t + (slot - page * p.page_size.d) * s.dst_r + h * s.dst_h;
+  } else {
+    d = s.dst + t * s.dst_t + h * s.dst_h;
+  }
+  x.dst = left_out ? nullptr : d;
+}
+
+// Adjacent pairs of a run of 8.
+template <class A>
+__device__ __forceinline__ void turn_run(uint32_t (&w)[4], const float2 *cs) {
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const float4 f = reinterpret_cast<const float4 *>(cs)[j];      // cos, sin, cos, sin
+    const float a0 = A::lo(w[2 * j]), a1 = A::hi(w[2 * j]), b0 = A::lo(w[2 * j + 1]), b1 = A::hi(w[2 * j + 1]);
+    w[2 * j] = A::pack2(a0 * f.x - a1 * f.y, a1 * f.x + a0 * f.y);
+    w[2 * j + 1] = A::pack2(b0 * f.z - b1 * f.w, b1 * f.z + b0 * f.w);
+  }
+}
+
+// Turns and stores a unit.
+template <class A, int VEC>
+__device__ __forceinline__ void store_unit(const float2 *turn, Unit<VEC> &x) {
+  if (!x.dst) return;
+  const float2 *cs = turn + x.turn;
+  if constexpr (VEC == 8) {
+    if (x.kind == 1) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float4 f = reinterpret_cast<const float4 *>(cs)[j];
+        const float a0 = A::lo(x.w[0][j]), a1 = A::hi(x.w[0][j]);
+        const float b0 = A::lo(x.w[1][j]), b1 = A::hi(x.w[1][j]);
+        x.w[0][j] = A::pack2(a0 * f.x - b0 * f.y, a1 * f.z - b1 * f.w);
+        x.w[1][j] = A::pack2(b0 * f.x + a0 * f.y, b1 * f.z + a1 * f.w);
+      }
+    } else {
+      if (x.kind >= 2) turn_run<A>(x.w[0], cs);
+      if (x.kind == 3) turn_run<A>(x.w[1], cs + 4);
+    }
+    *reinterpret_cast<uint4 *>(x.dst + x.e0) = make_uint4(x.w[0][0], x.w[0][1], x.w[0][2], x.w[0][3]);
+    if (x.e1 >= 0) *reinterpret_cast<uint4 *>(x.dst + x.e1) = make_uint4(x.w[1][0], x.w[1][1], x.w[1][2], x.w[1][3]);
+  } else if (x.kind == 1) {
+    const float2 f = *cs;
+    const float x0 = A::lo(x.w[0][0]), x1 = A::lo(x.w[1][0]);
+    x.dst[x.e0] = A::store(x0 * f.x - x1 * f.y);
+    x.dst[x.e1] = A::store(x1 * f.x + x0 * f.y);
+  } else {
+    x.dst[x.e0] = static_cast<uint16_t>(x.w[0][0]);
+    if (x.e1 >= 0) x.dst[x.e1] = static_cast<uint16_t>(x.w[1][0]);
   }
 }
 
 template <class A, int VEC>
-__global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kThreads, 3) rope_kernel(const __grid_constant__ RopeParams p) {
   extern __shared__ float2 turn[];       // [tokens][half]: cos, sin
   griddep_wait();
   griddep_launch_dependents();
   const int t0 = static_cast<int>(blockIdx.x) * p.tokens;
   const int count = min(p.tokens, p.T - t0);
+  const uint32_t units = static_cast<uint32_t>(count) * p.per_token.d;
+  Unit<VEC> x[kAhead];
+#pragma unroll
+  for (int a = 0; a < kAhead; ++a) fetch_unit(p, t0, threadIdx.x + a * kThreads, units, x[a]);
   if (p.half) {
-    for (uint32_t i = threadIdx.x; i < static_cast<uint32_t>(count * p.half); i += blockDim.x) {
+    for (uint32_t i = threadIdx.x; i < static_cast<uint32_t>(count * p.half); i += kThreads) {
       const uint32_t t = div_by(i, p.halves), pair = i - t * p.half;
       const uint64_t at = static_cast<uint64_t>(static_cast<int64_t>(p.positions ? __ldg(p.positions + t0 + t) : 0)) *
                           static_cast<uint64_t>(__ldg(p.table + pair));
@@ -105,104 +203,13 @@ __global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeP
     }
     __syncthreads();
   }
-  const uint32_t units = static_cast<uint32_t>(count) * p.per_token.d;
-  const int rot = 2 * p.half;
-  constexpr int kAhead = VEC == 8 ? 4 : 2;
-  for (uint32_t u0 = threadIdx.x; u0 < units; u0 += blockDim.x * kAhead) {
-    Unit<A, VEC> in[kAhead];
-    uint16_t *dst[kAhead];
-    const float2 *cs[kAhead];
-    int e0[kAhead], e1[kAhead];          // elements; e1 < 0: one run
+  for (uint32_t u0 = threadIdx.x;;) {
 #pragma unroll
-    for (int a = 0; a < kAhead; ++a) {
-      const uint32_t u = u0 + a * blockDim.x;
-      dst[a] = nullptr;
-      if (u >= units) continue;
-      const uint32_t tl = div_by(u, p.per_token);
-      const int t = t0 + static_cast<int>(tl);
-      int r = static_cast<int>(u - tl * p.per_token.d);
-      const int g = (p.segments > 1 && r >= p.first_unit[1]) + (p.segments > 2 && r >= p.first_unit[2]);
-      const Segment &s = p.seg[g];
-      r -= p.first_unit[g];
-      if (p.skip_negative && p.positions && __ldg(p.positions + t) < 0) continue;
-      const uint32_t h = div_by(static_cast<uint32_t>(r), s.per_head);
-      const int c = r - static_cast<int>(h * s.per_head.d);
-      uint16_t *d;
-      if (s.paged) {
-        const int slot = __ldg(p.slots + t);
-        if (slot < 0) continue;
-        const uint32_t page = div_by(static_cast<uint32_t>(slot), p.page_size);
-        if (page >= static_cast<uint32_t>(p.pages)) continue;
-        d = s.dst + page * s.dst_t + (slot - page * p.page_size.d) * s.dst_r + h * s.dst_h;
-      } else {
-        d = s.dst + t * s.dst_t + h * s.dst_h;
-      }
-      dst[a] = d;
-      cs[a] = nullptr;
-      e1[a] = -1;
-      if (s.rotate && !p.interleaved) {
-        // units of pairs first, then what is copied
-        const int pair = c * VEC;
-        if (pair < p.half) {
-          e0[a] = pair;
-          e1[a] = pair + p.half;
-          cs[a] = turn + tl * p.half + pair;
-        } else {
-          e0[a] = pair + p.half;
-        }
-      } else if (VEC == 1 && s.rotate) {
-        if (c < p.half) {
-          e0[a] = 2 * c;
-          e1[a] = 2 * c + 1;
-          cs[a] = turn + tl * p.half + c;
-        } else {
-          e0[a] = c + p.half;
-        }
-      } else {
-        e0[a] = c * VEC;
-        if (s.rotate && e0[a] < rot) cs[a] = turn + tl * p.half + e0[a] / 2;
-      }
-      load_unit<A, VEC>(s.src + t * s.src_t + h * s.src_h, e0[a], e1[a], e1[a] >= 0, in[a]);
-    }
+    for (int a = 0; a < kAhead; ++a) store_unit<A>(turn, x[a]);
+    u0 += kThreads * kAhead;
+    if (u0 >= units) break;
 #pragma unroll
-    for (int a = 0; a < kAhead; ++a) {
-      if (!dst[a]) continue;
-      if constexpr (VEC == 8) {
-        uint4 o0 = make_uint4(in[a].w[0][0], in[a].w[0][1], in[a].w[0][2], in[a].w[0][3]);
-        if (cs[a] && e1[a] >= 0) {
-          uint32_t y0[4], y1[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float4 f = reinterpret_cast<const float4 *>(cs[a])[j];     // cos, sin, cos, sin
-            const float a0 = A::lo(in[a].w[0][j]), a1 = A::hi(in[a].w[0][j]);
-            const float b0 = A::lo(in[a].w[1][j]), b1 = A::hi(in[a].w[1][j]);
-            y0[j] = A::pack2(a0 * f.x - b0 * f.y, a1 * f.z - b1 * f.w);
-            y1[j] = A::pack2(b0 * f.x + a0 * f.y, b1 * f.z + a1 * f.w);
-          }
-          o0 = make_uint4(y0[0], y0[1], y0[2], y0[3]);
-          *reinterpret_cast<uint4 *>(dst[a] + e1[a]) = make_uint4(y1[0], y1[1], y1[2], y1[3]);
-        } else if (cs[a]) {
-          uint32_t y[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 f = cs[a][j];
-            const float x0 = A::lo(in[a].w[0][j]), x1 = A::hi(in[a].w[0][j]);
-            y[j] = A::pack2(x0 * f.x - x1 * f.y, x1 * f.x + x0 * f.y);
-          }
-          o0 = make_uint4(y[0], y[1], y[2], y[3]);
-        }
-        *reinterpret_cast<uint4 *>(dst[a] + e0[a]) = o0;
-      } else {
-        if (cs[a]) {
-          const float2 f = *cs[a];
-          const float x0 = A::lo(in[a].w[0][0]), x1 = A::lo(in[a].w[1][0]);
-          dst[a][e0[a]] = A::store(x0 * f.x - x1 * f.y);
-          dst[a][e1[a]] = A::store(x1 * f.x + x0 * f.y);
-        } else {
-          dst[a][e0[a]] = static_cast<uint16_t>(in[a].w[0][0]);
-        }
-      }
-    }
+    for (int a = 0; a < kAhead; ++a) fetch_unit(p, t0, u0 + a * kThreads, units, x[a]);
   }
 }
 
@@ -251,27 +258,28 @@ cudaError_t launch_rope(const RopeArgs &a, int num_sms, cudaStream_t stream) {
   int units = 0;
   for (int i = 0; i < p.segments; ++i) {
     Segment &s = p.seg[i];
-    // a unit holds two runs where halves turn (or, element by element, any pair)
-    const int two = s.rotate && (!p.interleaved || !wide) ? p.half : 0;
-    const int per = (p.D - two) / vec;
+    const int across = s.rotate && (!p.interleaved || !wide) ? p.half : 0;
+    const int per = across / vec + (p.D - 2 * across + 2 * vec - 1) / (2 * vec);
     s.per_head = make_div(static_cast<uint32_t>(per));
     p.first_unit[i] = units;
     units += per * s.heads;
   }
   p.per_token = make_div(static_cast<uint32_t>(units));
   p.halves = make_div(static_cast<uint32_t>(p.half ? p.half : 1));
-  // four tokens a CTA where there are CTAs enough, so that its threads have a few units each
-  int64_t tokens = a.T / (2 * static_cast<int64_t>(num_sms));
-  tokens = tokens < 1 ? 1 : tokens > 4 ? 4 : tokens;
+  // as many tokens a CTA as its threads hold in one go, where there are CTAs enough
+  int64_t tokens = kThreads * kAhead / units;
+  const int64_t fair = a.T / (2 * static_cast<int64_t>(num_sms));
+  tokens = tokens > fair ? fair : tokens;
+  tokens = tokens < 1 ? 1 : tokens > 16 ? 16 : tokens;
   p.tokens = static_cast<int>(tokens);
   const dim3 grid(static_cast<unsigned>((a.T + tokens - 1) / tokens));
   const size_t smem = static_cast<size_t>(tokens) * p.half * sizeof(float2);
   const bool f16 = a.act == ActF16::kId;
   if (wide)
-    return f16 ? launch_on(rope_kernel<ActF16, 8>, grid, 256, smem, stream, false, p)
-               : launch_on(rope_kernel<ActBf16, 8>, grid, 256, smem, stream, false, p);
-  return f16 ? launch_on(rope_kernel<ActF16, 1>, grid, 256, smem, stream, false, p)
-             : launch_on(rope_kernel<ActBf16, 1>, grid, 256, smem, stream, false, p);
+    return f16 ? launch_on(rope_kernel<ActF16, 8>, grid, kThreads, smem, stream, false, p)
+               : launch_on(rope_kernel<ActBf16, 8>, grid, kThreads, smem, stream, false, p);
+  return f16 ? launch_on(rope_kernel<ActF16, 1>, grid, kThreads, smem, stream, false, p)
+             : launch_on(rope_kernel<ActBf16, 1>, grid, kThreads, smem, stream, false, p);
 }
 
 }  // namespace qsw
