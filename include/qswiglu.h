@@ -464,7 +464,7 @@ QSW_API qsw_status qsw_kv_append(const qsw_heads *q, const qsw_heads *k, const q
  * position p sees the keys p - window + 1 .. p.  A length counts as no less than 0 and
  * no more than max_pages * page_size; with offsets that decrease or pass T the values are
  * unspecified, but nothing is read or written out of range.  The plan holds
- * for calls with the same B, T, heads, D, window and cache geometry; it is only read by them, so that
+ * for calls with the same B, T, heads, D, window, max_pages and cache geometry; it is only read by them, so that
  * calls on several streams may share it.  B at most 65536, T at most 2^22, heads at
  * most 1024 and a multiple of kv_heads.
  */
@@ -483,11 +483,12 @@ QSW_API qsw_status qsw_paged_plan(const int *offsets, const int *lengths, int64_
  * that comes out infinite or NaN is computed again key by key, with f32 weights).
  * Statistics and sums in f32, the weights rounded to the activation dtype before they
  * meet v; long histories are split over CTAs and joined in f32 in a fixed order: the same bits
- * every time.  scale > 0.  workspace: qsw_paged_attention_workspace_bytes(...) bytes,
- * 256-byte aligned (0 bytes: may be NULL); it need not be cleared, and calls that can
+ * every time.  scale > 0.  workspace: qsw_paged_attention_workspace_bytes(...) bytes
+ * (max_len = max_pages * page_size), 256-byte aligned (0 bytes: may be NULL); it need not be cleared, and calls that can
  * run concurrently must not share it.  q, out: 16-byte aligned, as are q's strides.
  */
-QSW_API size_t qsw_paged_attention_workspace_bytes(int64_t B, int64_t T, int64_t heads, int64_t kv_heads, int64_t D);
+QSW_API size_t qsw_paged_attention_workspace_bytes(int64_t B, int64_t T, int64_t heads, int64_t kv_heads, int64_t D,
+                                                   int64_t max_len);
 QSW_API qsw_status qsw_paged_attention(const qsw_heads *q, const qsw_kv_cache *cache, const int *page_table,
                                       int64_t table_stride, int64_t max_pages, const void *plan, int64_t B,
                                       int64_t T, int64_t heads, int64_t D, int64_t window, float scale,

@@ -6,7 +6,8 @@
 // that share a kv head are rows of one tile, and K and V are read once for all of them.
 // A tile of rows over a range of keys is an item; a sequence whose history is long
 // against the number of rows is cut into splits, whose normalised results and
-// log-sum-exps are joined by a second kernel.
+// log-sum-exps are joined by a kernel of their own.  Sequences with few rows and with many
+// are two lists of items, each with a kernel.
 #pragma once
 
 #include <climits>
@@ -26,12 +27,14 @@ struct alignas(16) SeqRec {
   int blocks;    // row tiles per kv head
   int splits;
   int chunk;     // keys per split
-  int first;     // its first item
-  int pad;
+  int first[2];  // its first item in each list (it has items in one of them)
 };
 
-// The plan in device memory: words 0 (items) and 1 (whether any sequence is split), the
-// records, the sequence of each token (-1: none).
+// Lists of items: sequences with few rows, and with many.
+enum : int { LIST_ROWS = 0, LIST_TILES = 1 };
+
+// The plan in device memory: words 0 and 1 (items of each list) and 2 (whether any sequence
+// is split), the records, the sequence of each token (-1: none).
 struct PlanView {
   int *head;
   SeqRec *rec;       // [B]
@@ -58,7 +61,8 @@ struct AttnParams {
   int B, T, heads, kv_heads, group, D;
   int pages, page_size, max_pages;
   int window;                      // 0: none
-  int tile_rows, tile_keys;
+  int list, tile_rows, tile_keys;
+  int after_tiles;                 // few rows: launched as a dependent of the tiles' kernel
   float scale_log2;                // scale log2(e)
   float *part;                     // [splits][T][heads][D], normalised
   float *part_lse;                 // [splits][T][heads], log2
@@ -78,7 +82,7 @@ __device__ __forceinline__ void seen_keys(const SeqRec &s, int a, int b, int win
   lo = window ? max(s.len - s.n + a - window + 1, 0) : 0;
 }
 
-// Item `id` of the plan, by a converged warp: the sequence by a search 32 wide, whose last
+// Item `id` of the call's list, by a converged warp: the sequence by a search 32 wide, whose last
 // step holds the records themselves.  (An id past the last item gives an item that must
 // not be run: its loads need not wait for the number of items.)
 __device__ __forceinline__ Item find_item(const AttnParams &p, int id) {
@@ -87,18 +91,19 @@ __device__ __forceinline__ Item find_item(const AttnParams &p, int id) {
   while (n > 32) {
     const int step = (n + 31) / 32;
     const int at = lane * step;
-    const bool le = at < n && __ldg(&p.plan.rec[lo + at].first) <= id;
+    const bool le = at < n && __ldg(&p.plan.rec[lo + at].first[p.list]) <= id;
     const int last = 31 - __clz(__ballot_sync(0xffffffffu, le) | 1u);
     lo += last * step;
     n = min(step, n - last * step);
   }
-  int4 a = make_int4(0, 0, 0, 0), c = make_int4(1, 1, INT_MAX, 0);
+  int4 a = make_int4(0, 0, 0, 0), c = make_int4(1, 1, INT_MAX, INT_MAX);
   if (lane < n) {
     const int4 *r = reinterpret_cast<const int4 *>(p.plan.rec + lo + lane);
     a = __ldg(r);
     c = __ldg(r + 1);
   }
-  const int last = 31 - __clz(__ballot_sync(0xffffffffu, c.z <= id) | 1u);
+  const int first = p.list == LIST_ROWS ? c.z : c.w;
+  const int last = 31 - __clz(__ballot_sync(0xffffffffu, first <= id) | 1u);
   Item t;
   t.b = lo + last;
   t.s.row = __shfl_sync(0xffffffffu, a.x, last);
@@ -107,8 +112,7 @@ __device__ __forceinline__ Item find_item(const AttnParams &p, int id) {
   t.s.blocks = __shfl_sync(0xffffffffu, a.w, last);
   t.s.splits = __shfl_sync(0xffffffffu, c.x, last);
   t.s.chunk = __shfl_sync(0xffffffffu, c.y, last);
-  t.s.first = __shfl_sync(0xffffffffu, c.z, last);
-  const int local = id - t.s.first;
+  const int local = id - __shfl_sync(0xffffffffu, first, last);
   // the last rows first (they see the most keys), then splits, kv heads innermost: CTAs
   // that run together read the same keys of a head
   const int per = p.kv_heads * t.s.splits;
@@ -222,14 +226,18 @@ __device__ __noinline__ void exact_row(const AttnParams &p, const Item &t, int r
 
 // The form of a call, a function of its sizes alone: the plan and the attention work it
 // out for themselves and agree.
-struct AttnForm {
+struct ListForm {
   int tile_rows, tile_keys;
   int slots;              // CTAs that run at once
+  int64_t items;          // at most; 0: the list is not used
+};
+struct AttnForm {
+  ListForm list[2];
+  int64_t most_rows;      // of a sequence (and kv head) in the list of few rows
   int max_splits;         // 1: no history is split
-  int64_t items;          // at most
 };
 
-cudaError_t launch_attention_tiles(const AttnParams &p, const AttnForm &f, int act, const qsw_kv_cache &cache,
+cudaError_t launch_attention_tiles(const AttnParams &p, const ListForm &f, int act, const qsw_kv_cache &cache,
                                    cudaStream_t stream);
 
 }  // namespace qsw

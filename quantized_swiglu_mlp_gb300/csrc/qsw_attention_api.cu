@@ -138,10 +138,11 @@ qsw_status qsw_paged_plan(const int *offsets, const int *lengths, int64_t B, con
   return r;
 }
 
-size_t qsw_paged_attention_workspace_bytes(int64_t B, int64_t T, int64_t heads, int64_t kv_heads, int64_t D) {
-  if (B <= 0 || T < 0 || heads <= 0 || kv_heads <= 0 || heads % kv_heads || D <= 0 || D % 8 || D > kMaxHeadDim) return 0;
+size_t qsw_paged_attention_workspace_bytes(int64_t B, int64_t T, int64_t heads, int64_t kv_heads, int64_t D,
+                                           int64_t max_len) {
+  if (max_len < 0 || max_len > INT32_MAX || B <= 0 || T < 0 || heads <= 0 || kv_heads <= 0 || heads % kv_heads || D <= 0 || D % 8 || D > kMaxHeadDim) return 0;
   if (B > kMaxSequences || T > kMaxTokens || heads > kMaxHeads || T * heads > kMaxRows) return 0;
-  return qsw::attention_workspace_bytes(T, B, heads, kv_heads, D, qsw::device_sm_count());
+  return qsw::attention_workspace_bytes(T, B, heads, kv_heads, D, max_len, qsw::device_sm_count());
 }
 
 qsw_status qsw_paged_attention(const qsw_heads *q, const qsw_kv_cache *cache, const int *page_table,
@@ -156,7 +157,8 @@ qsw_status qsw_paged_attention(const qsw_heads *q, const qsw_kv_cache *cache, co
   if (!aligned(q->data, 16) || !aligned(out, 16) || !aligned(plan, 16) || !aligned(page_table, 4) ||
       !aligned(workspace, 256) || q->token_stride % 8 || q->head_stride % 8)
     return QSW_ERR_UNSUPPORTED;
-  const size_t need = qsw_paged_attention_workspace_bytes(B, T, heads, cache->kv_heads, D);
+  const size_t need =
+      qsw_paged_attention_workspace_bytes(B, T, heads, cache->kv_heads, D, max_pages * cache->page_size);
   if (workspace_bytes < need || (need && !workspace)) return QSW_ERR_INVALID_ARG;
   qsw::AttentionArgs a = {};
   a.q = *q;

@@ -644,7 +644,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_wait_drain(&full[c % stages], (c / stages) & 1, p.timeout_ns);
     } else if (warp == kWarpItems) {
       // ------------------------------------------------------------- items --
-      const int total = __ldg(p.plan.head);
+      const int total = __ldg(p.plan.head + LIST_TILES);
       for (int step = 0;; ++step) {
         const int slot = step % kItems, id = item_of(step);
         Item t = find_item(p, id);
@@ -716,7 +716,7 @@ cudaError_t launch_shape(const AttnParams &p, const TcMaps &maps, int grid, cuda
 
 }  // namespace
 
-cudaError_t launch_attention_tiles(const AttnParams &p, const AttnForm &f, int act, const qsw_kv_cache &cache,
+cudaError_t launch_attention_tiles(const AttnParams &p, const ListForm &f, int act, const qsw_kv_cache &cache,
                                    cudaStream_t stream) {
   const bool f16 = act == ActF16::kId;
   TcMaps maps = {};

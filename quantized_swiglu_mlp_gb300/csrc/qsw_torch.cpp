@@ -534,7 +534,8 @@ PyObject *paged_attention(Args a) {
     fail(PyExc_ValueError, "%s was made for other sizes", "plan");
   c10::cuda::CUDAGuard guard(q.device());
   at::Tensor out = output(a[13], "out", q.sizes(), q.scalar_type(), q);
-  const size_t bytes = g_fn.qsw_paged_attention_workspace_bytes_(B, T, heads, cache.kv_heads, D);
+  const size_t bytes = g_fn.qsw_paged_attention_workspace_bytes_(B, T, heads, cache.kv_heads, D,
+                                                                  table.size(1) * cache.page_size);
   at::Tensor ws;
   if (bytes) ws = empty({static_cast<int64_t>(bytes)}, at::kByte, q);
   const qsw_heads in = heads_arg(q);

@@ -162,7 +162,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.qsw_paged_plan_bytes.restype = sz
         lib.qsw_paged_plan.argtypes = [p, p, i64, p, i64, i64, i64, i64, i64, i64, c, p, p, p, p]
         lib.qsw_paged_plan.restype = i32
-        lib.qsw_paged_attention_workspace_bytes.argtypes = [i64, i64, i64, i64, i64]
+        lib.qsw_paged_attention_workspace_bytes.argtypes = [i64] * 6
         lib.qsw_paged_attention_workspace_bytes.restype = sz
         lib.qsw_paged_attention.argtypes = [h, c, p, i64, i64, p, i64, i64, i64, i64, i64, f32, i32, p, p, sz, p]
         lib.qsw_paged_attention.restype = i32

@@ -125,7 +125,9 @@ def test_sizes_that_no_call_accepts(lib):  # noqa: F811
     assert lib.qsw_paged_plan_bytes(4, -1) == lib.qsw_paged_plan_bytes(4, 1 << 62) == 0
     for a in ((0, 1, 8, 2, 64), (1, -1, 8, 2, 64), (1, 1, 8, 3, 64), (1, 1, 8, 0, 64), (1, 1, 1 << 40, 1, 64), (1, 1, 8, 2, 60),
               (1, 1, 8, 2, 1 << 40)):
-        assert lib.qsw_paged_attention_workspace_bytes(*a) == 0
+        assert lib.qsw_paged_attention_workspace_bytes(*a, 1000) == 0
+    assert lib.qsw_paged_attention_workspace_bytes(1, 1, 8, 2, 64, -1) == 0
+    assert lib.qsw_paged_attention_workspace_bytes(1, 1, 8, 2, 64, 1 << 31) == 0
 
 
 @pytest.mark.skipif(torch.cuda.is_available(), reason="the arguments are valid: with a device these would be launched")
