@@ -5,6 +5,8 @@
 namespace qsw {
 namespace {
 
+__device__ unsigned int g_rows_error;
+
 // -------------------------------------------------------------------- plan --
 
 // New tokens of sequence b.
@@ -198,13 +200,13 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
 // ---------------------------------------------------------------- few rows --
 
 constexpr int kKeyGroups = 4;      // of warps, each with keys of its own
-constexpr int kSubKeys = 16;       // keys of a group's step
-template <int RG>
-constexpr int row_stages = RG == 1 ? 3 : 6;      // two CTAs on an SM, or one
+// Keys of a group's step.  32 take a warp little longer than 16 (its softmax is mostly latency); with
+// 16 rows of 128 columns two CTAs of 16 keys a step fit on an SM, which is as fast.
+constexpr int step_keys(int DP, int RG) { return DP == 128 && RG == 1 ? 16 : 32; }
+constexpr int row_stage_bytes(int DP, int RG) { return 2 * step_keys(DP, RG) * DP * 2; }
+// Stages of a group's ring: 96 KB a CTA where two run on an SM, else 192 KB.
+constexpr int row_stages(int DP, int RG) { return (RG == 1 ? 98304 : 196608) / kKeyGroups / row_stage_bytes(DP, RG); }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
 __device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -231,52 +233,134 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <int DP>
-constexpr int row_stage_bytes = 2 * kSubKeys * DP * 2;
-
-// Up to 16 RG rows of one kv head.  Four groups of RG warps each take every fourth run of 16
-// keys with a ring of their own; a warp has 16 rows and a softmax of its own (no barrier over
-// the CTA in the loop), and the groups' results meet at the end.  With RG = 2 one warp of a
-// group copies K and the other V, and they meet once a step.  K and V rows lie in 16-byte
-// chunks, chunk c of key j at c ^ (j mod 8).
+// Up to 16 RG rows of one kv head.  Four groups of RG warps each take every fourth run of KEYS
+// keys with a ring of their own, which the group's first warp fills by TMA (boxes of 8 to 32
+// rows of a page); a warp has 16 rows and a softmax of its own (no barrier over the CTA in the loop),
+// and the groups' results meet at the end.  (With 16-byte copies by all lanes a step of 16 keys
+// took a warp 1200 cycles for their addresses and issue, as much as its products and softmax.)
 //
 // HBM-bound: 64 sequences of 128 to 16000 keys, 8 kv heads of 128: 162 us for 983 MB, 6.1 TB/s.
 template <class A, int DP, int RG>
 __global__ void __launch_bounds__(32 * kKeyGroups * RG, 3 - RG)
-    attn_rows_kernel(const __grid_constant__ AttnParams p) {
-  constexpr int kRowWarps = kKeyGroups * RG, kRowStages = row_stages<RG>, ROWS = 16 * RG;
-  constexpr int CH = DP / 8;                     // 16-byte chunks of a row
-  constexpr int PASS = 32 / CH;                  // keys per pass of a warp's copies
-  constexpr int STAGE = row_stage_bytes<DP>;
-  extern __shared__ __align__(128) uint8_t ring[];
+    attn_rows_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CacheMaps maps) {
+  constexpr int kRowWarps = kKeyGroups * RG, ROWS = 16 * RG;
+  constexpr int KEYS = DP == 128 && RG == 1 ? 16 : 32;                       // step_keys
+  constexpr int STAGE = 2 * KEYS * DP * 2;                                   // row_stage_bytes
+  constexpr int kRowStages = (RG == 1 ? 98304 : 196608) / kKeyGroups / STAGE;   // row_stages
+  constexpr int H = DP / 64;                     // halves of a head
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   __shared__ float warp_m[kKeyGroups][ROWS], warp_l[kKeyGroups][ROWS];
+  __shared__ uint64_t full[kKeyGroups][kRowStages], empty[kKeyGroups][kRowStages];
   __shared__ unsigned redo;
-  const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
+  __shared__ int abort_word;
+  volatile int *abort_flag = &abort_word;
+  unsigned int *err = &g_rows_error;
+  const int tid = static_cast<int>(threadIdx.x), warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int kg = warp / RG, rg = warp % RG;
-  if constexpr (kDebugBounds) debug_poison_smem(ring, kKeyGroups * kRowStages * STAGE);
+  if constexpr (kDebugBounds) {
+    debug_poison_smem(ring, kKeyGroups * kRowStages * STAGE);
+    fence_proxy_async_smem();
+  }
+  if (tid < kKeyGroups * kRowStages) {
+    mbar_init(&full[0][0] + tid, 1);
+    mbar_init(&empty[0][0] + tid, RG);
+    fence_mbar_init();
+  } else if (tid == kKeyGroups * kRowStages) {
+    abort_word = 0;
+    prefetch_tensormap(&maps.k);
+    prefetch_tensormap(&maps.v);
+  }
   if (!p.after_tiles) griddep_wait();      // (then all before the tiles' kernel is complete)
   griddep_launch_dependents();
   const int total = __ldg(p.plan.head + LIST_ROWS);
-  const int ch = lane % CH, sub = lane / CH;
-  const uint32_t mine = smem_u32(ring) + kg * kRowStages * STAGE;
+  uint8_t *mine = ring + kg * kRowStages * STAGE;
+
+  // Copies: boxes of rows, of all halves or of one; a lane per box of rows looks its page
+  // up.  In a stage a box's rows of 128 bytes lie half by half, chunk c of row j at c ^ (j mod 8).
+  const int subs = KEYS / maps.box, parts = H / maps.halves;
+  const int half_bytes = maps.box * 128;
+  uint32_t issued = 0, used = 0;           // stages
+  bool ok = true;
+  // row j of a stage's K or V; of its 16 keys b, this lane's in the K and the V operand
+  auto row_at = [&](int j) { return (j & -maps.box) * (H * 128) + (j & (maps.box - 1)) * 128; };
+  int k_row[KEYS / 16], v_row[KEYS / 16];
+#pragma unroll
+  for (int b = 0; b < KEYS / 16; ++b) {
+    k_row[b] = row_at(b * 16 + (lane >> 4) * 8 + (lane & 7));
+    v_row[b] = row_at(b * 16 + ((lane >> 3) & 1) * 8 + (lane & 7));
+  }
 
   for (int id = static_cast<int>(blockIdx.x);; id += static_cast<int>(gridDim.x)) {
     const Item t = find_item(p, id);
     if (id >= total) break;
     __syncthreads();      // the ring of the item before is free, its flags have been read
     if (tid == 0) redo = 0;
-    const int runs = (t.k1 - t.k0 + kSubKeys - 1) / kSubKeys;       // of the item
+    const int runs = (t.k1 - t.k0 + KEYS - 1) / KEYS;       // of the item
     const int my_runs = runs > kg ? (runs - kg + kKeyGroups - 1) / kKeyGroups : 0;
+    const int kv_head = __shfl_sync(0xffffffffu, t.head, 0);
+
+    // the page of a box of the group's run i, -1 (zeros) where no row of the item sees it; a step
+    // ahead: the table's entry arrives while the step is computed
+    auto look_up = [&](int i, int &page, int &row) {
+      const int64_t key =
+          static_cast<int64_t>(t.k0) + (static_cast<int64_t>(i) * kKeyGroups + kg) * KEYS + lane * maps.box;
+      page = -1;
+      row = 0;
+      if (lane < subs && key < t.k1 && key + maps.box > t.first) {
+        const int n = static_cast<int>(key) / p.page_size;
+        page = page_entry(p, t.b, n);
+        row = static_cast<int>(key) - n * p.page_size;
+      }
+    };
+    // the copies of the group's next run (its first warp)
+    auto issue = [&](int page, int row) {
+      const uint32_t slot = issued % kRowStages;
+      if (RG > 1) {
+        ok = ok && wait_all(&empty[kg][slot], ((issued / kRowStages) & 1) ^ 1, abort_flag, p.timeout_ns, err);
+        if (!ok) return;
+      }
+      const int checked = checked_page(p, page);
+      uint8_t *dst = mine + slot * STAGE;
+      if (elect_one()) mbar_arrive_expect_tx(&full[kg][slot], STAGE);
+      __syncwarp();
+      for (int j = 0; j < subs; ++j) {
+        const int pg = __shfl_sync(0xffffffffu, checked, j), rw = __shfl_sync(0xffffffffu, row, j);
+        if (elect_one()) {
+          tma_load_5d(dst, &maps.k, &full[kg][slot], 0, rw, 0, kv_head, pg);
+          tma_load_5d(dst + STAGE / 2, &maps.v, &full[kg][slot], 0, rw, 0, kv_head, pg);
+          if (H > 1 && parts > 1) {
+            tma_load_5d(dst + half_bytes, &maps.k, &full[kg][slot], 64, rw, 0, kv_head, pg);
+            tma_load_5d(dst + STAGE / 2 + half_bytes, &maps.v, &full[kg][slot], 64, rw, 0, kv_head, pg);
+          }
+        }
+        dst += H * half_bytes;
+        __syncwarp();
+      }
+      ++issued;
+    };
+    int page[kRowStages + 1], row[kRowStages + 1];
+    if (rg == 0) {
+#pragma unroll
+      for (int i = 0; i <= kRowStages; ++i) look_up(i, page[i], row[i]);
+#pragma unroll
+      for (int i = 0; i < kRowStages; ++i)
+        if (i < my_runs) issue(page[i], row[i]);
+    }
+    int next_page = page[kRowStages], next_row = row[kRowStages];
 
     // q, as the A operand: rows lane / 4 and + 8, pairs (lane % 4) of each 8 columns
     uint32_t q[DP / 16][4];
     int64_t token;
-    int head, pos[2];
+    int head, begin[2], end[2];      // keys that the rows see
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int r = rg * 16 + lane / 4 + 8 * h;
       const bool live = r < t.rows;
-      row_of(p, t, live ? r : 0, token, head, pos[h]);
+      int pos;
+      row_of(p, t, live ? r : 0, token, head, pos);
+      begin[h] = p.window ? pos - p.window + 1 : 0;
+      end[h] = min(pos + 1, t.k1);
       const uint16_t *src = p.q + token * p.q_t + head * p.q_h;
 #pragma unroll
       for (int kk = 0; kk < DP / 16; ++kk)
@@ -287,91 +371,50 @@ __global__ void __launch_bounds__(32 * kKeyGroups * RG, 3 - RG)
         }
     }
 
-    // pages of the warp's next runs: lane l has the 8 keys l % 2 of run l / 2
-    int page = -1, row = 0, page_next = -1, row_next = 0;
-    auto fetch_pages = [&](int from, int &pg, int &rw) {
-      const int run = (from + lane / 2) * kKeyGroups + kg;
-      const int64_t key = static_cast<int64_t>(t.k0) + static_cast<int64_t>(run) * kSubKeys + (lane & 1) * 8;
-      pg = -1;
-      rw = 0;
-      if (key < t.k1) {
-        const int n = static_cast<int>(key) / p.page_size;
-        pg = page_of(p, t.b, n);
-        rw = static_cast<int>(key) - n * p.page_size;
-      }
-    };
-    fetch_pages(0, page_next, row_next);
-    auto issue = [&](int i) {       // copies of the warp's run i
-      if (i < my_runs) {
-        if ((i & 15) == 0) {
-          page = page_next;
-          row = row_next;
-          fetch_pages(i + 16, page_next, row_next);
-        }
-        const uint32_t dst = mine + (i % kRowStages) * STAGE;
-        const int key0 = t.k0 + (i * kKeyGroups + kg) * kSubKeys;
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          const int pg = __shfl_sync(0xffffffffu, page, 2 * (i & 15) + g);
-          const int rw = __shfl_sync(0xffffffffu, row, 2 * (i & 15) + g);
-          const bool ok = pg >= 0 && ch * 8 < p.D;
-          const int64_t pg0 = ok ? pg : 0;
-          const int c0 = ok ? ch * 8 : 0;
-          const uint16_t *k = p.k + pg0 * p.k_page + t.head * p.k_head + (rw + sub) * p.k_row + c0;
-          const uint16_t *v = p.v + pg0 * p.v_page + t.head * p.v_head + (rw + sub) * p.v_row + c0;
-#pragma unroll
-          for (int x = 0; x < 8 / PASS; ++x) {
-            const int j = g * 8 + x * PASS + sub;
-            const uint32_t bytes = ok && key0 + j < t.k1 && key0 + j >= t.first ? 16u : 0u;
-            const uint32_t at = dst + j * (DP * 2) + ((ch ^ (j & 7)) << 4);
-            if (RG == 1 || rg == 0) cp_async16(at, k + x * PASS * p.k_row, bytes);
-            if (RG == 1 || rg == 1) cp_async16(at + kSubKeys * DP * 2, v + x * PASS * p.v_row, bytes);
-          }
-        }
-      }
-      asm volatile("cp.async.commit_group;" ::: "memory");
-    };
-
     float o[DP / 8][4];
 #pragma unroll
     for (int i = 0; i < DP / 8; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) o[i][j] = 0.0f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
-#pragma unroll
-    for (int i = 0; i < kRowStages - 1; ++i) issue(i);
     for (int i = 0; i < my_runs; ++i) {
-      if constexpr (RG == 1) {
-        __syncwarp();                  // every lane has read the stage that is filled next
-        issue(i + kRowStages - 1);
-        asm volatile("cp.async.wait_group %0;" ::"n"(kRowStages - 1) : "memory");
+      const uint32_t slot = used % kRowStages;
+      if (!(ok = ok && wait_all(&full[kg][slot], (used / kRowStages) & 1, abort_flag, p.timeout_ns, err))) break;
+      uint8_t *stage = mine + slot * STAGE;
+      const int run0 = t.k0 + (i * kKeyGroups + kg) * KEYS;
+      if (run0 + KEYS > t.k1 || run0 < t.first) {
+        // rows of V that no row of the item sees may hold anything: a weight of 0 does not take out
+        // infinities or NaN
+        for (int x = lane; x < KEYS * (DP / 8); x += 32) {
+          const int j = x / (DP / 8), c = x % (DP / 8);
+          if (run0 + j >= t.k1 || run0 + j < t.first)
+            *reinterpret_cast<uint4 *>(stage + STAGE / 2 + row_at(j) + (c >> 3) * half_bytes + (c & 7) * 16) =
+                make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
         __syncwarp();
-      } else {
-        // both halves of stage i are there, and stage i - 1 has been read
-        asm volatile("cp.async.wait_group %0;" ::"n"(kRowStages - 2) : "memory");
-        asm volatile("bar.sync %0, %1;" ::"r"(1 + kg), "n"(32 * RG) : "memory");
-        issue(i + kRowStages - 1);
       }
-      const uint32_t ks = mine + (i % kRowStages) * STAGE, vs = ks + kSubKeys * DP * 2;
-      float s[2][4] = {};
-      {
-        const int j = (lane >> 4) * 8 + (lane & 7);
+      const uint32_t ks = smem_u32(stage), vs = ks + STAGE / 2;
+      float s[KEYS / 8][4] = {};
 #pragma unroll
-        for (int kk = 0; kk < DP / 16; ++kk) {
+      for (int kk = 0; kk < DP / 16; ++kk) {
+        const int c = 2 * kk + ((lane >> 3) & 1);
+#pragma unroll
+        for (int n = 0; n < KEYS / 16; ++n) {
           uint32_t b[4];
-          ldmatrix4(ks + j * (DP * 2) + (((2 * kk + ((lane >> 3) & 1)) ^ (j & 7)) << 4), b);
-          mma16816<A>(s[0], q[kk], b[0], b[1]);
-          mma16816<A>(s[1], q[kk], b[2], b[3]);
+          ldmatrix4(ks + k_row[n] + (c >> 3) * half_bytes + (((c ^ lane) & 7) << 4), b);
+          mma16816<A>(s[2 * n], q[kk], b[0], b[1]);
+          mma16816<A>(s[2 * n + 1], q[kk], b[2], b[3]);
         }
       }
-      const int key0 = t.k0 + (i * kKeyGroups + kg) * kSubKeys + (lane & 3) * 2;
+      const int key0 = run0 + (lane & 3) * 2;
       float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+      for (int n = 0; n < KEYS / 8; ++n)
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          const int key = key0 + n * 8 + (x & 1), at = pos[x >> 1];
-          const bool seen = key <= at && key < t.k1 && (!p.window || key > at - p.window);
+          const int key = key0 + n * 8 + (x & 1);
+          const bool seen = key < end[x >> 1] && key >= begin[x >> 1];
           s[n][x] = seen ? s[n][x] * p.scale_log2 : -INFINITY;
           top[x >> 1] = fmaxf(top[x >> 1], s[n][x]);
         }
@@ -386,9 +429,9 @@ __global__ void __launch_bounds__(32 * kKeyGroups * RG, 3 - RG)
         m[h] = now;
         l[h] *= shrink[h];
       }
-      uint32_t a[4];
+      uint32_t a[KEYS / 16][4];
 #pragma unroll
-      for (int n = 0; n < 2; ++n) {
+      for (int n = 0; n < KEYS / 8; ++n) {
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           s[n][x] = ex2(s[n][x] - base[x >> 1]);
@@ -396,8 +439,8 @@ __global__ void __launch_bounds__(32 * kKeyGroups * RG, 3 - RG)
         }
         // weights as the products take them: rounded to the activations' type (one part in
         // 256 for bf16, of either sign); the sum l is that of the f32 weights
-        a[2 * n] = A::pack2(s[n][0], s[n][1]);
-        a[2 * n + 1] = A::pack2(s[n][2], s[n][3]);
+        a[n / 2][2 * (n & 1)] = A::pack2(s[n][0], s[n][1]);
+        a[n / 2][2 * (n & 1) + 1] = A::pack2(s[n][2], s[n][3]);
       }
       if (shrink[0] != 1.0f || shrink[1] != 1.0f) {
 #pragma unroll
@@ -408,24 +451,32 @@ __global__ void __launch_bounds__(32 * kKeyGroups * RG, 3 - RG)
           o[d][3] *= shrink[1];
         }
       }
-      {
-        const int j = ((lane >> 3) & 1) * 8 + (lane & 7);
+#pragma unroll
+      for (int n = 0; n < KEYS / 16; ++n)
 #pragma unroll
         for (int d = 0; d < DP / 16; ++d) {
+          const int c = 2 * d + (lane >> 4);
           uint32_t b[4];
-          ldmatrix4_trans(vs + j * (DP * 2) + (((2 * d + (lane >> 4)) ^ (j & 7)) << 4), b);
-          mma16816<A>(o[2 * d], a, b[0], b[1]);
-          mma16816<A>(o[2 * d + 1], a, b[2], b[3]);
+          ldmatrix4_trans(vs + v_row[n] + (c >> 3) * half_bytes + (((c ^ lane) & 7) << 4), b);
+          mma16816<A>(o[2 * d], a[n], b[0], b[1]);
+          mma16816<A>(o[2 * d + 1], a[n], b[2], b[3]);
         }
+      // the stage is read: the run kRowStages further takes its place
+      ++used;
+      __syncwarp();
+      if (RG > 1 && lane == 0) mbar_arrive(&empty[kg][slot]);
+      if (rg == 0 && i + kRowStages < my_runs) {
+        issue(next_page, next_row);
+        look_up(i + kRowStages + 1, next_page, next_row);
       }
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
       l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
     }
     __syncthreads();
+    if (*abort_flag) break;
     // the warps' sums, in the rings' place
     constexpr int PITCH = DP + 4;
     float *sum = reinterpret_cast<float *>(ring);
@@ -445,6 +496,7 @@ __global__ void __launch_bounds__(32 * kKeyGroups * RG, 3 - RG)
     __syncthreads();
     // a row to 8 threads, 8 columns at a time
     const int r = tid / 8;
+    fence_proxy_async_smem();      // (the next copies overwrite the sums)
     bool finite = true;
     if (r < t.rows) {
       float top = warp_m[0][r];
@@ -489,39 +541,47 @@ __global__ void __launch_bounds__(32 * kKeyGroups * RG, 3 - RG)
       if (x % kRowWarps == warp) exact_row<A>(p, t, x);
     }
   }
+  // given up: the copies in flight
+  if (rg == 0 && *abort_flag)
+    for (uint32_t c = used; c < issued; ++c)
+      mbar_wait_drain(&full[kg][c % kRowStages], (c / kRowStages) & 1, p.timeout_ns);
   if (p.after_tiles) griddep_wait();       // the next kernel comes after both
 }
 
 // -------------------------------------------------------------------- join --
 
-// Rows of split sequences: o = sum_s 2^(lse_s - top) o_s / sum_s 2^(lse_s - top), in the
-// order of the splits.  A warp per row; a split without a key the row sees holds zeros
-// and -infinity.  What the plan says is read before the attention has ended: it was
-// complete before that began.
-template <class A>
+// Rows of split sequences: o = sum_s 2^(lse_s - top) o_s / sum_s 2^(lse_s - top), in a fixed
+// order.  WARPS warps to a row (8 where there are few rows: each takes every eighth split);
+// a split without a key the row sees holds zeros and -infinity.  What the plan says is read
+// before the attention has ended: it was complete before that began.
+template <class A, int WARPS>
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ AttnParams p) {
   constexpr int kStep = 8;       // splits in flight
-  const int lane = static_cast<int>(lane_id()), c = lane * 4;
+  constexpr int kRowsOfCta = 8 / WARPS;
+  __shared__ float4 sums[WARPS > 1 ? 8 : 1][32];
+  __shared__ float2 tops[8];
+  const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(lane_id()), c = lane * 4;
   const int64_t rows = static_cast<int64_t>(p.T) * p.heads;
   const int any = __ldg(p.plan.head + 2);
-  int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  int64_t row = static_cast<int64_t>(blockIdx.x) * kRowsOfCta + warp / WARPS;
   bool waited = false;
-  for (; any && row < rows; row += static_cast<int64_t>(gridDim.x) * 8) {
+  for (; any && row < rows; row += static_cast<int64_t>(gridDim.x) * kRowsOfCta) {
     const int b = __ldg(p.plan.seq_of + row / p.heads);
     const int splits = b < 0 ? 1 : __ldg(&p.plan.rec[b].splits);
     if (!waited) griddep_wait();
     waited = true;
     if (splits <= 1) continue;
     float top = -INFINITY, all = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int s0 = 0; s0 < splits; s0 += kStep) {
+    for (int s0 = warp % WARPS; s0 < splits; s0 += kStep * WARPS) {
       float lse[kStep];
       float4 v[kStep];
 #pragma unroll
       for (int i = 0; i < kStep; ++i) {
-        const int64_t at = (s0 + i) * rows + row;
-        lse[i] = s0 + i < splits ? p.part_lse[at] : -INFINITY;
-        v[i] = s0 + i < splits && c < p.D ? *reinterpret_cast<const float4 *>(p.part + at * p.D + c)
-                                          : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        const int s = s0 + i * WARPS;
+        const int64_t at = s * rows + row;
+        lse[i] = s < splits ? p.part_lse[at] : -INFINITY;
+        v[i] = s < splits && c < p.D ? *reinterpret_cast<const float4 *>(p.part + at * p.D + c)
+                                     : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       }
       float now = top;
 #pragma unroll
@@ -541,6 +601,30 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ AttnP
         o[3] = fmaf(w, v[i].w, o[3]);
       }
     }
+    if constexpr (WARPS > 1) {
+      sums[warp][lane] = make_float4(o[0], o[1], o[2], o[3]);
+      if (lane == 0) tops[warp] = make_float2(top, all);
+      __syncthreads();
+      if (warp == 0) {
+        float now = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) now = fmaxf(now, tops[w].x);
+        const float base = now == -INFINITY ? 0.0f : now;
+        all = o[0] = o[1] = o[2] = o[3] = 0.0f;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) {
+          const float f = ex2(tops[w].x - base);
+          const float4 v = sums[w][lane];
+          all = fmaf(f, tops[w].y, all);
+          o[0] = fmaf(f, v.x, o[0]);
+          o[1] = fmaf(f, v.y, o[1]);
+          o[2] = fmaf(f, v.z, o[2]);
+          o[3] = fmaf(f, v.w, o[3]);
+        }
+      }
+      __syncthreads();
+      if (warp > 0) continue;
+    }
     const float inv = all == 0.0f ? 0.0f : 1.0f / all;
     if (c < p.D)
       *reinterpret_cast<uint2 *>(p.out + row * p.D + c) =
@@ -550,22 +634,47 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ AttnP
 }
 
 template <class A>
-cudaError_t launch_rows(const AttnParams &p, const ListForm &f, cudaStream_t stream) {
+cudaError_t launch_join(const AttnParams &p, int num_sms, cudaStream_t stream) {
+  // few CTAs: often no sequence is split, and they only begin and end
+  const int64_t rows = static_cast<int64_t>(p.T) * p.heads, most = 8 * static_cast<int64_t>(num_sms);
+  const auto grid = [&](int64_t ctas) { return dim3(static_cast<unsigned>(ctas < most ? ctas : most)); };
+  return rows <= most ? launch_on(join_kernel<A, 8>, grid(rows), 256, 0, stream, true, p)
+                      : launch_on(join_kernel<A, 1>, grid((rows + 7) / 8), 256, 0, stream, true, p);
+}
+
+template <class A, int DP, int RG>
+cudaError_t launch_rows_form(const AttnParams &p, const CacheMaps &maps, dim3 grid, cudaStream_t stream) {
+  const int bytes = kKeyGroups * row_stages(DP, RG) * row_stage_bytes(DP, RG) + 1024;
+  auto kernel = attn_rows_kernel<A, DP, RG>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  return e != cudaSuccess ? e
+                          : launch_on(kernel, grid, 32 * kKeyGroups * RG, bytes, stream, p.after_tiles != 0, p, maps);
+}
+
+template <class A>
+cudaError_t launch_rows(const AttnParams &p, const ListForm &f, const qsw_kv_cache &cache, cudaStream_t stream) {
   const int64_t most = 2 * static_cast<int64_t>(f.slots);
   const dim3 grid(static_cast<unsigned>(f.items < most ? f.items : most));
-  auto go = [&](auto kernel, int groups, int bytes) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    return e != cudaSuccess ? e : launch_on(kernel, grid, 32 * kKeyGroups * groups, bytes, stream, p.after_tiles, p);
-  };
   const bool one = f.tile_rows == 16;
+  CacheMaps maps = {};
+  if (!encode_cache_maps(&maps, cache, p.D, A::kId, step_keys(p.D <= 64 ? 64 : 128, one ? 1 : 2), true))
+    return cudaErrorInvalidValue;
   if (p.D <= 64)
-    return one ? go(attn_rows_kernel<A, 64, 1>, 1, kKeyGroups * row_stages<1> * row_stage_bytes<64>)
-               : go(attn_rows_kernel<A, 64, 2>, 2, kKeyGroups * row_stages<2> * row_stage_bytes<64>);
-  return one ? go(attn_rows_kernel<A, 128, 1>, 1, kKeyGroups * row_stages<1> * row_stage_bytes<128>)
-             : go(attn_rows_kernel<A, 128, 2>, 2, kKeyGroups * row_stages<2> * row_stage_bytes<128>);
+    return one ? launch_rows_form<A, 64, 1>(p, maps, grid, stream) : launch_rows_form<A, 64, 2>(p, maps, grid, stream);
+  return one ? launch_rows_form<A, 128, 1>(p, maps, grid, stream) : launch_rows_form<A, 128, 2>(p, maps, grid, stream);
 }
 
 }  // namespace
+
+cudaError_t attention_take_errors(unsigned int *out) {
+  unsigned int tiles = 0, rows = 0, zero = 0;
+  cudaError_t e = tiles_take_errors(&tiles);
+  if (e != cudaSuccess) return e;
+  e = cudaMemcpyFromSymbol(&rows, g_rows_error, sizeof rows);
+  if (e == cudaSuccess && rows) e = cudaMemcpyToSymbol(g_rows_error, &zero, sizeof zero);
+  *out = tiles | rows;
+  return e;
+}
 
 // Largest buffer of split results, and the most splits of a sequence.
 constexpr int64_t kPartBytes = int64_t(128) << 20;
@@ -580,7 +689,7 @@ AttnForm attention_form(int64_t T, int64_t B, int64_t heads, int64_t kv_heads, i
   const int64_t few = T <= B ? group : B == 1 ? T * group : 32;
   ListForm &r = f.list[LIST_ROWS], &t = f.list[LIST_TILES];
   r.tile_rows = few <= 16 ? 16 : 32;
-  r.tile_keys = kKeyGroups * kSubKeys;
+  r.tile_keys = kKeyGroups * step_keys(D <= 64 ? 64 : 128, r.tile_rows / 16);
   r.slots = r.tile_rows == 16 ? 2 * num_sms : num_sms;
   t.tile_rows = 256;
   t.tile_keys = 128;
@@ -687,13 +796,10 @@ cudaError_t launch_paged_attention(const AttentionArgs &a, int num_sms, uint64_t
     p.after_tiles = 1;
   }
   if (e == cudaSuccess && set(LIST_ROWS))
-    e = f16 ? launch_rows<ActF16>(p, f.list[LIST_ROWS], stream) : launch_rows<ActBf16>(p, f.list[LIST_ROWS], stream);
+    e = f16 ? launch_rows<ActF16>(p, f.list[LIST_ROWS], c, stream)
+            : launch_rows<ActBf16>(p, f.list[LIST_ROWS], c, stream);
   if (e != cudaSuccess || f.max_splits == 1) return e;
-  // (few CTAs: often no sequence is split, and they only begin and end)
-  const int64_t ctas = (a.T * a.heads + 7) / 8, most = 8 * static_cast<int64_t>(num_sms);
-  const dim3 grid(static_cast<unsigned>(ctas < most ? ctas : most));
-  return f16 ? launch_on(join_kernel<ActF16>, grid, 256, 0, stream, true, p)
-             : launch_on(join_kernel<ActBf16>, grid, 256, 0, stream, true, p);
+  return f16 ? launch_join<ActF16>(p, num_sms, stream) : launch_join<ActBf16>(p, num_sms, stream);
 }
 
 }  // namespace qsw

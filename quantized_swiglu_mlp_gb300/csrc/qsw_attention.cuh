@@ -148,11 +148,14 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// Page of a sequence's tokens [page * page_size, ..), -1 for one that no cache row belongs to.
+// Page of a sequence's tokens [page * page_size, ..) as the table has it, and as it is used: -1
+// where it is not in the cache.  (Apart, so that a copy's page can be asked for ahead.)
+__device__ __forceinline__ int page_entry(const AttnParams &p, int b, int page) {
+  return page < p.max_pages ? __ldg(p.page_table + b * p.table_stride + page) : -1;
+}
+__device__ __forceinline__ int checked_page(const AttnParams &p, int id) { return id >= 0 && id < p.pages ? id : -1; }
 __device__ __forceinline__ int page_of(const AttnParams &p, int b, int page) {
-  if (page >= p.max_pages) return -1;
-  const int id = __ldg(p.page_table + b * p.table_stride + page);
-  return id >= 0 && id < p.pages ? id : -1;
+  return checked_page(p, page_entry(p, b, page));
 }
 
 // Row r of an item by one warp, key by key with what the row does not see left out, for
@@ -237,7 +240,46 @@ struct AttnForm {
   int max_splits;         // 1: no history is split
 };
 
+// K and V of a cache as tensors of (column, row, half of a head, head, page), boxes of 64
+// columns by `box` rows of a page.  One box holds all halves of its rows where D is a
+// multiple of 64; else (halves == 1) a half is a box at its first column, and columns past D
+// read 0.
+struct CacheMaps {
+  CUtensorMap k, v;
+  int box;
+  int halves;            // of a box
+};
+// Boxes of at most `most_rows` rows (a power of two); `whole`: of all halves, if D allows.  False
+// where the cache cannot be described.
+bool encode_cache_maps(CacheMaps *maps, const qsw_kv_cache &cache, int64_t D, int act, int most_rows, bool whole);
+
+__device__ __forceinline__ void tma_load_5d(void *dst, const CUtensorMap *map, uint64_t *bar, int c0, int c1, int c2,
+                                            int c3, int c4) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6, %7}], "
+      "[%2];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
+      : "memory");
+}
+
+// One thread of a converged warp.  Copies are issued by a thread chosen this way, with
+// operands from one lane of a shuffle: with a lane per copy and operands of its own a copy
+// took about 400 cycles to issue.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
+// A wait of a whole warp, one vote where the phase is complete.
+__device__ __forceinline__ bool wait_all(uint64_t *bar, uint32_t parity, volatile int *abort, uint64_t timeout_ns,
+                                         unsigned int *err) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, timeout_ns, err));
+}
+
 cudaError_t launch_attention_tiles(const AttnParams &p, const ListForm &f, int act, const qsw_kv_cache &cache,
                                    cudaStream_t stream);
+cudaError_t tiles_take_errors(unsigned int *out);
 
 }  // namespace qsw

@@ -46,27 +46,6 @@ struct Shape {
   static constexpr int kSmem = (2 + kStages) * kTileBytes + 1024;
 };
 
-struct TcMaps {
-  CUtensorMap k, v;
-  int box;               // rows of a box
-  int k_head_first, v_head_first;   // order of the maps' dimensions
-};
-
-__device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, uint64_t *bar, int c0, int c1, int c2,
-                                            int c3) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], "
-      "[%2];" ::"r"(smem_u32(dst)),
-      "l"(map), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
-      : "memory");
-}
-
-__device__ __forceinline__ bool elect_one() {
-  uint32_t r;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(r));
-  return r != 0;
-}
-
 // D[tmem] (+)= A[tmem] . B[smem]
 __device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
                                         uint32_t accumulate) {
@@ -130,14 +109,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
-// A wait of a whole warp, one vote where the phase is complete (the products' issuer waits
-// four times a tile, and beside eight busy warps every instruction of it counts).
-__device__ __forceinline__ bool wait_all(uint64_t *bar, uint32_t parity, volatile int *abort, uint64_t timeout_ns,
-                                         unsigned int *err) {
-  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, timeout_ns, err));
-}
-
 // The item of a CTA's step: every second wave in reverse, since items come longest first.
 __device__ __forceinline__ int item_of(int step) {
   const int G = static_cast<int>(gridDim.x), c = static_cast<int>(blockIdx.x);
@@ -196,7 +167,7 @@ __device__ __forceinline__ int tiles_of_item(const Item *t) { return (t->k1 - t-
 
 template <class A, int DP>
 __global__ void __launch_bounds__(kThreads, 1)
-    attn_tiles_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ TcMaps maps) {
+    attn_tiles_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CacheMaps maps) {
   using S = Shape<DP>;
   constexpr int KS = S::kKStages, VS = S::kVStages;
   extern __shared__ uint8_t smem_raw[];
@@ -210,6 +181,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   unsigned int *err = &g_attn_error;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
+  griddep_wait();
+  griddep_launch_dependents();
+  // (often there are no such sequences: nothing to set up then)
+  const int total = __ldg(p.plan.head + LIST_TILES);
+  if (item_of(0) >= total) return;
   if constexpr (kDebugBounds) debug_poison_smem(smem, (2 + S::kStages) * S::kTileBytes);
   if (threadIdx.x == 0) {
     for (int i = 0; i < 4; ++i) {
@@ -245,8 +221,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
-  griddep_wait();
-  griddep_launch_dependents();
   // Tensor memory: S (and P) of the two row tiles, then O of both.
   const uint32_t o_col = 256;
 
@@ -601,25 +575,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint64_t *full = is_k ? bar.k_full : bar.v_full, *empty = is_k ? bar.k_empty : bar.v_empty;
       uint8_t *ring = is_k ? k_smem : v_smem;
       const CUtensorMap *map = is_k ? &maps.k : &maps.v;
-      const bool head_first = is_k ? maps.k_head_first : maps.v_head_first;
-      // a lane per box
-      const int per_half = kKeys / maps.box, half = lane / per_half, j = lane - half * per_half;
-      const bool has_box = half < S::kHalves;
+      // a lane per box of rows (of all halves, or of one) looks its page up
+      const int boxes = kKeys / maps.box, parts = S::kHalves / maps.halves;
       uint32_t count = 0;
       ItemCursor cursor;
       for (const Item *next; (next = cursor.next(bar, items, abort_flag, p.timeout_ns, err));) {
         const Item t = *next;
         const int n = tiles_of_item(next);
         cursor.done(bar, 0);
+        const int head = __shfl_sync(0xffffffffu, t.head, 0);
         int page = -1, row = 0;
         auto look_up = [&](int i) {
-          const int64_t key = static_cast<int64_t>(t.k0) + static_cast<int64_t>(i) * kKeys + j * maps.box;
+          const int64_t key = static_cast<int64_t>(t.k0) + static_cast<int64_t>(i) * kKeys + lane * maps.box;
           page = -1;
           row = 0;
-          if (has_box && key < t.k1 && key + maps.box > t.first) {
+          if (lane < boxes && key < t.k1 && key + maps.box > t.first) {
             const int x = static_cast<int>(key) / p.page_size;
             row = static_cast<int>(key) - x * p.page_size;
-            page = page_of(p, t.b, x);
+            page = page_entry(p, t.b, x);
           }
         };
         look_up(0);
@@ -627,13 +600,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < n; ++i, ++count) {
           const uint32_t slot = count % stages;
           if (!(ok = wait_all(&empty[slot], ((count / stages) & 1) ^ 1, abort_flag, p.timeout_ns, err))) break;
-          if (lane == 0) mbar_arrive_expect_tx(&full[slot], S::kTileBytes);
+          const int checked = checked_page(p, page);
+          if (elect_one()) mbar_arrive_expect_tx(&full[slot], S::kTileBytes);
           __syncwarp();
-          if (has_box) {
-            uint8_t *dst = ring + slot * S::kTileBytes + half * S::kHalfBytes + j * maps.box * 128;
-            tma_load_4d(dst, map, &full[slot], half * 64, head_first ? t.head : row, head_first ? row : t.head, page);
+          for (int j = 0; j < boxes; ++j) {
+            const int pg = __shfl_sync(0xffffffffu, checked, j), rw = __shfl_sync(0xffffffffu, row, j);
+            if (elect_one()) {
+              uint8_t *dst = ring + slot * S::kTileBytes + j * maps.box * 128;
+              tma_load_5d(dst, map, &full[slot], 0, rw, 0, head, pg);
+              if (S::kHalves > 1 && parts > 1) tma_load_5d(dst + S::kHalfBytes, map, &full[slot], 64, rw, 0, head, pg);
+            }
+            __syncwarp();
           }
-          __syncwarp();
           if (i + 1 < n) look_up(i + 1);
         }
         if (!ok) break;
@@ -644,7 +622,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_wait_drain(&full[c % stages], (c / stages) & 1, p.timeout_ns);
     } else if (warp == kWarpItems) {
       // ------------------------------------------------------------- items --
-      const int total = __ldg(p.plan.head + LIST_TILES);
       for (int step = 0;; ++step) {
         const int slot = step % kItems, id = item_of(step);
         Item t = find_item(p, id);
@@ -684,30 +661,25 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// A cache as a tensor of (D, rows, heads, pages), rows and heads in the order of their
-// strides; boxes of 64 columns by `box` rows of a page.
-bool encode_cache(CUtensorMap *map, int *head_first, const void *base, const int64_t (&strides)[3],
-                  const qsw_kv_cache &c, int64_t D, int box, bool f16) {
+bool encode_cache(CUtensorMap *map, const void *base, const int64_t (&strides)[3], const qsw_kv_cache &c, int64_t D,
+                  int act, int box, int halves) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
-  const bool hf = strides[1] < strides[2];
-  const cuuint64_t rows = static_cast<cuuint64_t>(c.page_size), heads = static_cast<cuuint64_t>(c.kv_heads);
-  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), hf ? heads : rows, hf ? rows : heads,
+  const cuuint64_t dims[5] = {static_cast<cuuint64_t>(halves > 1 ? 64 : D), static_cast<cuuint64_t>(c.page_size),
+                              static_cast<cuuint64_t>(halves), static_cast<cuuint64_t>(c.kv_heads),
                               static_cast<cuuint64_t>(c.pages)};
-  const cuuint64_t bytes[3] = {static_cast<cuuint64_t>(hf ? strides[1] : strides[2]) * 2,
-                               static_cast<cuuint64_t>(hf ? strides[2] : strides[1]) * 2,
+  const cuuint64_t bytes[4] = {static_cast<cuuint64_t>(strides[2]) * 2, 128, static_cast<cuuint64_t>(strides[1]) * 2,
                                static_cast<cuuint64_t>(strides[0]) * 2};
-  const cuuint32_t b = static_cast<cuuint32_t>(box);
-  const cuuint32_t boxes[4] = {64, hf ? 1 : b, hf ? b : 1, 1};
-  const cuuint32_t one[4] = {1, 1, 1, 1};
-  *head_first = hf;
-  return fn(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base),
-            dims, bytes, boxes, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  const cuuint32_t boxes[5] = {64, static_cast<cuuint32_t>(box), static_cast<cuuint32_t>(halves), 1, 1};
+  const cuuint32_t one[5] = {1, 1, 1, 1, 1};
+  return fn(map, act == ActF16::kId ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5,
+            const_cast<void *>(base), dims, bytes, boxes, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <class A, int DP>
-cudaError_t launch_shape(const AttnParams &p, const TcMaps &maps, int grid, cudaStream_t stream) {
+cudaError_t launch_shape(const AttnParams &p, const CacheMaps &maps, int grid, cudaStream_t stream) {
   auto kernel = attn_tiles_kernel<A, DP>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<DP>::kSmem);
   return e != cudaSuccess ? e : launch_on(kernel, dim3(static_cast<unsigned>(grid)), kThreads, Shape<DP>::kSmem, stream,
@@ -716,23 +688,29 @@ cudaError_t launch_shape(const AttnParams &p, const TcMaps &maps, int grid, cuda
 
 }  // namespace
 
+bool encode_cache_maps(CacheMaps *maps, const qsw_kv_cache &cache, int64_t D, int act, int most_rows, bool whole) {
+  // the largest power of two of a page's rows: no box leaves a page
+  const int64_t box = cache.page_size & -cache.page_size;
+  maps->box = static_cast<int>(box < most_rows ? box : most_rows);
+  maps->halves = whole && D % 64 == 0 ? static_cast<int>(D / 64) : 1;
+  return encode_cache(&maps->k, cache.k, cache.k_strides, cache, D, act, maps->box, maps->halves) &&
+         encode_cache(&maps->v, cache.v, cache.v_strides, cache, D, act, maps->box, maps->halves);
+}
+
 cudaError_t launch_attention_tiles(const AttnParams &p, const ListForm &f, int act, const qsw_kv_cache &cache,
                                    cudaStream_t stream) {
   const bool f16 = act == ActF16::kId;
-  TcMaps maps = {};
-  // the largest power of two of a page's rows, at most a tile: no box leaves a page
-  maps.box = static_cast<int>(cache.page_size & -cache.page_size);
-  if (maps.box > kKeys) maps.box = kKeys;
-  if (!encode_cache(&maps.k, &maps.k_head_first, cache.k, cache.k_strides, cache, p.D, maps.box, f16) ||
-      !encode_cache(&maps.v, &maps.v_head_first, cache.v, cache.v_strides, cache, p.D, maps.box, f16))
-    return cudaErrorInvalidValue;
+  CacheMaps maps = {};
+  // (the products take a tile's halves one after the other: only a box of a whole tile may
+  // hold both)
+  if (!encode_cache_maps(&maps, cache, p.D, act, kKeys, cache.page_size % kKeys == 0)) return cudaErrorInvalidValue;
   const int grid = static_cast<int>(f.items < f.slots ? f.items : f.slots);
   if (p.D <= 64)
     return f16 ? launch_shape<ActF16, 64>(p, maps, grid, stream) : launch_shape<ActBf16, 64>(p, maps, grid, stream);
   return f16 ? launch_shape<ActF16, 128>(p, maps, grid, stream) : launch_shape<ActBf16, 128>(p, maps, grid, stream);
 }
 
-cudaError_t attention_take_errors(unsigned int *out) {
+cudaError_t tiles_take_errors(unsigned int *out) {
   unsigned int v = 0, zero = 0;
   cudaError_t e = cudaMemcpyFromSymbol(&v, g_attn_error, sizeof v);
   if (e != cudaSuccess) return e;
