@@ -34,9 +34,10 @@ constexpr int kPlanThreads = 1024;
 // The split, for each list: a chunk of keys that its sequences are cut into, chosen among 32
 // (a warp each) by the time it would take in tiles -- the longest item, or the work of all
 // over the CTAs that run at once, in whole waves; an item costs kItemCost tiles more for its
-// beginning and end, and one of a split history kSplitCost more for what it leaves to the join.
+// beginning and end, and one of a split history kSplitCost more for what it leaves to the join
+// (up to 256 rows of f32 written and read again; 16 or 32 in the other list).
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ PlanParams p) {
-  constexpr float kItemCost = 3.0f, kSplitCost = 3.0f;
+  constexpr float kItemCost = 3.0f, kSplitCost[2] = {2.0f, 7.0f};
   constexpr int kLeast = 4;        // tiles of a split, at least
   griddep_wait();
   griddep_launch_dependents();
@@ -134,7 +135,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
       const SeqRec s = p.out.rec[b];
       if (!s.blocks || s.first[0] != list) continue;
       const int splits = max(1, min(p.max_splits, (s.chunk + c - 1) / c));
-      const float n = static_cast<float>(s.blocks) * p.kv_heads, cost = splits > 1 ? kItemCost + kSplitCost : kItemCost;
+      const float n = static_cast<float>(s.blocks) * p.kv_heads, cost = splits > 1 ? kItemCost + kSplitCost[list] : kItemCost;
       items += n * splits;
       work += n * (s.splits + cost * splits);
       long_item = fmaxf(long_item, (s.chunk + splits - 1) / splits + cost);

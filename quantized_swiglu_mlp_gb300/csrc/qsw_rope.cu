@@ -57,6 +57,7 @@ struct RopeParams {
   const int *slots;
   const int64_t *table;
   int T, D, half;                // half: pairs
+  int groups, turns;             // of 8 pairs, and 8 for each: of a token in shared memory
   int tokens;                    // per CTA
   int interleaved;
   int skip_negative;             // tokens at negative positions are left out
@@ -68,12 +69,21 @@ struct RopeParams {
 constexpr int kThreads = 256;
 constexpr int kAhead = 4;          // units of a thread in flight
 
+// Where the cos and sin of a token's pair lie: one after the other; with runs of 8 elements,
+// pairs 2 j and 2 j + 1 of all groups of 8 side by side, so that neighbouring threads, each with a
+// group, read neighbouring words (in order, four of them shared a bank: an append of 7363 tokens, 181
+// MB, took 42 us, so 36).
+template <int VEC>
+__device__ __forceinline__ int turn_at(const RopeParams &p, int pair) {
+  return VEC == 1 ? pair : (((pair & 7) >> 1) * p.groups + (pair >> 3)) * 2 + (pair & 1);
+}
+
 // Two runs of VEC elements.
 template <int VEC>
 struct Unit {
   uint32_t w[2][VEC == 8 ? 4 : 1];   // as they are stored
   uint16_t *dst;                     // the head's first element; null: nothing to do
-  int turn;                          // of the first run's first pair in shared memory; -1: both copied
+  int turn;                          // where its token's and first pair's turns lie in shared memory
   int e0, e1;                        // elements of the runs; e1 < 0: one run
   int kind;                          // 0: copied; 1: pairs across the runs; 2, 3: adjacent pairs in the first, in both
 };
@@ -92,21 +102,21 @@ __device__ __forceinline__ void fetch_unit(const RopeParams &p, int t0, uint32_t
   const uint32_t h = div_by(static_cast<uint32_t>(r), s.per_head);
   const int c = r - static_cast<int>(h * s.per_head.d);
   x.kind = 0;
-  x.turn = static_cast<int>(tl) * p.half;
+  x.turn = static_cast<int>(tl) * p.turns;
   // across: pairs half a rotation apart, and element by element any pairs
   const bool across = s.rotate && (VEC == 1 || !p.interleaved);
   if (across && c * VEC < p.half) {
     const int pair = c * VEC;
     x.e0 = p.interleaved ? 2 * pair : pair;
     x.e1 = p.interleaved ? 2 * pair + 1 : pair + p.half;
-    x.turn += pair;
+    x.turn += turn_at<VEC>(p, pair);
     x.kind = 1;
   } else {
     // (behind the rotation, if there are units across)
     x.e0 = across ? 2 * p.half + (c * VEC - p.half) * 2 : c * VEC * 2;
     x.e1 = x.e0 + VEC < p.D ? x.e0 + VEC : -1;
     if (s.rotate && !across && x.e0 < 2 * p.half) {
-      x.turn += x.e0 / 2;
+      x.turn += turn_at<VEC>(p, x.e0 / 2);
       x.kind = x.e0 + VEC < 2 * p.half ? 3 : 2;
     }
   }
@@ -139,10 +149,10 @@ __device__ __forceinline__ void fetch_unit(const RopeParams &p, int t0, uint32_t
 
 // Adjacent pairs of a run of 8.
 template <class A>
-__device__ __forceinline__ void turn_run(uint32_t (&w)[4], const float2 *cs) {
+__device__ __forceinline__ void turn_run(uint32_t (&w)[4], const float2 *cs, int groups) {
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
-    const float4 f = reinterpret_cast<const float4 *>(cs)[j];      // cos, sin, cos, sin
+    const float4 f = reinterpret_cast<const float4 *>(cs)[j * groups];      // cos, sin, cos, sin
     const float a0 = A::lo(w[2 * j]), a1 = A::hi(w[2 * j]), b0 = A::lo(w[2 * j + 1]), b1 = A::hi(w[2 * j + 1]);
     w[2 * j] = A::pack2(a0 * f.x - a1 * f.y, a1 * f.x + a0 * f.y);
     w[2 * j + 1] = A::pack2(b0 * f.z - b1 * f.w, b1 * f.z + b0 * f.w);
@@ -151,22 +161,22 @@ __device__ __forceinline__ void turn_run(uint32_t (&w)[4], const float2 *cs) {
 
 // Turns and stores a unit.
 template <class A, int VEC>
-__device__ __forceinline__ void store_unit(const float2 *turn, Unit<VEC> &x) {
+__device__ __forceinline__ void store_unit(const float2 *turn, int groups, Unit<VEC> &x) {
   if (!x.dst) return;
   const float2 *cs = turn + x.turn;
   if constexpr (VEC == 8) {
     if (x.kind == 1) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float4 f = reinterpret_cast<const float4 *>(cs)[j];
+        const float4 f = reinterpret_cast<const float4 *>(cs)[j * groups];
         const float a0 = A::lo(x.w[0][j]), a1 = A::hi(x.w[0][j]);
         const float b0 = A::lo(x.w[1][j]), b1 = A::hi(x.w[1][j]);
         x.w[0][j] = A::pack2(a0 * f.x - b0 * f.y, a1 * f.z - b1 * f.w);
         x.w[1][j] = A::pack2(b0 * f.x + a0 * f.y, b1 * f.z + a1 * f.w);
       }
     } else {
-      if (x.kind >= 2) turn_run<A>(x.w[0], cs);
-      if (x.kind == 3) turn_run<A>(x.w[1], cs + 4);
+      if (x.kind >= 2) turn_run<A>(x.w[0], cs, groups);
+      if (x.kind == 3) turn_run<A>(x.w[1], cs + 4 * groups, groups);
     }
     *reinterpret_cast<uint4 *>(x.dst + x.e0) = make_uint4(x.w[0][0], x.w[0][1], x.w[0][2], x.w[0][3]);
     if (x.e1 >= 0) *reinterpret_cast<uint4 *>(x.dst + x.e1) = make_uint4(x.w[1][0], x.w[1][1], x.w[1][2], x.w[1][3]);
@@ -183,7 +193,7 @@ __device__ __forceinline__ void store_unit(const float2 *turn, Unit<VEC> &x) {
 
 template <class A, int VEC>
 __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const __grid_constant__ RopeParams p) {
-  extern __shared__ float2 turn[];       // [tokens][half]: cos, sin
+  extern __shared__ __align__(16) float2 turn[];       // [tokens][turns]: cos, sin
   griddep_wait();
   griddep_launch_dependents();
   const int t0 = static_cast<int>(blockIdx.x) * p.tokens;
@@ -199,13 +209,13 @@ __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const __grid_constant
                           static_cast<uint64_t>(__ldg(p.table + pair));
       float s, c;
       sincospif(static_cast<float>(static_cast<int32_t>(at >> 32)) * 0x1p-31f, &s, &c);
-      turn[i] = make_float2(c * p.scale, s * p.scale);
+      turn[t * p.turns + turn_at<VEC>(p, static_cast<int>(pair))] = make_float2(c * p.scale, s * p.scale);
     }
     __syncthreads();
   }
   for (uint32_t u0 = threadIdx.x;;) {
 #pragma unroll
-    for (int a = 0; a < kAhead; ++a) store_unit<A>(turn, x[a]);
+    for (int a = 0; a < kAhead; ++a) store_unit<A>(turn, p.groups, x[a]);
     u0 += kThreads * kAhead;
     if (u0 >= units) break;
 #pragma unroll
@@ -273,7 +283,9 @@ cudaError_t launch_rope(const RopeArgs &a, int num_sms, cudaStream_t stream) {
   tokens = tokens < 1 ? 1 : tokens > 16 ? 16 : tokens;
   p.tokens = static_cast<int>(tokens);
   const dim3 grid(static_cast<unsigned>((a.T + tokens - 1) / tokens));
-  const size_t smem = static_cast<size_t>(tokens) * p.half * sizeof(float2);
+  p.groups = (p.half + 7) / 8;
+  p.turns = p.groups * 8;
+  const size_t smem = static_cast<size_t>(tokens) * p.turns * sizeof(float2);
   const bool f16 = a.act == ActF16::kId;
   if (wide)
     return f16 ? launch_on(rope_kernel<ActF16, 8>, grid, kThreads, smem, stream, false, p)
