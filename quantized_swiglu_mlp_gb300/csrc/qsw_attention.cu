@@ -259,6 +259,13 @@ __global__ void __launch_bounds__(32 * kKeyGroups * RG, 3 - RG)
   unsigned int *err = &g_rows_error;
   const int tid = static_cast<int>(threadIdx.x), warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int kg = warp / RG, rg = warp % RG;
+  if (!p.after_tiles) griddep_wait();      // (then all before the tiles' kernel is complete)
+  griddep_launch_dependents();
+  const int total = __ldg(p.plan.head + LIST_ROWS);
+  if (static_cast<int>(blockIdx.x) >= total) {
+    if (p.after_tiles) griddep_wait();
+    return;
+  }
   if constexpr (kDebugBounds) {
     debug_poison_smem(ring, kKeyGroups * kRowStages * STAGE);
     fence_proxy_async_smem();
@@ -272,9 +279,6 @@ __global__ void __launch_bounds__(32 * kKeyGroups * RG, 3 - RG)
     prefetch_tensormap(&maps.k);
     prefetch_tensormap(&maps.v);
   }
-  if (!p.after_tiles) griddep_wait();      // (then all before the tiles' kernel is complete)
-  griddep_launch_dependents();
-  const int total = __ldg(p.plan.head + LIST_ROWS);
   uint8_t *mine = ring + kg * kRowStages * STAGE;
 
   // Copies: boxes of rows, of all halves or of one; a lane per box of rows looks its page
@@ -687,7 +691,9 @@ AttnForm attention_form(int64_t T, int64_t B, int64_t heads, int64_t kv_heads, i
   // Which lists there are: one token a sequence, as far as the sizes say, or the rows of a
   // single one, need one; else sequences with up to 32 rows go with the few.
   f.most_rows = B == 1 || T <= B ? (T <= B || T * group <= 32 ? INT32_MAX : 0) : 32;
-  const int64_t few = T <= B ? group : B == 1 ? T * group : 32;
+  // (8 rows a sequence on average: most have up to 16, and two CTAs of 16 rows on an SM hide more
+  // latency than one of 32)
+  const int64_t few = T <= B ? group : B == 1 || T * group <= 8 * B ? T * group / seqs : 32;
   ListForm &r = f.list[LIST_ROWS], &t = f.list[LIST_TILES];
   r.tile_rows = few <= 16 ? 16 : 32;
   r.tile_keys = kKeyGroups * step_keys(D <= 64 ? 64 : 128, r.tile_rows / 16);

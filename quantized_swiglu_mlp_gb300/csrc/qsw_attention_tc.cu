@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             base = now;
             sum *= shrink;
             if (i > 0) {
-#pragma unroll
+#pragma unroll 1
               for (int c = 0; c < DP; c += 16) {
                 uint32_t o[16];
                 tmem_ld16(o_addr + c, o);
@@ -413,7 +413,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int size = split ? 4 : 2;
         const int64_t mine_at = live ? (split ? part_at : at) * p.D * size : -1;
         float odd = 0.0f;             // 0 times every value: NaN if one is not finite
-#pragma unroll
+        // (loops that run once a tile or less are not unrolled: a call of few items spends much of its
+        // time on fetching code)
+#pragma unroll 1
         for (int c = 0; c < DP; c += 32) {
           uint32_t o[32];
           if (n > 0) {
