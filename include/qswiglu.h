@@ -417,7 +417,8 @@ typedef struct {
  * elements of a row contiguous, strides (page, head, row) in elements.  Token p of a
  * sequence is row p % page_size of page page_table[sequence][p / page_size].
  * page_size a multiple of 8, D a multiple of 8 from 8 to 128; pages * page_size
- * below 2^31.  k, v and all strides are multiples of 16 bytes. */
+ * below 2^31.  k, v and all strides are multiples of 16 bytes, the strides positive and below
+ * 2^40 bytes. */
 typedef struct {
     void *k, *v;
     int64_t pages, kv_heads, page_size;
@@ -480,7 +481,8 @@ QSW_API qsw_status qsw_paged_plan(const int *offsets, const int *lengths, int64_
  * head h / (heads / kv_heads).  out is [T, heads, D], contiguous.  A token that sees no key gets 0; rows
  * of no sequence are left as they were.  A page that is not in the cache counts as
  * zeros; what a row does not see has no effect on it, infinities and NaN among them (a row
- * that comes out infinite or NaN is computed again key by key, with f32 weights).
+ * that comes out infinite or NaN for that reason is computed again key by key, with f32
+ * weights).
  * Statistics and sums in f32, the weights rounded to the activation dtype before they
  * meet v; long histories are split over CTAs and joined in f32 in a fixed order: the same bits
  * every time.  scale > 0.  workspace: qsw_paged_attention_workspace_bytes(...) bytes
@@ -560,6 +562,9 @@ QSW_API void qsw_debug_withhold_next_fill(void);
 /* The same for the next 4-bit product (qsw_fp4_linear, qsw_fp4_grouped_linear or the
  * first of qsw_fp4_moe_mlp): it never requests its weights, so its waits run out. */
 QSW_API void qsw_debug_withhold_next_product(void);
+
+/* The same for the next qsw_paged_attention: it never requests its first keys. */
+QSW_API void qsw_debug_withhold_next_attention(void);
 
 /* Dispatch counters (process-wide, monotonically increasing). `out` receives
  * min(n, QSW_NUM_COUNTERS) values. */

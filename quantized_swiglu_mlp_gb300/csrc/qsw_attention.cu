@@ -1,11 +1,14 @@
 // Attention over a paged cache (qsw_attention.cuh): the plan of a step, the kernel for
 // few rows, the join of split histories.
+#include <atomic>
+
 #include "qsw_attention.cuh"
 
 namespace qsw {
 namespace {
 
 __device__ unsigned int g_rows_error;
+std::atomic<int> g_withhold{0};
 
 // -------------------------------------------------------------------- plan --
 
@@ -325,6 +328,10 @@ __global__ void __launch_bounds__(32 * kKeyGroups * RG, 3 - RG)
         ok = ok && wait_all(&empty[kg][slot], ((issued / kRowStages) & 1) ^ 1, abort_flag, p.timeout_ns, err);
         if (!ok) return;
       }
+      if (p.withhold && issued == 0) {
+        ++issued;
+        return;
+      }
       const int checked = checked_page(p, page);
       uint8_t *dst = mine + slot * STAGE;
       if (elect_one()) mbar_arrive_expect_tx(&full[kg][slot], STAGE);
@@ -332,6 +339,7 @@ __global__ void __launch_bounds__(32 * kKeyGroups * RG, 3 - RG)
       for (int j = 0; j < subs; ++j) {
         const int pg = __shfl_sync(0xffffffffu, checked, j), rw = __shfl_sync(0xffffffffu, row, j);
         if (elect_one()) {
+          debug_check(rw >= 0 && rw + maps.box <= p.page_size && pg < p.pages, err);
           tma_load_5d(dst, &maps.k, &full[kg][slot], 0, rw, 0, kv_head, pg);
           tma_load_5d(dst + STAGE / 2, &maps.v, &full[kg][slot], 0, rw, 0, kv_head, pg);
           if (H > 1 && parts > 1) {
@@ -502,7 +510,7 @@ __global__ void __launch_bounds__(32 * kKeyGroups * RG, 3 - RG)
     // a row to 8 threads, 8 columns at a time
     const int r = tid / 8;
     fence_proxy_async_smem();      // (the next copies overwrite the sums)
-    bool finite = true;
+    bool finite = true;        // or rightly not
     if (r < t.rows) {
       float top = warp_m[0][r];
 #pragma unroll
@@ -517,6 +525,7 @@ __global__ void __launch_bounds__(32 * kKeyGroups * RG, 3 - RG)
       const float inv = all == 0.0f ? 0.0f : 1.0f / all;
       int at_pos;
       row_of(p, t, r, token, head, at_pos);
+      debug_check(token >= 0 && token < p.T && head >= 0 && head < p.heads, err);
       const int64_t at = token * p.heads + head, part = t.split * static_cast<int64_t>(p.T) * p.heads + at;
       for (int c = (tid & 7) * 8; c < p.D; c += 64) {
         float y[8];
@@ -537,6 +546,7 @@ __global__ void __launch_bounds__(32 * kKeyGroups * RG, 3 - RG)
               make_uint4(A::pack2(y[0], y[1]), A::pack2(y[2], y[3]), A::pack2(y[4], y[5]), A::pack2(y[6], y[7]));
         }
       }
+      finite |= all != all;
       if (t.s.splits > 1 && (tid & 7) == 0) p.part_lse[part] = all == 0.0f ? -INFINITY : base + __log2f(all);
     }
     if (!finite) atomicOr(&redo, 1u << r);
@@ -650,8 +660,9 @@ cudaError_t launch_join(const AttnParams &p, int num_sms, cudaStream_t stream) {
 template <class A, int DP, int RG>
 cudaError_t launch_rows_form(const AttnParams &p, const CacheMaps &maps, dim3 grid, cudaStream_t stream) {
   const int bytes = kKeyGroups * row_stages(DP, RG) * row_stage_bytes(DP, RG) + 1024;
+  static SmemOnce once;
   auto kernel = attn_rows_kernel<A, DP, RG>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  const cudaError_t e = allow_smem(once, kernel, bytes);
   return e != cudaSuccess ? e
                           : launch_on(kernel, grid, 32 * kKeyGroups * RG, bytes, stream, p.after_tiles != 0, p, maps);
 }
@@ -670,6 +681,8 @@ cudaError_t launch_rows(const AttnParams &p, const ListForm &f, const qsw_kv_cac
 }
 
 }  // namespace
+
+void attention_withhold_next() { g_withhold.store(1); }
 
 cudaError_t attention_take_errors(unsigned int *out) {
   unsigned int tiles = 0, rows = 0, zero = 0;
@@ -786,6 +799,7 @@ cudaError_t launch_paged_attention(const AttentionArgs &a, int num_sms, uint64_t
   p.window = static_cast<int>(a.window);
   p.scale_log2 = a.scale * kLog2e;
   p.timeout_ns = timeout_ns;
+  p.withhold = g_withhold.exchange(0, std::memory_order_relaxed);
   p.part = static_cast<float *>(a.workspace);
   p.part_lse = p.part + static_cast<int64_t>(f.max_splits) * a.T * a.heads * a.D;
   const bool f16 = a.act == ActF16::kId;

@@ -11,6 +11,7 @@
 #pragma once
 
 #include <climits>
+#include <mutex>
 
 #include "qsw_fp4.cuh"
 #include "qsw_internal.h"
@@ -62,6 +63,7 @@ struct AttnParams {
   int pages, page_size, max_pages;
   int window;                      // 0: none
   int list, tile_rows, tile_keys;
+  int withhold;                    // test hook: the first keys are never requested
   int after_tiles;                 // few rows: launched as a dependent of the tiles' kernel
   float scale_log2;                // scale log2(e)
   float *part;                     // [splits][T][heads][D], normalised
@@ -159,8 +161,10 @@ __device__ __forceinline__ int page_of(const AttnParams &p, int b, int page) {
 }
 
 // Row r of an item by one warp, key by key with what the row does not see left out, for
-// rows that came out infinite or NaN: in the tiles a masked key has the weight 0, and
-// 0 * inf is NaN.  Slow (a key at a time), and only ever run for such rows.
+// rows that came out infinite or NaN although the sum of their weights is a number: in the
+// tiles a masked key has the weight 0, and 0 * inf is NaN.  Slow (a key at a time), and only
+// ever run for such rows; a NaN among the scores makes the sum of weights NaN, and the row
+// rightly so.
 template <class A>
 __device__ __noinline__ void exact_row(const AttnParams &p, const Item &t, int r) {
   const int lane = static_cast<int>(lane_id());
@@ -174,10 +178,14 @@ __device__ __noinline__ void exact_row(const AttnParams &p, const Item &t, int r
     if (page < 0) return 0.0f;
     const uint16_t *k = p.k + page * p.k_page + t.head * p.k_head + (j % p.page_size) * p.k_row;
     float s = 0.0f;
-    for (int d = 0; d < p.D; d += 2) {
-      const uint32_t a = *reinterpret_cast<const uint32_t *>(q + d), b = *reinterpret_cast<const uint32_t *>(k + d);
-      s = fmaf(A::lo(a), A::lo(b), s);
-      s = fmaf(A::hi(a), A::hi(b), s);
+    for (int d = 0; d < p.D; d += 8) {
+      const uint4 a = *reinterpret_cast<const uint4 *>(q + d), b = *reinterpret_cast<const uint4 *>(k + d);
+      const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s = fmaf(A::lo(x[i]), A::lo(y[i]), s);
+        s = fmaf(A::hi(x[i]), A::hi(y[i]), s);
+      }
     }
     return s * p.scale_log2;
   };
@@ -260,6 +268,23 @@ __device__ __forceinline__ void tma_load_5d(void *dst, const CUtensorMap *map, u
       "[%2];" ::"r"(smem_u32(dst)),
       "l"(map), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
       : "memory");
+}
+
+// A kernel's shared memory, allowed once per device: `once` belongs to the kernel.
+struct SmemOnce {
+  std::once_flag flag[64];
+  cudaError_t error[64];
+};
+template <class K>
+cudaError_t allow_smem(SmemOnce &once, K kernel, int bytes) {
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  std::call_once(once.flag[dev], [&] {
+    once.error[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  });
+  return once.error[dev];
 }
 
 // One thread of a converged warp.  Copies are issued by a thread chosen this way, with

@@ -20,14 +20,16 @@ qsw_status from_cuda(cudaError_t e) { return e == cudaSuccess ? QSW_OK : QSW_ERR
 bool act_ok(int act) { return act == QSW_ACT_BF16 || act == QSW_ACT_F16; }
 
 qsw_status check_cache(const qsw_kv_cache *c, int64_t D) {
-  if (!c || c->pages < 0 || c->kv_heads <= 0 || c->page_size <= 0 || D <= 0) return QSW_ERR_INVALID_ARG;
-  if (c->pages > 0 && (!c->k || !c->v)) return QSW_ERR_INVALID_ARG;
+  if (!c || c->pages <= 0 || c->kv_heads <= 0 || c->page_size <= 0 || D <= 0) return QSW_ERR_INVALID_ARG;
+  if (!c->k || !c->v) return QSW_ERR_INVALID_ARG;
   if (c->page_size % 8 || D % 8 || D > kMaxHeadDim || c->kv_heads > kMaxHeads) return QSW_ERR_UNSUPPORTED;
   if (c->page_size > INT32_MAX || c->pages > INT32_MAX / c->page_size) return QSW_ERR_UNSUPPORTED;
   if (!aligned(c->k, 16) || !aligned(c->v, 16)) return QSW_ERR_UNSUPPORTED;
+  // (strides as a copy takes them: below 2^40 bytes)
   for (int i = 0; i < 3; ++i) {
-    if (c->k_strides[i] < 0 || c->v_strides[i] < 0) return QSW_ERR_INVALID_ARG;
+    if (c->k_strides[i] <= 0 || c->v_strides[i] <= 0) return QSW_ERR_INVALID_ARG;
     if (c->k_strides[i] % 8 || c->v_strides[i] % 8) return QSW_ERR_UNSUPPORTED;
+    if (c->k_strides[i] >= (int64_t(1) << 39) || c->v_strides[i] >= (int64_t(1) << 39)) return QSW_ERR_UNSUPPORTED;
   }
   return QSW_OK;
 }
@@ -176,5 +178,7 @@ qsw_status qsw_paged_attention(const qsw_heads *q, const qsw_kv_cache *cache, co
   if (r == QSW_OK) qsw::count_call(QSW_CNT_PAGED_ATTENTION);
   return r;
 }
+
+void qsw_debug_withhold_next_attention(void) { qsw::attention_withhold_next(); }
 
 }  // extern "C"

@@ -16,7 +16,6 @@
 //
 // The base of a row is raised (and O rescaled in tensor memory) only when a score passes
 // it by 8, so that weights reach 256 at most and most tiles leave O alone.
-#include <mutex>
 #include <type_traits>
 
 #include "qsw_attention.cuh"
@@ -221,12 +220,26 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
+  if constexpr (kDebugBounds) {
+    // every column := NaN before the first product (a warp per lane quarter)
+    if (warp < 4) {
+      uint32_t nan16[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) nan16[i] = ~0u;
+      for (uint32_t col = 0; col < 512; col += 16) tmem_st16(tmem + (static_cast<uint32_t>(warp) << 21) + col, nan16);
+      tmem_st_wait();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+  }
   // Tensor memory: S (and P) of the two row tiles, then O of both.
   const uint32_t o_col = 256;
 
   if (warp < 8) {
     // ------------------------------------------------------------- softmax --
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    // (2 x 224 + 56 = 3 x 168, the registers of the launch; with 208 some of a row's values spilled)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
     const int tile = warp >> 2;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;      // this warp's 32 lanes
     const uint32_t s_addr = tmem + lanes + tile * 128, o_addr = tmem + lanes + o_col + tile * DP;
@@ -458,9 +471,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
+        debug_check(!live || (token >= 0 && token < p.T && head >= 0 && head < p.heads), err);
         if (split && live) p.part_lse[part_at] = sum == 0.0f ? -INFINITY : base + __log2f(sum);
         tc_fence_before();
-        for (unsigned x = __ballot_sync(0xffffffffu, live && odd != 0.0f); x; x &= x - 1)
+        for (unsigned x = __ballot_sync(0xffffffffu, live && odd != 0.0f && sum == sum); x; x &= x - 1)
           exact_row<A>(p, *t, tile * kRows + (warp & 3) * 32 + __ffs(x) - 1);
       }
       cursor.done(bar, 1);
@@ -468,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == kWarpMma) {
       // ---------------------------------------------------------- products --
       const uint32_t idesc_s = umma_idesc_f16kind(kRows, kKeys, A::kUmmaFormat);
@@ -603,12 +617,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t slot = count % stages;
           if (!(ok = wait_all(&empty[slot], ((count / stages) & 1) ^ 1, abort_flag, p.timeout_ns, err))) break;
           const int checked = checked_page(p, page);
-          if (elect_one()) mbar_arrive_expect_tx(&full[slot], S::kTileBytes);
+          const bool withheld = p.withhold && is_k && count == 0;
+          if (!withheld && elect_one()) mbar_arrive_expect_tx(&full[slot], S::kTileBytes);
           __syncwarp();
-          for (int j = 0; j < boxes; ++j) {
+          for (int j = 0; j < boxes && !withheld; ++j) {
             const int pg = __shfl_sync(0xffffffffu, checked, j), rw = __shfl_sync(0xffffffffu, row, j);
             if (elect_one()) {
               uint8_t *dst = ring + slot * S::kTileBytes + j * maps.box * 128;
+              debug_check(rw >= 0 && rw + maps.box <= p.page_size && pg < p.pages, err);
               tma_load_5d(dst, map, &full[slot], 0, rw, 0, head, pg);
               if (S::kHalves > 1 && parts > 1) tma_load_5d(dst + S::kHalfBytes, map, &full[slot], 64, rw, 0, head, pg);
             }
@@ -682,8 +698,9 @@ bool encode_cache(CUtensorMap *map, const void *base, const int64_t (&strides)[3
 
 template <class A, int DP>
 cudaError_t launch_shape(const AttnParams &p, const CacheMaps &maps, int grid, cudaStream_t stream) {
+  static SmemOnce once;
   auto kernel = attn_tiles_kernel<A, DP>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<DP>::kSmem);
+  const cudaError_t e = allow_smem(once, kernel, Shape<DP>::kSmem);
   return e != cudaSuccess ? e : launch_on(kernel, dim3(static_cast<unsigned>(grid)), kThreads, Shape<DP>::kSmem, stream,
                                           false, p, maps);
 }

@@ -187,6 +187,7 @@ struct AttentionArgs {
 size_t attention_workspace_bytes(int64_t T, int64_t B, int64_t heads, int64_t kv_heads, int64_t D, int64_t max_len,
                                  int num_sms);
 cudaError_t attention_take_errors(unsigned int *out);
+void attention_withhold_next();   // test hook: the next attention's waits run out
 cudaError_t launch_paged_attention(const AttentionArgs &a, int num_sms, uint64_t timeout_ns, cudaStream_t stream);
 
 // Shared state of the C entry points (qsw_api.cu).

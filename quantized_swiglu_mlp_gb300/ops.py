@@ -55,7 +55,7 @@ EXPORTED = ("qswiglu_forward", "affine_qmm", "qswiglu_forward_ws", "affine_qmm_w
             "qsw_fp4_linear", "qsw_fp4_grouped_linear", "qsw_moe_route", "qsw_fp4_moe_workspace_bytes",
             "qsw_fp4_moe_mlp", "qsw_rms_norm", "qsw_post_norm", "qsw_debug_withhold_next_product",
             "qsw_rope", "qsw_kv_append", "qsw_paged_plan_bytes", "qsw_paged_plan",
-            "qsw_paged_attention_workspace_bytes", "qsw_paged_attention")
+            "qsw_paged_attention_workspace_bytes", "qsw_paged_attention", "qsw_debug_withhold_next_attention")
 
 _lock = threading.Lock()
 _lib = None
@@ -747,6 +747,11 @@ def qsw_debug_withhold_next_fill() -> None:
 def qsw_debug_withhold_next_product() -> None:
     """Test hook: the next 4-bit product never requests its weights, so its waits run out."""
     load_library().qsw_debug_withhold_next_product()
+
+
+def qsw_debug_withhold_next_attention() -> None:
+    """Test hook: the next paged_attention never requests its first keys, so its waits run out."""
+    load_library().qsw_debug_withhold_next_attention()
 
 
 def qsw_debug_build() -> bool:

@@ -64,11 +64,12 @@ def test_rope_rejects(lib, kw, code):  # noqa: F811
 
 
 BAD_CACHES = [
-    (dict(pages=-1), INVALID), (dict(kv_heads=0), INVALID), (dict(page_size=0), INVALID), (dict(k=0), INVALID),
+    (dict(pages=-1), INVALID), (dict(pages=0), INVALID), (dict(kv_heads=0), INVALID), (dict(page_size=0), INVALID), (dict(k=0), INVALID),
     (dict(v=0), INVALID), (dict(page_size=12), UNSUPPORTED), (dict(kv_heads=1025), UNSUPPORTED),
     (dict(pages=1 << 27), UNSUPPORTED), (dict(pages=1 << 62), UNSUPPORTED), (dict(k=FAKE + 8), UNSUPPORTED),
     (dict(v=FAKE + 2), UNSUPPORTED), (dict(k_strides=(2048, 1024, 68)), UNSUPPORTED),
-    (dict(v_strides=(2044, 1024, 64)), UNSUPPORTED), (dict(v_strides=(2048, -1024, 64)), INVALID)]
+    (dict(v_strides=(2044, 1024, 64)), UNSUPPORTED), (dict(v_strides=(2048, -1024, 64)), INVALID),
+    (dict(k_strides=(2048, 0, 64)), INVALID), (dict(k_strides=(1 << 39, 1024, 64)), UNSUPPORTED)]
 
 
 @pytest.mark.parametrize("kw,code", BAD_CACHES)
