@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
   __shared__ unsigned long long best[2];
   const int warp = tid >> 5, lane = tid & 31;
   if (tid < 2) best[tid] = ~0ull;
-  int longest[2] = {0, 0}, top = 0;
+  int longest[2] = {0, 0}, top = 0, tile_blocks = 0;
   for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
     // offsets as an ascending table: an entry counts as no less than any before it (no row
     // then belongs to two sequences, and there are no more items than rows allow)
@@ -119,8 +119,22 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     s.splits = (mean + tile_keys - 1) / tile_keys;
     s.first[0] = list;
     if (s.blocks) longest[list] = max(longest[list], s.chunk);
+    if (list == LIST_TILES) tile_blocks += s.blocks;
     p.out.rec[b] = s;
   }
+  // Two kv heads an item, for sequences of the list of many rows whose rows fill half a tile at
+  // most: where the items without that are more than run at once.  (An item of one head's 128
+  // rows takes as long as one of two.)
+  tile_blocks = __reduce_add_sync(0xffffffffu, tile_blocks);
+  if (lane == 0) sums[warp] = tile_blocks;
+  __syncthreads();
+  tile_blocks = __reduce_add_sync(0xffffffffu, sums[lane]);
+  __syncthreads();
+  const bool pairing =
+      p.kv_heads % 2 == 0 && static_cast<int64_t>(tile_blocks) * p.kv_heads > p.cta_slots[LIST_TILES];
+  auto pair_of = [&](const SeqRec &s, int list) {
+    return pairing && list == LIST_TILES && s.n * p.group <= p.tile_rows[LIST_TILES] / 2;
+  };
   int chunk[2];
 #pragma unroll
   for (int list = 0; list < 2; ++list) {
@@ -138,7 +152,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
       const SeqRec s = p.out.rec[b];
       if (!s.blocks || s.first[0] != list) continue;
       const int splits = max(1, min(p.max_splits, (s.chunk + c - 1) / c));
-      const float n = static_cast<float>(s.blocks) * p.kv_heads, cost = splits > 1 ? kItemCost + kSplitCost[list] : kItemCost;
+      const float n = static_cast<float>(s.blocks) * (p.kv_heads >> pair_of(s, list)), cost = splits > 1 ? kItemCost + kSplitCost[list] : kItemCost;
       items += n * splits;
       work += n * (s.splits + cost * splits);
       long_item = fmaxf(long_item, (s.chunk + splits - 1) / splits + cost);
@@ -172,7 +186,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
       s.splits = s.blocks && p.max_splits > 1 ? max(1, min(p.max_splits, (s.chunk + c - 1) / c)) : 1;
       any |= s.splits > 1;
       s.chunk = max(1, (s.chunk + s.splits - 1) / s.splits) * p.tile_keys[list];
-      items = s.blocks * s.splits * p.kv_heads;
+      const bool pair = pair_of(s, list);
+      items = s.blocks * s.splits * (p.kv_heads >> pair);
     }
 #pragma unroll
     for (int l = 0; l < 2; ++l) {
@@ -191,7 +206,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
       total[l] += all;
       __syncthreads();
     }
-    if (b < p.B) p.out.rec[b] = s;
+    if (b < p.B) {
+      if (pair_of(s, list)) s.splits |= kPairBit;
+      p.out.rec[b] = s;
+    }
   }
   any = __syncthreads_or(any);
   if (tid == 0) {
@@ -262,7 +280,7 @@ __global__ void __launch_bounds__(32 * kKeyGroups * RG, 3 - RG)
   unsigned int *err = &g_rows_error;
   const int tid = static_cast<int>(threadIdx.x), warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int kg = warp / RG, rg = warp % RG;
-  if (!p.after_tiles) griddep_wait();      // (then all before the tiles' kernel is complete)
+  if (!p.after_tiles) griddep_wait();      // (else all before the tiles' kernel is complete)
   griddep_launch_dependents();
   const int total = __ldg(p.plan.head + LIST_ROWS);
   if (static_cast<int>(blockIdx.x) >= total) {
@@ -371,7 +389,7 @@ __global__ void __launch_bounds__(32 * kKeyGroups * RG, 3 - RG)
       const int r = rg * 16 + lane / 4 + 8 * h;
       const bool live = r < t.rows;
       int pos;
-      row_of(p, t, live ? r : 0, token, head, pos);
+      row_of(p, t, t.head, live ? r : 0, token, head, pos);
       begin[h] = p.window ? pos - p.window + 1 : 0;
       end[h] = min(pos + 1, t.k1);
       const uint16_t *src = p.q + token * p.q_t + head * p.q_h;
@@ -524,7 +542,7 @@ __global__ void __launch_bounds__(32 * kKeyGroups * RG, 3 - RG)
       }
       const float inv = all == 0.0f ? 0.0f : 1.0f / all;
       int at_pos;
-      row_of(p, t, r, token, head, at_pos);
+      row_of(p, t, t.head, r, token, head, at_pos);
       debug_check(token >= 0 && token < p.T && head >= 0 && head < p.heads, err);
       const int64_t at = token * p.heads + head, part = t.split * static_cast<int64_t>(p.T) * p.heads + at;
       for (int c = (tid & 7) * 8; c < p.D; c += 64) {
@@ -553,7 +571,7 @@ __global__ void __launch_bounds__(32 * kKeyGroups * RG, 3 - RG)
     __syncthreads();
     for (unsigned again = redo; again; again &= again - 1) {
       const int x = __ffs(again) - 1;
-      if (x % kRowWarps == warp) exact_row<A>(p, t, x);
+      if (x % kRowWarps == warp) exact_row<A>(p, t, t.head, x);
     }
   }
   // given up: the copies in flight
@@ -582,7 +600,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ AttnP
   bool waited = false;
   for (; any && row < rows; row += static_cast<int64_t>(gridDim.x) * kRowsOfCta) {
     const int b = __ldg(p.plan.seq_of + row / p.heads);
-    const int splits = b < 0 ? 1 : __ldg(&p.plan.rec[b].splits);
+    const int splits = b < 0 ? 1 : __ldg(&p.plan.rec[b].splits) & (kPairBit - 1);
     if (!waited) griddep_wait();
     waited = true;
     if (splits <= 1) continue;

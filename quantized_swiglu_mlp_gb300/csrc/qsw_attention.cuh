@@ -26,10 +26,12 @@ struct alignas(16) SeqRec {
   int n;         // new tokens
   int len;       // tokens in the cache, the new ones among them
   int blocks;    // row tiles per kv head
-  int splits;
+  int splits;    // and kPairBit: two kv heads an item
   int chunk;     // keys per split
   int first[2];  // its first item in each list (it has items in one of them)
 };
+
+constexpr int kPairBit = 1 << 16;
 
 // Lists of items: sequences with few rows, and with many.
 enum : int { LIST_ROWS = 0, LIST_TILES = 1 };
@@ -72,10 +74,11 @@ struct AttnParams {
 };
 
 // One item: rows [row0, row0 + rows) (token * group + head in the group) of a sequence's
-// kv head, keys [k0, k1), of which no row sees those before `first`.
+// kv head, keys [k0, k1), of which no row sees those before `first`.  A pair: the same rows
+// of two kv heads, head and head + 1.
 struct Item {
   SeqRec s;
-  int b, head, row0, rows, k0, k1, first, split;
+  int b, head, row0, rows, k0, k1, first, split, pair;
 };
 
 // First and last + 1 key that the tokens [a, b) of a sequence see.
@@ -112,16 +115,18 @@ __device__ __forceinline__ Item find_item(const AttnParams &p, int id) {
   t.s.n = __shfl_sync(0xffffffffu, a.y, last);
   t.s.len = __shfl_sync(0xffffffffu, a.z, last);
   t.s.blocks = __shfl_sync(0xffffffffu, a.w, last);
-  t.s.splits = __shfl_sync(0xffffffffu, c.x, last);
+  const int splits = __shfl_sync(0xffffffffu, c.x, last);
+  t.s.splits = splits & (kPairBit - 1);
+  t.pair = splits >= kPairBit;
   t.s.chunk = __shfl_sync(0xffffffffu, c.y, last);
   const int local = id - __shfl_sync(0xffffffffu, first, last);
   // the last rows first (they see the most keys), then splits, kv heads innermost: CTAs
   // that run together read the same keys of a head
-  const int per = p.kv_heads * t.s.splits;
+  const int heads = p.kv_heads >> t.pair, per = heads * t.s.splits;
   const int up = local / per, r2 = local - up * per;
   const int block = t.s.blocks - 1 - up;
-  t.split = r2 / p.kv_heads;
-  t.head = r2 - t.split * p.kv_heads;
+  t.split = r2 / heads;
+  t.head = (r2 - t.split * heads) << t.pair;
   t.row0 = block * p.tile_rows;
   t.rows = min(p.tile_rows, t.s.n * p.group - t.row0);
   int end;
@@ -136,11 +141,12 @@ __device__ __forceinline__ Item find_item(const AttnParams &p, int id) {
   return t;
 }
 
-// Token and head of row r of an item.
-__device__ __forceinline__ void row_of(const AttnParams &p, const Item &t, int r, int64_t &token, int &head, int &pos) {
+// Token and head of row r of an item and kv head.
+__device__ __forceinline__ void row_of(const AttnParams &p, const Item &t, int kv_head, int r, int64_t &token, int &head,
+                                       int &pos) {
   const int row = t.row0 + r, i = row / p.group;
   token = t.s.row + i;
-  head = t.head * p.group + row - i * p.group;
+  head = kv_head * p.group + row - i * p.group;
   pos = t.s.len - t.s.n + i;
 }
 
@@ -160,23 +166,23 @@ __device__ __forceinline__ int page_of(const AttnParams &p, int b, int page) {
   return checked_page(p, page_entry(p, b, page));
 }
 
-// Row r of an item by one warp, key by key with what the row does not see left out, for
+// Row r of an item and kv head by one warp, key by key with what the row does not see left out, for
 // rows that came out infinite or NaN although the sum of their weights is a number: in the
 // tiles a masked key has the weight 0, and 0 * inf is NaN.  Slow (a key at a time), and only
 // ever run for such rows; a NaN among the scores makes the sum of weights NaN, and the row
 // rightly so.
 template <class A>
-__device__ __noinline__ void exact_row(const AttnParams &p, const Item &t, int r) {
+__device__ __noinline__ void exact_row(const AttnParams &p, const Item &t, int kv_head, int r) {
   const int lane = static_cast<int>(lane_id());
   int64_t token;
   int head, pos;
-  row_of(p, t, r, token, head, pos);
+  row_of(p, t, kv_head, r, token, head, pos);
   const int lo = max(t.k0, p.window ? pos - p.window + 1 : 0), hi = min(t.k1, pos + 1);
   const uint16_t *q = p.q + token * p.q_t + head * p.q_h;
   auto score = [&](int j) {
     const int page = page_of(p, t.b, j / p.page_size);
     if (page < 0) return 0.0f;
-    const uint16_t *k = p.k + page * p.k_page + t.head * p.k_head + (j % p.page_size) * p.k_row;
+    const uint16_t *k = p.k + page * p.k_page + kv_head * p.k_head + (j % p.page_size) * p.k_row;
     float s = 0.0f;
     for (int d = 0; d < p.D; d += 8) {
       const uint4 a = *reinterpret_cast<const uint4 *>(q + d), b = *reinterpret_cast<const uint4 *>(k + d);
@@ -207,7 +213,7 @@ __device__ __noinline__ void exact_row(const AttnParams &p, const Item &t, int r
       const float w = __shfl_sync(0xffffffffu, mine, i);
       const int page = page_of(p, t.b, (j0 + i) / p.page_size);
       if (page < 0) continue;
-      const uint16_t *v = p.v + page * p.v_page + t.head * p.v_head + ((j0 + i) % p.page_size) * p.v_row;
+      const uint16_t *v = p.v + page * p.v_page + kv_head * p.v_head + ((j0 + i) % p.page_size) * p.v_row;
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const int d = 2 * lane + 64 * x;

@@ -7,7 +7,8 @@
 //   O = O + P V    f32 in tensor memory
 //
 // An item is 256 rows: two tiles of 128 rows that share K and V and take turns, so that one
-// tile's softmax runs under the other's products.  12 warps: warps 0-3 and 4-7 each own a
+// tile's softmax runs under the other's products.  (Where a head's rows are 128 or fewer and items
+// many, two kv heads make an item, a row tile and keys of its own each.)  12 warps: warps 0-3 and 4-7 each own a
 // row tile (a thread per row: row maximum and sum need no exchange), warp 8 issues the
 // products, warps 9 and 10 copy K and V pages by TMA (a box per page, or per 8 to 128 rows
 // of one; a page outside the cache is a coordinate outside the tensor and reads zeros), warp
@@ -247,16 +248,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t *q_tile = q_smem + tile * S::kTileBytes;
     uint32_t s_count = 0, o_count = 0, v_count = 0;
     const float scale = p.scale_log2;
-    const bool first_half = tile == 0;
 
+    // The tile's first row and kv head: 128 rows on, or the pair's other head.
+    auto row_base = [&](const Item *t) { return t->pair ? 0 : tile * kRows; };
+    auto kv_head = [&](const Item *t) { return t->head + (t->pair ? tile : 0); };
     // The tile's rows of an item, from q into shared memory as the products take them: this
     // warp's 32, a row to 16 (8) lanes.
     auto load_q = [&](const Item *t) {
       constexpr int CH = DP / 8, PER = 32 / CH;      // lanes of a row, rows at once
-      const int x = tile * kRows + r;
+      const int x = row_base(t) + r;
       int64_t token;
       int head, pos;
-      row_of(p, *t, x < t->rows ? x : 0, token, head, pos);
+      row_of(p, *t, kv_head(t), x < t->rows ? x : 0, token, head, pos);
       const uint64_t row = x < t->rows ? reinterpret_cast<uint64_t>(p.q + token * p.q_t + head * p.q_h) : 0;
       const int c = lane % CH;
 #pragma unroll
@@ -275,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.q_full[tile]);
     };
-    auto needs_q = [&](const Item *t) { return t->rows > tile * kRows && t->k1 > t->k0; };
+    auto needs_q = [&](const Item *t) { return t->rows > row_base(t) && t->k1 > t->k0; };
 
     ItemCursor cursor;
     const Item *t = cursor.next(bar, items, abort_flag, p.timeout_ns, err);
@@ -286,10 +289,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     while (t) {
       const int n = tiles_of_item(t);
-      const int mine = t->rows - tile * kRows;                          // live rows of the tile
+      const int base_row = row_base(t), mine = t->rows - base_row;      // live rows of the tile
+      const int v_tiles = t->pair ? 2 * n : n;
       const Item *after = nullptr;
       if (mine <= 0) {
-        v_count += n;
+        v_count += v_tiles;
         after = cursor.next(bar, items, abort_flag, p.timeout_ns, err);
         if (after && needs_q(after)) {
           load_q(after);
@@ -302,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool live = r < mine, warp_live = (warp & 3) * 32 < mine;
       int64_t token;
       int head, pos;
-      row_of(p, *t, live ? tile * kRows + r : 0, token, head, pos);
+      row_of(p, *t, kv_head(t), live ? base_row + r : 0, token, head, pos);
       // keys that the row sees, from the item's first on: [lo, hi); a row of nobody all, so that
       // it asks for no mask
       const int hi = live ? min(pos + 1, t->k1) - t->k0 : INT_MAX;
@@ -317,11 +321,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           after = cursor.next(bar, items, abort_flag, p.timeout_ns, err);
           if (after && needs_q(after)) load_q(after);
         }
-        if (first_half && (key0 + kKeys > t->k1 || key0 < t->first)) {
+        if ((t->pair || tile == 0) && (key0 + kKeys > t->k1 || key0 < t->first)) {
           // rows of V that no row of the item sees may hold anything: a weight of 0 does
           // not take out infinities or NaN.  (Before both tiles' products: tile 0's go
-          // first.)
-          const uint32_t at = v_count + i;
+          // first; of a pair, each has its own.)
+          const uint32_t at = v_count + (t->pair ? 2 * i + tile : i);
           if (!(ok = wait_all(&bar.v_full[at % VS], (at / VS) & 1, abort_flag, p.timeout_ns, err))) break;
           if (key0 + r >= t->k1 || key0 + r < t->first) {
             uint8_t *v = v_smem + (at % VS) * S::kTileBytes + r * 128;
@@ -404,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&bar.p_full[tile]);
       }
       if (!ok) break;
-      v_count += n;
+      v_count += v_tiles;
       if (n == 0) {
         after = cursor.next(bar, items, abort_flag, p.timeout_ns, err);
         if (after && needs_q(after)) load_q(after);
@@ -475,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (split && live) p.part_lse[part_at] = sum == 0.0f ? -INFINITY : base + __log2f(sum);
         tc_fence_before();
         for (unsigned x = __ballot_sync(0xffffffffu, live && odd != 0.0f && sum == sum); x; x &= x - 1)
-          exact_row<A>(p, *t, tile * kRows + (warp & 3) * 32 + __ffs(x) - 1);
+          exact_row<A>(p, *t, kv_head(t), base_row + (warp & 3) * 32 + __ffs(x) - 1);
       }
       cursor.done(bar, 1);
       t = after;
@@ -546,13 +550,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (const Item *t; ok && (t = cursor.next(bar, items, abort_flag, p.timeout_ns, err));) {
         // (from one lane: the compiler then knows them, and what the loop carries, as uniform)
         const int n = __shfl_sync(0xffffffffu, tiles_of_item(t), 0);
-        const bool two = __shfl_sync(0xffffffffu, t->rows, 0) > kRows;
+        // two tiles share a tile of keys, or, as a pair, have one each
+        const bool pair = __shfl_sync(0xffffffffu, t->pair, 0), two = pair || __shfl_sync(0xffffffffu, t->rows, 0) > kRows;
+        const bool share = two && !pair;
         cursor.done(bar, 0);
         if (n <= 0) continue;
         if (!wait(&bar.k_full[k_slot], k_turn) || !wait(&bar.q_full[0], q_count[0]++)) break;
         tc_fence_after();
-        scores(X0, k_slot, two ? nullptr : &bar.k_empty[k_slot]);
+        scores(X0, k_slot, share ? nullptr : &bar.k_empty[k_slot]);
         if (two) {
+          if (pair) {
+            next_k();
+            if (!wait(&bar.k_full[k_slot], k_turn)) break;
+          }
           if (!wait(&bar.q_full[1], q_count[1]++)) break;
           tc_fence_after();
           scores(X1, k_slot, &bar.k_empty[k_slot]);
@@ -561,9 +571,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int i = 0; i < n - 1; ++i) {
           if (!wait(&bar.k_full[k_slot], k_turn) || !wait(&bar.v_full[v_slot], v_turn)) break;
-          if (!values(X0, v_slot, i == 0, two ? nullptr : &bar.v_empty[v_slot])) break;
-          scores(X0, k_slot, two ? nullptr : &bar.k_empty[k_slot]);
+          if (!values(X0, v_slot, i == 0, share ? nullptr : &bar.v_empty[v_slot])) break;
+          scores(X0, k_slot, share ? nullptr : &bar.k_empty[k_slot]);
           if (two) {
+            if (pair) {
+              next_v();
+              next_k();
+              if (!wait(&bar.k_full[k_slot], k_turn) || !wait(&bar.v_full[v_slot], v_turn)) break;
+            }
             if (!values(X1, v_slot, i == 0, &bar.v_empty[v_slot])) break;
             scores(X1, k_slot, &bar.k_empty[k_slot]);
           }
@@ -571,9 +586,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           next_k();
         }
         if (!ok || !wait(&bar.v_full[v_slot], v_turn)) break;
-        if (!values(X0, v_slot, n == 1, two ? nullptr : &bar.v_empty[v_slot])) break;
+        if (!values(X0, v_slot, n == 1, share ? nullptr : &bar.v_empty[v_slot])) break;
         commit(&bar.o_full[0]);
         if (two) {
+          if (pair) {
+            next_v();
+            if (!wait(&bar.v_full[v_slot], v_turn)) break;
+          }
           if (!values(X1, v_slot, n == 1, &bar.v_empty[v_slot])) break;
           commit(&bar.o_full[1]);
         }
@@ -599,7 +618,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Item t = *next;
         const int n = tiles_of_item(next);
         cursor.done(bar, 0);
-        const int head = __shfl_sync(0xffffffffu, t.head, 0);
+        const int head = __shfl_sync(0xffffffffu, t.head, 0), heads = __shfl_sync(0xffffffffu, t.pair, 0) + 1;
         int page = -1, row = 0;
         auto look_up = [&](int i) {
           const int64_t key = static_cast<int64_t>(t.k0) + static_cast<int64_t>(i) * kKeys + lane * maps.box;
@@ -613,24 +632,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         look_up(0);
         bool ok = true;
-        for (int i = 0; i < n; ++i, ++count) {
-          const uint32_t slot = count % stages;
-          if (!(ok = wait_all(&empty[slot], ((count / stages) & 1) ^ 1, abort_flag, p.timeout_ns, err))) break;
-          const int checked = checked_page(p, page);
-          const bool withheld = p.withhold && is_k && count == 0;
-          if (!withheld && elect_one()) mbar_arrive_expect_tx(&full[slot], S::kTileBytes);
-          __syncwarp();
-          for (int j = 0; j < boxes && !withheld; ++j) {
-            const int pg = __shfl_sync(0xffffffffu, checked, j), rw = __shfl_sync(0xffffffffu, row, j);
-            if (elect_one()) {
-              uint8_t *dst = ring + slot * S::kTileBytes + j * maps.box * 128;
-              debug_check(rw >= 0 && rw + maps.box <= p.page_size && pg < p.pages, err);
-              tma_load_5d(dst, map, &full[slot], 0, rw, 0, head, pg);
-              if (S::kHalves > 1 && parts > 1) tma_load_5d(dst + S::kHalfBytes, map, &full[slot], 64, rw, 0, head, pg);
-            }
+        for (int i = 0; i < n && ok; ++i) {
+          const int checked = checked_page(p, page), checked_row = row;
+          for (int x = 0; x < heads; ++x, ++count) {
+            const uint32_t slot = count % stages;
+            if (!(ok = wait_all(&empty[slot], ((count / stages) & 1) ^ 1, abort_flag, p.timeout_ns, err))) break;
+            const bool withheld = p.withhold && is_k && count == 0;
+            if (!withheld && elect_one()) mbar_arrive_expect_tx(&full[slot], S::kTileBytes);
             __syncwarp();
+            for (int j = 0; j < boxes && !withheld; ++j) {
+              const int pg = __shfl_sync(0xffffffffu, checked, j), rw = __shfl_sync(0xffffffffu, checked_row, j);
+              if (elect_one()) {
+                uint8_t *dst = ring + slot * S::kTileBytes + j * maps.box * 128;
+                debug_check(rw >= 0 && rw + maps.box <= p.page_size && pg < p.pages, err);
+                tma_load_5d(dst, map, &full[slot], 0, rw, 0, head + x, pg);
+                if (S::kHalves > 1 && parts > 1) tma_load_5d(dst + S::kHalfBytes, map, &full[slot], 64, rw, 0, head + x, pg);
+              }
+              __syncwarp();
+            }
+            if (x == 0 && i + 1 < n) look_up(i + 1);
           }
-          if (i + 1 < n) look_up(i + 1);
         }
         if (!ok) break;
       }

@@ -153,3 +153,25 @@ def test_attention_block_example(prompts, head_dim, heads, kv_heads):
     # (between 1 and 1.5, less elsewhere), about 0.09 in the mean square; the norms before and the
     # softmax between do not enlarge it
     assert max(off) < 0.125, off
+
+
+@pytest.mark.parametrize("heads,kv_heads,D,page,window", [(8, 8, 128, 16, 0), (12, 4, 64, 8, 0), (16, 2, 80, 24, 150), (4, 2, 128, 128, 0),
+                                                          (6, 3, 64, 16, 0)])
+def test_many_sequences_of_a_few_dozen_rows(heads, kv_heads, D, page, window):
+    """More items than run at once, each of half a row tile at most: two kv heads an item where
+    they are even in number; with longer and shorter sequences among them."""
+    group = heads // kv_heads
+    seqs = [(max(1, (33 + i * 7 % 96) // group), 40 + 53 * i % 700) for i in range(100)] + [(300, 500), (1, 900), (40, 6000), (0, 3)]
+    seqs = [(n, max(n, total)) for n, total in seqs]
+    s = Step(seqs, heads, kv_heads, D, page, window=window)
+    clean = s.check()
+    # what only a last token sees, of one head of each pair
+    for b in (3, 50):
+        p = seqs[b][1] - 1
+        s.v[int(s.table[b, p // page]), kv_heads - 1, p % page] = float("nan")
+    got, (want, bound) = s.attend(), s.want()
+    check(got, want, bound)
+    rows = torch.ones(s.tokens, dtype=torch.bool, device="cuda")
+    for b in (3, 50):
+        rows[s.offsets[b]:s.offsets[b + 1]] = False
+    assert torch.equal(got[rows], clean[rows])
