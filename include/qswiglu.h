@@ -467,7 +467,8 @@ QSW_API qsw_status qsw_kv_append(const qsw_heads *q, const qsw_heads *k, const q
  * unspecified, but nothing is read or written out of range.  The plan holds
  * for calls with the same B, T, heads, D, window, max_pages and cache geometry; it is only read by them, so that
  * calls on several streams may share it.  B at most 65536, T at most 2^22, heads at
- * most 1024 and a multiple of kv_heads.
+ * most 1024 and a multiple of kv_heads, T * heads at most 2^30, max_pages * page_size
+ * below 2^31 - 1024.
  */
 QSW_API size_t qsw_paged_plan_bytes(int64_t B, int64_t T);
 QSW_API qsw_status qsw_paged_plan(const int *offsets, const int *lengths, int64_t B, const int *page_table,

@@ -166,24 +166,39 @@ __device__ __forceinline__ int page_of(const AttnParams &p, int b, int page) {
   return checked_page(p, page_entry(p, b, page));
 }
 
-// Row r of an item and kv head by one warp, key by key with what the row does not see left out, for
-// rows that came out infinite or NaN although the sum of their weights is a number: in the
-// tiles a masked key has the weight 0, and 0 * inf is NaN.  Slow (a key at a time), and only
-// ever run for such rows; a NaN among the scores makes the sum of weights NaN, and the row
-// rightly so.
+// Row r of an item and kv head by one warp, key by key with what the row does not see left
+// out, for rows that came out infinite or NaN although the sum of their weights is a number (a
+// NaN among the scores makes the sum NaN, and the row rightly so): in the tiles a masked key
+// has the weight 0, and 0 * inf is NaN.  Only where such a key of the tiles has a value that
+// is not finite; else what the row sees made it so.  Slow, a key at a time.
 template <class A>
 __device__ __noinline__ void exact_row(const AttnParams &p, const Item &t, int kv_head, int r) {
   const int lane = static_cast<int>(lane_id());
   int64_t token;
   int head, pos;
   row_of(p, t, kv_head, r, token, head, pos);
-  const int lo = max(t.k0, p.window ? pos - p.window + 1 : 0), hi = min(t.k1, pos + 1);
+  const int begin = max(t.k0, t.first);          // of what the tiles hold: the rest of V is zeros there
+  const int lo = max(begin, p.window ? pos - p.window + 1 : 0), hi = max(min(t.k1, pos + 1), lo);
   const uint16_t *q = p.q + token * p.q_t + head * p.q_h;
+  const int unseen = (lo - begin) + (t.k1 - hi);
+  bool odd = false;
+  for (int i = lane; i < unseen; i += 32) {
+    const int j = begin + i < lo ? begin + i : hi + (i - (lo - begin));
+    const int page = page_of(p, t.b, j / p.page_size);
+    if (page < 0) continue;
+    const uint16_t *v = p.v + page * p.v_page + kv_head * p.v_head + (j % p.page_size) * p.v_row;
+    for (int d = 0; d < p.D; d += 2) {
+      const uint32_t x = *reinterpret_cast<const uint32_t *>(v + d);
+      odd |= !isfinite(A::lo(x)) || !isfinite(A::hi(x));
+    }
+  }
+  if (!__any_sync(0xffffffffu, odd)) return;
   auto score = [&](int j) {
     const int page = page_of(p, t.b, j / p.page_size);
     if (page < 0) return 0.0f;
     const uint16_t *k = p.k + page * p.k_page + kv_head * p.k_head + (j % p.page_size) * p.k_row;
     float s = 0.0f;
+#pragma unroll 4
     for (int d = 0; d < p.D; d += 8) {
       const uint4 a = *reinterpret_cast<const uint4 *>(q + d), b = *reinterpret_cast<const uint4 *>(k + d);
       const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
@@ -195,30 +210,42 @@ __device__ __noinline__ void exact_row(const AttnParams &p, const Item &t, int k
     }
     return s * p.scale_log2;
   };
-  float m = -INFINITY;
-  for (int j = lo + lane; j < hi; j += 32) m = fmaxf(m, score(j));
+  float m = -INFINITY, sum = 0.0f;        // of the lane's keys
+  for (int j = lo + lane; j < hi; j += 32) {
+    const float s = score(j), now = fmaxf(m, s);
+    if (now == -INFINITY) continue;
+    sum = sum * ex2(m - now) + ex2(s - now);
+    m = now;
+  }
+  float top = m;
 #pragma unroll
-  for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-  const float base = m == -INFINITY ? 0.0f : m;
-  float sum = 0.0f;
-  for (int j = lo + lane; j < hi; j += 32) sum += ex2(score(j) - base);
+  for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+  const float base = top == -INFINITY ? 0.0f : top;
+  sum *= ex2(m - base);
 #pragma unroll
   for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
   float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   for (int j0 = lo; j0 < hi; j0 += 32) {
-    const float mine = j0 + lane < hi ? ex2(score(j0 + lane) - base) * inv : 0.0f;
-    const int end = min(32, hi - j0);
-    for (int i = 0; i < end; ++i) {
+    // each lane a key: its weight, and where its value lies (0: nowhere)
+    float mine = 0.0f;
+    uint64_t mine_at = 0;
+    if (j0 + lane < hi) {
+      mine = ex2(score(j0 + lane) - base) * inv;
+      const int page = page_of(p, t.b, (j0 + lane) / p.page_size);
+      if (page >= 0)
+        mine_at = reinterpret_cast<uint64_t>(p.v + page * p.v_page + kv_head * p.v_head +
+                                             ((j0 + lane) % p.page_size) * p.v_row);
+    }
+#pragma unroll 8
+    for (int i = 0; i < 32; ++i) {
       const float w = __shfl_sync(0xffffffffu, mine, i);
-      const int page = page_of(p, t.b, (j0 + i) / p.page_size);
-      if (page < 0) continue;
-      const uint16_t *v = p.v + page * p.v_page + kv_head * p.v_head + ((j0 + i) % p.page_size) * p.v_row;
+      const auto *v = reinterpret_cast<const uint16_t *>(__shfl_sync(0xffffffffu, mine_at, i));
+      if (!v) continue;
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const int d = 2 * lane + 64 * x;
-        if (d >= p.D) continue;
-        const uint32_t c = *reinterpret_cast<const uint32_t *>(v + d);
+        const uint32_t c = d < p.D ? *reinterpret_cast<const uint32_t *>(v + d) : 0u;
         o[2 * x] = fmaf(w, A::lo(c), o[2 * x]);
         o[2 * x + 1] = fmaf(w, A::hi(c), o[2 * x + 1]);
       }

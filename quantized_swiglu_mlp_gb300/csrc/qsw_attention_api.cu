@@ -47,7 +47,8 @@ qsw_status check_step(int64_t B, int64_t T, int64_t heads, int64_t max_pages, in
   if (heads % c->kv_heads) return QSW_ERR_INVALID_ARG;
   if (B > kMaxSequences || T > kMaxTokens || heads > kMaxHeads || T * heads > kMaxRows || window > kMaxWindow)
     return QSW_ERR_UNSUPPORTED;
-  return max_pages > INT32_MAX / c->page_size ? QSW_ERR_UNSUPPORTED : QSW_OK;
+  // (the end of a length's last tile is a 32-bit number too)
+  return max_pages > (INT32_MAX - 1024) / c->page_size ? QSW_ERR_UNSUPPORTED : QSW_OK;
 }
 
 }  // namespace

@@ -276,15 +276,17 @@ cudaError_t launch_rope(const RopeArgs &a, int num_sms, cudaStream_t stream) {
   }
   p.per_token = make_div(static_cast<uint32_t>(units));
   p.halves = make_div(static_cast<uint32_t>(p.half ? p.half : 1));
-  // as many tokens a CTA as its threads hold in one go, where there are CTAs enough
+  p.groups = (p.half + 7) / 8;
+  p.turns = p.groups * 8;
+  // as many tokens a CTA as its threads hold in one go, where there are CTAs enough; their turns
+  // 32 KB at most
   int64_t tokens = kThreads * kAhead / units;
-  const int64_t fair = a.T / (2 * static_cast<int64_t>(num_sms));
+  const int64_t fair = a.T / (2 * static_cast<int64_t>(num_sms)), most = p.turns ? 4096 / p.turns : 16;
   tokens = tokens > fair ? fair : tokens;
+  tokens = tokens > most ? most : tokens;
   tokens = tokens < 1 ? 1 : tokens > 16 ? 16 : tokens;
   p.tokens = static_cast<int>(tokens);
   const dim3 grid(static_cast<unsigned>((a.T + tokens - 1) / tokens));
-  p.groups = (p.half + 7) / 8;
-  p.turns = p.groups * 8;
   const size_t smem = static_cast<size_t>(tokens) * p.turns * sizeof(float2);
   const bool f16 = a.act == ActF16::kId;
   if (wide)

@@ -46,7 +46,7 @@ def check(got, want, bound, what=""):
 @pytest.mark.parametrize("interleaved", [False, True], ids=["half", "pairs"])
 @pytest.mark.parametrize("T,heads,D,rot", [(1, 1, 64, 64), (3, 5, 128, 128), (1000, 8, 128, 64), (37, 3, 80, 80),
                                            (5, 2, 96, 46), (2, 3, 7, 6), (4, 1, 256, 16), (9, 2, 64, 0),
-                                           (2500, 2, 72, 24)])
+                                           (2500, 2, 72, 24), (9000, 1, 1024, 1024), (700, 1, 1022, 1020)])
 def test_rope(dt, interleaved, T, heads, D, rot):
     x = randn(T + D, T, heads, D, dt=dt)
     f = ops.rope_frequencies(rot) if rot else torch.zeros(0)
