@@ -431,7 +431,7 @@ typedef struct {
  * copied.  Pairs are (i, i + rot / 2), or (2 i, 2 i + 1) with `interleaved`.
  * table[i] (int64 [rot / 2] on the device) is f_i in turns per position times 2^64,
  * modulo 2^64: positions (int32, of either sign; NULL: all 0) of any size keep their
- * angle to 2^-24.  rot is even, from 0 to D; D at most 1024, heads at most 4096.  Any
+ * angle to 2^-23 rad.  rot is even, from 0 to D; D at most 1024, heads at most 4096.  Any
  * strides; 2-byte alignment (16-byte alignment of everything is faster).  out may be
  * x with the same strides.
  */

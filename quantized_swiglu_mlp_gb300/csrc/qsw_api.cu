@@ -355,6 +355,6 @@ const char *qsw_status_string(qsw_status s) {
   }
 }
 
-int qsw_version(void) { return 107; }
+int qsw_version(void) { return 108; }
 
 }  // extern "C"
