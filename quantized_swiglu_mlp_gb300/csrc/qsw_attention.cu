@@ -723,9 +723,11 @@ AttnForm attention_form(int64_t T, int64_t B, int64_t heads, int64_t kv_heads, i
   // Which lists there are: one token a sequence, as far as the sizes say, or the rows of a
   // single one, need one; else sequences with up to 32 rows go with the few.
   f.most_rows = B == 1 || T <= B ? (T <= B || T * group <= 32 ? INT32_MAX : 0) : 32;
-  // (8 rows a sequence on average: most have up to 16, and two CTAs of 16 rows on an SM hide more
-  // latency than one of 32)
-  const int64_t few = T <= B ? group : B == 1 || T * group <= 8 * B ? T * group / seqs : 32;
+  // Row tiles of 16 or 32 in that list.  Two CTAs of 16 rows on an SM hide more latency than one of
+  // 32, which reads keys once for twice the rows.  Up to 8 rows a sequence on average, most have up
+  // to 16; above 32, the few are decoding, one token each, beside chunks of prompts.
+  const int64_t mean = T * group / seqs;
+  const int64_t few = T <= B || (B > 1 && mean > 32) ? group : B == 1 || mean <= 8 ? mean : 32;
   ListForm &r = f.list[LIST_ROWS], &t = f.list[LIST_TILES];
   r.tile_rows = few <= 16 ? 16 : 32;
   r.tile_keys = kKeyGroups * step_keys(D <= 64 ? 64 : 128, r.tile_rows / 16);
