@@ -221,13 +221,12 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
 
 // ---------------------------------------------------------------- few rows --
 
-constexpr int kKeyGroups = 4;      // of warps, each with keys of its own
-// Keys of a group's step.  32 take a warp little longer than 16 (its softmax is mostly latency); with
-// 16 rows of 128 columns two CTAs of 16 keys a step fit on an SM, which is as fast.
-constexpr int step_keys(int DP, int RG) { return DP == 128 && RG == 1 ? 16 : 32; }
-constexpr int row_stage_bytes(int DP, int RG) { return 2 * step_keys(DP, RG) * DP * 2; }
-// Stages of a group's ring: 96 KB a CTA where two run on an SM, else 192 KB.
-constexpr int row_stages(int DP, int RG) { return (RG == 1 ? 98304 : 196608) / kKeyGroups / row_stage_bytes(DP, RG); }
+constexpr int kRowWarps = 4;       // each with keys of its own
+// Keys of a warp's step: 8 KB of K and V.  32 take a warp little longer than 16 (its softmax is mostly
+// latency), but of 128 columns two CTAs then no longer fit on an SM.
+constexpr int step_keys(int DP) { return DP == 128 ? 16 : 32; }
+constexpr int kRowStages = 3;      // 96 KB of ring a CTA: two on an SM
+constexpr int kRowStageBytes = 8192;
 
 __device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -255,32 +254,27 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Up to 16 RG rows of one kv head.  Four groups of RG warps each take every fourth run of KEYS
-// keys with a ring of their own, which the group's first warp fills by TMA (boxes of 8 to 32
-// rows of a page); a warp has 16 rows and a softmax of its own (no barrier over the CTA in the loop),
-// and the groups' results meet at the end.  (With 16-byte copies by all lanes and 16 keys a step
-// 16 sequences with 5 drafted tokens each took 34 us, so 26.)
+// Up to 16 rows of one kv head.  Each of four warps takes every fourth run of KEYS keys with a
+// ring of its own, which it fills by TMA (boxes of 8 to 32 rows of a page), and a softmax of its
+// own (no barrier over the CTA in the loop); the warps' results meet at the end.
 //
 // HBM-bound: 64 sequences of 128 to 16000 keys, 8 kv heads of 128: 156 us for 983 MB, 6.3 TB/s. With few
 // keys latency: 4 sequences of up to 180 keys take 5.5 us.
-template <class A, int DP, int RG>
-__global__ void __launch_bounds__(32 * kKeyGroups * RG, 3 - RG)
+template <class A, int DP>
+__global__ void __launch_bounds__(32 * kRowWarps, 2)
     attn_rows_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CacheMaps maps) {
-  constexpr int kRowWarps = kKeyGroups * RG, ROWS = 16 * RG;
-  constexpr int KEYS = DP == 128 && RG == 1 ? 16 : 32;                       // step_keys
-  constexpr int STAGE = 2 * KEYS * DP * 2;                                   // row_stage_bytes
-  constexpr int kRowStages = (RG == 1 ? 98304 : 196608) / kKeyGroups / STAGE;   // row_stages
+  constexpr int KEYS = DP == 128 ? 16 : 32, STAGE = 2 * KEYS * DP * 2;      // step_keys
+  static_assert(STAGE == kRowStageBytes, "a step's K and V");
   constexpr int H = DP / 64;                     // halves of a head
   extern __shared__ uint8_t smem_raw[];
   uint8_t *ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  __shared__ float warp_m[kKeyGroups][ROWS], warp_l[kKeyGroups][ROWS];
-  __shared__ uint64_t full[kKeyGroups][kRowStages], empty[kKeyGroups][kRowStages];
+  __shared__ float warp_m[kRowWarps][16], warp_l[kRowWarps][16];
+  __shared__ uint64_t full[kRowWarps][kRowStages];
   __shared__ unsigned redo;
   __shared__ int abort_word;
   volatile int *abort_flag = &abort_word;
   unsigned int *err = &g_rows_error;
   const int tid = static_cast<int>(threadIdx.x), warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-  const int kg = warp / RG, rg = warp % RG;
   if (!p.after_tiles) griddep_wait();      // (else all before the tiles' kernel is complete)
   griddep_launch_dependents();
   const int total = __ldg(p.plan.head + LIST_ROWS);
@@ -289,19 +283,18 @@ __global__ void __launch_bounds__(32 * kKeyGroups * RG, 3 - RG)
     return;
   }
   if constexpr (kDebugBounds) {
-    debug_poison_smem(ring, kKeyGroups * kRowStages * STAGE);
+    debug_poison_smem(ring, kRowWarps * kRowStages * STAGE);
     fence_proxy_async_smem();
   }
-  if (tid < kKeyGroups * kRowStages) {
+  if (tid < kRowWarps * kRowStages) {
     mbar_init(&full[0][0] + tid, 1);
-    mbar_init(&empty[0][0] + tid, RG);
     fence_mbar_init();
-  } else if (tid == kKeyGroups * kRowStages) {
+  } else if (tid == kRowWarps * kRowStages) {
     abort_word = 0;
     prefetch_tensormap(&maps.k);
     prefetch_tensormap(&maps.v);
   }
-  uint8_t *mine = ring + kg * kRowStages * STAGE;
+  uint8_t *mine = ring + warp * kRowStages * STAGE;
 
   // Copies: boxes of rows, of all halves or of one; a lane per box of rows looks its page
   // up.  In a stage a box's rows of 128 bytes lie half by half, chunk c of row j at c ^ (j mod 8).
@@ -324,14 +317,14 @@ __global__ void __launch_bounds__(32 * kKeyGroups * RG, 3 - RG)
     __syncthreads();      // the ring of the item before is free, its flags have been read
     if (tid == 0) redo = 0;
     const int runs = (t.k1 - t.k0 + KEYS - 1) / KEYS;       // of the item
-    const int my_runs = runs > kg ? (runs - kg + kKeyGroups - 1) / kKeyGroups : 0;
+    const int my_runs = runs > warp ? (runs - warp + kRowWarps - 1) / kRowWarps : 0;
     const int kv_head = __shfl_sync(0xffffffffu, t.head, 0);
 
-    // the page of a box of the group's run i, -1 (zeros) where no row of the item sees it; a step
+    // the page of a box of the warp's run i, -1 (zeros) where no row of the item sees it; a step
     // ahead: the table's entry arrives while the step is computed
     auto look_up = [&](int i, int &page, int &row) {
       const int64_t key =
-          static_cast<int64_t>(t.k0) + (static_cast<int64_t>(i) * kKeyGroups + kg) * KEYS + lane * maps.box;
+          static_cast<int64_t>(t.k0) + (static_cast<int64_t>(i) * kRowWarps + warp) * KEYS + lane * maps.box;
       page = -1;
       row = 0;
       if (lane < subs && key < t.k1 && key + maps.box > t.first) {
@@ -340,30 +333,26 @@ __global__ void __launch_bounds__(32 * kKeyGroups * RG, 3 - RG)
         row = static_cast<int>(key) - n * p.page_size;
       }
     };
-    // the copies of the group's next run (its first warp)
+    // the copies of the warp's next run
     auto issue = [&](int page, int row) {
       const uint32_t slot = issued % kRowStages;
-      if (RG > 1) {
-        ok = ok && wait_all(&empty[kg][slot], ((issued / kRowStages) & 1) ^ 1, abort_flag, p.timeout_ns, err);
-        if (!ok) return;
-      }
       if (p.withhold && issued == 0) {
         ++issued;
         return;
       }
       const int checked = checked_page(p, page);
       uint8_t *dst = mine + slot * STAGE;
-      if (elect_one()) mbar_arrive_expect_tx(&full[kg][slot], STAGE);
+      if (elect_one()) mbar_arrive_expect_tx(&full[warp][slot], STAGE);
       __syncwarp();
       for (int j = 0; j < subs; ++j) {
         const int pg = __shfl_sync(0xffffffffu, checked, j), rw = __shfl_sync(0xffffffffu, row, j);
         if (elect_one()) {
           debug_check(rw >= 0 && rw + maps.box <= p.page_size && pg < p.pages, err);
-          tma_load_5d(dst, &maps.k, &full[kg][slot], 0, rw, 0, kv_head, pg);
-          tma_load_5d(dst + STAGE / 2, &maps.v, &full[kg][slot], 0, rw, 0, kv_head, pg);
+          tma_load_5d(dst, &maps.k, &full[warp][slot], 0, rw, 0, kv_head, pg);
+          tma_load_5d(dst + STAGE / 2, &maps.v, &full[warp][slot], 0, rw, 0, kv_head, pg);
           if (H > 1 && parts > 1) {
-            tma_load_5d(dst + half_bytes, &maps.k, &full[kg][slot], 64, rw, 0, kv_head, pg);
-            tma_load_5d(dst + STAGE / 2 + half_bytes, &maps.v, &full[kg][slot], 64, rw, 0, kv_head, pg);
+            tma_load_5d(dst + half_bytes, &maps.k, &full[warp][slot], 64, rw, 0, kv_head, pg);
+            tma_load_5d(dst + STAGE / 2 + half_bytes, &maps.v, &full[warp][slot], 64, rw, 0, kv_head, pg);
           }
         }
         dst += H * half_bytes;
@@ -372,13 +361,11 @@ __global__ void __launch_bounds__(32 * kKeyGroups * RG, 3 - RG)
       ++issued;
     };
     int page[kRowStages + 1], row[kRowStages + 1];
-    if (rg == 0) {
 #pragma unroll
-      for (int i = 0; i <= kRowStages; ++i) look_up(i, page[i], row[i]);
+    for (int i = 0; i <= kRowStages; ++i) look_up(i, page[i], row[i]);
 #pragma unroll
-      for (int i = 0; i < kRowStages; ++i)
-        if (i < my_runs) issue(page[i], row[i]);
-    }
+    for (int i = 0; i < kRowStages; ++i)
+      if (i < my_runs) issue(page[i], row[i]);
     int next_page = page[kRowStages], next_row = row[kRowStages];
 
     // q, as the A operand: rows lane / 4 and + 8, pairs (lane % 4) of each 8 columns
@@ -387,7 +374,7 @@ __global__ void __launch_bounds__(32 * kKeyGroups * RG, 3 - RG)
     int head, begin[2], end[2];      // keys that the rows see
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int r = rg * 16 + lane / 4 + 8 * h;
+      const int r = lane / 4 + 8 * h;
       const bool live = r < t.rows;
       int pos;
       row_of(p, t, t.head, live ? r : 0, token, head, pos);
@@ -411,9 +398,9 @@ __global__ void __launch_bounds__(32 * kKeyGroups * RG, 3 - RG)
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
     for (int i = 0; i < my_runs; ++i) {
       const uint32_t slot = used % kRowStages;
-      if (!(ok = ok && wait_all(&full[kg][slot], (used / kRowStages) & 1, abort_flag, p.timeout_ns, err))) break;
+      if (!(ok = ok && wait_all(&full[warp][slot], (used / kRowStages) & 1, abort_flag, p.timeout_ns, err))) break;
       uint8_t *stage = mine + slot * STAGE;
-      const int run0 = t.k0 + (i * kKeyGroups + kg) * KEYS;
+      const int run0 = t.k0 + (i * kRowWarps + warp) * KEYS;
       if (run0 + KEYS > t.k1 || run0 < t.first) {
         // rows of V that no row of the item sees may hold anything: a weight of 0 does not take out
         // infinities or NaN
@@ -496,8 +483,7 @@ __global__ void __launch_bounds__(32 * kKeyGroups * RG, 3 - RG)
       // the stage is read: the run kRowStages further takes its place
       ++used;
       __syncwarp();
-      if (RG > 1 && lane == 0) mbar_arrive(&empty[kg][slot]);
-      if (rg == 0 && i + kRowStages < my_runs) {
+      if (i + kRowStages < my_runs) {
         issue(next_page, next_row);
         look_up(i + kRowStages + 1, next_page, next_row);
       }
@@ -512,17 +498,17 @@ __global__ void __launch_bounds__(32 * kKeyGroups * RG, 3 - RG)
     // the warps' sums, in the rings' place
     constexpr int PITCH = DP + 4;
     float *sum = reinterpret_cast<float *>(ring);
-    static_assert(kKeyGroups * ROWS * PITCH * 4 <= kKeyGroups * kRowStages * STAGE, "the sums fit");
+    static_assert(kRowWarps * 16 * PITCH * 4 <= kRowWarps * kRowStages * STAGE, "the sums fit");
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int r = rg * 16 + lane / 4 + 8 * h;
+      const int r = lane / 4 + 8 * h;
       if ((lane & 3) == 0) {
-        warp_m[kg][r] = m[h];
-        warp_l[kg][r] = l[h];
+        warp_m[warp][r] = m[h];
+        warp_l[warp][r] = l[h];
       }
 #pragma unroll
       for (int d = 0; d < DP / 8; ++d)
-        *reinterpret_cast<float2 *>(sum + (kg * ROWS + r) * PITCH + d * 8 + (lane & 3) * 2) =
+        *reinterpret_cast<float2 *>(sum + (warp * 16 + r) * PITCH + d * 8 + (lane & 3) * 2) =
             make_float2(o[d][2 * h], o[d][2 * h + 1]);
     }
     __syncthreads();
@@ -533,11 +519,11 @@ __global__ void __launch_bounds__(32 * kKeyGroups * RG, 3 - RG)
     if (r < t.rows) {
       float top = warp_m[0][r];
 #pragma unroll
-      for (int w = 1; w < kKeyGroups; ++w) top = fmaxf(top, warp_m[w][r]);
+      for (int w = 1; w < kRowWarps; ++w) top = fmaxf(top, warp_m[w][r]);
       const float base = top == -INFINITY ? 0.0f : top;
-      float f[kKeyGroups], all = 0.0f;
+      float f[kRowWarps], all = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kKeyGroups; ++w) {
+      for (int w = 0; w < kRowWarps; ++w) {
         f[w] = ex2(warp_m[w][r] - base);
         all = fmaf(f[w], warp_l[w][r], all);
       }
@@ -552,7 +538,7 @@ __global__ void __launch_bounds__(32 * kKeyGroups * RG, 3 - RG)
         for (int x = 0; x < 8; ++x) {
           float v = 0.0f;
 #pragma unroll
-          for (int w = 0; w < kKeyGroups; ++w) v = fmaf(f[w], sum[(w * ROWS + r) * PITCH + c + x], v);
+          for (int w = 0; w < kRowWarps; ++w) v = fmaf(f[w], sum[(w * 16 + r) * PITCH + c + x], v);
           y[x] = v * inv;
           finite &= isfinite(y[x]) != 0;
         }
@@ -576,9 +562,9 @@ __global__ void __launch_bounds__(32 * kKeyGroups * RG, 3 - RG)
     }
   }
   // given up: the copies in flight
-  if (rg == 0 && *abort_flag)
+  if (*abort_flag)
     for (uint32_t c = used; c < issued; ++c)
-      mbar_wait_drain(&full[kg][c % kRowStages], (c / kRowStages) & 1, p.timeout_ns);
+      mbar_wait_drain(&full[warp][c % kRowStages], (c / kRowStages) & 1, p.timeout_ns);
   if (p.after_tiles) griddep_wait();       // the next kernel comes after both
 }
 
@@ -676,27 +662,23 @@ cudaError_t launch_join(const AttnParams &p, int num_sms, cudaStream_t stream) {
                       : launch_on(join_kernel<A, 1>, grid((rows + 7) / 8), 256, 0, stream, true, p);
 }
 
-template <class A, int DP, int RG>
-cudaError_t launch_rows_form(const AttnParams &p, const CacheMaps &maps, dim3 grid, cudaStream_t stream) {
-  const int bytes = kKeyGroups * row_stages(DP, RG) * row_stage_bytes(DP, RG) + 1024;
+template <class A, int DP>
+cudaError_t launch_rows_form(const AttnParams &p, const ListForm &f, const qsw_kv_cache &cache, cudaStream_t stream) {
+  constexpr int bytes = kRowWarps * kRowStages * kRowStageBytes + 1024;
   static SmemOnce once;
-  auto kernel = attn_rows_kernel<A, DP, RG>;
+  auto kernel = attn_rows_kernel<A, DP>;
   const cudaError_t e = allow_smem(once, kernel, bytes);
-  return e != cudaSuccess ? e
-                          : launch_on(kernel, grid, 32 * kKeyGroups * RG, bytes, stream, p.after_tiles != 0, p, maps);
+  if (e != cudaSuccess) return e;
+  const int64_t most = 2 * static_cast<int64_t>(f.slots);
+  const dim3 grid(static_cast<unsigned>(f.items < most ? f.items : most));
+  CacheMaps maps = {};
+  if (!encode_cache_maps(&maps, cache, p.D, A::kId, step_keys(DP), true)) return cudaErrorInvalidValue;
+  return launch_on(kernel, grid, 32 * kRowWarps, bytes, stream, p.after_tiles != 0, p, maps);
 }
 
 template <class A>
 cudaError_t launch_rows(const AttnParams &p, const ListForm &f, const qsw_kv_cache &cache, cudaStream_t stream) {
-  const int64_t most = 2 * static_cast<int64_t>(f.slots);
-  const dim3 grid(static_cast<unsigned>(f.items < most ? f.items : most));
-  const bool one = f.tile_rows == 16;
-  CacheMaps maps = {};
-  if (!encode_cache_maps(&maps, cache, p.D, A::kId, step_keys(p.D <= 64 ? 64 : 128, one ? 1 : 2), true))
-    return cudaErrorInvalidValue;
-  if (p.D <= 64)
-    return one ? launch_rows_form<A, 64, 1>(p, maps, grid, stream) : launch_rows_form<A, 64, 2>(p, maps, grid, stream);
-  return one ? launch_rows_form<A, 128, 1>(p, maps, grid, stream) : launch_rows_form<A, 128, 2>(p, maps, grid, stream);
+  return p.D <= 64 ? launch_rows_form<A, 64>(p, f, cache, stream) : launch_rows_form<A, 128>(p, f, cache, stream);
 }
 
 }  // namespace
@@ -720,18 +702,16 @@ constexpr int kMaxSplits = 128;
 AttnForm attention_form(int64_t T, int64_t B, int64_t heads, int64_t kv_heads, int64_t D, int64_t max_len, int num_sms) {
   AttnForm f = {};
   const int64_t group = heads / kv_heads, seqs = T < B ? T : B;
-  // Which lists there are: one token a sequence, as far as the sizes say, or the rows of a
-  // single one, need one; else sequences with up to 32 rows go with the few.
-  f.most_rows = B == 1 || T <= B ? (T <= B || T * group <= 32 ? INT32_MAX : 0) : 32;
-  // Row tiles of 16 or 32 in that list.  Two CTAs of 16 rows on an SM hide more latency than one of
-  // 32, which reads keys once for twice the rows.  Up to 8 rows a sequence on average, most have up
-  // to 16; above 32, the few are decoding, one token each, beside chunks of prompts.
-  const int64_t mean = T * group / seqs;
-  const int64_t few = T <= B || (B > 1 && mean > 32) ? group : B == 1 || mean <= 8 ? mean : 32;
+  // Up to 16 rows go with the few, which one warp's products take (us, tiles of 256 rows for more
+  // than 16 / for more than 32 rows, two warps sharing keys: 64 sequences of 1000 keys with 24 rows 65 / 80,
+  // with 12 on the lone warp's kernel 55 / 78; 16 drafting ones 27.9 / 26.0).  Where the sizes
+  // alone say which, there is one list: one token a sequence, or a single sequence.
+  const int64_t rows = T <= B ? group : T * group;
+  f.most_rows = T <= B || B == 1 ? (rows <= 16 ? INT32_MAX : 0) : 16;
   ListForm &r = f.list[LIST_ROWS], &t = f.list[LIST_TILES];
-  r.tile_rows = few <= 16 ? 16 : 32;
-  r.tile_keys = kKeyGroups * step_keys(D <= 64 ? 64 : 128, r.tile_rows / 16);
-  r.slots = r.tile_rows == 16 ? 2 * num_sms : num_sms;
+  r.tile_rows = 16;
+  r.tile_keys = kRowWarps * step_keys(D <= 64 ? 64 : 128);
+  r.slots = 2 * num_sms;
   t.tile_rows = 256;
   t.tile_keys = 128;
   t.slots = num_sms;
