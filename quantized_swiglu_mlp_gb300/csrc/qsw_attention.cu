@@ -38,7 +38,7 @@ constexpr int kPlanThreads = 1024;
 // (a warp each) by the time it would take in tiles -- the longest item, or the work of all
 // over the CTAs that run at once, in whole waves; an item costs kItemCost tiles more for its
 // beginning and end, and one of a split history kSplitCost more for what it leaves to the join
-// (up to 256 rows of f32 written and read again; 16 or 32 in the other list).
+// (up to 256 rows of f32 written and read again; 16 in the other list).
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ PlanParams p) {
   constexpr float kItemCost = 3.0f, kSplitCost[2] = {2.0f, 7.0f};
   constexpr int kLeast = 4;        // tiles of a split, at least
