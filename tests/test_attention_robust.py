@@ -175,3 +175,9 @@ def test_many_sequences_of_a_few_dozen_rows(heads, kv_heads, D, page, window):
     for b in (3, 50):
         rows[s.offsets[b]:s.offsets[b + 1]] = False
     assert torch.equal(got[rows], clean[rows])
+
+
+@pytest.mark.parametrize("heads,kv_heads", [(8, 2), (32, 1), (17, 1)])
+def test_fewer_tokens_than_sequences_unevenly(heads, kv_heads):
+    """The sizes look like one token a sequence; one of them has them all."""
+    Step([(0, 7)] * 20 + [(30, 300)] + [(0, 0)] * 20, heads, kv_heads, 128, 16).check()
