@@ -171,6 +171,31 @@ struct ItemCursor {
 
 __device__ __forceinline__ int tiles_of_item(const Item *t) { return (t->k1 - t->k0 + kKeys - 1) / kKeys; }
 
+// Rows of one warp (of four of a row tile) that came out infinite or NaN, in all items of the
+// CTA: once the warp is through with them and no other one waits for it, since they may take long.
+template <class A>
+__device__ __noinline__ void redo_rows(const AttnParams &p, int tile, int quarter, int total) {
+  const int lane = static_cast<int>(lane_id());
+  __syncwarp();
+#pragma unroll 1
+  for (int step = 0, id; (id = item_of(step)) < total; ++step) {
+    const Item t = find_item(p, id);
+    const int first = (t.pair ? 0 : tile * kRows) + quarter * 32, kv_head = t.head + (t.pair ? tile : 0);
+    const int n = min(t.rows - first, 32);
+#pragma unroll 1
+    for (int r = first; r < first + n; ++r) {
+      int64_t token;
+      int head, pos;
+      row_of(p, t, kv_head, r, token, head, pos);
+      const int64_t at = token * p.heads + head, part = t.split * static_cast<int64_t>(p.T) * p.heads + at;
+      bool odd = false;
+      for (int d = lane; d < p.D; d += 32)
+        odd |= !isfinite(t.s.splits > 1 ? __ldcg(p.part + part * p.D + d) : A::lo(__ldcg(p.out + at * p.D + d)));
+      if (__any_sync(0xffffffffu, odd)) exact_row<A>(p, t, kv_head, r);
+    }
+  }
+}
+
 template <class A, int DP>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tiles_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CacheMaps maps) {
@@ -292,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       load_q(t);
       q_loaded();
     }
-    bool ok = true;
+    bool ok = true, again = false;
     while (t) {
       const int n = tiles_of_item(t);
       const int base_row = row_base(t), mine = t->rows - base_row;      // live rows of the tile
@@ -484,13 +509,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         debug_check(!live || (token >= 0 && token < p.T && head >= 0 && head < p.heads), err);
         if (split && live) p.part_lse[part_at] = sum == 0.0f ? -INFINITY : base + __log2f(sum);
         tc_fence_before();
-        for (unsigned x = __ballot_sync(0xffffffffu, live && odd != 0.0f && sum == sum); x; x &= x - 1)
-          exact_row<A>(p, *t, kv_head(t), base_row + (warp & 3) * 32 + __ffs(x) - 1);
+        again |= __any_sync(0xffffffffu, live && odd != 0.0f && sum == sum);
       }
       cursor.done(bar, 1);
       t = after;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
+    if (again && ok) redo_rows<A>(p, tile, warp & 3, total);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == kWarpMma) {
