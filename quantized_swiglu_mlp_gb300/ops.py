@@ -607,7 +607,8 @@ def rope_frequencies(dim: int, base: float = 10000.0, scaling: str = "none", fac
                 by the factor, the fastest not at all;
       "ramp"    pairs that turn over `fast` times within original_length positions are left, those
                 that turn less than `slow` times interpolated, a linear ramp over the pair's
-                index between.
+                index between (Peng et al. 2023, "YaRN"; its ends are rounded outwards to whole
+                pairs and may lie behind the last one).
     """
     if dim < 2 or dim % 2:
         raise ValueError("dim must be even and positive")
@@ -630,8 +631,10 @@ def rope_frequencies(dim: int, base: float = 10000.0, scaling: str = "none", fac
 
     def pair_of(turns):      # the pair that turns so often within original_length
         return dim * math.log(original_length / (turns * 2 * math.pi)) / (2 * math.log(base))
+    if pair_of(slow) < 0:      # every pair turns less
+        return f / factor
     first = min(max(math.floor(pair_of(fast)), 0), dim // 2 - 1)
-    last = min(max(math.ceil(pair_of(slow)), 0), dim // 2 - 1)
+    last = min(math.ceil(pair_of(slow)), dim - 1)
     ramp = ((i - first) / max(last - first, 0.001)).clamp(0, 1)
     return f / factor * ramp + f * (1 - ramp)
 
