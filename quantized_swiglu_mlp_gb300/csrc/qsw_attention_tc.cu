@@ -431,8 +431,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           unpair(sums[1], c, d);
           sum += (a + b) + (c + d);
           tmem_st_wait();
-        } else if (lane == 0) {
-          mbar_arrive(&bar.p_half[tile]);
+        } else {
+          // (all lanes' zeros of V come before the products)
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar.p_half[tile]);
         }
         tc_fence_before();
         __syncwarp();

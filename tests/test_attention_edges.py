@@ -1,0 +1,39 @@
+"""Attention and its plan where a tile, a list or a type ends."""
+from __future__ import annotations
+
+import math
+
+import pytest
+import torch
+
+from quantized_swiglu_mlp_gb300 import ops
+from tests.test_attention_ops import Step, dev  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def poison_unseen(s, page_size, value):
+    """Everything in the cache but the sequences' own keys and values := value."""
+    k, v = s.k.clone(), s.v.clone()
+    s.k.fill_(value), s.v.fill_(value)
+    for b, total in enumerate(s.lengths):
+        p = torch.arange(total, device="cuda")
+        rows = s.table[b].long()[p // page_size], slice(None), p % page_size
+        s.k[rows], s.v[rows] = k[rows], v[rows]
+
+
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("tokens,group", [(5, 4), (17, 1), (4, 8), (9, 7)])
+@pytest.mark.parametrize("behind", [31, 36, 96])
+def test_warps_without_rows_take_out_what_lies_behind_the_end(tokens, group, D, value, behind):
+    """17 to 63 rows: some warps of a row tile have none, but all take out rows of V behind the
+    sequence's end, here among the last tile's first 64 keys.  Once alone, once as pairs of
+    kv heads among many sequences."""
+    for seqs in ([(tokens, 128 + behind)], [(tokens, 128 * (i % 3 + 1) + behind) for i in range(170)]):
+        s = Step(seqs, 2 * group, 2, D, 128, spare=3)
+        clean = s.check() if len(seqs) == 1 else s.attend()
+        poison_unseen(s, 128, value)
+        for _ in range(5):
+            assert torch.equal(s.attend(), clean)
+    ops.qsw_check_device_errors()
