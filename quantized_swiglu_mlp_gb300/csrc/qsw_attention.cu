@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     __syncthreads();
     most = __reduce_max_sync(0xffffffffu, sums[lane]);
     __syncthreads();
-    chunk[list] = most;
+    chunk[list] = max(most, 1);      // (no keys at all: it divides)
     if (p.max_splits == 1 || most <= kLeast) continue;
     const int parts = 1 + warp * (p.max_splits - 1) / 31;
     const int c = max((most + parts - 1) / parts, kLeast);

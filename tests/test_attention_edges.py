@@ -37,3 +37,20 @@ def test_warps_without_rows_take_out_what_lies_behind_the_end(tokens, group, D, 
         for _ in range(5):
             assert torch.equal(s.attend(), clean)
     ops.qsw_check_device_errors()
+
+
+@pytest.mark.parametrize("lengths", [[0, 0, 0], [-3, 0, -2 ** 31]])
+@pytest.mark.parametrize("group", [1, 4, 32])
+def test_tokens_without_any_key(group, lengths):
+    """Lengths of 0, as in a step captured before the first request, with a table wide enough to
+    split histories: positions and slots of nobody, and zeros in both lists."""
+    s = Step([(1, 900), (70, 900), (3, 900)], 2 * group, 2, 64, 16)
+    s.lengths = lengths
+    s.k.fill_(math.nan), s.v.fill_(math.nan)
+    p = s.plan()
+    assert (p.positions == -1).all() and (p.slots == -1).all()
+    # word 0 and 1: the items of both lists, one per row tile and kv head, nothing split
+    rows = [n * group for n in (1, 70, 3)]
+    items = p.work[:12].view(torch.int32).tolist()
+    assert items == [2 * sum(-(-r // 16) for r in rows if r <= 16), 2 * sum(-(-r // 256) for r in rows if r > 16), 0]
+    assert (s.attend(p) == 0).all()
