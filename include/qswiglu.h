@@ -479,7 +479,8 @@ QSW_API qsw_status qsw_paged_plan(const int *offsets, const int *lengths, int64_
 /*
  * out[t, h] = sum_j softmax_j(scale q[t, h] . k_j) v_j over the keys j that token t
  * sees: those of its sequence up to its own position (and within the window), of kv
- * head h / (heads / kv_heads).  out is [T, heads, D], contiguous.  A token that sees no key gets 0; rows
+ * head h / (heads / kv_heads).  out is [T, heads, D], contiguous, and
+ * shares no memory with q (refused) or the cache.  A token that sees no key gets 0; rows
  * of no sequence are left as they were.  A page that is not in the cache counts as
  * zeros; what a row does not see has no effect on it, infinities and NaN among them (a row
  * that comes out infinite or NaN for that reason is computed again key by key, with f32

@@ -51,6 +51,30 @@ qsw_status check_step(int64_t B, int64_t T, int64_t heads, int64_t max_pages, in
   return max_pages > (INT32_MAX - 1024) / c->page_size ? QSW_ERR_UNSUPPORTED : QSW_OK;
 }
 
+// Whether an element of the heads x [T, heads, D] lies in the `n` elements at p.
+bool heads_meet(const qsw_heads &x, int64_t T, int64_t heads, int64_t D, const void *p, int64_t n) {
+  using Wide = __int128;
+  const Wide off = (static_cast<Wide>(reinterpret_cast<uintptr_t>(x.data)) - reinterpret_cast<uintptr_t>(p)) / 2;
+  Wide ts = x.token_stride, hs = x.head_stride;
+  const Wide t_span = (T - 1) * ts, h_span = (heads - 1) * hs;
+  const Wide low = off + (t_span < 0 ? t_span : 0) + (h_span < 0 ? h_span : 0);
+  const Wide high = off + (t_span > 0 ? t_span : 0) + (h_span > 0 ? h_span : 0) + D;
+  if (low >= n || high <= 0) return false;
+  // tokens counted so that they ascend
+  const Wide first = off + (ts < 0 ? t_span : 0);
+  ts = ts < 0 ? -ts : ts;
+  for (int64_t h = 0; h < heads; ++h) {
+    // a token t with -D < at + t ts < n
+    const Wide at = first + h * hs;
+    if (at >= n) continue;
+    if (at > -D) return true;
+    if (ts == 0) continue;
+    const Wide t = (-D - at) / ts + 1;        // the first past -D
+    if (t < T && at + t * ts < n) return true;
+  }
+  return false;
+}
+
 }  // namespace
 
 extern "C" {
@@ -160,6 +184,10 @@ qsw_status qsw_paged_attention(const qsw_heads *q, const qsw_kv_cache *cache, co
   if (!aligned(q->data, 16) || !aligned(out, 16) || !aligned(plan, 16) || !aligned(page_table, 4) ||
       !aligned(workspace, 256) || q->token_stride % 8 || q->head_stride % 8)
     return QSW_ERR_UNSUPPORTED;
+  const int sms = qsw::device_sm_count();
+  if (sms <= 0) return QSW_ERR_CUDA;
+  // (a row of q may be read after another is written)
+  if (heads_meet(*q, T, heads, D, out, T * heads * D)) return QSW_ERR_INVALID_ARG;
   const size_t need =
       qsw_paged_attention_workspace_bytes(B, T, heads, cache->kv_heads, D, max_pages * cache->page_size);
   if (workspace_bytes < need || (need && !workspace)) return QSW_ERR_INVALID_ARG;
@@ -174,7 +202,7 @@ qsw_status qsw_paged_attention(const qsw_heads *q, const qsw_kv_cache *cache, co
   a.act = act_dtype;
   a.out = out;
   a.workspace = workspace;
-  const qsw_status r = from_cuda(qsw::launch_paged_attention(a, qsw::device_sm_count(), qsw::wait_timeout_ns(),
+  const qsw_status r = from_cuda(qsw::launch_paged_attention(a, sms, qsw::wait_timeout_ns(),
                                                              static_cast<cudaStream_t>(stream)));
   if (r == QSW_OK) qsw::count_call(QSW_CNT_PAGED_ATTENTION);
   return r;

@@ -716,7 +716,7 @@ def paged_attention(q, k_cache, v_cache, plan, scale=None, out=None, stream=None
 
     plan: paged_plan's result, made after the lengths and for caches of this shape.  Heads
     of q share kv heads in runs of heads / kv_heads.  scale: of the scores, D^-0.5 by
-    default.  Rows of no sequence are left as they are.
+    default.  Rows of no sequence are left as they are.  `out` must not share memory with q.
     """
     if not isinstance(plan, PagedPlan):
         raise TypeError("plan must be a PagedPlan")
