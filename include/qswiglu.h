@@ -433,7 +433,8 @@ typedef struct {
  * modulo 2^64: positions (int32, of either sign; NULL: all 0) of any size keep their
  * angle to 2^-23 rad.  rot is even, from 0 to D; D at most 1024, heads at most 4096.  Any
  * strides; 2-byte alignment (16-byte alignment of everything is faster).  out may be
- * x with the same strides.
+ * x with the same strides; else its rows share no memory with x's, nor with each other
+ * (refused, of rows at other strides than x's only the latter).
  */
 QSW_API qsw_status qsw_rope(const qsw_heads *x, int64_t T, int64_t heads, int64_t D, const int *positions,
                            const int64_t *table, int64_t rot, int interleaved, float scale, int act_dtype,
@@ -446,7 +447,8 @@ QSW_API qsw_status qsw_rope(const qsw_heads *x, int64_t T, int64_t heads, int64_
  * below 0 or past the cache is not written; a token at a negative position is left
  * out altogether, its row of q_out included.  Slots of two tokens should differ (else
  * the row is of either, or of parts of both).  The cache's alignment as stated there;
- * q, k, v and q_out as in qsw_rope; q_out may be q with the same strides.
+ * q, k, v and q_out as in qsw_rope; q_out may be q with the same strides, and is refused where
+ * qsw_rope refuses it.
  */
 QSW_API qsw_status qsw_kv_append(const qsw_heads *q, const qsw_heads *k, const qsw_heads *v, int64_t T, int64_t heads,
                                 int64_t D, const int *slots, const int *positions, const int64_t *table,

@@ -75,6 +75,40 @@ bool heads_meet(const qsw_heads &x, int64_t T, int64_t heads, int64_t D, const v
   return false;
 }
 
+// Whether rows of heads [T, heads, D] share memory with each other (off 0), or with those of a
+// tensor of the same strides `off` elements on.  (Differences of rows are of either sign: so may
+// the strides be.)
+bool rows_meet(int64_t T, int64_t heads, int64_t D, int64_t token_stride, int64_t head_stride, __int128 off) {
+  using Wide = __int128;
+  const auto size = [](Wide x) { return x < 0 ? -x : x; };
+  const Wide ts = T == 1 ? 0 : size(token_stride), hs = heads == 1 ? 0 : size(head_stride);
+  const Wide t_span = (T - 1) * ts, h_span = (heads - 1) * hs;
+  if (off == 0) {
+    // the usual: a token's heads one after the other, or a head's tokens
+    if ((heads == 1 || hs >= D) && (T == 1 || ts >= h_span + D)) return false;
+    if ((T == 1 || ts >= D) && (heads == 1 || hs >= t_span + D)) return false;
+    if (T > 1 && ts < D) return true;
+  } else if (size(off) >= t_span + h_span + D) {
+    return false;
+  }
+  for (int64_t dh = off == 0 ? 1 : 1 - heads; dh < heads; ++dh) {
+    // rows `dh` heads apart, and the number of tokens that brings them closest, or one more
+    const Wide at = size(off + dh * hs);
+    Wide dt = ts ? at / ts : 0;
+    dt = dt < T ? dt : T - 1;
+    if (at - dt * ts < D || (dt + 1 < T && (dt + 1) * ts - at < D)) return true;
+  }
+  return false;
+}
+// Whether `out` may take the heads of x: rows of its own, and either x's or none that meet them.
+bool output_ok(const qsw_heads &x, int64_t T, int64_t heads, int64_t D, const void *out, int64_t token_stride,
+               int64_t head_stride) {
+  if (rows_meet(T, heads, D, token_stride, head_stride, 0)) return false;
+  const bool alike = (T == 1 || token_stride == x.token_stride) && (heads == 1 || head_stride == x.head_stride);
+  const __int128 off = static_cast<__int128>(reinterpret_cast<uintptr_t>(out)) - reinterpret_cast<uintptr_t>(x.data);
+  return !alike || off == 0 || !rows_meet(T, heads, D, token_stride, head_stride, off / 2);
+}
+
 }  // namespace
 
 extern "C" {
@@ -89,6 +123,7 @@ qsw_status qsw_rope(const qsw_heads *x, int64_t T, int64_t heads, int64_t D, con
   if (T == 0) return QSW_OK;
   if (!x->data || !out) return QSW_ERR_INVALID_ARG;
   if (!aligned(x->data, 2) || !aligned(out, 2) || !aligned(positions, 4)) return QSW_ERR_UNSUPPORTED;
+  if (!output_ok(*x, T, heads, D, out, out_token_stride, out_head_stride)) return QSW_ERR_INVALID_ARG;
   qsw::RopeArgs a = {};
   a.q = *x;
   a.T = T, a.heads = heads, a.D = D, a.rot = rot;
@@ -117,6 +152,7 @@ qsw_status qsw_kv_append(const qsw_heads *q, const qsw_heads *k, const qsw_heads
   if (!aligned(k->data, 2) || !aligned(v->data, 2) || !aligned(slots, 4) || !aligned(positions, 4) ||
       (q && (!aligned(q->data, 2) || !aligned(q_out, 2))))
     return QSW_ERR_UNSUPPORTED;
+  if (q && !output_ok(*q, T, heads, D, q_out, q_out_token_stride, q_out_head_stride)) return QSW_ERR_INVALID_ARG;
   qsw::RopeArgs a = {};
   if (q) {
     a.q = *q;

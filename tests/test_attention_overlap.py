@@ -80,3 +80,33 @@ def test_attention_into_the_room_between_its_queries(order):
         assert torch.equal(q, s.q)
         if free:
             assert torch.equal(buf[at:at + size].view(T, heads, D), want)
+
+
+def test_outputs_whose_rows_share_memory_are_refused():
+    """Expanded outputs of rope and kv_append, and those that cover other rows of the input;
+    the input's own place and its neighbours in one buffer are fine."""
+    T, H, D = 5, 3, 64
+    x = randn(1, T, H, D)
+    table = ops.rope_table(ops.rope_frequencies(D))
+    pos = ints(range(T))
+    want = ops.rope(x, pos, table)
+    kc, vc = (torch.zeros(2, H, 8, D, dtype=BF16, device="cuda") for _ in range(2))
+
+    def into(x, out):
+        return (lambda: ops.rope(x, pos, table, out=out),
+                lambda: ops.kv_append(x, x, kc, vc, pos, pos, table, q=x, q_out=out))
+    buf = torch.zeros(T + 1, 2 * H, D, dtype=BF16, device="cuda")
+    view = buf[:T, :H]
+    view.copy_(x)
+    for source, out in ((x, torch.zeros(T, 1, D, dtype=BF16, device="cuda").expand(T, H, D)),
+                        (x, torch.zeros(1, H, D, dtype=BF16, device="cuda").expand(T, H, D)),
+                        (view, buf[1:, :H]), (view, buf[:T, 1:H + 1])):
+        for call in into(source, out):
+            with pytest.raises(ops.QswError):
+                call()
+    assert torch.equal(view, x)
+    for out in (buf[:T, H:], view):
+        for call in into(view, out):
+            view.copy_(x)
+            call()
+            assert torch.equal(out, want)
