@@ -23,7 +23,8 @@ LIB_PATH = os.path.join(OUT_DIR, "libqswiglu.so")
 SOURCES = ["qsw_api.cu", "qsw_gemv.cu", "qsw_gemv_stream.cu", "qsw_prefill.cu", "qsw_elementwise.cu",
            "qsw_block_api.cu", "qsw_fp4.cu", "qsw_fp4_gemm.cu", "qsw_moe.cu", "qsw_norm.cu",
            "qsw_attention_api.cu", "qsw_rope.cu", "qsw_attention.cu", "qsw_attention_tc.cu"]
-HEADERS = ["qsw_device.cuh", "qsw_smallm.cuh", "qsw_fp4.cuh", "qsw_tiles.h", "qsw_attention.cuh", "qsw_internal.h"]
+HEADERS = ["qsw_device.cuh", "qsw_smallm.cuh", "qsw_fp4.cuh", "qsw_tiles.h", "qsw_attention.cuh", "qsw_internal.h",
+           "qsw_once.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

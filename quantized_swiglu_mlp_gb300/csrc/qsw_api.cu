@@ -7,7 +7,6 @@
 // 32, H a multiple of 32, gate and up specs independent.
 #include <atomic>
 #include <cstdlib>
-#include <mutex>
 
 #include "qswiglu.h"
 #include "qsw_device.cuh"
@@ -43,16 +42,13 @@ int gemv_max_m() {
 }
 
 int sm_count() {
-  static int counts[64];
-  static std::once_flag flags[64];
+  static std::atomic<int> counts[64];      // 0: not known yet
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-  std::call_once(flags[dev], [dev] {
-    int n = 0;
-    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-    counts[dev] = n;
-  });
-  return counts[dev];
+  int n = counts[dev].load(std::memory_order_relaxed);
+  if (n == 0 && cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess)
+    counts[dev].store(n, std::memory_order_relaxed);
+  return n;
 }
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }

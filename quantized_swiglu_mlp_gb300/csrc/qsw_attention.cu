@@ -665,7 +665,7 @@ cudaError_t launch_join(const AttnParams &p, int num_sms, cudaStream_t stream) {
 template <class A, int DP>
 cudaError_t launch_rows_form(const AttnParams &p, const ListForm &f, const qsw_kv_cache &cache, cudaStream_t stream) {
   constexpr int bytes = kRowWarps * kRowStages * kRowStageBytes + 1024;
-  static SmemOnce once;
+  static DeviceOnce once;
   auto kernel = attn_rows_kernel<A, DP>;
   const cudaError_t e = allow_smem(once, kernel, bytes);
   if (e != cudaSuccess) return e;

@@ -11,10 +11,10 @@
 #pragma once
 
 #include <climits>
-#include <mutex>
 
 #include "qsw_fp4.cuh"
 #include "qsw_internal.h"
+#include "qsw_once.h"
 
 namespace qsw {
 
@@ -304,20 +304,10 @@ __device__ __forceinline__ void tma_load_5d(void *dst, const CUtensorMap *map, u
 }
 
 // A kernel's shared memory, allowed once per device: `once` belongs to the kernel.
-struct SmemOnce {
-  std::once_flag flag[64];
-  cudaError_t error[64];
-};
 template <class K>
-cudaError_t allow_smem(SmemOnce &once, K kernel, int bytes) {
-  int dev = 0;
-  const cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  std::call_once(once.flag[dev], [&] {
-    once.error[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  });
-  return once.error[dev];
+cudaError_t allow_smem(DeviceOnce &once, K kernel, int bytes) {
+  return once_per_device(once,
+                         [&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes); });
 }
 
 // One thread of a converged warp.  Copies are issued by a thread chosen this way, with

@@ -716,26 +716,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                   const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void *ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(ptr);
-  });
-  return fn;
-}
-
 bool encode_cache(CUtensorMap *map, const void *base, const int64_t (&strides)[3], const qsw_kv_cache &c, int64_t D,
                   int act, int box, int halves) {
-  EncodeTiledFn fn = encode_fn();
+  const EncodeTiledFn fn = encode_tiled_fn();
   if (!fn) return false;
   const cuuint64_t dims[5] = {static_cast<cuuint64_t>(halves > 1 ? 64 : D), static_cast<cuuint64_t>(c.page_size),
                               static_cast<cuuint64_t>(halves), static_cast<cuuint64_t>(c.kv_heads),
@@ -752,7 +735,7 @@ bool encode_cache(CUtensorMap *map, const void *base, const int64_t (&strides)[3
 
 template <class A, int DP>
 cudaError_t launch_shape(const AttnParams &p, const CacheMaps &maps, int grid, cudaStream_t stream) {
-  static SmemOnce once;
+  static DeviceOnce once;
   auto kernel = attn_tiles_kernel<A, DP>;
   const cudaError_t e = allow_smem(once, kernel, Shape<DP>::kSmem);
   return e != cudaSuccess ? e : launch_on(kernel, dim3(static_cast<unsigned>(grid)), kThreads, Shape<DP>::kSmem, stream,

@@ -38,11 +38,11 @@
 // complete before the launch in front of this one began (each kernel of a chain
 // lets the next one start only after its own wait).
 #include <atomic>
-#include <mutex>
 #include <type_traits>
 
 #include "qsw_fp4.cuh"
 #include "qsw_internal.h"
+#include "qsw_once.h"
 #include "qsw_tiles.h"
 
 namespace qsw {
@@ -969,27 +969,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // -------------------------------------------------------------------- host --
 
-using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                   const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void *ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(ptr);
-  });
-  return fn;
-}
-
 // Codes [rows, K/2] bytes, boxes of 128 bytes by `box` rows, 128-byte swizzle.
 bool encode_codes(CUtensorMap *map, const void *base, int64_t rows, int64_t K, int box) {
-  EncodeTiledFn fn = encode_fn();
+  const EncodeTiledFn fn = encode_tiled_fn();
   if (!fn) return false;
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K / 2), static_cast<cuuint64_t>(rows)};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(K / 2)};
@@ -1020,7 +1002,7 @@ int align_up(int v, int a) { return (v + a - 1) / a * a; }
 // Scale blocks [row blocks, k blocks] of 512 bytes as 128 words each; a box is a
 // stage's blocks of `rows` row blocks.
 bool encode_scales(CUtensorMap *map, const void *base, int64_t row_blocks, int64_t k_blocks, int per_stage, int rows) {
-  EncodeTiledFn fn = encode_fn();
+  const EncodeTiledFn fn = encode_tiled_fn();
   if (!fn) return false;
   const cuuint64_t dims[3] = {kSfBytes / 4, static_cast<cuuint64_t>(k_blocks), static_cast<cuuint64_t>(row_blocks)};
   const cuuint64_t strides[2] = {kSfBytes, static_cast<cuuint64_t>(k_blocks) * kSfBytes};
@@ -1036,16 +1018,11 @@ cudaError_t launch_gemm(const Fp4GemmArgs &a, GemmParams p, int num_sms, cudaStr
   constexpr int kSfPerStage = kStageK / Fp4<FMT>::kSfK;
   constexpr bool PAIR = MODE == PAIRED;
   auto *kernel = fp4_gemm_kernel<A, FMT, SWIGLU, MODE>;
-  static std::once_flag once[64];
-  static cudaError_t attr[64];
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  std::call_once(once[dev], [&] {
-    attr[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
+  static DeviceOnce once;
+  cudaError_t e = once_per_device(once, [&] {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
   });
-  if (attr[dev] != cudaSuccess) return attr[dev];
+  if (e != cudaSuccess) return e;
 
   // shared memory: x stages, weight stages, scale stages, exchange buffers,
   // tile records, group table
