@@ -488,7 +488,7 @@ QSW_API qsw_status qsw_paged_plan(const int *offsets, const int *lengths, int64_
  * that comes out infinite or NaN for that reason is computed again key by key, with f32
  * weights).
  * Statistics and sums in f32, the weights rounded to the activation dtype before they
- * meet v; long histories are split over CTAs and joined in f32 in a fixed order: the same bits
+ * meet v (half a step of each, in f16 and below that 2^-32 of the row's largest); long histories are split over CTAs and joined in f32 in a fixed order: the same bits
  * every time.  scale > 0.  workspace: qsw_paged_attention_workspace_bytes(...) bytes
  * (max_len = max_pages * page_size), 256-byte aligned (0 bytes: may be NULL); it need not be cleared, and calls that can
  * run concurrently must not share it.  q, out: 16-byte aligned, as are q's strides.

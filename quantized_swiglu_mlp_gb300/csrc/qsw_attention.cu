@@ -225,6 +225,7 @@ constexpr int kRowWarps = 4;       // each with keys of its own
 // Keys of a warp's step: 8 KB of K and V.  32 take a warp little longer than 16 (its softmax is mostly
 // latency), but of 128 columns two CTAs then no longer fit on an SM.
 constexpr int step_keys(int DP) { return DP == 128 ? 16 : 32; }
+constexpr float kRowLift = 14.0f;
 constexpr int kRowStages = 3;      // 96 KB of ring a CTA: two on an SM
 constexpr int kRowStageBytes = 8192;
 
@@ -442,7 +443,7 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2)
       for (int h = 0; h < 2; ++h) {
         top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 1));
         top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 2));
-        const float now = fmaxf(m[h], top[h]);
+        const float now = fmaxf(m[h], top[h] - lift_of<A>(top[h], kRowLift));
         base[h] = now == -INFINITY ? 0.0f : now;       // nothing seen yet
         shrink[h] = ex2(m[h] - base[h]);
         m[h] = now;
@@ -456,8 +457,9 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2)
           s[n][x] = ex2(s[n][x] - base[x >> 1]);
           l[x >> 1] += s[n][x];
         }
-        // weights as the products take them: rounded to the activations' type (one part in
-        // 256 for bf16, of either sign); the sum l is that of the f32 weights
+        // weights as the products take them: rounded to the activations' type (half a step, 2^-8
+        // of a weight in bf16, 2^-11 in f16, of either sign, and in f16 2^-39 of the largest); the sum l is that
+        // of the f32 weights
         a[n / 2][2 * (n & 1)] = A::pack2(s[n][0], s[n][1]);
         a[n / 2][2 * (n & 1) + 1] = A::pack2(s[n][2], s[n][3]);
       }

@@ -156,6 +156,16 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// The softmax weights as the products take them are f16 or bf16.  f16 has 5 bits of exponent: weights
+// of up to 1 would lose bits below 2^-14 and vanish below 2^-25, though many of them may lie behind
+// one large one.  There a row's base lies `lift` below its maximum, and weights reach 2^lift: what
+// they are off by is then at most 2^-(25 + lift) of the largest, each.  (Not where scores are
+// so far from 0 that the difference would be rounded.)
+template <class A>
+__device__ __forceinline__ float lift_of(float top, float lift) {
+  return A::kId != 0 && fabsf(top) < 0x1p20f ? lift : 0.0f;
+}
+
 // Page of a sequence's tokens [page * page_size, ..) as the table has it, and as it is used: -1
 // where it is not in the cache.  (Apart, so that a copy's page can be asked for ahead.)
 __device__ __forceinline__ int page_entry(const AttnParams &p, int b, int page) {

@@ -22,7 +22,8 @@
 // read K and V twice as often.)
 //
 // The base of a row is raised (and O rescaled in tensor memory) only when a score passes
-// it by 8, so that weights reach 256 at most and most tiles leave O alone.
+// it by 8, so that weights reach 256 at most and most tiles leave O alone; in f16 it lies 7 below the
+// score that raised it and weights reach 2^15.
 #include <type_traits>
 
 #include "qsw_attention.cuh"
@@ -39,7 +40,7 @@ constexpr int kThreads = 384;
 constexpr int kWarpMma = 8, kWarpK = 9, kWarpV = 10, kWarpItems = 11;
 constexpr int kItems = 4;             // items worked out ahead
 constexpr int kItemReaders = 11;      // warps that read them
-constexpr float kRaise = 8.0f;
+constexpr float kRaise = 8.0f, kTileLift = 7.0f;
 
 template <int DP>
 struct Shape {
@@ -384,9 +385,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           top[0] = max3(top[0], s[124], s[125]);
           top[1] = max3(top[1], s[126], s[127]);
           const float most = fmaxf(max3(top[0], top[1], top[2]), top[3]) * scale;
-          const bool raise = most > base + kRaise;
+          const float lift = lift_of<A>(most, kTileLift);
+          const bool raise = most - base > kRaise + lift;      // (false between infinities of one sign)
           if (__any_sync(0xffffffffu, raise)) {
-            const float now = raise ? most : base;
+            const float now = raise ? most - lift : base;
             const float shrink = raise ? ex2(base - now) : 1.0f;
             base = now;
             sum *= shrink;

@@ -54,3 +54,35 @@ def test_tokens_without_any_key(group, lengths):
     items = p.work[:12].view(torch.int32).tolist()
     assert items == [2 * sum(-(-r // 16) for r in rows if r <= 16), 2 * sum(-(-r // 256) for r in rows if r > 16), 0]
     assert (s.attend(p) == 0).all()
+
+
+@pytest.mark.parametrize("dt", [torch.float16, torch.bfloat16], ids=["f16", "bf16"])
+@pytest.mark.parametrize("tokens", [1, 3, 9], ids=["few", "twelve", "tile"])
+@pytest.mark.parametrize("late", [False, True], ids=["first", "last"])
+@pytest.mark.parametrize("score,keys", [(12, 250), (15, 250), (18, 250), (12, 40000), (18, 1 << 18), (20, 1 << 20)])
+def test_a_long_tail_behind_one_large_weight(dt, tokens, late, score, keys):
+    """One key with nearly all the weight and a value of 0, and many with e^-score of it each and
+    a value of 1024: what is left is their sum, though in f16 each would be below 2^-14 or 0."""
+    D, group, value = 64, 4, 1024
+    s = Step([(tokens, keys)], group, 1, D, 256, dt=dt)
+    s.q.zero_(), s.k.zero_()
+    s.q[..., 0] = 8.0
+    s.v.fill_(value)
+    at = keys - tokens if late else 0         # (every token sees it)
+    row = int(s.table[0, at // 256]), 0, at % 256
+    s.k[row + (0,)] = float(score)            # 8 score / 8
+    s.v[row] = 0.0
+    got = s.attend().double()
+    n = torch.arange(keys - tokens, keys, device="cuda").double()      # keys seen but the large one
+    tail = n * math.exp(-score)
+    want = (value * tail / (1 + tail))[:, None, None].expand_as(got)
+    half = {torch.float16: 2.0 ** -11, torch.bfloat16: 2.0 ** -8}[dt]
+    # scores are exact but for their factors' rounding (scale log2 e, and the product: 2^-23 of it, times
+    # ln 2 and a weight); weights: half a step, the exponential's 2^-21, and in f16 half of the smallest step
+    # 2^-24 against weights of 2^14 (few rows) or 2^7 (tiles) for the large one; f32 sums of
+    # up to 2^20 equal terms, 128 or 64 at a time: 2^-24 (n / 64 + 70) of them; the end's half step
+    rel = 2.0 ** -22 * score + half + 2.0 ** -21 + 2.0 ** -24 * (keys / 64 + 70) + half
+    least = 0.0 if dt != torch.float16 else 2.0 ** -25 * (2.0 ** -14 if tokens * group <= 16 else 2.0 ** -7)
+    err = (got - want).abs()
+    bound = want * rel + least * value * n[:, None, None]
+    assert (err <= bound).all(), (float(err.max()), float((err / bound).max()))
