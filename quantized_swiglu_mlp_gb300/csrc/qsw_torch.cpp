@@ -9,6 +9,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -368,6 +369,17 @@ PyObject *post_norm(Args a) {
   return r;
 }
 
+// The attention's operators have no derivatives: a tensor that autograd would follow is
+// refused instead of cut off.
+void check_no_grad(const at::Tensor &t, const char *name) {
+  if (c10::GradMode::is_enabled() && t.requires_grad())
+    fail(PyExc_RuntimeError, "%s requires grad, and this operator has no derivative; detach it or use torch.no_grad()", name);
+}
+// What a call has written: autograd then knows that a value saved before is gone.
+void written(const at::Tensor &t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 // Heads [T, heads, D] of an activation type, a head's elements contiguous.
 const at::Tensor &heads_of(PyObject *o, const char *name, const at::Tensor *like) {
   const at::Tensor &t = tensor(o, name);
@@ -376,6 +388,7 @@ const at::Tensor &heads_of(PyObject *o, const char *name, const at::Tensor *like
   if (like && t.device() != like->device()) fail(PyExc_ValueError, "%s is on another device", name);
   if (t.dim() != 3) fail(PyExc_ValueError, "%s must be [tokens, heads, head_dim]", name);
   if (t.size(2) > 1 && t.stride(2) != 1) fail(PyExc_ValueError, "%s must have contiguous heads", name);
+  check_no_grad(t, name);
   return t;
 }
 // The stride of dimension d, for one of a single element that of a dense tensor.
@@ -399,6 +412,8 @@ qsw_kv_cache cache_arg(PyObject *ko, PyObject *vo, const at::Tensor *like) {
     fail(PyExc_ValueError, "%s and v_cache must be [pages, kv_heads, page_size, head_dim]", "k_cache");
   if (k.size(3) > 1 && (k.stride(3) != 1 || v.stride(3) != 1))
     fail(PyExc_ValueError, "%s and v_cache must have contiguous rows", "k_cache");
+  check_no_grad(k, "k_cache");
+  check_no_grad(v, "v_cache");
   qsw_kv_cache c = {data(k), data(v), k.size(0), k.size(1), k.size(2), {}, {}};
   for (int i = 0; i < 3; ++i) {
     c.k_strides[i] = step_of(k, i);
@@ -445,6 +460,7 @@ PyObject *rope(Args a) {
                g_fn.qsw_rope_(&in, heads ? T : 0, heads ? heads : 1, D, r.positions, r.table, r.rot, truth(a[3]),
                               number(a[4]), act_code(x.scalar_type()), data(out), step_of(out, 0), step_of(out, 1),
                               current_stream(x)));
+  written(out);
   return wrap(std::move(out));
 }
 
@@ -477,7 +493,10 @@ PyObject *kv_append(Args a) {
                                    truth(a[8]), number(a[9]), act_code(k.scalar_type()), &cache,
                                    heads ? data(q_out) : nullptr, heads ? step_of(q_out, 0) : 0,
                                    heads ? step_of(q_out, 1) : 0, current_stream(k)));
+  written(kc);
+  written(THPVariable_Unpack(a[3]));
   if (!heads) Py_RETURN_NONE;
+  written(q_out);
   return wrap(std::move(q_out));
 }
 
@@ -534,6 +553,7 @@ PyObject *paged_attention(Args a) {
     fail(PyExc_ValueError, "%s was made for other sizes", "plan");
   c10::cuda::CUDAGuard guard(q.device());
   at::Tensor out = output(a[13], "out", q.sizes(), q.scalar_type(), q);
+  check_no_grad(out, "out");
   const size_t bytes = g_fn.qsw_paged_attention_workspace_bytes_(B, T, heads, cache.kv_heads, D,
                                                                   table.size(1) * cache.page_size);
   at::Tensor ws;
@@ -544,6 +564,7 @@ PyObject *paged_attention(Args a) {
                                          data(plan), B, T, heads, D, integer(a[7]), number(a[12]),
                                          act_code(q.scalar_type()), data(out), bytes ? data(ws) : nullptr, bytes,
                                          current_stream(q)));
+  written(out);
   return wrap(std::move(out));
 }
 

@@ -594,7 +594,8 @@ def post_norm(h, y, weight=None, gate=None, scale=1.0, next_weight=None, eps=1e-
 
 # ------------------------------------------------------------------------
 # The attention half of a block: rotary positions, a paged cache, attention of new
-# tokens over it.  Layouts and formulas: include/qswiglu.h.
+# tokens over it.  Layouts and formulas: include/qswiglu.h.  For inference: tensors that
+# require grad are refused while autograd records.
 # ------------------------------------------------------------------------
 
 def rope_frequencies(dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
