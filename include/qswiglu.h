@@ -484,9 +484,7 @@ QSW_API qsw_status qsw_paged_plan(const int *offsets, const int *lengths, int64_
  * head h / (heads / kv_heads).  out is [T, heads, D], contiguous, and
  * shares no memory with q (refused) or the cache.  A token that sees no key gets 0; rows
  * of no sequence are left as they were.  A page that is not in the cache counts as
- * zeros; what a row does not see has no effect on it, infinities and NaN among them (a row
- * that comes out infinite or NaN for that reason is computed again key by key, with f32
- * weights).
+ * zeros; what a row does not see has no effect on any bit of it, infinities and NaN among it.
  * Statistics and sums in f32, the weights rounded to the activation dtype before they
  * meet v (half a step of each, in f16 and below that 2^-32 of the row's largest); long histories are split over CTAs and joined in f32 in a fixed order: the same bits
  * every time.  scale > 0.  workspace: qsw_paged_attention_workspace_bytes(...) bytes

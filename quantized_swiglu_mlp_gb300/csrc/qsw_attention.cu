@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2)
   uint8_t *ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   __shared__ float warp_m[kRowWarps][16], warp_l[kRowWarps][16];
   __shared__ uint64_t full[kRowWarps][kRowStages];
-  __shared__ unsigned redo;
+  __shared__ int redo;           // values were taken out of V
   __shared__ int abort_word;
   volatile int *abort_flag = &abort_word;
   unsigned int *err = &g_rows_error;
@@ -397,19 +397,27 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2)
 #pragma unroll
       for (int j = 0; j < 4; ++j) o[i][j] = 0.0f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+    bool odd = false;
     for (int i = 0; i < my_runs; ++i) {
       const uint32_t slot = used % kRowStages;
       if (!(ok = ok && wait_all(&full[warp][slot], (used / kRowStages) & 1, abort_flag, p.timeout_ns, err))) break;
       uint8_t *stage = mine + slot * STAGE;
       const int run0 = t.k0 + (i * kRowWarps + warp) * KEYS;
-      if (run0 + KEYS > t.k1 || run0 < t.first) {
-        // rows of V that no row of the item sees may hold anything: a weight of 0 does not take out
-        // infinities or NaN
-        for (int x = lane; x < KEYS * (DP / 8); x += 32) {
-          const int j = x / (DP / 8), c = x % (DP / 8);
-          if (run0 + j >= t.k1 || run0 + j < t.first)
-            *reinterpret_cast<uint4 *>(stage + STAGE / 2 + row_at(j) + (c >> 3) * half_bytes + (c & 7) * 16) =
-                make_uint4(0, 0, 0, 0);
+      if (!all_seen(t, run0, KEYS)) {
+        // rows of V that no row of the item sees, or not every one, may hold anything: a weight of 0 does
+        // not take out infinities or NaN
+        // (rows before those that all see, and behind them)
+        const int from = min(max(max(t.first, t.all_lo) - run0, 0), KEYS);
+        const int to = min(max(min(t.k1, t.all_hi) - run0, from), KEYS);
+        for (int x = lane; x < (KEYS - to + from) * (DP / 8); x += 32) {
+          const int i = x / (DP / 8), c = x % (DP / 8), j = i < from ? i : i + to - from;
+          auto *at = reinterpret_cast<uint4 *>(stage + STAGE / 2 + row_at(j) + (c >> 3) * half_bytes + (c & 7) * 16);
+          const bool seen = run0 + j < t.k1 && run0 + j >= t.first;
+          const uint4 v = *at;
+          if (!seen || Odd<A>::of(v)) {
+            *at = seen ? Odd<A>::without(v) : make_uint4(0, 0, 0, 0);
+            odd |= seen;
+          }
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -497,6 +505,7 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2)
     }
     __syncthreads();
     if (*abort_flag) break;
+    if (odd) redo = 1;
     // the warps' sums, in the rings' place
     constexpr int PITCH = DP + 4;
     float *sum = reinterpret_cast<float *>(ring);
@@ -517,7 +526,6 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2)
     // a row to 8 threads, 8 columns at a time
     const int r = tid / 8;
     fence_proxy_async_smem();      // (the next copies overwrite the sums)
-    bool finite = true;        // or rightly not
     if (r < t.rows) {
       float top = warp_m[0][r];
 #pragma unroll
@@ -542,7 +550,6 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2)
 #pragma unroll
           for (int w = 0; w < kRowWarps; ++w) v = fmaf(f[w], sum[(w * 16 + r) * PITCH + c + x], v);
           y[x] = v * inv;
-          finite &= isfinite(y[x]) != 0;
         }
         if (t.s.splits > 1) {
           float4 *dst = reinterpret_cast<float4 *>(p.part + part * p.D + c);
@@ -553,15 +560,12 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2)
               make_uint4(A::pack2(y[0], y[1]), A::pack2(y[2], y[3]), A::pack2(y[4], y[5]), A::pack2(y[6], y[7]));
         }
       }
-      finite |= all != all;
       if (t.s.splits > 1 && (tid & 7) == 0) p.part_lse[part] = all == 0.0f ? -INFINITY : base + __log2f(all);
     }
-    if (!finite) atomicOr(&redo, 1u << r);
-    __syncthreads();
-    for (unsigned again = redo; again; again &= again - 1) {
-      const int x = __ffs(again) - 1;
-      if (x % kRowWarps == warp) exact_row<A>(p, t, t.head, x);
-    }
+    // (a warp's rows are those it has written)
+    constexpr int kOfWarp = 16 / kRowWarps;
+    if (redo && t.rows > warp * kOfWarp)
+      add_odd<A>(p, t, t.head, warp * kOfWarp, min(t.rows - warp * kOfWarp, kOfWarp));
   }
   // given up: the copies in flight
   if (*abort_flag)

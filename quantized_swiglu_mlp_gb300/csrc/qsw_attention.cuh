@@ -74,11 +74,11 @@ struct AttnParams {
 };
 
 // One item: rows [row0, row0 + rows) (token * group + head in the group) of a sequence's
-// kv head, keys [k0, k1), of which no row sees those before `first`.  A pair: the same rows
-// of two kv heads, head and head + 1.
+// kv head, keys [k0, k1), of which no row sees those before `first`, and all rows see those of
+// [all_lo, all_hi).  A pair: the same rows of two kv heads, head and head + 1.
 struct Item {
   SeqRec s;
-  int b, head, row0, rows, k0, k1, first, split, pair;
+  int b, head, row0, rows, k0, k1, first, all_lo, all_hi, split, pair;
 };
 
 // First and last + 1 key that the tokens [a, b) of a sequence see.
@@ -130,7 +130,10 @@ __device__ __forceinline__ Item find_item(const AttnParams &p, int id) {
   t.row0 = block * p.tile_rows;
   t.rows = min(p.tile_rows, t.s.n * p.group - t.row0);
   int end;
-  seen_keys(t.s, t.row0 / p.group, (t.row0 + t.rows - 1) / p.group + 1, p.window, t.first, end);
+  const int from = t.row0 / p.group, to = (t.row0 + t.rows - 1) / p.group;
+  seen_keys(t.s, from, to + 1, p.window, t.first, end);
+  t.all_lo = p.window ? t.s.len - t.s.n + to - p.window + 1 : 0;
+  t.all_hi = t.s.len - t.s.n + from + 1;
   const int start = t.first / p.tile_keys * p.tile_keys;
   // (64 bits: the last split's end)
   t.k0 = static_cast<int>(min(static_cast<int64_t>(start) + static_cast<int64_t>(t.split) * t.s.chunk,
@@ -176,106 +179,107 @@ __device__ __forceinline__ int page_of(const AttnParams &p, int b, int page) {
   return checked_page(p, page_entry(p, b, page));
 }
 
-// Row r of an item and kv head by one warp, key by key with what the row does not see left
-// out, for rows that came out infinite or NaN although the sum of their weights is a number (a
-// NaN among the scores makes the sum NaN, and the row rightly so): in the tiles a masked key
-// has the weight 0, and 0 * inf is NaN.  Only where such a key of the tiles has a value that
-// is not finite; else what the row sees made it so.  Slow, a key at a time.
+// Values that are infinite or NaN.  Of a key that some rows of an item see and others do not, the
+// products would give the others 0 * inf = NaN.  Such values are taken out of the tile of V, and
+// add_odd gives them to the rows that see them: who does not keeps every bit, and only those keys,
+// as many as an item has tokens (twice, with a window), are looked through.
 template <class A>
-__device__ __noinline__ void exact_row(const AttnParams &p, const Item &t, int kv_head, int r) {
+struct Odd {
+  static constexpr uint32_t kExp = A::kId == 0 ? 0x7F807F80u : 0x7C007C00u;       // of two values
+  static constexpr uint32_t kLeast = A::kId == 0 ? 0x00800080u : 0x04000400u;
+  // The sign bit of each that is odd: an exponent of all ones carries into it.
+  static __device__ __forceinline__ uint32_t of(uint32_t x) { return ((x & kExp) + kLeast) & 0x80008000u; }
+  static __device__ __forceinline__ uint32_t of(const uint4 &x) { return of(x.x) | of(x.y) | of(x.z) | of(x.w); }
+  // Adds 0 times each: odd where one of them is.  (An instruction a pair, instead of three.)
+  static __device__ __forceinline__ void gather(uint32_t x, uint32_t &sum) {
+    if constexpr (A::kId == 0)
+      asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(sum) : "r"(x), "r"(0u));
+    else
+      asm("fma.rn.f16x2 %0, %1, %2, %0;" : "+r"(sum) : "r"(x), "r"(0u));
+  }
+  static __device__ __forceinline__ void gather(const uint4 &x, uint32_t (&sum)[2]) {
+    gather(x.x, sum[0]), gather(x.y, sum[1]), gather(x.z, sum[0]), gather(x.w, sum[1]);
+  }
+  static __device__ __forceinline__ uint32_t without(uint32_t x) { return x & ~((of(x) >> 15) * 0xFFFFu); }
+  static __device__ __forceinline__ uint4 without(const uint4 &x) {
+    return make_uint4(without(x.x), without(x.y), without(x.z), without(x.w));
+  }
+};
+
+// Whether all rows of the item see the keys [key, key + n).
+__device__ __forceinline__ bool all_seen(const Item &t, int key, int n) {
+  return key >= max(t.first, t.all_lo) && key + n <= min(t.k1, t.all_hi);
+}
+
+// Adds the odd values of the keys that not all rows of an item see to its rows [row0, row0 +
+// rows), at most 32, a lane each, once the warp has written them.
+template <class A>
+__device__ __noinline__ void add_odd(const AttnParams &p, const Item &t, int kv_head, int row0, int rows) {
   const int lane = static_cast<int>(lane_id());
   int64_t token;
   int head, pos;
-  row_of(p, t, kv_head, r, token, head, pos);
-  const int begin = max(t.k0, t.first);          // of what the tiles hold: the rest of V is zeros there
-  const int lo = max(begin, p.window ? pos - p.window + 1 : 0), hi = max(min(t.k1, pos + 1), lo);
+  row_of(p, t, kv_head, row0 + (lane < rows ? lane : 0), token, head, pos);
   const uint16_t *q = p.q + token * p.q_t + head * p.q_h;
-  const int unseen = (lo - begin) + (t.k1 - hi);
-  bool odd = false;
-  for (int i = lane; i < unseen; i += 32) {
-    const int j = begin + i < lo ? begin + i : hi + (i - (lo - begin));
-    const int page = page_of(p, t.b, j / p.page_size);
-    if (page < 0) continue;
-    const uint16_t *v = p.v + page * p.v_page + kv_head * p.v_head + (j % p.page_size) * p.v_row;
-    for (int d = 0; d < p.D; d += 2) {
-      const uint32_t x = *reinterpret_cast<const uint32_t *>(v + d);
-      odd |= !isfinite(A::lo(x)) || !isfinite(A::hi(x));
-    }
-  }
-  if (!__any_sync(0xffffffffu, odd)) return;
-  auto score = [&](int j) {
-    const int page = page_of(p, t.b, j / p.page_size);
-    if (page < 0) return 0.0f;
-    const uint16_t *k = p.k + page * p.k_page + kv_head * p.k_head + (j % p.page_size) * p.k_row;
-    float s = 0.0f;
-#pragma unroll 4
-    for (int d = 0; d < p.D; d += 8) {
-      const uint4 a = *reinterpret_cast<const uint4 *>(q + d), b = *reinterpret_cast<const uint4 *>(k + d);
-      const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        s = fmaf(A::lo(x[i]), A::lo(y[i]), s);
-        s = fmaf(A::hi(x[i]), A::hi(y[i]), s);
+  const int64_t at = (token * p.heads + head) * p.D;
+  float *part = t.s.splits > 1 ? p.part + t.split * static_cast<int64_t>(p.T) * p.heads * p.D + at : nullptr;
+  __syncwarp();
+  // the keys before those that all see, and behind them
+  const int begin = max(t.k0, t.first), lo_end = min(max(t.all_lo, begin), t.k1);
+#pragma unroll 1
+  for (int side = 0; side < 2; ++side) {
+    const int from = side ? max(max(begin, t.all_hi), lo_end) : begin, to = side ? t.k1 : lo_end;
+    for (int first = from; first < to; first += 32) {
+      // each lane a key: where its value lies, and whether something in it is odd
+      const int mine = first + lane;
+      uint64_t v_at = 0, k_at = 0;
+      bool odd = false;
+      if (mine < to) {
+        const int page = page_of(p, t.b, mine / p.page_size);
+        if (page >= 0) {
+          const uint16_t *v = p.v + page * p.v_page + kv_head * p.v_head + (mine % p.page_size) * p.v_row;
+          v_at = reinterpret_cast<uint64_t>(v);
+          k_at = reinterpret_cast<uint64_t>(p.k + page * p.k_page + kv_head * p.k_head + (mine % p.page_size) * p.k_row);
+          for (int c = 0; c < p.D; c += 8) odd |= Odd<A>::of(*reinterpret_cast<const uint4 *>(v + c)) != 0;
+        }
       }
-    }
-    return s * p.scale_log2;
-  };
-  float m = -INFINITY, sum = 0.0f;        // of the lane's keys
-  for (int j = lo + lane; j < hi; j += 32) {
-    const float s = score(j), now = fmaxf(m, s);
-    if (now == -INFINITY) continue;
-    sum = sum * ex2(m - now) + ex2(s - now);
-    m = now;
-  }
-  float top = m;
-#pragma unroll
-  for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-  const float base = top == -INFINITY ? 0.0f : top;
-  sum *= ex2(m - base);
-#pragma unroll
-  for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int j0 = lo; j0 < hi; j0 += 32) {
-    // each lane a key: its weight, and where its value lies (0: nowhere)
-    float mine = 0.0f;
-    uint64_t mine_at = 0;
-    if (j0 + lane < hi) {
-      mine = ex2(score(j0 + lane) - base) * inv;
-      const int page = page_of(p, t.b, (j0 + lane) / p.page_size);
-      if (page >= 0)
-        mine_at = reinterpret_cast<uint64_t>(p.v + page * p.v_page + kv_head * p.v_head +
-                                             ((j0 + lane) % p.page_size) * p.v_row);
-    }
-#pragma unroll 8
-    for (int i = 0; i < 32; ++i) {
-      const float w = __shfl_sync(0xffffffffu, mine, i);
-      const auto *v = reinterpret_cast<const uint16_t *>(__shfl_sync(0xffffffffu, mine_at, i));
-      if (!v) continue;
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int d = 2 * lane + 64 * x;
-        const uint32_t c = d < p.D ? *reinterpret_cast<const uint32_t *>(v + d) : 0u;
-        o[2 * x] = fmaf(w, A::lo(c), o[2 * x]);
-        o[2 * x + 1] = fmaf(w, A::hi(c), o[2 * x + 1]);
+      const unsigned keys = __ballot_sync(0xffffffffu, odd);
+      if (!keys) continue;
+      // which of them the lane's row sees, and of those the ones of weight 0 (0 * inf is NaN)
+      unsigned seen = 0, none = 0;
+      for (unsigned left = keys; left; left &= left - 1) {
+        const int i = __ffs(left) - 1, key = first + i;
+        const auto *k = reinterpret_cast<const uint16_t *>(__shfl_sync(0xffffffffu, k_at, i));
+        if (lane >= rows || key > pos || (p.window && key <= pos - p.window)) continue;
+        seen |= 1u << i;
+        float s = 0.0f;
+        for (int c = 0; c < p.D; c += 2) {
+          const uint32_t x = *reinterpret_cast<const uint32_t *>(q + c), y = *reinterpret_cast<const uint32_t *>(k + c);
+          s = fmaf(A::hi(x), A::hi(y), fmaf(A::lo(x), A::lo(y), s));
+        }
+        if (s == -INFINITY) none |= 1u << i;
+      }
+      for (int c = 0; c < p.D; c += 2) {
+        float lo = 0.0f, hi = 0.0f;
+        for (unsigned left = keys; left; left &= left - 1) {
+          const int i = __ffs(left) - 1;
+          const auto *v = reinterpret_cast<const uint16_t *>(__shfl_sync(0xffffffffu, v_at, i));
+          const uint32_t x = *reinterpret_cast<const uint32_t *>(v + c), which = Odd<A>::of(x);
+          if (!(seen >> i & 1)) continue;
+          const float w = none >> i & 1 ? 0.0f : 1.0f;
+          if (which & 0x8000u) lo = fmaf(w, A::lo(x), lo);
+          if (which >> 16) hi = fmaf(w, A::hi(x), hi);
+        }
+        if (part) {
+          if (lo != 0.0f) part[c] = __ldcg(part + c) + lo;
+          if (hi != 0.0f) part[c + 1] = __ldcg(part + c + 1) + hi;
+        } else if (lo != 0.0f || hi != 0.0f) {
+          uint32_t *out = reinterpret_cast<uint32_t *>(p.out + at + c);
+          const uint32_t x = __ldcg(out);
+          *out = A::pack2(lo != 0.0f ? A::lo(x) + lo : A::lo(x), hi != 0.0f ? A::hi(x) + hi : A::hi(x));
+        }
       }
     }
   }
-  const int64_t at = token * p.heads + head;
-#pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    const int d = 2 * lane + 64 * x;
-    if (d >= p.D) continue;
-    if (t.s.splits > 1) {
-      float *dst = p.part + (t.split * static_cast<int64_t>(p.T) * p.heads + at) * p.D + d;
-      dst[0] = o[2 * x];
-      dst[1] = o[2 * x + 1];
-    } else {
-      *reinterpret_cast<uint32_t *>(p.out + at * p.D + d) = A::pack2(o[2 * x], o[2 * x + 1]);
-    }
-  }
-  if (t.s.splits > 1 && lane == 0)
-    p.part_lse[t.split * static_cast<int64_t>(p.T) * p.heads + at] = sum == 0.0f ? -INFINITY : base + __log2f(sum);
 }
 
 // The form of a call, a function of its sizes alone: the plan and the attention work it

@@ -172,28 +172,15 @@ struct ItemCursor {
 
 __device__ __forceinline__ int tiles_of_item(const Item *t) { return (t->k1 - t->k0 + kKeys - 1) / kKeys; }
 
-// Rows of one warp (of four of a row tile) that came out infinite or NaN, in all items of the
-// CTA: once the warp is through with them and no other one waits for it, since they may take long.
+// The odd values taken out of the tiles of all items of the CTA, for the rows of one warp (of four of
+// a row tile): once the row tiles are through with them and no other warp waits.
 template <class A>
-__device__ __noinline__ void redo_rows(const AttnParams &p, int tile, int quarter, int total) {
-  const int lane = static_cast<int>(lane_id());
-  __syncwarp();
+__device__ __noinline__ void add_odd_values(const AttnParams &p, int tile, int quarter, int total) {
 #pragma unroll 1
   for (int step = 0, id; (id = item_of(step)) < total; ++step) {
     const Item t = find_item(p, id);
     const int first = (t.pair ? 0 : tile * kRows) + quarter * 32, kv_head = t.head + (t.pair ? tile : 0);
-    const int n = min(t.rows - first, 32);
-#pragma unroll 1
-    for (int r = first; r < first + n; ++r) {
-      int64_t token;
-      int head, pos;
-      row_of(p, t, kv_head, r, token, head, pos);
-      const int64_t at = token * p.heads + head, part = t.split * static_cast<int64_t>(p.T) * p.heads + at;
-      bool odd = false;
-      for (int d = lane; d < p.D; d += 32)
-        odd |= !isfinite(t.s.splits > 1 ? __ldcg(p.part + part * p.D + d) : A::lo(__ldcg(p.out + at * p.D + d)));
-      if (__any_sync(0xffffffffu, odd)) exact_row<A>(p, t, kv_head, r);
-    }
+    if (t.rows > first) add_odd<A>(p, t, kv_head, first, min(t.rows - first, 32));
   }
 }
 
@@ -209,6 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ Item items[kItems];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_word;
+  __shared__ int taken;          // values were taken out of V
   volatile int *abort_flag = &abort_word;
   unsigned int *err = &g_attn_error;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -238,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bar.item_empty[i], kItemReaders);
     }
     mbar_init(&bar.mma_done, 1);
-    abort_word = 0;
+    abort_word = taken = 0;
     fence_mbar_init();
     prefetch_tensormap(&maps.k);
     prefetch_tensormap(&maps.v);
@@ -318,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       load_q(t);
       q_loaded();
     }
-    bool ok = true, again = false;
+    bool ok = true;
     while (t) {
       const int n = tiles_of_item(t);
       const int base_row = row_base(t), mine = t->rows - base_row;      // live rows of the tile
@@ -353,19 +341,33 @@ __global__ void __launch_bounds__(kThreads, 1)
           after = cursor.next(bar, items, abort_flag, p.timeout_ns, err);
           if (after && needs_q(after)) load_q(after);
         }
-        if ((t->pair || tile == 0) && (key0 + kKeys > t->k1 || key0 < t->first)) {
-          // rows of V that no row of the item sees may hold anything: a weight of 0 does
-          // not take out infinities or NaN.  (Before both tiles' products: tile 0's go
+        if ((t->pair || tile == 0) && !all_seen(*t, key0, kKeys)) {
+          // rows of V that no row of the item sees, or not every one, may hold anything: a weight of 0
+          // does not take out infinities or NaN.  (Before both tiles' products: tile 0's go
           // first; of a pair, each has its own.)
           const uint32_t at = v_count + (t->pair ? 2 * i + tile : i);
           if (!(ok = wait_all(&bar.v_full[at % VS], (at / VS) & 1, abort_flag, p.timeout_ns, err))) break;
-          if (key0 + r >= t->k1 || key0 + r < t->first) {
-            uint8_t *v = v_smem + (at % VS) * S::kTileBytes + r * 128;
+          const int key = key0 + r;
+          uint8_t *v = v_smem + (at % VS) * S::kTileBytes + r * 128;
+          // (neighbouring lanes in different banks)
+          auto piece = [&](int c) {
+            return reinterpret_cast<uint4 *>(v + (c >> 3) * S::kHalfBytes + (((c ^ r) & 7) << 4));
+          };
+          if (key >= t->k1 || key < t->first) {
 #pragma unroll
-            for (int c = 0; c < DP / 8; ++c)
-              *reinterpret_cast<uint4 *>(v + (c >> 3) * S::kHalfBytes + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+            for (int c = 0; c < DP / 8; ++c) *piece(c) = make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
+          } else if (!all_seen(*t, key, 1)) {
+            uint32_t sum[2] = {0, 0};
+#pragma unroll
+            for (int c = 0; c < DP / 8; ++c) Odd<A>::gather(*piece(c), sum);
+            if (Odd<A>::of(sum[0]) | Odd<A>::of(sum[1])) {
+#pragma unroll 1
+              for (int c = 0; c < DP / 8; ++c) *piece(c) = Odd<A>::without(*piece(c));
+              taken = 1;
+              fence_proxy_async_smem();
+            }
           }
-          fence_proxy_async_smem();
         }
         if (warp_live) {
           float s[128];
@@ -464,7 +466,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint8_t *const to = split ? reinterpret_cast<uint8_t *>(p.part) : reinterpret_cast<uint8_t *>(p.out);
         const int size = split ? 4 : 2;
         const int64_t mine_at = live ? (split ? part_at : at) * p.D * size : -1;
-        float odd = 0.0f;             // 0 times every value: NaN if one is not finite
         // (loops that run once a tile or less are not unrolled: a call of few items spends much of its
         // time on fetching code)
 #pragma unroll 1
@@ -476,10 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           float y[32];
 #pragma unroll
-          for (int x = 0; x < 32; ++x) {
-            y[x] = sum == 0.0f ? 0.0f : __uint_as_float(o[x]) * inv;
-            odd = fmaf(y[x], 0.0f, odd);
-          }
+          for (int x = 0; x < 32; ++x) y[x] = sum == 0.0f ? 0.0f : __uint_as_float(o[x]) * inv;
           // 8 lanes turn their rows so that a store covers runs of each row: 128 bytes of f32, or 64
           // of the type, 4 lanes to a row
           if (split) {
@@ -513,13 +511,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         debug_check(!live || (token >= 0 && token < p.T && head >= 0 && head < p.heads), err);
         if (split && live) p.part_lse[part_at] = sum == 0.0f ? -INFINITY : base + __log2f(sum);
         tc_fence_before();
-        again |= __any_sync(0xffffffffu, live && odd != 0.0f && sum == sum);
       }
       cursor.done(bar, 1);
       t = after;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-    if (again && ok) redo_rows<A>(p, tile, warp & 3, total);
+    // (all row tiles' warps: what one has taken out another may have to add)
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+    if (taken && !*abort_flag) add_odd_values<A>(p, tile, warp & 3, total);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == kWarpMma) {
