@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2)
   uint8_t *ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   __shared__ float warp_m[kRowWarps][16], warp_l[kRowWarps][16];
   __shared__ uint64_t full[kRowWarps][kRowStages];
-  __shared__ int redo;           // values were taken out of V
+  __shared__ int taken;          // values were taken out of V
   __shared__ int abort_word;
   volatile int *abort_flag = &abort_word;
   unsigned int *err = &g_rows_error;
@@ -316,7 +316,7 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2)
     const Item t = find_item(p, id);
     if (id >= total) break;
     __syncthreads();      // the ring of the item before is free, its flags have been read
-    if (tid == 0) redo = 0;
+    if (tid == 0) taken = 0;
     const int runs = (t.k1 - t.k0 + KEYS - 1) / KEYS;       // of the item
     const int my_runs = runs > warp ? (runs - warp + kRowWarps - 1) / kRowWarps : 0;
     const int kv_head = __shfl_sync(0xffffffffu, t.head, 0);
@@ -505,7 +505,7 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2)
     }
     __syncthreads();
     if (*abort_flag) break;
-    if (odd) redo = 1;
+    if (odd) taken = 1;
     // the warps' sums, in the rings' place
     constexpr int PITCH = DP + 4;
     float *sum = reinterpret_cast<float *>(ring);
@@ -564,8 +564,8 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2)
     }
     // (a warp's rows are those it has written)
     constexpr int kOfWarp = 16 / kRowWarps;
-    if (redo && t.rows > warp * kOfWarp)
-      add_odd<A>(p, t, t.head, warp * kOfWarp, min(t.rows - warp * kOfWarp, kOfWarp));
+    const int mine0 = warp * kOfWarp;
+    if (taken && t.rows > mine0) add_odd<A>(p, t, t.head, mine0, min(t.rows - mine0, kOfWarp));
   }
   // given up: the copies in flight
   if (*abort_flag)
