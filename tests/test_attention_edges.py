@@ -86,3 +86,37 @@ def test_a_long_tail_behind_one_large_weight(dt, tokens, late, score, keys):
     err = (got - want).abs()
     bound = want * rel + least * value * n[:, None, None]
     assert (err <= bound).all(), (float(err.max()), float((err / bound).max()))
+
+
+@pytest.mark.parametrize("dt", [torch.float16, torch.bfloat16], ids=["f16", "bf16"])
+@pytest.mark.parametrize("tokens", [3, 200], ids=["few", "tile"])
+@pytest.mark.parametrize("step", [64.0, 4096.0, 32768.0])
+@pytest.mark.parametrize("order", ["up", "down", "twice"])
+def test_scores_far_from_zero(dt, tokens, step, order):
+    """Scores of up to 2^24, exact in f32, hundreds apart: all the weight on the largest one that a row
+    sees, or on two equal ones, wherever the bases of the rows lie."""
+    keys, D = 250, 64
+    s = Step([(tokens, keys)], 4, 2, D, 16, dt=dt)
+    s.scale = 2.0
+    s.q.zero_(), s.k.zero_()
+    s.q[..., 0] = step
+    p = torch.arange(keys, device="cuda")
+    at = {"up": p, "down": -p, "twice": p // 2}[order]
+    rows = s.table[0].long()[p // 16], slice(None), p % 16
+    k = s.k[rows]
+    k[..., 0] = at[:, None].to(dt)
+    s.k[rows] = k
+    v = s.v[rows].double()                                           # [keys, kv_heads, D]
+    pos = torch.arange(keys - tokens, keys, device="cuda")
+    if order == "up":
+        want = v[pos]
+    elif order == "down":
+        want = v[torch.zeros_like(pos)]
+    else:
+        want = torch.where((pos % 2 == 0)[:, None, None], v[pos], (v[pos] + v[pos - 1]) / 2)
+    got = s.attend().double().unflatten(1, (2, 2))
+    # weights of one or two equal powers of two, or their roundings alike: v's rounding at the end, and
+    # with two a sum of the same size (f32 between: 2^-20)
+    half = {torch.float16: 2.0 ** -11, torch.bfloat16: 2.0 ** -8}[dt]
+    err, size = (got - want[:, :, None]).abs(), v.abs().amax()
+    assert (err <= want[:, :, None].abs() * half * 2 + size * (2.0 ** -20 + 2 * half)).all(), float(err.max())

@@ -109,3 +109,21 @@ def test_they_hold_nobody_up(n, total, many):
     p = torch.arange(total - many, total, device="cuda")
     s.v[s.table[0].long()[p // 64], :, p % 64] = math.inf
     assert milliseconds(lambda: s.attend(plan)) < clean + 20.0
+
+
+@pytest.mark.parametrize("seqs,window", [([(5, 3), (1, 30)], 0), ([(40, 25), (2, 9)], 0), ([(40, 25), (6, 2)], 4), ([(300, 180)], 0)])
+def test_tokens_before_the_first_key(seqs, window):
+    """More new tokens than the length counts: those before its first key see nothing, whatever
+    the others' keys hold, among pages that are not in the cache."""
+    s = Step(seqs, 4, 2, 64, 8, window=window)
+    s.table[0, 1] = -1
+    n, total = seqs[0]
+    clean = s.attend()
+    assert (clean[:n - total] == 0).all()
+    for at in (0, total - 1):
+        s.v[int(s.table[0, at // 8]), 1, at % 8, 5] = math.inf
+    got = s.attend()
+    rows = seers(s, 0, 0) | seers(s, 0, total - 1)
+    assert (got[rows][:, 2:, 5] == math.inf).all()
+    got[:, 2:, 5] = torch.where(rows[:, None], clean[:, 2:, 5], got[:, 2:, 5])
+    assert torch.equal(got, clean)
