@@ -259,8 +259,8 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 // ring of its own, which it fills by TMA (boxes of 8 to 32 rows of a page), and a softmax of its
 // own (no barrier over the CTA in the loop); the warps' results meet at the end.
 //
-// HBM-bound: 64 sequences of 128 to 16000 keys, 8 kv heads of 128: 156 us for 983 MB, 6.3 TB/s. With few
-// keys latency: 4 sequences of up to 180 keys take 5.5 us.
+// HBM-bound: 64 sequences of 128 to 16000 keys, 8 kv heads of 128: 152 us for 983 MB, 6.4 TB/s. With few
+// keys latency: 4 sequences of up to 180 keys take 6 us.
 template <class A, int DP>
 __global__ void __launch_bounds__(32 * kRowWarps, 2)
     attn_rows_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CacheMaps maps) {

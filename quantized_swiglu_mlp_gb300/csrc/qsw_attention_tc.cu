@@ -18,7 +18,7 @@
 // What bounds it (GB300): the products.  A step of two row tiles and 128 keys is four products of
 // 128 x 128 x 128, 2048 cycles at the full rate and about 2480 as measured alone, since S takes
 // both operands from shared memory, at all it delivers.  A prompt of 8192 tokens with 32 heads of 128
-// takes 341 us, 1.61 PFLOP/s.  (Two tiles of 64 rows, or one tile and the keys of two, would
+// takes 337 us, 1.63 PFLOP/s.  (Two tiles of 64 rows, or one tile and the keys of two, would
 // read K and V twice as often.)
 //
 // The base of a row is raised (and O rescaled in tensor memory) only when a score passes
